@@ -38,8 +38,9 @@
 extern "C" {
 #endif
 
-/* element types: input, output and (internally) fp32 accumulation */
-enum { TG_F16 = 0, TG_BF16 = 1 };
+/* element types: input, output and (internally) fp32 accumulation; TG_F32 is taken by the training
+   operators only */
+enum { TG_F16 = 0, TG_BF16 = 1, TG_F32 = 2 };
 
 /* kernel variants (tg_gemm_persistent_ex, tg_gemm_persistent_debug, tg_gemm_launch_shape) */
 enum {
@@ -357,6 +358,66 @@ int tg_gemm_mxfp8_debug(const void* A_dev, const void* SFA_dev, const void* B_de
                         const void* SFB_dev, void* C_dev, int64_t M, int64_t N, int64_t K,
                         int out_dtype, void* stream, int flags, int32_t* trace_dev,
                         uint64_t watchdog_ns, int64_t inject_skip_phase);
+
+/*
+ * ---- Training operators around the GEMM: layer norm, activation checkpoints in 8 bits, and what
+ * the backward pass takes from them.  Matrices are [rows, cols] with unit stride along a row and
+ * a row stride ``ld`` >= cols given in elements; rows and cols are >= 0 and < 2^31.  Any element
+ * alignment is accepted; rows that start on 16-byte boundaries are moved in wider accesses.  No
+ * output may overlap an input or another output.  Asynchronous on ``stream``, deterministic, no
+ * allocation; errors as for tg_gemm_persistent.
+ *
+ * A checkpoint of x [rows, cols] is two arrays: q [rows, 32 ceil(cols / 32)] of E4M3 bytes, 16-byte
+ * aligned, zero past column ``cols``, and s [rows, ceil(cols / 32)] of E8M0 bytes; it stands for
+ * the values q * 2^(s - 127).  For cols % 128 == 0 they are an operand of tg_gemm_mxfp8 (s by way
+ * of tg_mxfp8_pack_scales).  A scale is 2^(floor(log2 amax) - 8) with amax over the finite values
+ * of 32 neighbours and the exponent clamped to [-127, 127]; quotients are rounded to nearest even
+ * and saturate at 448 (a block's largest value can so lose up to 1/8 of itself).  NaN and
+ * infinities become NaN.  As an input, any bytes are valid: E4M3 NaN and scale 255 stand for NaN.
+ */
+
+/*
+ * tg_layernorm_fwd -- y = (x - mean) rstd gamma + beta, row by row, in 32 bits and rounded once;
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps).
+ *   x_dev, y_dev: [rows, cols] of ``dtype`` (TG_F16, TG_BF16 or TG_F32).  gamma_dev, beta_dev:
+ *   [cols] of ``param_dtype`` (TG_F32 or dtype); NULL: ones, zeros.  mean_dev, rstd_dev: [rows]
+ *   fp32, either may be NULL.  yq_dev, ys_dev: NULL, or a checkpoint of the rounded y, made in the
+ *   same pass.  rows == 0 or cols == 0: nothing is done.  A row with a NaN or an infinity gives NaN.
+ */
+int tg_layernorm_fwd(const void* x_dev, const void* gamma_dev, const void* beta_dev, void* y_dev,
+                     float* mean_dev, float* rstd_dev, void* yq_dev, void* ys_dev, int64_t rows,
+                     int64_t cols, int64_t ld_x, int64_t ld_y, int dtype, int param_dtype,
+                     float eps, void* stream);
+
+/*
+ * tg_layernorm_bwd -- the gradients of tg_layernorm_fwd.  With xh = (x - mean) rstd and g = dy gamma:
+ *     dx = rstd (g - sum g / cols - xh sum (g xh) / cols)
+ *     dgamma = sum over rows of dy xh,   dbeta = sum over rows of dy
+ *   dy_dev, dx_dev: [rows, cols] of ``dtype``; x_dev the same, or NULL with xq_dev, xs_dev a
+ *   checkpoint of x.  gamma_dev as in the forward pass; mean_dev, rstd_dev: what it wrote.
+ *   dgamma_dev, dbeta_dev: [cols] of ``param_dtype``, either may be NULL; sums are kept in fp32 and
+ *   added in a fixed order.  workspace_dev (256-byte aligned): tg_layernorm_bwd_workspace_bytes
+ *   bytes, needed when dgamma or dbeta is asked for, in use until the call's work is done.
+ *   rows == 0: dgamma and dbeta are zero-filled.  cols == 0: nothing is done.
+ */
+int tg_layernorm_bwd(const void* dy_dev, const void* x_dev, const void* xq_dev, const void* xs_dev,
+                     const void* gamma_dev, const float* mean_dev, const float* rstd_dev,
+                     void* dx_dev, void* dgamma_dev, void* dbeta_dev, int64_t rows, int64_t cols,
+                     int64_t ld_dy, int64_t ld_x, int64_t ld_dx, int dtype, int param_dtype,
+                     void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* Workspace of tg_layernorm_bwd on the current device, in bytes; negative: an error. */
+int64_t tg_layernorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+
+/* tg_ckpt8_pack -- the checkpoint q, s of x [rows, cols] of ``dtype``. */
+int tg_ckpt8_pack(const void* x_dev, void* q_dev, void* s_dev, int64_t rows, int64_t cols,
+                  int64_t ld_x, int dtype, void* stream);
+
+/* tg_ckpt8_unpack -- out [rows, cols] of ``dtype``: the values a checkpoint stands for, rounded
+   once to nearest even (bf16 and fp32 hold what was packed from them exactly, fp16 what was packed
+   from fp16). */
+int tg_ckpt8_unpack(const void* q_dev, const void* s_dev, void* out_dev, int64_t rows, int64_t cols,
+                    int64_t ld_out, int dtype, void* stream);
 
 #ifdef __cplusplus
 }

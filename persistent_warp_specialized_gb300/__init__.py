@@ -9,6 +9,7 @@ is missing or fails to load, every call raises.
 Build the library with ``persistent_warp_specialized_gb300._build.build()`` (nvcc, sm_103a).
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -17,6 +18,7 @@ LIB_PATH = os.path.join(HERE, "libtg.so")
 
 TG_F16 = 0
 TG_BF16 = 1
+TG_F32 = 2                 # the training operators only
 TG_OK = 0
 TG_ERR_ARG = -1
 TG_ERR_ALIGN = -2
@@ -38,7 +40,7 @@ TG_SCHEDULE_NOALLOC_MAX_UNITS = 65536   # scratch rows of tg_tile_schedule_noall
 VARIANTS = {"auto": TG_VARIANT_AUTO, "single": TG_VARIANT_SINGLE, "pair": TG_VARIANT_PAIR,
             "wide": TG_VARIANT_PAIR_WIDE}
 
-DTYPES = {"f16": TG_F16, "bf16": TG_BF16}
+DTYPES = {"f16": TG_F16, "bf16": TG_BF16, "f32": TG_F32}
 
 EXPORTED = (
     "tg_gemm_persistent",
@@ -59,6 +61,11 @@ EXPORTED = (
     "tg_gemm_mxfp8_debug",
     "tg_mxfp8_scale_bytes",
     "tg_mxfp8_pack_scales",
+    "tg_layernorm_fwd",
+    "tg_layernorm_bwd",
+    "tg_layernorm_bwd_workspace_bytes",
+    "tg_ckpt8_pack",
+    "tg_ckpt8_unpack",
 )
 
 
@@ -122,6 +129,17 @@ def load_library(path=LIB_PATH):
     lib.tg_mxfp8_scale_bytes.restype = i64
     lib.tg_mxfp8_pack_scales.argtypes = [vp, vp, i64, i64, vp]
     lib.tg_mxfp8_pack_scales.restype = i32
+    f32 = ctypes.c_float
+    lib.tg_layernorm_fwd.argtypes = [vp] * 8 + [i64] * 4 + [i32, i32, f32, vp]
+    lib.tg_layernorm_fwd.restype = i32
+    lib.tg_layernorm_bwd.argtypes = [vp] * 10 + [i64] * 5 + [i32, i32, vp, i64, vp]
+    lib.tg_layernorm_bwd.restype = i32
+    lib.tg_layernorm_bwd_workspace_bytes.argtypes = [i64, i64]
+    lib.tg_layernorm_bwd_workspace_bytes.restype = i64
+    lib.tg_ckpt8_pack.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp]
+    lib.tg_ckpt8_pack.restype = i32
+    lib.tg_ckpt8_unpack.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp]
+    lib.tg_ckpt8_unpack.restype = i32
     _lib = lib
     return lib
 
@@ -388,4 +406,202 @@ def mxfp8_gemm(a, sa, b, sb, out=None, out_dtype="bf16", stream=None):
                           device=a.device)
     tg_gemm_mxfp8(a, mxfp8_pack(sa, K, stream), b, mxfp8_pack(sb, K, stream), out, M, N, K,
                   out_dtype, stream)
+    return out
+
+
+# ---------------------------------------------------------------- training operators
+def tg_layernorm_fwd(x, gamma, beta, y, mean, rstd, yq, ys, rows, cols, ld_x, ld_y, dtype,
+                     param_dtype="f32", eps=1e-5, stream=None):
+    """y = layer norm of the rows of x; optionally the statistics and y's 8-bit checkpoint."""
+    return _check(load_library().tg_layernorm_fwd(
+        _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd), _ptr(yq), _ptr(ys),
+        rows, cols, ld_x, ld_y, _dtype(dtype), _dtype(param_dtype), eps, _stream(stream)))
+
+
+def tg_layernorm_bwd(dy, x, xq, xs, gamma, mean, rstd, dx, dgamma, dbeta, rows, cols, ld_dy, ld_x,
+                     ld_dx, dtype, param_dtype="f32", workspace=None, stream=None,
+                     workspace_bytes=None):
+    """The gradients of tg_layernorm_fwd, from x or from its checkpoint (xq, xs)."""
+    return _check(load_library().tg_layernorm_bwd(
+        _ptr(dy), _ptr(x), _ptr(xq), _ptr(xs), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
+        _ptr(dgamma), _ptr(dbeta), rows, cols, ld_dy, ld_x, ld_dx, _dtype(dtype),
+        _dtype(param_dtype), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+        _stream(stream)))
+
+
+def tg_layernorm_bwd_workspace_bytes(rows, cols):
+    return _check(load_library().tg_layernorm_bwd_workspace_bytes(rows, cols))
+
+
+def tg_ckpt8_pack(x, q, s, rows, cols, ld_x, dtype, stream=None):
+    return _check(load_library().tg_ckpt8_pack(_ptr(x), _ptr(q), _ptr(s), rows, cols, ld_x,
+                                               _dtype(dtype), _stream(stream)))
+
+
+def tg_ckpt8_unpack(q, s, out, rows, cols, ld_out, dtype, stream=None):
+    return _check(load_library().tg_ckpt8_unpack(_ptr(q), _ptr(s), _ptr(out), rows, cols, ld_out,
+                                                 _dtype(dtype), _stream(stream)))
+
+
+class Checkpoint8:
+    """Activations [rows, cols] kept in 8 bits: q, uint8 E4M3 bytes [rows, 32 ceil(cols / 32)], and
+    s, uint8 E8M0 scales [rows, ceil(cols / 32)], standing for q * 2^(s - 127).  Both contiguous."""
+
+    __slots__ = ("q", "s", "cols")
+
+    def __init__(self, q, s, cols):
+        nb = (cols + 31) // 32
+        rows = q.shape[0] if q.dim() == 2 else -1
+        if q.shape != (rows, 32 * nb) or s.shape != (rows, nb):
+            raise ValueError(f"a checkpoint of {cols} columns is q [rows, {32 * nb}] and "
+                             f"s [rows, {nb}], not {tuple(q.shape)} and {tuple(s.shape)}")
+        if q.element_size() != 1 or s.element_size() != 1:
+            raise TypeError("q and s must be byte tensors")
+        if not (q.is_contiguous() and s.is_contiguous()):
+            raise ValueError("q and s must be contiguous")
+        self.q, self.s, self.cols = q, s, cols
+
+    @property
+    def rows(self):
+        return self.q.shape[0]
+
+    @classmethod
+    def empty(cls, rows, cols, device):
+        """An unfilled checkpoint of [rows, cols] values."""
+        import torch
+
+        nb = (cols + 31) // 32
+        return cls(torch.empty((rows, 32 * nb), dtype=torch.uint8, device=device),
+                   torch.empty((rows, nb), dtype=torch.uint8, device=device), cols)
+
+
+def _allocating_on(stream):
+    """Context in which torch allocates for ``stream``, so that memory freed after the call returns
+    is handed out again only to work that follows on it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
+                             else stream)
+
+
+_TYPE_NAMES = None
+
+
+def _type_name(dtype):
+    global _TYPE_NAMES
+    if _TYPE_NAMES is None:
+        import torch
+
+        _TYPE_NAMES = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}
+    if dtype not in _TYPE_NAMES:
+        raise TypeError(f"{dtype} is not float16, bfloat16 or float32")
+    return _TYPE_NAMES[dtype]
+
+
+def _rows_of(x, name):
+    """(rows, cols, row stride) of a 2-D tensor with unit stride along its rows."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D tensor with unit stride along its rows")
+    rows, cols = x.shape
+    ld = x.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return rows, cols, ld
+
+
+def _param_type(dtype, cols, **params):
+    """The common type name of the parameters given (f32 if none), each [cols] and contiguous."""
+    found = set()
+    for name, p in params.items():
+        if p is None:
+            continue
+        if tuple(p.shape) != (cols,) or not p.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of {cols} values")
+        found.add(_type_name(p.dtype))
+    if len(found) > 1 or (found and not found <= {"f32", dtype}):
+        raise TypeError("parameters must all be float32, or all of the values' type")
+    return found.pop() if found else "f32"
+
+
+def layer_norm(x, gamma=None, beta=None, eps=1e-5, out=None, checkpoint=False, stream=None):
+    """torch convenience: (y, mean, rstd) of a CUDA tensor x [rows, cols] (float16, bfloat16 or
+    float32), normalised along its rows; with ``checkpoint`` also y's Checkpoint8, made in the same
+    pass.  gamma, beta: [cols] of float32 or x's type, or None."""
+    import torch
+
+    dtype = _type_name(x.dtype)
+    rows, cols, ld_x = _rows_of(x, "x")
+    params = _param_type(dtype, cols, gamma=gamma, beta=beta)
+    if out is not None and (out.dtype != x.dtype or out.shape != x.shape):
+        raise ValueError("out must have x's shape and type")
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        kept = Checkpoint8.empty(rows, cols, x.device) if checkpoint else None
+    ld_y = _rows_of(out, "out")[2]
+    tg_layernorm_fwd(x, gamma, beta, out, mean, rstd, kept.q if kept else None,
+                     kept.s if kept else None, rows, cols, ld_x, ld_y, dtype, params, eps, stream)
+    return (out, mean, rstd, kept) if checkpoint else (out, mean, rstd)
+
+
+def layer_norm_backward(dy, x, mean, rstd, gamma=None, stream=None):
+    """torch convenience: (dx, dgamma, dbeta) of layer_norm from dy [rows, cols], the statistics it
+    returned, and x as a tensor or as its Checkpoint8.  dgamma and dbeta have gamma's type (float32
+    without gamma)."""
+    import torch
+
+    dtype = _type_name(dy.dtype)
+    rows, cols, ld_dy = _rows_of(dy, "dy")
+    params = _param_type(dtype, cols, gamma=gamma)
+    kept = x if isinstance(x, Checkpoint8) else None
+    if kept is not None:
+        if (kept.rows, kept.cols) != (rows, cols):
+            raise ValueError("the checkpoint and dy differ in shape")
+        ld_x = cols
+    else:
+        if x.dtype != dy.dtype or x.shape != dy.shape:
+            raise ValueError("x and dy must have the same shape and type")
+        ld_x = _rows_of(x, "x")[2]
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or tuple(t.shape) != (rows,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of {rows} values")
+    nbytes = tg_layernorm_bwd_workspace_bytes(rows, cols)
+    pt = gamma.dtype if gamma is not None else torch.float32
+    with _allocating_on(stream):
+        dx = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
+        dgamma = torch.empty(cols, dtype=pt, device=dy.device)
+        dbeta = torch.empty(cols, dtype=pt, device=dy.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes else None
+    tg_layernorm_bwd(dy, None if kept else x, kept.q if kept else None, kept.s if kept else None,
+                     gamma, mean, rstd, dx, dgamma, dbeta, rows, cols, ld_dy, ld_x, cols, dtype,
+                     params, ws, stream)
+    return dx, dgamma, dbeta
+
+
+def ckpt8_pack(x, stream=None):
+    """torch convenience: the Checkpoint8 of a CUDA tensor x [rows, cols]."""
+    dtype = _type_name(x.dtype)
+    rows, cols, ld = _rows_of(x, "x")
+    with _allocating_on(stream):
+        kept = Checkpoint8.empty(rows, cols, x.device)
+    tg_ckpt8_pack(x, kept.q, kept.s, rows, cols, ld, dtype, stream)
+    return kept
+
+
+def ckpt8_unpack(kept, dtype, out=None, stream=None):
+    """torch convenience: the values of a Checkpoint8 as a tensor of ``dtype``."""
+    import torch
+
+    name = _type_name(dtype)
+    if out is None:
+        with _allocating_on(stream):
+            out = torch.empty((kept.rows, kept.cols), dtype=dtype, device=kept.q.device)
+    elif out.dtype != dtype or tuple(out.shape) != (kept.rows, kept.cols):
+        raise ValueError("out must have the checkpoint's shape and the type asked for")
+    tg_ckpt8_unpack(kept.q, kept.s, out, kept.rows, kept.cols, _rows_of(out, "out")[2], name,
+                    stream)
     return out

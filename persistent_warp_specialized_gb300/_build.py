@@ -2,7 +2,7 @@
 
     python -m persistent_warp_specialized_gb300._build [--force] [-v]
 
-Two translation units compile in parallel (the kernels, and the C-ABI host code) and are
+Four translation units compile in parallel (kernels and C-ABI host code) and are
 linked into ``persistent_warp_specialized_gb300/libtg.so`` with the CUDA runtime linked
 statically.  A stamp of the sources and flags skips rebuilding when nothing changed.
 """
@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libtg.so")
 STAMP = os.path.join(BUILD_DIR, "libtg.stamp")
 
-SOURCES = ["tg_gemm.cu", "tg_api.cu"]
+SOURCES = ["tg_gemm.cu", "tg_train.cu", "tg_api.cu", "tg_train_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                 "-Xcompiler", "-Wall", "-diag-suppress", "177"]

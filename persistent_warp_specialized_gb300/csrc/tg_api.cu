@@ -17,12 +17,14 @@
 #include <mutex>
 
 #include "../../include/tg.h"
+#include "tg_api_common.h"
 #include "tg_config.h"
 #include "tg_wide_config.h"
 #include "tg_internal.h"
 #include "tg_tile_scheduler.cuh"
 
-namespace {
+namespace tg {
+namespace abi {
 
 thread_local char g_err[1024] = "";
 
@@ -98,7 +100,6 @@ int device_ready(int* sms_out, int* max_pairs_out) {
   return TG_OK;
 }
 
-// The pointer must be device memory of the current device (TMA reads it directly).
 int check_device_ptr(const void* p, const char* name) {
   cudaPointerAttributes a;
   cudaError_t e = cudaPointerGetAttributes(&a, p);
@@ -118,15 +119,13 @@ bool overlaps(const void* a, uint64_t abytes, const void* b, uint64_t bbytes) {
   return a0 < b0 + bbytes && b0 < a0 + abytes;
 }
 
-// A row-major [outer, inner] matrix of ``elem_bytes``-byte elements, boxes of
-// box_outer rows x box_inner elements landing with the 128-byte swizzle (or none).
 int encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, uint32_t elem_bytes, const void* base,
                  uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
-                 const char* name, bool swizzle = true) {
+                 const char* name, bool swizzle, uint64_t pitch_bytes) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(TG_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
   const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {inner * elem_bytes};  // bytes between rows
+  const cuuint64_t strides[1] = {pitch_bytes ? pitch_bytes : inner * elem_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
@@ -138,6 +137,13 @@ int encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, uint32_t elem_bytes, 
   return TG_OK;
 }
 
+}  // namespace abi
+}  // namespace tg
+
+using namespace tg::abi;
+
+namespace {
+
 int encode_2d(CUtensorMap* map, int dtype, const void* base, uint64_t inner, uint64_t outer,
               uint32_t box_inner, uint32_t box_outer, const char* name) {
   return encode_tiled(map,
@@ -145,8 +151,6 @@ int encode_2d(CUtensorMap* map, int dtype, const void* base, uint64_t inner, uin
                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                       tg::kElemBytes, base, inner, outer, box_inner, box_outer, name);
 }
-
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 // Shared validation of the GEMM entry points.  *nothing_to_do is set for M == 0 or N == 0.
 int validate(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int dtype,

@@ -3,12 +3,11 @@
 // CTA pair and wide CTA pair), the
 // block-scaled MXFP8 GEMM (single CTA and CTA pair), the tile-schedule inspection kernel, and the zero fill used when
 // K == 0.  All kernels share this translation unit's watchdog status word.
-#include <utility>
-
 #include "tg_gemm_kernel.cuh"
 #include "tg_gemm_pair_kernel.cuh"
 #include "tg_gemm_pair_wide_kernel.cuh"
 #include "tg_internal.h"
+#include "tg_launch.cuh"
 #include "tg_mx_kernel.cuh"
 #include "tg_mx_pack.cuh"
 #include "tg_mx_pair_kernel.cuh"
@@ -74,27 +73,6 @@ GemmParams params_of(const GemmLaunch& l) {
   p.sk_flags = l.sk_flags;
   p.sk_partials = l.sk_partials;
   return p;
-}
-
-// Launches ``kernel`` with programmatic stream serialization: it may be scheduled while the
-// previous kernel in the stream is still finishing (as that kernel's CTAs exit).  Every kernel
-// launched this way issues griddepcontrol.wait before its first global memory access, so the
-// stream's ordering of memory effects is unchanged; what overlaps is the launch itself and each
-// CTA's set-up (barriers, TMEM allocation, descriptor prefetch).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, uint32_t threads, size_t smem,
-                       cudaStream_t stream, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 template <int DT, bool DEBUG>

@@ -1,5 +1,5 @@
-// tg_internal.h -- interface between the C-ABI translation unit (tg_api.cu) and the
-// translation unit that holds the kernels (tg_gemm.cu).  Not installed, not part of the ABI.
+// tg_internal.h -- interface between the C-ABI translation units (tg_api.cu, tg_train_api.cu) and
+// those that hold the kernels (tg_gemm.cu, tg_train.cu).  Not installed, not part of the ABI.
 #pragma once
 
 #include <cuda.h>
@@ -68,6 +68,40 @@ cudaError_t launch_zero_fill(void* C, uint64_t bytes, cudaStream_t stream);
 cudaError_t launch_tile_schedule(uint32_t m_blocks, uint32_t n_blocks, uint32_t num_workers,
                                  uint32_t group, uint32_t split_from, uint32_t units,
                                  uint32_t column_major, int32_t* out_dev, cudaStream_t stream);
+
+// ---------------------------------------------------------------- training operators
+// Layer norm of x [rows, cols] (tg_norm_kernel.cuh).  dtype, param_dtype: TG_F16, TG_BF16, TG_F32;
+// param_dtype is TG_F32 or dtype.  Null pointers leave out what they stand for.
+struct NormLaunch {
+  const void *x, *gamma, *beta;
+  void* y;
+  float *mean, *rstd;
+  void *q, *s;           // the checkpoint of y, or null
+  int64_t rows, cols, ld_x, ld_y;
+  int dtype, param_dtype;
+  float eps;
+};
+cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream);
+
+struct NormBwdLaunch {
+  const void *dy, *x, *q, *s, *gamma;   // x, or its checkpoint q and s
+  const float *mean, *rstd;
+  void *dx, *dgamma, *dbeta;
+  float* partials;
+  int64_t rows, cols, ld_dy, ld_x, ld_dx;
+  int dtype, param_dtype;
+  int sms;
+};
+// Rows of [2][cols] fp32 partial sums that launch_norm_bwd writes for dgamma and dbeta.
+uint32_t norm_bwd_parts(int64_t rows, int64_t cols, int sms);
+cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream);
+
+// 8-bit checkpoints (tg_ckpt8_kernel.cuh)
+cudaError_t launch_ckpt8_pack(const void* x, void* q, void* s, int64_t rows, int64_t cols,
+                              int64_t ld_x, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_ckpt8_unpack(const void* q, const void* s, void* out, int64_t rows, int64_t cols,
+                                int64_t ld_out, int dtype, int sms, cudaStream_t stream);
+
 cudaError_t clear_watchdog_status(cudaStream_t stream);
 // synchronises ``stream``, returns the status word in *out and clears it
 cudaError_t read_and_clear_watchdog_status(unsigned int* out, cudaStream_t stream);

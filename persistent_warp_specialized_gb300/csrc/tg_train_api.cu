@@ -1,0 +1,267 @@
+// tg_train_api.cu -- the C ABI of the training operators (include/tg.h): argument checks and
+// launches of layer norm and of activation checkpoints in 8 bits.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/tg.h"
+#include "tg_api_common.h"
+#include "tg_internal.h"
+
+using namespace tg::abi;
+
+namespace {
+
+bool known_dtype(int d) { return d == TG_F16 || d == TG_BF16 || d == TG_F32; }
+uint64_t elem_bytes(int d) { return d == TG_F32 ? 4 : 2; }
+uint64_t kept_blocks(int64_t cols) { return (static_cast<uint64_t>(cols) + 31) / 32; }
+
+bool off_by(const void* p, uint64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+
+// bytes from the first to the last element of a [rows, cols] matrix with row stride ld
+uint64_t span(int64_t rows, int64_t cols, int64_t ld, uint64_t elem) {
+  return rows == 0 ? 0 : ((static_cast<uint64_t>(rows) - 1) * ld + cols) * elem;
+}
+
+int check_sizes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim)
+    return fail(TG_ERR_ARG, "sizes must be in [0, 2^31): rows=%lld cols=%lld", (long long)rows,
+                (long long)cols);
+  return TG_OK;
+}
+
+int check_ld(int64_t ld, int64_t cols, const char* name) {
+  if (ld < cols || ld > kMaxDim)
+    return fail(TG_ERR_ARG, "%s=%lld must be at least the row's %lld values and below 2^31", name,
+                (long long)ld, (long long)cols);
+  return TG_OK;
+}
+
+// A required device array of ``elem``-byte elements.
+int check_array(const void* p, uint64_t elem, const char* name) {
+  if (!p) return fail(TG_ERR_ARG, "null pointer: %s", name);
+  if (off_by(p, elem))
+    return fail(TG_ERR_ALIGN, "%s must be %llu-byte aligned", name, (unsigned long long)elem);
+  return check_device_ptr(p, name);
+}
+
+// The array ``p`` if the caller gave it.
+int check_optional(const void* p, uint64_t elem, const char* name) {
+  return p ? check_array(p, elem, name) : TG_OK;
+}
+
+struct Region {
+  const void* p;
+  uint64_t bytes;
+  const char* name;
+};
+
+// No output may overlap an input or another output (regions [0, outs) are the outputs).
+int check_apart(const Region* r, int outs, int n) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (r[i].p && r[j].p && overlaps(r[i].p, r[i].bytes, r[j].p, r[j].bytes))
+        return fail(TG_ERR_ARG, "%s overlaps %s", r[i].name, r[j].name);
+  return TG_OK;
+}
+
+int check_params(int dtype, int param_dtype) {
+  if (!known_dtype(dtype)) return fail(TG_ERR_ARG, "unknown dtype %d", dtype);
+  if (param_dtype != TG_F32 && param_dtype != dtype)
+    return fail(TG_ERR_ARG, "param_dtype %d must be TG_F32 or the values' type %d", param_dtype,
+                dtype);
+  return TG_OK;
+}
+
+#define TG_TRY(call)                 \
+  do {                               \
+    const int rc_ = (call);          \
+    if (rc_ != TG_OK) return rc_;    \
+  } while (0)
+
+}  // namespace
+
+extern "C" {
+
+int tg_layernorm_fwd(const void* x_dev, const void* gamma_dev, const void* beta_dev, void* y_dev,
+                     float* mean_dev, float* rstd_dev, void* yq_dev, void* ys_dev, int64_t rows,
+                     int64_t cols, int64_t ld_x, int64_t ld_y, int dtype, int param_dtype,
+                     float eps, void* stream) {
+  TG_TRY(check_params(dtype, param_dtype));
+  TG_TRY(check_sizes(rows, cols));
+  TG_TRY(check_ld(ld_x, cols, "ld_x"));
+  TG_TRY(check_ld(ld_y, cols, "ld_y"));
+  if (!(eps >= 0.0f)) return fail(TG_ERR_ARG, "eps must not be negative");
+  if ((yq_dev == nullptr) != (ys_dev == nullptr))
+    return fail(TG_ERR_ARG, "a checkpoint of y needs both yq and ys");
+  if (rows == 0 || cols == 0) return TG_OK;
+  const uint64_t e = elem_bytes(dtype), pe = elem_bytes(param_dtype), kb = kept_blocks(cols);
+  TG_TRY(check_array(x_dev, e, "x"));
+  TG_TRY(check_array(y_dev, e, "y"));
+  TG_TRY(check_optional(gamma_dev, pe, "gamma"));
+  TG_TRY(check_optional(beta_dev, pe, "beta"));
+  TG_TRY(check_optional(mean_dev, 4, "mean"));
+  TG_TRY(check_optional(rstd_dev, 4, "rstd"));
+  TG_TRY(check_optional(yq_dev, 16, "yq"));
+  TG_TRY(check_optional(ys_dev, 1, "ys"));
+  const uint64_t stat = 4 * static_cast<uint64_t>(rows), param = pe * cols;
+  const Region r[] = {{y_dev, span(rows, cols, ld_y, e), "y"},
+                      {mean_dev, stat, "mean"},
+                      {rstd_dev, stat, "rstd"},
+                      {yq_dev, rows * kb * 32, "yq"},
+                      {ys_dev, rows * kb, "ys"},
+                      {x_dev, span(rows, cols, ld_x, e), "x"},
+                      {gamma_dev, param, "gamma"},
+                      {beta_dev, param, "beta"}};
+  TG_TRY(check_apart(r, 5, 8));
+  TG_TRY(device_ready(nullptr, nullptr));
+  tg::NormLaunch l;
+  l.x = x_dev;
+  l.gamma = gamma_dev;
+  l.beta = beta_dev;
+  l.y = y_dev;
+  l.mean = mean_dev;
+  l.rstd = rstd_dev;
+  l.q = yq_dev;
+  l.s = ys_dev;
+  l.rows = rows;
+  l.cols = cols;
+  l.ld_x = ld_x;
+  l.ld_y = ld_y;
+  l.dtype = dtype;
+  l.param_dtype = param_dtype;
+  l.eps = eps;
+  const cudaError_t err = tg::launch_norm_fwd(l, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? TG_OK : fail_cuda("layer norm launch", err);
+}
+
+int64_t tg_layernorm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+  TG_TRY(check_sizes(rows, cols));
+  if (rows == 0 || cols == 0) return 0;
+  int sms = 0;
+  TG_TRY(device_ready(&sms, nullptr));
+  return static_cast<int64_t>(tg::norm_bwd_parts(rows, cols, sms)) * 2 * cols * 4;
+}
+
+int tg_layernorm_bwd(const void* dy_dev, const void* x_dev, const void* xq_dev, const void* xs_dev,
+                     const void* gamma_dev, const float* mean_dev, const float* rstd_dev,
+                     void* dx_dev, void* dgamma_dev, void* dbeta_dev, int64_t rows, int64_t cols,
+                     int64_t ld_dy, int64_t ld_x, int64_t ld_dx, int dtype, int param_dtype,
+                     void* workspace_dev, int64_t workspace_bytes, void* stream) {
+  TG_TRY(check_params(dtype, param_dtype));
+  TG_TRY(check_sizes(rows, cols));
+  TG_TRY(check_ld(ld_dy, cols, "ld_dy"));
+  TG_TRY(check_ld(ld_dx, cols, "ld_dx"));
+  if (x_dev) TG_TRY(check_ld(ld_x, cols, "ld_x"));
+  if ((xq_dev == nullptr) != (xs_dev == nullptr))
+    return fail(TG_ERR_ARG, "a checkpoint of x is both xq and xs");
+  if (x_dev && xq_dev) return fail(TG_ERR_ARG, "give x or its checkpoint, not both");
+  if (workspace_bytes < 0) return fail(TG_ERR_ARG, "negative workspace size");
+  if (cols == 0) return TG_OK;
+  const uint64_t e = elem_bytes(dtype), pe = elem_bytes(param_dtype), kb = kept_blocks(cols);
+  if (rows > 0) {
+    TG_TRY(check_array(dy_dev, e, "dy"));
+    if (xq_dev) {
+      TG_TRY(check_array(xq_dev, 16, "xq"));
+      TG_TRY(check_array(xs_dev, 1, "xs"));
+    } else {
+      TG_TRY(check_array(x_dev, e, "x"));
+    }
+    TG_TRY(check_array(mean_dev, 4, "mean"));
+    TG_TRY(check_array(rstd_dev, 4, "rstd"));
+    TG_TRY(check_array(dx_dev, e, "dx"));
+    TG_TRY(check_optional(gamma_dev, pe, "gamma"));
+  }
+  TG_TRY(check_optional(dgamma_dev, pe, "dgamma"));
+  TG_TRY(check_optional(dbeta_dev, pe, "dbeta"));
+  int sms = 0;
+  TG_TRY(device_ready(&sms, nullptr));
+  const bool sums = dgamma_dev || dbeta_dev;
+  const int64_t need =
+      sums ? static_cast<int64_t>(tg::norm_bwd_parts(rows, cols, sms)) * 2 * cols * 4 : 0;
+  if (need > 0) {
+    if (!workspace_dev || workspace_bytes < need)
+      return fail(TG_ERR_ARG, "workspace of %lld bytes; dgamma and dbeta need %lld",
+                  (long long)(workspace_dev ? workspace_bytes : 0), (long long)need);
+    TG_TRY(check_array(workspace_dev, 256, "workspace"));
+  }
+  const uint64_t stat = 4 * static_cast<uint64_t>(rows), param = pe * cols;
+  const Region r[] = {{rows > 0 ? dx_dev : nullptr, span(rows, cols, ld_dx, e), "dx"},
+                      {dgamma_dev, param, "dgamma"},
+                      {dbeta_dev, param, "dbeta"},
+                      {need > 0 ? workspace_dev : nullptr, static_cast<uint64_t>(need), "workspace"},
+                      {dy_dev, span(rows, cols, ld_dy, e), "dy"},
+                      {x_dev, span(rows, cols, ld_x, e), "x"},
+                      {xq_dev, rows * kb * 32, "xq"},
+                      {xs_dev, rows * kb, "xs"},
+                      {mean_dev, stat, "mean"},
+                      {rstd_dev, stat, "rstd"},
+                      {gamma_dev, param, "gamma"}};
+  TG_TRY(check_apart(r, 4, 11));
+  tg::NormBwdLaunch l;
+  l.dy = dy_dev;
+  l.x = x_dev;
+  l.q = xq_dev;
+  l.s = xs_dev;
+  l.gamma = gamma_dev;
+  l.mean = mean_dev;
+  l.rstd = rstd_dev;
+  l.dx = dx_dev;
+  l.dgamma = dgamma_dev;
+  l.dbeta = dbeta_dev;
+  l.partials = static_cast<float*>(workspace_dev);
+  l.rows = rows;
+  l.cols = cols;
+  l.ld_dy = ld_dy;
+  l.ld_x = ld_x;
+  l.ld_dx = ld_dx;
+  l.dtype = dtype;
+  l.param_dtype = param_dtype;
+  l.sms = sms;
+  const cudaError_t err = tg::launch_norm_bwd(l, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? TG_OK : fail_cuda("layer norm backward launch", err);
+}
+
+int tg_ckpt8_pack(const void* x_dev, void* q_dev, void* s_dev, int64_t rows, int64_t cols,
+                  int64_t ld_x, int dtype, void* stream) {
+  if (!known_dtype(dtype)) return fail(TG_ERR_ARG, "unknown dtype %d", dtype);
+  TG_TRY(check_sizes(rows, cols));
+  TG_TRY(check_ld(ld_x, cols, "ld_x"));
+  if (rows == 0 || cols == 0) return TG_OK;
+  TG_TRY(check_array(x_dev, elem_bytes(dtype), "x"));
+  TG_TRY(check_array(q_dev, 16, "q"));
+  TG_TRY(check_array(s_dev, 1, "s"));
+  const uint64_t kb = kept_blocks(cols);
+  const Region r[] = {{q_dev, rows * kb * 32, "q"},
+                      {s_dev, rows * kb, "s"},
+                      {x_dev, span(rows, cols, ld_x, elem_bytes(dtype)), "x"}};
+  TG_TRY(check_apart(r, 2, 3));
+  int sms = 0;
+  TG_TRY(device_ready(&sms, nullptr));
+  const cudaError_t err = tg::launch_ckpt8_pack(x_dev, q_dev, s_dev, rows, cols, ld_x, dtype, sms,
+                                                static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? TG_OK : fail_cuda("checkpoint pack launch", err);
+}
+
+int tg_ckpt8_unpack(const void* q_dev, const void* s_dev, void* out_dev, int64_t rows, int64_t cols,
+                    int64_t ld_out, int dtype, void* stream) {
+  if (!known_dtype(dtype)) return fail(TG_ERR_ARG, "unknown dtype %d", dtype);
+  TG_TRY(check_sizes(rows, cols));
+  TG_TRY(check_ld(ld_out, cols, "ld_out"));
+  if (rows == 0 || cols == 0) return TG_OK;
+  TG_TRY(check_array(q_dev, 16, "q"));
+  TG_TRY(check_array(s_dev, 1, "s"));
+  TG_TRY(check_array(out_dev, elem_bytes(dtype), "out"));
+  const uint64_t kb = kept_blocks(cols);
+  const Region r[] = {{out_dev, span(rows, cols, ld_out, elem_bytes(dtype)), "out"},
+                      {q_dev, rows * kb * 32, "q"},
+                      {s_dev, rows * kb, "s"}};
+  TG_TRY(check_apart(r, 1, 3));
+  int sms = 0;
+  TG_TRY(device_ready(&sms, nullptr));
+  const cudaError_t err = tg::launch_ckpt8_unpack(q_dev, s_dev, out_dev, rows, cols, ld_out, dtype,
+                                                  sms, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? TG_OK : fail_cuda("checkpoint unpack launch", err);
+}
+
+}  // extern "C"
