@@ -419,6 +419,34 @@ int tg_ckpt8_pack(const void* x_dev, void* q_dev, void* s_dev, int64_t rows, int
 int tg_ckpt8_unpack(const void* q_dev, const void* s_dev, void* out_dev, int64_t rows, int64_t cols,
                     int64_t ld_out, int dtype, void* stream);
 
+/*
+ * tg_ckpt8_wgrad -- a linear layer's weight gradient from the checkpoint of its input:
+ *     dW[i, n] = sum over rows t of x[t, i] dY[t, n],   x = q * 2^(s - 127)
+ *   q_dev, s_dev: a checkpoint of x [rows, cols].  dY_dev: [rows, outs] of ``dtype`` (TG_F16 or
+ *   TG_BF16), dW_dev: [cols, outs] of the same type.  x is rounded to ``dtype`` where it is outside
+ *   its range (in bf16 only below 2^-126, in fp16 also past 65504, to infinity); products are
+ *   exact, sums fp32, and each result is rounded once.  outs, ld_dy and ld_dw are multiples of 8;
+ *   q, dY and dW are 16-byte aligned; rows and cols are any.  rows == 0: dW is zero-filled.
+ *   cols == 0 or outs == 0: nothing is done.
+ * One CTA pair per 256 x 256 tile of dW, persistent.  When the tiles do not fill the device, the
+ * rows are split into ranges whose fp32 sums go through workspace_dev (256-byte aligned,
+ * tg_ckpt8_wgrad_workspace_bytes bytes, in use until the call's work is done; NULL if that is 0)
+ * and are added in a fixed order.
+ */
+int tg_ckpt8_wgrad(const void* q_dev, const void* s_dev, const void* dY_dev, void* dW_dev,
+                   int64_t rows, int64_t cols, int64_t outs, int64_t ld_dy, int64_t ld_dw,
+                   int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* Workspace of tg_ckpt8_wgrad on the current device, in bytes (0: none); negative: an error. */
+int64_t tg_ckpt8_wgrad_workspace_bytes(int64_t rows, int64_t cols, int64_t outs);
+
+/* tg_ckpt8_wgrad, synchronously, with the watchdog limit and the injected missing fill of
+   tg_gemm_persistent_debug (its CTA-pair form). */
+int tg_ckpt8_wgrad_debug(const void* q_dev, const void* s_dev, const void* dY_dev, void* dW_dev,
+                         int64_t rows, int64_t cols, int64_t outs, int64_t ld_dy, int64_t ld_dw,
+                         int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream,
+                         uint64_t watchdog_ns, int64_t inject_skip_phase);
+
 #ifdef __cplusplus
 }
 #endif

@@ -66,6 +66,9 @@ EXPORTED = (
     "tg_layernorm_bwd_workspace_bytes",
     "tg_ckpt8_pack",
     "tg_ckpt8_unpack",
+    "tg_ckpt8_wgrad",
+    "tg_ckpt8_wgrad_workspace_bytes",
+    "tg_ckpt8_wgrad_debug",
 )
 
 
@@ -140,6 +143,12 @@ def load_library(path=LIB_PATH):
     lib.tg_ckpt8_pack.restype = i32
     lib.tg_ckpt8_unpack.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp]
     lib.tg_ckpt8_unpack.restype = i32
+    lib.tg_ckpt8_wgrad.argtypes = [vp] * 4 + [i64] * 5 + [i32, vp, i64, vp]
+    lib.tg_ckpt8_wgrad.restype = i32
+    lib.tg_ckpt8_wgrad_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.tg_ckpt8_wgrad_workspace_bytes.restype = i64
+    lib.tg_ckpt8_wgrad_debug.argtypes = [vp] * 4 + [i64] * 5 + [i32, vp, i64, vp, u64, i64]
+    lib.tg_ckpt8_wgrad_debug.restype = i32
     _lib = lib
     return lib
 
@@ -443,6 +452,26 @@ def tg_ckpt8_unpack(q, s, out, rows, cols, ld_out, dtype, stream=None):
                                                  _dtype(dtype), _stream(stream)))
 
 
+def tg_ckpt8_wgrad(q, s, dY, dW, rows, cols, outs, ld_dy, ld_dw, dtype, workspace=None,
+                   stream=None, workspace_bytes=None):
+    """dW [cols, outs] = x^T dY for the x [rows, cols] that the checkpoint (q, s) stands for."""
+    return _check(load_library().tg_ckpt8_wgrad(
+        _ptr(q), _ptr(s), _ptr(dY), _ptr(dW), rows, cols, outs, ld_dy, ld_dw, _dtype(dtype),
+        _ptr(workspace), _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def tg_ckpt8_wgrad_workspace_bytes(rows, cols, outs):
+    return _check(load_library().tg_ckpt8_wgrad_workspace_bytes(rows, cols, outs))
+
+
+def tg_ckpt8_wgrad_debug(q, s, dY, dW, rows, cols, outs, ld_dy, ld_dw, dtype, workspace=None,
+                         stream=None, watchdog_ns=0, inject_skip_phase=-1, workspace_bytes=None):
+    return _check(load_library().tg_ckpt8_wgrad_debug(
+        _ptr(q), _ptr(s), _ptr(dY), _ptr(dW), rows, cols, outs, ld_dy, ld_dw, _dtype(dtype),
+        _ptr(workspace), _nbytes(workspace, workspace_bytes), _stream(stream), watchdog_ns,
+        inject_skip_phase))
+
+
 class Checkpoint8:
     """Activations [rows, cols] kept in 8 bits: q, uint8 E4M3 bytes [rows, 32 ceil(cols / 32)], and
     s, uint8 E8M0 scales [rows, ceil(cols / 32)], standing for q * 2^(s - 127).  Both contiguous."""
@@ -604,4 +633,25 @@ def ckpt8_unpack(kept, dtype, out=None, stream=None):
         raise ValueError("out must have the checkpoint's shape and the type asked for")
     tg_ckpt8_unpack(kept.q, kept.s, out, kept.rows, kept.cols, _rows_of(out, "out")[2], name,
                     stream)
+    return out
+
+
+def ckpt8_wgrad(kept, dy, out=None, stream=None):
+    """torch convenience: the weight gradient x^T dy [cols, outs], in dy's type, of a linear layer
+    whose input x is the Checkpoint8 ``kept``; dy [rows, outs] is float16 or bfloat16."""
+    import torch
+
+    dtype = _type_name(dy.dtype)
+    rows, outs, ld_dy = _rows_of(dy, "dy")
+    if kept.rows != rows:
+        raise ValueError(f"the checkpoint has {kept.rows} rows and dy {rows}")
+    if out is not None and (out.dtype != dy.dtype or tuple(out.shape) != (kept.cols, outs)):
+        raise ValueError(f"out must be [{kept.cols}, {outs}] of dy's type")
+    nbytes = tg_ckpt8_wgrad_workspace_bytes(rows, kept.cols, outs)
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty((kept.cols, outs), dtype=dy.dtype, device=dy.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes else None
+    tg_ckpt8_wgrad(kept.q, kept.s, dy, out, rows, kept.cols, outs, ld_dy, _rows_of(out, "out")[2],
+                   dtype, ws, stream)
     return out

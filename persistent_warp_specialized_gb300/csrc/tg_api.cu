@@ -137,6 +137,10 @@ int encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, uint32_t elem_bytes, 
   return TG_OK;
 }
 
+uint64_t default_watchdog_ns(uint32_t k_blocks) {
+  return tg::kDefaultWatchdogNs + uint64_t(k_blocks) * 2000u;
+}
+
 }  // namespace abi
 }  // namespace tg
 
@@ -185,15 +189,6 @@ int validate(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_
       return fail(TG_ERR_ARG, "C overlaps A or B");
   }
   return TG_OK;
-}
-
-// The default limit of every bounded wait in the kernels when the caller gives none: the
-// fixed kDefaultWatchdogNs plus 2 us per k-block of K.  The longest legitimate wait spans one
-// unit's whole K (the epilogue waiting for its accumulator), and a k-block takes at most about
-// 0.5 us on GB300 even on a CTA pair's half-width unit, so with K near 2^31 (2^25 k-blocks of
-// 64, ~12 s per unit, measured) a fixed limit of ~4 s stopped a correct GEMM.
-uint64_t default_watchdog_ns(uint32_t k_blocks) {
-  return tg::kDefaultWatchdogNs + uint64_t(k_blocks) * 2000u;
 }
 
 // The variant TG_VARIANT_AUTO resolves to (both GEMMs): the CTA-pair kernel once its 256 x 256

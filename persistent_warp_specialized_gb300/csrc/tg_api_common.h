@@ -32,5 +32,12 @@ int encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, uint32_t elem_bytes, 
                  uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
                  const char* name, bool swizzle = true, uint64_t pitch_bytes = 0);
 
+// The default limit of every bounded wait in the kernels when the caller gives none: the
+// fixed kDefaultWatchdogNs plus 2 us per k-block of K.  The longest legitimate wait spans one
+// unit's whole K (the epilogue waiting for its accumulator), and a k-block takes at most about
+// 0.5 us on GB300 even on a CTA pair's half-width unit, so with K near 2^31 (2^25 k-blocks of
+// 64, ~12 s per unit, measured) a fixed limit of ~4 s stopped a correct GEMM.
+uint64_t default_watchdog_ns(uint32_t k_blocks);
+
 }  // namespace abi
 }  // namespace tg

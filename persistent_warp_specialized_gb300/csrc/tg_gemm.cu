@@ -1,8 +1,8 @@
 // tg_gemm.cu -- instantiations and launchers of the sm_103a kernels behind the C ABI:
 // the persistent warp-specialized GEMM (fp16 and bf16, product and debug builds; single CTA,
 // CTA pair and wide CTA pair), the
-// block-scaled MXFP8 GEMM (single CTA and CTA pair), the tile-schedule inspection kernel, and the zero fill used when
-// K == 0.  All kernels share this translation unit's watchdog status word.
+// block-scaled MXFP8 GEMM (single CTA and CTA pair), the weight gradient from an 8-bit checkpoint,
+// the tile-schedule inspection kernel, and the zero fill used when K == 0.  All kernels share this translation unit's watchdog status word.
 #include "tg_gemm_kernel.cuh"
 #include "tg_gemm_pair_kernel.cuh"
 #include "tg_gemm_pair_wide_kernel.cuh"
@@ -11,6 +11,7 @@
 #include "tg_mx_kernel.cuh"
 #include "tg_mx_pack.cuh"
 #include "tg_mx_pair_kernel.cuh"
+#include "tg_wgrad_kernel.cuh"
 
 namespace tg {
 
@@ -153,7 +154,71 @@ cudaError_t set_mx_smem_attr() {
                               static_cast<int>(kMxPairSmemBytes));
 }
 
+WgradParams wgrad_params_of(const WgradLaunch& l) {
+  WgradParams p = {};
+  p.C = l.dw;
+  p.M = l.cols;
+  p.N = l.outs;
+  p.K = l.tokens;
+  p.m_blocks = l.m_blocks;
+  p.n_blocks = l.n_blocks;
+  p.k_blocks = l.k_blocks;
+  p.group = l.group;
+  p.split_from = l.split_from;
+  p.total_units = l.total_units;
+  p.column_major = l.column_major;
+  p.watchdog_ns = l.watchdog_ns;
+  p.inject_skip_phase = l.inject_skip_phase;
+  p.scales = static_cast<const uint8_t*>(l.scales);
+  p.scale_cols = l.scale_cols;
+  p.splits = l.splits;
+  p.blocks_per_split = l.blocks_per_split;
+  return p;
+}
+
+template <int DT, bool SPLIT, bool DEBUG>
+cudaError_t launch_wgrad_pair(const WgradLaunch& l, cudaStream_t stream) {
+  cudaError_t e = launch_pdl(wgrad_pair_kernel<DT, SPLIT, DEBUG>, l.grid, kWgThreads, kWgSmemBytes,
+                             stream, l.tmQ, l.tmB, l.tmC, wgrad_params_of(l));
+  if (e != cudaSuccess || !SPLIT) return e;
+  const uint64_t vecs = static_cast<uint64_t>(l.cols) * (l.outs / 8u);
+  const uint64_t want = (vecs + 255) / 256, most = static_cast<uint64_t>(l.sms) * 8;
+  return launch_pdl(wgrad_join_kernel<DT>, static_cast<uint32_t>(want < most ? want : most), 256, 0,
+                    stream, static_cast<const float*>(l.partials), l.splits,
+                    static_cast<uint64_t>(l.m_blocks) * kPairBM * l.outs, l.cols, l.outs, l.dw,
+                    l.ld_dw);
+}
+
+template <int DT>
+cudaError_t set_wgrad_smem_attr() {
+  const int bytes = static_cast<int>(kWgSmemBytes);
+  cudaError_t e;
+  const auto a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if ((e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, false, false>, a, bytes)) != cudaSuccess)
+    return e;
+  if ((e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, true, false>, a, bytes)) != cudaSuccess)
+    return e;
+  if ((e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, false, true>, a, bytes)) != cudaSuccess)
+    return e;
+  return cudaFuncSetAttribute(wgrad_pair_kernel<DT, true, true>, a, bytes);
+}
+
 }  // namespace
+
+cudaError_t launch_wgrad(int dtype, bool debug, const WgradLaunch& l, cudaStream_t stream) {
+  if (dtype == 0) {
+    if (l.splits > 1)
+      return debug ? launch_wgrad_pair<0, true, true>(l, stream)
+                   : launch_wgrad_pair<0, true, false>(l, stream);
+    return debug ? launch_wgrad_pair<0, false, true>(l, stream)
+                 : launch_wgrad_pair<0, false, false>(l, stream);
+  }
+  if (l.splits > 1)
+    return debug ? launch_wgrad_pair<1, true, true>(l, stream)
+                 : launch_wgrad_pair<1, true, false>(l, stream);
+  return debug ? launch_wgrad_pair<1, false, true>(l, stream)
+               : launch_wgrad_pair<1, false, false>(l, stream);
+}
 
 cudaError_t prepare_gemm_kernels(int* max_pairs) {
   cudaError_t e;
@@ -165,6 +230,8 @@ cudaError_t prepare_gemm_kernels(int* max_pairs) {
   if ((e = set_mx_smem_attr<1, false>()) != cudaSuccess) return e;
   if ((e = set_mx_smem_attr<0, true>()) != cudaSuccess) return e;
   if ((e = set_mx_smem_attr<1, true>()) != cudaSuccess) return e;
+  if ((e = set_wgrad_smem_attr<0>()) != cudaSuccess) return e;
+  if ((e = set_wgrad_smem_attr<1>()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -176,7 +243,7 @@ cudaError_t prepare_gemm_kernels(int* max_pairs) {
   cfg.dynamicSmemBytes = kPairSmemBytes;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int clusters = 0, mx_clusters = 0, wide_clusters = 0;
+  int clusters = 0, mx_clusters = 0, wide_clusters = 0;   // the least of all pair kernels counts
   e = cudaOccupancyMaxActiveClusters(&clusters, gemm_pair_ws_kernel<1, false>, &cfg);
   if (e != cudaSuccess) return e;
   cfg.dynamicSmemBytes = kWideSmemBytes;
@@ -186,7 +253,13 @@ cudaError_t prepare_gemm_kernels(int* max_pairs) {
   cfg.dynamicSmemBytes = kMxPairSmemBytes;
   e = cudaOccupancyMaxActiveClusters(&mx_clusters, gemm_mxfp8_pair_ws_kernel<1, false>, &cfg);
   if (e != cudaSuccess) return e;
-  *max_pairs = clusters < mx_clusters ? clusters : mx_clusters;
+  if (mx_clusters < clusters) clusters = mx_clusters;
+  int wgrad_clusters = 0;
+  cfg.blockDim = dim3(kWgThreads, 1, 1);
+  cfg.dynamicSmemBytes = kWgSmemBytes;
+  e = cudaOccupancyMaxActiveClusters(&wgrad_clusters, wgrad_pair_kernel<1, false, false>, &cfg);
+  if (e != cudaSuccess) return e;
+  *max_pairs = wgrad_clusters < clusters ? wgrad_clusters : clusters;
   return cudaSuccess;
 }
 

@@ -102,6 +102,25 @@ cudaError_t launch_ckpt8_pack(const void* x, void* q, void* s, int64_t rows, int
 cudaError_t launch_ckpt8_unpack(const void* q, const void* s, void* out, int64_t rows, int64_t cols,
                                 int64_t ld_out, int dtype, int sms, cudaStream_t stream);
 
+// Weight gradient from a checkpoint (tg_wgrad_kernel.cuh): the pair kernel, then, with splits > 1,
+// the join of its partial sums.
+struct WgradLaunch {
+  CUtensorMap tmQ, tmB, tmC;    // tmC: dW, or the workspace when splits > 1
+  const void* scales;
+  void* dw;
+  float* partials;
+  uint32_t cols, outs, tokens, scale_cols;
+  int64_t ld_dw;
+  uint32_t m_blocks, n_blocks, k_blocks, group, column_major;
+  uint32_t split_from, total_units;   // per split
+  uint32_t splits, blocks_per_split;
+  uint32_t grid;                // CTAs
+  uint64_t watchdog_ns;
+  int64_t inject_skip_phase;
+  int sms;
+};
+cudaError_t launch_wgrad(int dtype, bool debug, const WgradLaunch& l, cudaStream_t stream);
+
 cudaError_t clear_watchdog_status(cudaStream_t stream);
 // synchronises ``stream``, returns the status word in *out and clears it
 cudaError_t read_and_clear_watchdog_status(unsigned int* out, cudaStream_t stream);

@@ -7,6 +7,8 @@
 #include "../../include/tg.h"
 #include "tg_api_common.h"
 #include "tg_internal.h"
+#include "tg_tile_scheduler.cuh"
+#include "tg_wgrad_config.h"
 
 using namespace tg::abi;
 
@@ -73,11 +75,149 @@ int check_params(int dtype, int param_dtype) {
   return TG_OK;
 }
 
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+// How the weight gradient [cols, outs] over ``tokens`` tokens is cut into units.
+struct WgradPlan {
+  uint32_t m_tiles, n_tiles, k_blocks, splits, blocks_per_split, split_from, units, pairs;
+  uint64_t workspace;   // bytes of partial sums (0: one split)
+};
+
+// Tiles that fill a wave of CTA pairs are each one unit over all tokens.  Fewer tiles: the tokens
+// are split so that every pair has a unit, as long as a unit keeps kWgMinBlocks k-blocks.
+constexpr uint64_t kWgMinBlocks = 8;
+
+WgradPlan wgrad_plan(int64_t tokens, int64_t cols, int64_t outs, int max_pairs) {
+  WgradPlan w;
+  w.m_tiles = static_cast<uint32_t>(ceil_div(cols, tg::kPairBM));
+  w.n_tiles = static_cast<uint32_t>(ceil_div(outs, tg::kBN));
+  w.k_blocks = static_cast<uint32_t>(ceil_div(tokens, tg::kWgBK));
+  const uint64_t tiles = static_cast<uint64_t>(w.m_tiles) * w.n_tiles;
+  const uint64_t pairs = static_cast<uint64_t>(max_pairs);
+  uint64_t splits = tiles < pairs ? pairs / tiles : 1;
+  if (splits > w.k_blocks / kWgMinBlocks) splits = w.k_blocks / kWgMinBlocks;
+  if (splits < 1) splits = 1;
+  w.blocks_per_split = static_cast<uint32_t>(ceil_div(w.k_blocks, splits));
+  w.splits = w.k_blocks ? static_cast<uint32_t>(ceil_div(w.k_blocks, w.blocks_per_split)) : 1;
+  w.workspace = 0;
+  w.split_from = w.units = static_cast<uint32_t>(tiles);
+  if (w.splits > 1)
+    w.workspace = static_cast<uint64_t>(w.splits) * w.m_tiles * tg::kPairBM * outs * 4;
+  else
+    tg::PersistentTileScheduler::tail_split(static_cast<uint32_t>(tiles), max_pairs, w.split_from,
+                                            w.units);
+  const uint64_t all = static_cast<uint64_t>(w.units) * w.splits;
+  w.pairs = static_cast<uint32_t>(all < pairs ? all : pairs);
+  return w;
+}
+
+int check_wgrad_sizes(int64_t tokens, int64_t cols, int64_t outs) {
+  if (int rc = check_sizes(tokens, cols)) return rc;
+  if (outs < 0 || outs > kMaxDim)
+    return fail(TG_ERR_ARG, "outs=%lld must be in [0, 2^31)", (long long)outs);
+  if (outs % 8 != 0)
+    return fail(TG_ERR_ALIGN, "outs=%lld must be a multiple of 8 (16-byte rows)", (long long)outs);
+  if (ceil_div(cols, 128) * ceil_div(outs, 256) > static_cast<uint64_t>(kMaxDim))
+    return fail(TG_ERR_ARG, "too many output tiles");
+  return TG_OK;
+}
+
 #define TG_TRY(call)                 \
   do {                               \
     const int rc_ = (call);          \
     if (rc_ != TG_OK) return rc_;    \
   } while (0)
+
+int wgrad_impl(const void* q, const void* sc, const void* dy, void* dw, int64_t tokens, int64_t cols,
+               int64_t outs, int64_t ld_dy, int64_t ld_dw, int dtype, void* ws, int64_t ws_bytes,
+               void* stream, bool debug, uint64_t watchdog_ns, int64_t inject) {
+  if (dtype != TG_F16 && dtype != TG_BF16) return fail(TG_ERR_ARG, "unknown dtype %d", dtype);
+  TG_TRY(check_wgrad_sizes(tokens, cols, outs));
+  TG_TRY(check_ld(ld_dy, outs, "ld_dy"));
+  TG_TRY(check_ld(ld_dw, outs, "ld_dw"));
+  if (ws_bytes < 0) return fail(TG_ERR_ARG, "negative workspace size");
+  if (cols == 0 || outs == 0) return TG_OK;
+  if (ld_dy % 8 != 0 || ld_dw % 8 != 0)
+    return fail(TG_ERR_ALIGN, "ld_dy=%lld and ld_dw=%lld must be multiples of 8 (16-byte rows)",
+                (long long)ld_dy, (long long)ld_dw);
+  TG_TRY(check_array(dw, 16, "dW"));
+  const uint64_t kb = kept_blocks(cols);
+  if (tokens > 0) {
+    TG_TRY(check_array(q, 16, "q"));
+    TG_TRY(check_array(sc, 1, "s"));
+    TG_TRY(check_array(dy, 16, "dY"));
+  }
+  int sms = 0, max_pairs = 0;
+  TG_TRY(device_ready(&sms, &max_pairs));
+  if (max_pairs < 1)
+    return fail(TG_ERR_CUDA, "no CTA pair of the weight-gradient kernel fits on this device");
+  const WgradPlan w = wgrad_plan(tokens, cols, outs, max_pairs);
+  if (w.workspace > 0) {
+    if (!ws || static_cast<uint64_t>(ws_bytes) < w.workspace)
+      return fail(TG_ERR_ARG, "workspace of %lld bytes; the split sums need %llu",
+                  (long long)(ws ? ws_bytes : 0), (unsigned long long)w.workspace);
+    TG_TRY(check_array(ws, 256, "workspace"));
+  }
+  const Region r[] = {{dw, span(cols, outs, ld_dw, 2), "dW"},
+                      {w.workspace ? ws : nullptr, w.workspace, "workspace"},
+                      {q, tokens * kb * 32, "q"},
+                      {sc, tokens * kb, "s"},
+                      {dy, span(tokens, outs, ld_dy, 2), "dY"}};
+  TG_TRY(check_apart(r, 2, 5));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (tokens == 0) {
+    e = cudaMemset2DAsync(dw, ld_dw * 2, 0, outs * 2, cols, st);
+    return e == cudaSuccess ? TG_OK : fail_cuda("zero fill of dW", e);
+  }
+  const CUtensorMapDataType t16 =
+      dtype == TG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  tg::WgradLaunch l;
+  TG_TRY(encode_tiled(&l.tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q, kb * 32, tokens, tg::kBM,
+                      tg::kWgBK, "q", false));
+  TG_TRY(encode_tiled(&l.tmB, t16, 2, dy, outs, tokens, tg::kBChunkCols, tg::kWgBK, "dY", true,
+                      ld_dy * 2));
+  if (w.splits > 1)
+    TG_TRY(encode_tiled(&l.tmC, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ws, outs,
+                        static_cast<uint64_t>(w.splits) * w.m_tiles * tg::kPairBM, 32, 32,
+                        "workspace"));
+  else
+    TG_TRY(encode_tiled(&l.tmC, t16, 2, dw, outs, cols, tg::kEpiN, 32, "dW", true, ld_dw * 2));
+  l.scales = sc;
+  l.dw = dw;
+  l.partials = static_cast<float*>(ws);
+  l.cols = static_cast<uint32_t>(cols);
+  l.outs = static_cast<uint32_t>(outs);
+  l.tokens = static_cast<uint32_t>(tokens);
+  l.scale_cols = static_cast<uint32_t>(kb);
+  l.ld_dw = ld_dw;
+  l.m_blocks = w.m_tiles;
+  l.n_blocks = w.n_tiles;
+  l.k_blocks = w.k_blocks;
+  l.group = tg::kGroup;
+  l.column_major = 0;
+  l.split_from = w.split_from;
+  l.total_units = w.units;
+  l.splits = w.splits;
+  l.blocks_per_split = w.blocks_per_split;
+  l.grid = 2 * w.pairs;
+  l.watchdog_ns = watchdog_ns ? watchdog_ns : default_watchdog_ns(w.k_blocks);
+  l.inject_skip_phase = inject;
+  l.sms = sms;
+  if (debug && (e = tg::clear_watchdog_status(st)) != cudaSuccess)
+    return fail_cuda("clearing the watchdog word", e);
+  if ((e = tg::launch_wgrad(dtype, debug, l, st)) != cudaSuccess)
+    return fail_cuda("weight gradient launch", e);
+  if (debug) {
+    unsigned int word = 0;
+    if ((e = tg::read_and_clear_watchdog_status(&word, st)) != cudaSuccess)
+      return fail_cuda("weight gradient execution", e);
+    if (word)
+      return fail(TG_ERR_TIMEOUT, "watchdog: a wait gave up (roles 0x%x: 1 producer or conversion, "
+                  "2 MMA, 4 epilogue, 8 shutdown)", word);
+  }
+  return TG_OK;
+}
 
 }  // namespace
 
@@ -262,6 +402,31 @@ int tg_ckpt8_unpack(const void* q_dev, const void* s_dev, void* out_dev, int64_t
   const cudaError_t err = tg::launch_ckpt8_unpack(q_dev, s_dev, out_dev, rows, cols, ld_out, dtype,
                                                   sms, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? TG_OK : fail_cuda("checkpoint unpack launch", err);
+}
+
+int64_t tg_ckpt8_wgrad_workspace_bytes(int64_t rows, int64_t cols, int64_t outs) {
+  TG_TRY(check_wgrad_sizes(rows, cols, outs));
+  if (rows == 0 || cols == 0 || outs == 0) return 0;
+  int max_pairs = 0;
+  TG_TRY(device_ready(nullptr, &max_pairs));
+  if (max_pairs < 1)
+    return fail(TG_ERR_CUDA, "no CTA pair of the weight-gradient kernel fits on this device");
+  return static_cast<int64_t>(wgrad_plan(rows, cols, outs, max_pairs).workspace);
+}
+
+int tg_ckpt8_wgrad(const void* q_dev, const void* s_dev, const void* dY_dev, void* dW_dev,
+                   int64_t rows, int64_t cols, int64_t outs, int64_t ld_dy, int64_t ld_dw,
+                   int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream) {
+  return wgrad_impl(q_dev, s_dev, dY_dev, dW_dev, rows, cols, outs, ld_dy, ld_dw, dtype,
+                    workspace_dev, workspace_bytes, stream, false, 0, -1);
+}
+
+int tg_ckpt8_wgrad_debug(const void* q_dev, const void* s_dev, const void* dY_dev, void* dW_dev,
+                         int64_t rows, int64_t cols, int64_t outs, int64_t ld_dy, int64_t ld_dw,
+                         int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream,
+                         uint64_t watchdog_ns, int64_t inject_skip_phase) {
+  return wgrad_impl(q_dev, s_dev, dY_dev, dW_dev, rows, cols, outs, ld_dy, ld_dw, dtype,
+                    workspace_dev, workspace_bytes, stream, true, watchdog_ns, inject_skip_phase);
 }
 
 }  // extern "C"

@@ -120,3 +120,34 @@ def test_python_layer():
         tg.layer_norm_backward(x, kept, stat, stat)
     with pytest.raises(ValueError):
         tg.ckpt8_unpack(kept, torch.float16, out=x)
+
+
+# q, s, dY, dW, rows, cols, outs, ld_dy, ld_dw, dtype
+WGRAD = [256, 512, 1024, 2048, 16, 40, 64, 64, 64, "bf16"]
+
+
+@pytest.mark.parametrize("code,at,value", [
+    (tg.TG_ERR_ARG, 9, "f32"), (tg.TG_ERR_ARG, 9, 5), (tg.TG_ERR_ARG, 4, -1),
+    (tg.TG_ERR_ARG, 5, 1 << 31), (tg.TG_ERR_ARG, 6, -8), (tg.TG_ERR_ALIGN, 6, 60),
+    (tg.TG_ERR_ARG, 7, 56), (tg.TG_ERR_ALIGN, 7, 68), (tg.TG_ERR_ARG, 8, 56),
+    (tg.TG_ERR_ALIGN, 8, 66), (tg.TG_ERR_ARG, 3, None), (tg.TG_ERR_ALIGN, 3, 2056)])
+def test_weight_gradient(code, at, value):
+    args = list(WGRAD)
+    args[at] = value
+    refused(code, tg.tg_ckpt8_wgrad, *args)
+
+
+def test_weight_gradient_sizes():
+    for args in ((-1, 8, 8), (8, -1, 8), (8, 8, 1 << 31), (8, 1 << 31, 8), (8, 8, 12),
+                 (8, (1 << 31) - 1, (1 << 31) - 8)):
+        with pytest.raises(tg.TgError):
+            tg.tg_ckpt8_wgrad_workspace_bytes(*args)
+    assert tg.tg_ckpt8_wgrad_workspace_bytes(0, 8, 8) == 0
+    refused(tg.TG_ERR_ARG, tg.tg_ckpt8_wgrad, *WGRAD, workspace=4096, workspace_bytes=-1)
+    assert tg.tg_ckpt8_wgrad(*WGRAD[:5], 0, *WGRAD[6:], stream=0) == 0
+    kept = tg.Checkpoint8.empty(4, 72, "cpu")
+    with pytest.raises(ValueError):
+        tg.ckpt8_wgrad(kept, torch.zeros((5, 8), dtype=torch.float16))
+    with pytest.raises(ValueError):
+        tg.ckpt8_wgrad(kept, torch.zeros((4, 8), dtype=torch.float16),
+                       out=torch.zeros((72, 16), dtype=torch.float16))
