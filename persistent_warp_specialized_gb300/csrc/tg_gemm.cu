@@ -171,15 +171,17 @@ WgradParams wgrad_params_of(const WgradLaunch& l) {
   p.inject_skip_phase = l.inject_skip_phase;
   p.scales = static_cast<const uint8_t*>(l.scales);
   p.scale_cols = l.scale_cols;
+  p.tma_scales = l.tma_scales;
   p.splits = l.splits;
   p.blocks_per_split = l.blocks_per_split;
   return p;
 }
 
-template <int DT, bool SPLIT, bool DEBUG>
+template <int DT, int NH, bool SPLIT, bool DEBUG>
 cudaError_t launch_wgrad_pair(const WgradLaunch& l, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(wgrad_pair_kernel<DT, SPLIT, DEBUG>, l.grid, kWgThreads, kWgSmemBytes,
-                             stream, l.tmQ, l.tmB, l.tmC, wgrad_params_of(l));
+  cudaError_t e = launch_pdl(wgrad_pair_kernel<DT, NH, SPLIT, DEBUG>, l.grid, kWgThreads,
+                             WgradConfig<NH>::kSmemBytes, stream, l.tmQ, l.tmB, l.tmC,
+                             l.tmS, wgrad_params_of(l));
   if (e != cudaSuccess || !SPLIT) return e;
   const uint64_t vecs = static_cast<uint64_t>(l.cols) * (l.outs / 8u);
   const uint64_t want = (vecs + 255) / 256, most = static_cast<uint64_t>(l.sms) * 8;
@@ -189,35 +191,42 @@ cudaError_t launch_wgrad_pair(const WgradLaunch& l, cudaStream_t stream) {
                     l.ld_dw);
 }
 
-template <int DT>
+template <int DT, int NH, bool SPLIT>
+cudaError_t launch_wgrad_one(bool debug, const WgradLaunch& l, cudaStream_t stream) {
+  return debug ? launch_wgrad_pair<DT, NH, SPLIT, true>(l, stream)
+               : launch_wgrad_pair<DT, NH, SPLIT, false>(l, stream);
+}
+
+template <int DT, int NH>
 cudaError_t set_wgrad_smem_attr() {
-  const int bytes = static_cast<int>(kWgSmemBytes);
-  cudaError_t e;
   const auto a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  if ((e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, false, false>, a, bytes)) != cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, true, false>, a, bytes)) != cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, false, true>, a, bytes)) != cudaSuccess)
-    return e;
-  return cudaFuncSetAttribute(wgrad_pair_kernel<DT, true, true>, a, bytes);
+  const int bytes = static_cast<int>(WgradConfig<NH>::kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, NH, false, false>, a, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, NH, true, false>, a, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, NH, false, true>, a, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(wgrad_pair_kernel<DT, NH, true, true>, a, bytes);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t launch_wgrad(int dtype, bool debug, const WgradLaunch& l, cudaStream_t stream) {
+  const bool split = l.splits > 1;
   if (dtype == 0) {
-    if (l.splits > 1)
-      return debug ? launch_wgrad_pair<0, true, true>(l, stream)
-                   : launch_wgrad_pair<0, true, false>(l, stream);
-    return debug ? launch_wgrad_pair<0, false, true>(l, stream)
-                 : launch_wgrad_pair<0, false, false>(l, stream);
+    if (l.halves == 2)
+      return split ? launch_wgrad_one<0, 2, true>(debug, l, stream)
+                   : launch_wgrad_one<0, 2, false>(debug, l, stream);
+    return split ? launch_wgrad_one<0, 1, true>(debug, l, stream)
+                 : launch_wgrad_one<0, 1, false>(debug, l, stream);
   }
-  if (l.splits > 1)
-    return debug ? launch_wgrad_pair<1, true, true>(l, stream)
-                 : launch_wgrad_pair<1, true, false>(l, stream);
-  return debug ? launch_wgrad_pair<1, false, true>(l, stream)
-               : launch_wgrad_pair<1, false, false>(l, stream);
+  if (l.halves == 2)
+    return split ? launch_wgrad_one<1, 2, true>(debug, l, stream)
+                 : launch_wgrad_one<1, 2, false>(debug, l, stream);
+  return split ? launch_wgrad_one<1, 1, true>(debug, l, stream)
+               : launch_wgrad_one<1, 1, false>(debug, l, stream);
 }
 
 cudaError_t prepare_gemm_kernels(int* max_pairs) {
@@ -230,8 +239,10 @@ cudaError_t prepare_gemm_kernels(int* max_pairs) {
   if ((e = set_mx_smem_attr<1, false>()) != cudaSuccess) return e;
   if ((e = set_mx_smem_attr<0, true>()) != cudaSuccess) return e;
   if ((e = set_mx_smem_attr<1, true>()) != cudaSuccess) return e;
-  if ((e = set_wgrad_smem_attr<0>()) != cudaSuccess) return e;
-  if ((e = set_wgrad_smem_attr<1>()) != cudaSuccess) return e;
+  if ((e = set_wgrad_smem_attr<0, 1>()) != cudaSuccess) return e;
+  if ((e = set_wgrad_smem_attr<1, 1>()) != cudaSuccess) return e;
+  if ((e = set_wgrad_smem_attr<0, 2>()) != cudaSuccess) return e;
+  if ((e = set_wgrad_smem_attr<1, 2>()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -256,8 +267,8 @@ cudaError_t prepare_gemm_kernels(int* max_pairs) {
   if (mx_clusters < clusters) clusters = mx_clusters;
   int wgrad_clusters = 0;
   cfg.blockDim = dim3(kWgThreads, 1, 1);
-  cfg.dynamicSmemBytes = kWgSmemBytes;
-  e = cudaOccupancyMaxActiveClusters(&wgrad_clusters, wgrad_pair_kernel<1, false, false>, &cfg);
+  cfg.dynamicSmemBytes = WgradConfig<2>::kSmemBytes;
+  e = cudaOccupancyMaxActiveClusters(&wgrad_clusters, wgrad_pair_kernel<1, 2, false, false>, &cfg);
   if (e != cudaSuccess) return e;
   *max_pairs = wgrad_clusters < clusters ? wgrad_clusters : clusters;
   return cudaSuccess;

@@ -106,6 +106,8 @@ cudaError_t launch_ckpt8_unpack(const void* q, const void* s, void* out, int64_t
 // the join of its partial sums.
 struct WgradLaunch {
   CUtensorMap tmQ, tmB, tmC;    // tmC: dW, or the workspace when splits > 1
+  CUtensorMap tmS;              // the scales, when tma_scales
+  uint32_t tma_scales;
   const void* scales;
   void* dw;
   float* partials;
@@ -114,6 +116,7 @@ struct WgradLaunch {
   uint32_t m_blocks, n_blocks, k_blocks, group, column_major;
   uint32_t split_from, total_units;   // per split
   uint32_t splits, blocks_per_split;
+  uint32_t halves;              // N-halves of 256 columns in a tile: 1 or 2
   uint32_t grid;                // CTAs
   uint64_t watchdog_ns;
   int64_t inject_skip_phase;

@@ -79,7 +79,7 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 // How the weight gradient [cols, outs] over ``tokens`` tokens is cut into units.
 struct WgradPlan {
-  uint32_t m_tiles, n_tiles, k_blocks, splits, blocks_per_split, split_from, units, pairs;
+  uint32_t halves, m_tiles, n_tiles, k_blocks, splits, blocks_per_split, split_from, units, pairs;
   uint64_t workspace;   // bytes of partial sums (0: one split)
 };
 
@@ -87,10 +87,24 @@ struct WgradPlan {
 // are split so that every pair has a unit, as long as a unit keeps kWgMinBlocks k-blocks.
 constexpr uint64_t kWgMinBlocks = 8;
 
+// N-halves of 256 columns in a tile of dW.  Two halve the bytes that have to be widened for each
+// multiplication, and give the MMA thread eight MMAs a k-block instead of four; one leaves smaller
+// units when there are few.  Measured (GB300, bf16, one / two halves, us, L2 flushed): tokens x
+// cols x outs 8192^3 861 / 615, 4096^3 134 / 99, 1024 x 4096 x 4096 43.6 / 37.5, 16384 x 2048 x
+// 2048 132 / 103 (32 wide tiles), 32768 x 1000 x 512 49.8 / 51.8 and 2048 x 512 x 512 19.1 / 21.1
+// (4 and 2 wide tiles).
+constexpr uint64_t kWgWideTiles = 16;
+
+uint32_t wgrad_halves(int64_t cols, int64_t outs) {
+  const uint64_t wide = ceil_div(cols, tg::kPairBM) * ceil_div(outs, 2 * tg::kBN);
+  return outs > tg::kBN && wide >= kWgWideTiles ? 2 : 1;
+}
+
 WgradPlan wgrad_plan(int64_t tokens, int64_t cols, int64_t outs, int max_pairs) {
   WgradPlan w;
   w.m_tiles = static_cast<uint32_t>(ceil_div(cols, tg::kPairBM));
-  w.n_tiles = static_cast<uint32_t>(ceil_div(outs, tg::kBN));
+  w.halves = wgrad_halves(cols, outs);
+  w.n_tiles = static_cast<uint32_t>(ceil_div(outs, w.halves * tg::kBN));
   w.k_blocks = static_cast<uint32_t>(ceil_div(tokens, tg::kWgBK));
   const uint64_t tiles = static_cast<uint64_t>(w.m_tiles) * w.n_tiles;
   const uint64_t pairs = static_cast<uint64_t>(max_pairs);
@@ -183,6 +197,11 @@ int wgrad_impl(const void* q, const void* sc, const void* dy, void* dw, int64_t 
                         "workspace"));
   else
     TG_TRY(encode_tiled(&l.tmC, t16, 2, dw, outs, cols, tg::kEpiN, 32, "dW", true, ld_dw * 2));
+  l.tma_scales = kb % 16 == 0 && !off_by(sc, 16) ? 1u : 0u;
+  l.tmS = l.tmQ;
+  if (l.tma_scales)
+    TG_TRY(encode_tiled(&l.tmS, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, sc, kb, tokens,
+                        tg::kWgScalePitch, tg::kWgBK, "s", false));
   l.scales = sc;
   l.dw = dw;
   l.partials = static_cast<float*>(ws);
@@ -200,6 +219,7 @@ int wgrad_impl(const void* q, const void* sc, const void* dy, void* dw, int64_t 
   l.total_units = w.units;
   l.splits = w.splits;
   l.blocks_per_split = w.blocks_per_split;
+  l.halves = w.halves;
   l.grid = 2 * w.pairs;
   l.watchdog_ns = watchdog_ns ? watchdog_ns : default_watchdog_ns(w.k_blocks);
   l.inject_skip_phase = inject;

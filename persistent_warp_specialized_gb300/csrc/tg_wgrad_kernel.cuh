@@ -8,14 +8,17 @@
 // becomes 16-bit in shared memory: E4M3 has 4 significant bits, so x is exact in bf16 and fp16
 // (rounded once where it leaves their range), products are exact and sums are fp32.
 //
-// The pair structure is that of tg_gemm_pair_kernel.cuh (256 x 256 tiles, CTA r holding columns
-// 128 r .. of x as its rows of A, and half of the tile's columns of dY) with one more role: per
-// k-block of 64 tokens the producer loads 64 x 128 bytes of q (``raw``) and the dY boxes, warps
-// 8..11 turn the bytes into the A operand (two chunks of 64 columns x 64 tokens, 128-byte swizzle)
-// and report to the even CTA's ``made`` barrier, and the MMA thread waits for both CTAs' reports
-// and dY bytes.  Turning 8192 bytes a k-block takes each of the 128 threads 64 values, about half
-// of the 512 cycles that the MMAs of the k-block take.
+// The pair structure is that of tg_gemm_pair_kernel.cuh and, for tiles of two N-halves (256 x 512),
+// of tg_gemm_pair_wide_kernel.cuh: CTA r holds columns 128 r .. of x as its rows of A, and half of
+// each N-half's columns of dY.  One more role: per k-block of 64 tokens warp 3 loads 64 x 128 bytes
+// of q and their scales into a ring of their own, and the eight warps 8..15, four to a k-block,
+// turn them into the A operand (two chunks of 64 columns x 64 tokens, 128-byte swizzle) and report
+// to the even CTA's ``made`` barrier (there also for the dY bytes of both CTAs), which the MMA
+// thread waits for.
 //
+// What bounds it, at 8192^3 with two N-halves: shared memory and the MMA thread's hand-over.  The
+// MMAs of a k-block take 1024 cycles; with the widening left out (in a copy) the kernel ran at the
+// dense GEMM's 1980 TFLOP/s, its reads and writes of 8 + 16 KiB a k-block cost 12 %.
 // Few tiles: the tokens are split into ``splits`` ranges, (tile, range) units write fp32 partial
 // sums to a workspace [splits][m_blocks * 256][outs], and wgrad_join_kernel adds them in order.
 //
@@ -31,6 +34,7 @@ namespace tg {
 struct WgradParams : GemmParams {   // M = cols, N = outs, K = tokens
   const uint8_t* scales;            // [tokens][scale_cols]
   uint32_t scale_cols;
+  uint32_t tma_scales;              // 1: rows of scales are whole 16-byte units (tmS)
   uint32_t splits, blocks_per_split;
 };
 
@@ -62,25 +66,68 @@ struct WgradUnits {
   }
 };
 
+template <int NH>
 struct __align__(8) WgradCtl {
-  uint64_t loaded[kWgStages];        // dY boxes of both CTAs; used in the even CTA only
-  uint64_t made[kWgStages];          // A operand of both CTAs; used in the even CTA only
-  uint64_t raw[kWgStages];           // this CTA's checkpoint bytes
-  uint64_t consumed[kWgStages];
-  uint64_t tmem_full[2];
+  using Cfg = WgradConfig<NH>;
+  uint64_t loaded[Cfg::kStages];     // dY boxes of both CTAs; used in the even CTA only
+  uint64_t made[Cfg::kStages];       // and the A operand as well; used in the even CTA only
+  uint64_t consumed[Cfg::kStages];
+  uint64_t raw_full[Cfg::kRaws];     // this CTA's checkpoint bytes
+  uint64_t scale_full[Cfg::kRaws];   // and their scales
+  uint64_t raw_empty[Cfg::kRaws];    // both are in registers
+  uint64_t tmem_full[2];             // accumulators: columns 0..255 and 256..511 of TMEM
   uint64_t tmem_empty[2];            // used in the even CTA only
   uint64_t drain;
   uint64_t odd_done;
-  PairFills<kWgStages> fills;
-  uint32_t sink[kEpiWarps + kWgMakeWarps];
+  PairFills<Cfg::kStages> fills;
+  uint32_t sink[kEpiWarps + kWgMakeGroups * kWgMakeWarps];
   uint32_t tmem_base;
   int abort;
+};
+
+// Asynchronous copy of ``bytes`` (0..4) bytes to shared memory, the rest of the 4 zero-filled; both
+// addresses 4-byte aligned.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+// Arrives on ``bar`` (one of its initial count) once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// A position in a ring of N slots and the parity of its present turn.
+template <uint32_t N>
+struct RingPos {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void advance(uint32_t by) {   // by <= N
+    slot += by;
+    if (slot >= N) {
+      slot -= N;
+      parity ^= 1u;
+    }
+  }
 };
 
 // 16 E4M3 bytes times 2^(s - 127), to 16-bit values packed in pairs; exact but for the final
 // rounding, any bytes.
 template <int DT>
-__device__ __noinline__ void widen_any(const uint32_t (&in)[4], uint32_t s, uint32_t (&out)[8]) {
+__device__ __forceinline__ void widen_any(const uint32_t (&in)[4], uint32_t s, uint32_t (&out)[8]) {
   const float scale = e8m0_value(s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -89,20 +136,22 @@ __device__ __noinline__ void widen_any(const uint32_t (&in)[4], uint32_t s, uint
   }
 }
 
-// The same for bytes without NaN and scales up to 2^7, by moving bits: E4M3's exponent and fraction
-// put in the place of the 16-bit type's read as the value times 2^-120 (bf16) or 2^-8 (fp16),
-// subnormals included, and one multiplication by 2^(s - 7) or 2^(s - 119) sets that right with one
-// rounding.  Larger scales, where that factor would leave the type (and fp16's below 2^-24, s < 95),
-// and NaN go the long way.
+// Whether the short way below is exact for these bytes: no NaN among them and a scale under which
+// its factor is a number of the type.
 template <int DT>
-__device__ __forceinline__ void widen16(const uint32_t (&in)[4], uint32_t s, uint32_t (&out)[8]) {
+__device__ __forceinline__ bool widens_short(const uint32_t (&in)[4], uint32_t s) {
   uint32_t nan = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) nan |= ((in[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-  if (nan != 0u || s > 134u || (DT == 0 && s < 95u)) {
-    widen_any<DT>(in, s, out);
-    return;
-  }
+  for (int i = 0; i < 4; ++i) nan |= (in[i] & 0x7F7F7F7Fu) + 0x01010101u;
+  return (nan & 0x80808080u) == 0u && s <= 134u && (DT == 1 || s >= 95u);
+}
+
+// The same by moving bits: E4M3's exponent and fraction put in the place of the 16-bit type's read
+// as the value times 2^-120 (bf16) or 2^-8 (fp16), subnormals included, and one multiplication by
+// 2^(s - 7) or 2^(s - 119) sets that right with one rounding.
+template <int DT>
+__device__ __forceinline__ void widen_short(const uint32_t (&in)[4], uint32_t s,
+                                            uint32_t (&out)[8]) {
   uint32_t factor;   // the power of two in both halves
   if constexpr (DT == 1) {
     factor = (s + 120u) << 7;
@@ -154,15 +203,18 @@ __device__ __forceinline__ void wgrad_store_partial(const uint32_t (&v)[64], uin
   __syncwarp();
 }
 
-// DT: 0 = fp16, 1 = bf16 (dY and dW).  SPLIT: partial sums to the workspace (tmC is then the
-// workspace's map).  DEBUG adds fault injection.
-template <int DT, bool SPLIT, bool DEBUG>
+// DT: 0 = fp16, 1 = bf16 (dY and dW).  NH: N-halves per tile.  SPLIT: partial sums to the workspace
+// (tmC is then the workspace's map).  DEBUG adds fault injection.
+template <int DT, int NH, bool SPLIT, bool DEBUG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
     wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmC, const WgradParams p) {
+                      const __grid_constant__ CUtensorMap tmC,
+                      const __grid_constant__ CUtensorMap tmS, const WgradParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ WgradCtl ctl;
+  using Cfg = WgradConfig<NH>;
+  constexpr uint32_t kStages = Cfg::kStages, kRaws = Cfg::kRaws, kStageBytes = Cfg::kStageBytes;
+  __shared__ WgradCtl<NH> ctl;
 
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
@@ -170,27 +222,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
   const uint32_t pair = blockIdx.x >> 1;
   const uint32_t num_pairs = gridDim.x >> 1;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sA0 = sbase;                      // stage s: A, then B, then the raw bytes
+  const uint32_t sA0 = sbase;                      // stage s: A, then dY chunks (2 h + c)
   const uint32_t sB0 = sA0 + kWgABytes;
-  const uint32_t sR0 = sB0 + kWgBBytes;
-  const uint32_t sEpi = sbase + kWgStages * kWgStageBytes;
+  const uint32_t sR0 = sbase + kStages * kStageBytes;
+  const uint32_t sEpi = sR0 + kRaws * kWgRawBytes;
+  const uint32_t sS0 = sEpi + kEpiSmemBytes;       // scales of raw slot r: sS0 + r * kWgScaleBytes
 
   const uint32_t bar_loaded = smem_u32(&ctl.loaded[0]);
   const uint32_t bar_made = smem_u32(&ctl.made[0]);
-  const uint32_t bar_raw = smem_u32(&ctl.raw[0]);
   const uint32_t bar_consumed = smem_u32(&ctl.consumed[0]);
+  const uint32_t bar_raw_full = smem_u32(&ctl.raw_full[0]);
+  const uint32_t bar_scale_full = smem_u32(&ctl.scale_full[0]);
+  const uint32_t bar_raw_empty = smem_u32(&ctl.raw_empty[0]);
   const uint32_t bar_tmem_full = smem_u32(&ctl.tmem_full[0]);
   const uint32_t bar_tmem_empty = smem_u32(&ctl.tmem_empty[0]);
   const uint32_t bar_drain = smem_u32(&ctl.drain);
 
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int s = 0; s < kWgStages; ++s) {
+    for (uint32_t s = 0; s < kStages; ++s) {
       mbar_init(bar_loaded + 8u * s, 1);
       mbar_init(bar_made + 8u * s, kWgMakeWarps);
-      mbar_init(bar_raw + 8u * s, 1);
       mbar_init(bar_consumed + 8u * s, 1);
       ctl.fills.par[s] = 0;
+    }
+#pragma unroll
+    for (uint32_t r = 0; r < kRaws; ++r) {
+      mbar_init(bar_raw_full + 8u * r, 1);
+      mbar_init(bar_scale_full + 8u * r, 32);
+      mbar_init(bar_raw_empty + 8u * r, kWgMakeWarps);
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -206,6 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
     prefetch_tensormap(&tmQ);
     prefetch_tensormap(&tmB);
     prefetch_tensormap(&tmC);
+    if (p.tma_scales) prefetch_tensormap(&tmS);
   }
   __syncwarp();
   if (warp == 2) {
@@ -224,56 +285,130 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
   const uint64_t limit = p.watchdog_ns;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (both CTAs)
+    // ------------------------------------------------------------ dY loads (both CTAs)
     if (lane == 0) {
-      uint32_t pending = 0, pending_par = 0;   // raw fills that may still be in flight
       bool ok = true;
       uint64_t phase = 0;
+      RingPos<kStages> at;
       for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
         const PersistentTileScheduler& sched = un.sched;
         const bool half = sched.half_unit();
-        const int32_t m0 = static_cast<int32_t>(sched.m_idx * kPairBM + rank * kBM);
-        const int32_t n0 = static_cast<int32_t>(sched.n_idx * kBN) +
-                           (half ? sched.part * (kBN / 2) +
-                                       static_cast<int32_t>(rank) * (kPairBNHalf / 2)
-                                 : static_cast<int32_t>(rank) * kPairBNHalf);
-        const uint32_t b_chunks = half ? 1u : 2u;
-        const uint32_t tx_bytes = 2u * b_chunks * kWgChunkBytes;
-        for (uint32_t k = un.k_lo; k < un.k_hi; ++k, ++phase) {
-          const uint32_t s = static_cast<uint32_t>(phase % kWgStages);
-          const uint32_t par = static_cast<uint32_t>((phase / kWgStages) & 1u);
+        // chunks of 64 columns this CTA loads, and the first column of each N-half's share
+        const uint32_t chunks = half ? NH : 2u * NH;
+        const int32_t n0 =
+            static_cast<int32_t>(sched.n_idx) * Cfg::kTileN +
+            (half ? sched.part * (Cfg::kTileN / 2) : 0) +
+            static_cast<int32_t>(rank) * (half && NH == 1 ? kPairBNHalf / 2 : kPairBNHalf);
+        const uint32_t tx_bytes = 2u * chunks * kWgChunkBytes;
+        for (uint32_t k = un.k_lo; k < un.k_hi; ++k, ++phase, at.advance(1)) {
+          const uint32_t s = at.slot, par = at.parity;
           if (!pair_wait_or_abort(bar_consumed + 8u * s, par ^ 1u, abort_flag, peer_abort, limit,
                                   kRoleProducer)) {
             ok = false;
             break;
           }
-          pending &= ~(1u << s);   // its bytes were turned and multiplied
           if (DEBUG && injected_skip(p.inject_skip_phase, phase))
             continue;  // injected fault: this CTA never arms or fills this phase
           const int32_t kx = static_cast<int32_t>(k) * kWgBK;
-          mbar_arrive_expect_tx(bar_raw + 8u * s, kWgRawBytes);
-          tma_load_2d(sR0 + s * kWgStageBytes, &tmQ, bar_raw + 8u * s, m0, kx);
-          pending |= 1u << s;
-          pending_par = (pending_par & ~(1u << s)) | (par << s);
           const uint32_t full_even = mapa_shared(bar_loaded + 8u * s, 0);
           if (rank == 0) mbar_arrive_expect_tx(bar_loaded + 8u * s, tx_bytes);
 #pragma unroll
-          for (uint32_t c = 0; c < 2; ++c) {
-            if (c >= b_chunks) break;
-            tma_load_2d_pair(sB0 + s * kWgStageBytes + c * kWgChunkBytes, &tmB, full_even,
-                             n0 + static_cast<int32_t>(c * kBChunkCols), kx);
+          for (uint32_t c = 0; c < 2u * NH; ++c) {
+            if (c >= chunks) break;
+            tma_load_2d_pair(sB0 + s * kStageBytes + c * kWgChunkBytes, &tmB, full_even,
+                             n0 + static_cast<int32_t>((c / 2u) * kBN + (c % 2u) * kBChunkCols),
+                             kx);
           }
           record_fill(ctl.fills, s, phase, par, tx_bytes / 2u);
         }
       }
-      if (!ok) {
-        for (uint32_t s = 0; s < kWgStages; ++s)
-          if ((pending >> s) & 1u)
-            wait_bounded(bar_raw + 8u * s, (pending_par >> s) & 1u, limit, kRoleDrain);
-      }
       // the odd producer has stopped filling: its records are final (see pair_drain_fills)
       if (rank == 1) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl.odd_done), 0));
     }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ checkpoint loads (both CTAs)
+    if (lane == 0) {
+      uint32_t pending = 0, pending_par = 0;   // fills that may still be in flight
+      bool ok = true;
+      RingPos<kRaws> at;
+      for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
+        const int32_t m0 = static_cast<int32_t>(un.sched.m_idx * kPairBM + rank * kBM);
+        // scales by TMA: 16 neighbouring bytes of each token's row, from a 16-byte boundary on
+        const int32_t sc = (m0 / kCkptBlock) & ~15;
+        for (uint32_t k = un.k_lo; k < un.k_hi; ++k, at.advance(1)) {
+          const uint32_t r = at.slot, par = at.parity;
+          if (!pair_wait_or_abort(bar_raw_empty + 8u * r, par ^ 1u, abort_flag, peer_abort, limit,
+                                  kRoleProducer)) {
+            ok = false;
+            break;
+          }
+          const int32_t kx = static_cast<int32_t>(k) * kWgBK;
+          mbar_arrive_expect_tx(bar_raw_full + 8u * r,
+                                kWgRawBytes + (p.tma_scales ? kWgScaleBytes : 0u));
+          tma_load_2d(sR0 + r * kWgRawBytes, &tmQ, bar_raw_full + 8u * r, m0, kx);
+          if (p.tma_scales)
+            tma_load_2d(sS0 + r * kWgScaleBytes, &tmS, bar_raw_full + 8u * r, sc, kx);
+          pending |= 1u << r;
+          pending_par = (pending_par & ~(1u << r)) | (par << r);
+        }
+      }
+      if (!ok) {
+        for (uint32_t r = 0; r < kRaws; ++r)
+          if ((pending >> r) & 1u)
+            wait_bounded(bar_raw_full + 8u * r, (pending_par >> r) & 1u, limit, kRoleDrain);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scale loads (both CTAs)
+    // A lane takes tokens lane and lane + 32 of the k-block: the 4 scales of this CTA's 128 columns
+    // start at byte o of the scale array, and are copied with the 4-byte words around them, so
+    // scale j lies at byte o % 4 + j of the token's place.  Bytes past the array's end are zero-filled.
+    // (Past the row's end they are the next row's, and multiply zeros.)  An array that does not
+    // start on a 4-byte boundary is read byte by byte, without running ahead.  Where rows of scales
+    // are whole 16-byte units warp 3 loads them by TMA instead, one box a k-block: these copies
+    // take a shared-memory cycle for each word (8192^3: 678 us with them, 640 without).
+    const bool words = (reinterpret_cast<uintptr_t>(p.scales) & 3u) == 0u;
+    const uint64_t total = static_cast<uint64_t>(p.K) * p.scale_cols;
+    bool ok = !p.tma_scales;
+    RingPos<kRaws> ring;
+    for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
+      const uint32_t sc = (un.sched.m_idx * kPairBM + rank * kBM) / kCkptBlock;
+      for (uint32_t k = un.k_lo; k < un.k_hi; ++k, ring.advance(1)) {
+        const uint32_t r = ring.slot, par = ring.parity;
+        const bool got = pair_wait_or_abort(bar_raw_empty + 8u * r, par ^ 1u, abort_flag,
+                                            peer_abort, limit, kRoleProducer);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i) {
+          const uint32_t row = i * 32u + lane;
+          const uint64_t o = (static_cast<uint64_t>(k) * kWgBK + row) * p.scale_cols + sc;
+          const uint32_t dst = sS0 + r * kWgScaleBytes + row * kWgScalePitch;
+          if (words) {
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+              const uint64_t at = (o & ~3ull) + 4u * h;
+              const uint64_t left = at < total ? total - at : 0;
+              cp_async_4(dst + 4u * h, p.scales + (left ? at : 0),
+                         static_cast<uint32_t>(left < 4 ? left : 4));
+            }
+          } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+              st_shared_u8(dst + (o & 3u) + j, o + j < total ? p.scales[o + j] : 0u);
+          }
+        }
+        if (words)
+          cp_async_arrive(bar_scale_full + 8u * r);
+        else
+          mbar_arrive(bar_scale_full + 8u * r);
+      }
+    }
+    cp_async_wait_all();
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
@@ -281,41 +416,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
       constexpr uint32_t idesc_full = idesc_f16(DT, kPairBM, kBN, /*A M-major*/ 1, /*B N-major*/ 1);
       constexpr uint32_t idesc_half = idesc_f16(DT, kPairBM, kBN / 2, 1, 1);
       bool ok = true;
-      uint64_t phase = 0;
-      for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
-        const uint32_t w = un.w;
-        const uint32_t buf = w & 1u;
-        if (!pair_wait_or_abort<true>(bar_tmem_empty + 8u * buf, ((w >> 1) & 1u) ^ 1u, abort_flag,
-                                      peer_abort, limit, kRoleMma)) {
-          ok = false;
-          break;
+      RingPos<kStages> ring;
+      uint32_t uses[2] = {0, 0};      // units that have used each accumulator
+      // MMAs of N-half h into accumulator ``acc`` for the k-block in ring slot s
+      auto issue_half = [&](uint32_t s, uint32_t h, uint32_t acc, bool first, uint32_t idesc) {
+#pragma unroll
+        for (uint32_t kk = 0; kk < kWgBK / kUmmaK; ++kk) {
+          // both operands: 16 tokens = 2048 bytes on; LBO = the next 64 columns
+          const uint32_t off = s * kStageBytes + kk * kUmmaK * 128u;
+          const uint64_t a_desc = smem_desc_sw128(sA0 + off, kWgChunkBytes, 1024);
+          const uint64_t b_desc =
+              smem_desc_sw128(sB0 + off + h * 2u * kWgChunkBytes, kWgChunkBytes, 1024);
+          umma_f16_pair(tmem_base + acc * kBN, a_desc, b_desc, idesc, !first || kk != 0u ? 1u : 0u);
         }
+      };
+      auto acc_free = [&](uint32_t acc) {   // both CTAs' epilogues have read its last unit out
+        const bool got = pair_wait_or_abort<true>(bar_tmem_empty + 8u * acc, (uses[acc] & 1u) ^ 1u,
+                                                  abort_flag, peer_abort, limit, kRoleMma);
+        ++uses[acc];
         tcgen05_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + buf * kBN;
-        const uint32_t idesc = un.sched.half_unit() ? idesc_half : idesc_full;
-        for (uint32_t k = un.k_lo; k < un.k_hi; ++k, ++phase) {
-          const uint32_t s = static_cast<uint32_t>(phase % kWgStages);
-          const uint32_t par = static_cast<uint32_t>((phase / kWgStages) & 1u);
-          if (!pair_wait_or_abort(bar_loaded + 8u * s, par, abort_flag, peer_abort, limit,
-                                  kRoleMma) ||
-              !pair_wait_or_abort<true>(bar_made + 8u * s, par, abort_flag, peer_abort, limit,
-                                        kRoleMma)) {
+        return got;
+      };
+      for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
+        const bool half = un.sched.half_unit();
+        const uint32_t halves = half ? 1u : NH;
+        const uint32_t acc0 = NH == 1 ? un.w & 1u : 0u;
+        const uint32_t idesc = half && NH == 1 ? idesc_half : idesc_full;
+        const uint32_t nk = un.k_hi - un.k_lo;
+        // N-half 1 of the first k-block waits until the epilogue has handed accumulator 1 back;
+        // that slot is released once both halves have read it
+        const uint32_t defer = halves == 2u && nk > 1u ? 1u : 0u;
+        const uint32_t s0 = ring.slot;
+        for (uint32_t k = 0; k < nk; ++k, ring.advance(1)) {
+          const uint32_t s = ring.slot, par = ring.parity;
+          if (!pair_wait_or_abort<true>(bar_made + 8u * s, par, abort_flag, peer_abort, limit,
+                                        kRoleMma) ||
+              (k == 0 && !acc_free(acc0))) {
             ok = false;
             break;
           }
           tcgen05_fence_after_sync();
-#pragma unroll
-          for (uint32_t kk = 0; kk < kWgBK / kUmmaK; ++kk) {
-            // both operands: 16 tokens = 2048 bytes on; LBO = the next 64 columns
-            const uint32_t off = s * kWgStageBytes + kk * kUmmaK * 128u;
-            const uint64_t a_desc = smem_desc_sw128(sA0 + off, kWgChunkBytes, 1024);
-            const uint64_t b_desc = smem_desc_sw128(sB0 + off, kWgChunkBytes, 1024);
-            umma_f16_pair(d_tmem, a_desc, b_desc, idesc, (k != un.k_lo || kk != 0u) ? 1u : 0u);
+          issue_half(s, 0, acc0, k == 0, idesc);
+          if (halves == 2u) {
+            if (k < defer) continue;
+            if (k == defer) {
+              if (!acc_free(1)) {
+                ok = false;
+                break;
+              }
+              if (defer) {   // catch N-half 1 up
+                issue_half(s0, 1, 1, true, idesc);
+                umma_commit_pair_multicast(bar_consumed + 8u * s0, 0x3);
+              }
+            }
+            issue_half(s, 1, 1, k == 0, idesc);
           }
           umma_commit_pair_multicast(bar_consumed + 8u * s, 0x3);
         }
         if (!ok) break;
-        umma_commit_pair_multicast(bar_tmem_full + 8u * buf, 0x3);
+        umma_commit_pair_multicast(bar_tmem_full + 8u * acc0, 0x3);
+        if (halves == 2u) umma_commit_pair_multicast(bar_tmem_full + 8u, 0x3);
       }
       umma_commit_pair_multicast(bar_drain, 0x1);
       wait_bounded(bar_drain, 0, limit, kRoleDrain);
@@ -323,65 +483,105 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
     __syncwarp();
   } else if (warp >= kWgFirstMakeWarp) {
     // ------------------------------------------------------------ checkpoint bytes -> A operand
-    // Eight threads take a token's 128 bytes, 16 each; the warps' threads cover 16 tokens at a
-    // time.  A warp reads 512 neighbouring bytes; a thread writes its 32 bytes as two 16-byte
-    // chunks of the token's row of column chunk c / 4, and the threads of column chunk 1 write
-    // their second one first, so that eight threads never meet in a bank.
-    const uint32_t tt = threadIdx.x - kWgFirstMakeWarp * 32u;
+    // Group g takes k-blocks g, g + groups, ...  Eight threads take a token's 128 bytes, 16 each;
+    // the group's threads cover 16 tokens at a time.  A warp reads 512 neighbouring bytes; a thread
+    // writes its 32 bytes as two 16-byte chunks of the token's row of column chunk c / 4, and the
+    // threads of column chunk 1 write their second one first, so that eight threads never meet in
+    // a bank.
+    const uint32_t group = (warp - kWgFirstMakeWarp) / kWgMakeWarps;
+    const uint32_t tt = threadIdx.x - (kWgFirstMakeWarp + group * kWgMakeWarps) * 32u;
     const uint32_t c = tt & 7u, r0 = tt >> 3;
     const uint32_t sink_even = mapa_shared(smem_u32(&ctl.sink[warp - kFirstEpiWarp]), 0);
-    uint64_t phase = 0;
+    const bool swap = c >= 4u;
+    // where the thread's two chunks of token row r0 go (r0 + 16 i has the same r % 8)
+    const uint32_t base = (c / 4u) * kWgChunkBytes + r0 * 128u;
+    const uint32_t at0 = base + (((2u * (c & 3u) + (swap ? 1u : 0u)) ^ (r0 & 7u)) << 4);
+    const uint32_t at1 = base + (((2u * (c & 3u) + (swap ? 0u : 1u)) ^ (r0 & 7u)) << 4);
+    RingPos<kStages> ring;
+    RingPos<kRaws> raw;
+    ring.advance(group);
+    raw.advance(group);
+    uint32_t skip = group;   // k-blocks of the units ahead until this group's next one
     bool ok = true;
     for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
-      const uint32_t m0 = un.sched.m_idx * kPairBM + rank * kBM;
-      const uint32_t sc = m0 / kCkptBlock + c / 2u;     // this thread's scale column
-      const bool sc_in = sc < p.scale_cols;
-      uint32_t next_s[kWgPasses];
-      auto fetch_scales = [&](uint32_t k) {             // zero bytes lie past the ends: any scale
-#pragma unroll
-        for (uint32_t i = 0; i < kWgPasses; ++i) {
-          const uint32_t t = k * kWgBK + i * 16u + r0;
-          next_s[i] = sc_in && k < un.k_hi && t < p.K
-                          ? p.scales[static_cast<uint64_t>(t) * p.scale_cols + sc]
-                          : 127u;
-        }
-      };
-      fetch_scales(un.k_lo);
-      for (uint32_t k = un.k_lo; k < un.k_hi; ++k, ++phase) {
-        const uint32_t s = static_cast<uint32_t>(phase % kWgStages);
-        const uint32_t par = static_cast<uint32_t>((phase / kWgStages) & 1u);
-        uint32_t scale[kWgPasses];
-#pragma unroll
-        for (uint32_t i = 0; i < kWgPasses; ++i) scale[i] = next_s[i];
-        fetch_scales(k + 1);
-        const bool got = pair_wait_or_abort(bar_raw + 8u * s, par, abort_flag, peer_abort, limit,
-                                            kRoleProducer);
+      const uint32_t nk = un.k_hi - un.k_lo;
+      // this thread's scale of token r0: by TMA at the unit's place in its 16 bytes, else at byte
+      // o % 4 (the same for r0 + 16 i in every k-block)
+      const uint32_t sc = (un.sched.m_idx * kPairBM + rank * kBM) / kCkptBlock;
+      const uint32_t scale_at = sS0 + r0 * kWgScalePitch + c / 2u +
+                                (p.tma_scales ? sc & 15u : (r0 * p.scale_cols) & 3u);
+      uint32_t k = skip;
+      for (; k < nk; k += kWgMakeGroups, ring.advance(kWgMakeGroups), raw.advance(kWgMakeGroups)) {
+        const uint32_t r = raw.slot, s = ring.slot;
+        bool got = pair_wait_or_abort(bar_raw_full + 8u * r, raw.parity, abort_flag, peer_abort,
+                                      limit, kRoleProducer) &&
+                   (p.tma_scales ||
+                    pair_wait_or_abort(bar_scale_full + 8u * r, raw.parity, abort_flag, peer_abort,
+                                       limit, kRoleProducer));
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
-        const uint32_t raw = sR0 + s * kWgStageBytes, a = sA0 + s * kWgStageBytes;
+        uint32_t in[kWgPasses][4], scale[kWgPasses];
 #pragma unroll
         for (uint32_t i = 0; i < kWgPasses; ++i) {
-          const uint32_t r = i * 16u + r0;
-          uint32_t in[4], out[8];
-          ld_shared_v4(raw + r * 128u + c * 16u, in[0], in[1], in[2], in[3]);
-          widen16<DT>(in, scale[i], out);
-          const uint32_t row = a + (c / 4u) * kWgChunkBytes + r * 128u;
-          const uint32_t u0 = 2u * (c & 3u);
-          const bool swap = c >= 4u;
+          ld_shared_v4(sR0 + r * kWgRawBytes + (i * 16u + r0) * 128u + c * 16u, in[i][0], in[i][1],
+                       in[i][2], in[i][3]);
+          scale[i] = ld_shared_u8(scale_at + r * kWgScaleBytes + i * 16u * kWgScalePitch);
+        }
+        bool is_short = true;
 #pragma unroll
-          for (uint32_t h = 0; h < 2; ++h) {
-            const uint32_t unit = u0 + (swap ? 1u - h : h);
-            const bool second = swap ? h == 0u : h == 1u;
-            st_shared_v4(row + ((unit ^ (r & 7u)) << 4), second ? out[4] : out[0],
-                         second ? out[5] : out[1], second ? out[6] : out[2],
-                         second ? out[7] : out[3]);
+        for (uint32_t i = 0; i < kWgPasses; ++i) {
+          is_short = is_short && widens_short<DT>(in[i], scale[i]);
+          // the half that is written first comes first
+          const uint32_t w0 = in[i][0], w1 = in[i][1];
+          in[i][0] = swap ? in[i][2] : w0;
+          in[i][1] = swap ? in[i][3] : w1;
+          in[i][2] = swap ? w0 : in[i][2];
+          in[i][3] = swap ? w1 : in[i][3];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_raw_empty + 8u * r);   // the bytes are in registers
+        got = pair_wait_or_abort(bar_consumed + 8u * s, ring.parity ^ 1u, abort_flag, peer_abort,
+                                 limit, kRoleProducer);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        const uint32_t a = sA0 + s * kStageBytes;
+        auto put = [&](uint32_t i, const uint32_t (&out)[8]) {
+          st_shared_v4(a + at0 + i * 2048u, out[0], out[1], out[2], out[3]);
+          st_shared_v4(a + at1 + i * 2048u, out[4], out[5], out[6], out[7]);
+        };
+        if (__all_sync(0xffffffffu, is_short)) {
+#pragma unroll
+          for (uint32_t i = 0; i < kWgPasses; ++i) {
+            uint32_t out[8];
+            widen_short<DT>(in[i], scale[i], out);
+            put(i, out);
+          }
+        } else {
+#pragma unroll
+          for (uint32_t i = 0; i < kWgPasses; ++i) {
+            uint32_t out[8];
+            widen_any<DT>(in[i], scale[i], out);
+            put(i, out);
           }
         }
         fence_proxy_async_shared();
+        // the report of the even CTA's first warp of the group also says that dY has landed, so
+        // the MMA thread has one barrier to wait for (two took it 100 cycles more a k-block)
+        if (rank == 0 && tt < 32u) {
+          got = pair_wait_or_abort(bar_loaded + 8u * s, ring.parity, abort_flag, peer_abort, limit,
+                                   kRoleProducer);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+        }
         pair_report_warp(bar_made + 8u * s, rank, lane, sink_even);
       }
+      skip = k - nk;
     }
     __syncwarp();
   } else if (warp >= kFirstEpiWarp) {
@@ -389,36 +589,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
     const uint32_t q = warp - kFirstEpiWarp;
     const uint32_t sink_even = mapa_shared(smem_u32(&ctl.sink[q]), 0);
     uint32_t chunk = 0;
-    for (WgradUnits un(p, pair, num_pairs); un.valid(); un.next()) {
-      const uint32_t w = un.w;
-      const uint32_t buf = w & 1u;
-      const bool got = pair_wait_or_abort(bar_tmem_full + 8u * buf, (w >> 1) & 1u, abort_flag,
-                                          peer_abort, limit, kRoleEpilogue);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tcgen05_fence_after_sync();
+    uint32_t uses[2] = {0, 0};
+    bool ok = true;
+    for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
       const bool half = un.sched.half_unit();
+      const uint32_t halves = half ? 1u : NH;
+      const uint32_t chunks = half && NH == 1 ? kBN / kEpiN / 2 : kBN / kEpiN;
       const int32_t row0 =
           static_cast<int32_t>(un.sched.m_idx * kPairBM + rank * kBM + q * 32u);
-      const int32_t col0 = static_cast<int32_t>(un.sched.n_idx) * kBN +
-                           (half ? un.sched.part * (kBN / 2) : 0);
-      const uint32_t chunks = half ? kBN / kEpiN / 2 : kBN / kEpiN;
-      const uint32_t t_row = tmem_base + ((q * 32u) << 16) + buf * kBN;
 #pragma unroll 1
-      for (uint32_t j = 0; j < chunks; ++j, ++chunk) {
-        uint32_t v[64];
-        tmem_ld_32x32b_x64(t_row + j * kEpiN, v);
-        if (j == chunks - 1) {
-          tcgen05_fence_before_sync();
-          pair_report_warp(bar_tmem_empty + 8u * buf, rank, lane, sink_even);
+      for (uint32_t h = 0; h < halves; ++h) {
+        const uint32_t acc = NH == 1 ? un.w & 1u : h;
+        const bool got = pair_wait_or_abort(bar_tmem_full + 8u * acc, uses[acc] & 1u, abort_flag,
+                                            peer_abort, limit, kRoleEpilogue);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
         }
-        const int32_t x = col0 + static_cast<int32_t>(j * kEpiN);
-        if constexpr (SPLIT) {
-          wgrad_store_partial(v, lane, sEpi + q * 2u * kEpiBufBytes, &tmC,
-                              static_cast<int32_t>(un.split * p.m_blocks * kPairBM) + row0, x,
-                              p.N);
-        } else {
-          epilogue_store_chunk<DT>(v, lane, sEpi + (q * 2u + (chunk & 1u)) * kEpiBufBytes, &tmC, p,
-                                   row0, x);
+        ++uses[acc];
+        tcgen05_fence_after_sync();
+        const int32_t col0 = static_cast<int32_t>(un.sched.n_idx) * Cfg::kTileN +
+                             (half ? un.sched.part * (Cfg::kTileN / 2) : 0) +
+                             static_cast<int32_t>(h) * kBN;
+        const uint32_t t_row = tmem_base + ((q * 32u) << 16) + acc * kBN;
+#pragma unroll 1
+        for (uint32_t j = 0; j < chunks; ++j, ++chunk) {
+          uint32_t v[64];
+          tmem_ld_32x32b_x64(t_row + j * kEpiN, v);
+          if (j == chunks - 1) {
+            tcgen05_fence_before_sync();
+            pair_report_warp(bar_tmem_empty + 8u * acc, rank, lane, sink_even);
+          }
+          const int32_t x = col0 + static_cast<int32_t>(j * kEpiN);
+          if constexpr (SPLIT) {
+            wgrad_store_partial(v, lane, sEpi + q * 2u * kEpiBufBytes, &tmC,
+                                static_cast<int32_t>(un.split * p.m_blocks * kPairBM) + row0, x,
+                                p.N);
+          } else {
+            epilogue_store_chunk<DT>(v, lane, sEpi + (q * 2u + (chunk & 1u)) * kEpiBufBytes, &tmC,
+                                     p, row0, x);
+          }
         }
       }
     }

@@ -160,6 +160,18 @@ def test_row_strides(pad_y, pad_w):
     assert torch.isnan(whole[:, 64:]).all()
 
 
+@pytest.mark.parametrize("rows,cols,outs", [(500, 600, 256), (300, 1024, 512), (9000, 512, 64)])
+@pytest.mark.parametrize("first", [1, 2, 3, 16])
+def test_rows_of_a_larger_checkpoint(rows, cols, outs, first):
+    # scales that start on no 4- or 16-byte boundary
+    q, s, dy = integers(rows + first, cols, outs, "f16", 9)
+    s = s[:, :-(-cols // 32)].contiguous()
+    qd, sd = q.cuda()[first:], s.cuda()[first:]
+    got = tg.ckpt8_wgrad(tg.Checkpoint8(qd, sd, cols), dy[first:].cuda())
+    want = torch.from_numpy(reference(q[first:], s[first:], cols, dy[first:])).half()
+    assert torch.equal(got.cpu(), want)
+
+
 def test_nothing_to_sum_and_nothing_to_do():
     kept = tg.Checkpoint8.empty(0, 100, "cuda")
     out = torch.full((100, 24), float("nan"), dtype=torch.float16, device="cuda")[:, :16]
