@@ -80,6 +80,7 @@ struct NormLaunch {
   int64_t rows, cols, ld_x, ld_y;
   int dtype, param_dtype;
   float eps;
+  int sms;
 };
 cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream);
 
@@ -92,8 +93,8 @@ struct NormBwdLaunch {
   int dtype, param_dtype;
   int sms;
 };
-// Rows of [2][cols] fp32 partial sums that launch_norm_bwd writes for dgamma and dbeta.
-uint32_t norm_bwd_parts(int64_t rows, int64_t cols, int sms);
+// Bytes of fp32 partial sums that launch_norm_bwd writes for dgamma and dbeta.
+int64_t norm_bwd_workspace(int64_t rows, int64_t cols, int sms);
 cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream);
 
 // 8-bit checkpoints (tg_ckpt8_kernel.cuh)

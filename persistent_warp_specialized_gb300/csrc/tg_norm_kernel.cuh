@@ -6,163 +6,302 @@
 // Backward, with xh = (x - mean) rstd and g = dy gamma:
 //   dx = rstd (g - sum g / cols - xh sum (g xh) / cols),  dgamma = sum_rows dy xh,
 //   dbeta = sum_rows dy;  x is the tensor, or its 8-bit checkpoint.
-// Both are bound by memory: a row stays in registers from its one read to the result's write.
+// Both are bound by memory: a row stays on the SM from its one read to the result's write.
 //
-// The variance is the sum of squares about the mean in two steps that need one exchange between
-// warps: each warp takes the mean of its own values and their squares about that mean, and
-// sum (x - mean)^2 = sum over warps of [M2_w + n_w (mean_w - mean)^2].  No difference of large
-// sums is formed, so a large mean costs no digits.
+// Rows go to groups of G threads, 16 values a thread (G a multiple of 32); a CTA, one per SM, holds
+// as many groups as its threads allow.  A group takes two rows a turn: one barrier, and one chain of
+// shuffles, serves both.  Each thread copies its own values of the rows ahead to shared memory
+// (cp.async), so that 64 KiB are on their way to an SM at any time.  Rows of any alignment are read
+// and written in whole 16-byte granules (UNAL, tg_rows.cuh).
+//
+// The variance: each thread takes the mean of its own values and their squares about that mean
+// (n, m, M2); lanes, and then warps, are joined about the mean c of the first of them,
+//   A = sum [M2 + n (m - c)^2],  B = sum n (m - c);  mean = c + B / n,  M2 = A - B^2 / n,
+// two sums that run side by side.  No difference of large sums is formed, so a large mean costs no
+// digits: B^2 / n <= (1 - 1 / k) sum n (m - c)^2 for k equal parts, at most 5 bits for 32.
 #pragma once
 
 #include "tg_rows.cuh"
 
 namespace tg {
 
+constexpr int kNormValues = 16;      // of a thread
+constexpr int kNormMaxGroups = 15;   // one named barrier each
+// Threads of a CTA: 512 with 128 registers hold the parameters (forward) or the sums over rows
+// (backward) and two rows a turn.  Rows of more than 8192 values take 1024 threads of 64 registers,
+// one row a turn, parameters read again for each row (backward: 16-bit values only, and some of the
+// sums spill; 32-bit values would need more shared memory than there is).
+constexpr int kNormThreads = 512;
+constexpr int kNormWideThreads = 1024;
+
+// Rows a turn: two, unless two turns of them are too much for shared memory (backward, 32 bits).
+template <typename T, int THREADS, int TENSORS>
+constexpr int kNormRows = THREADS == kNormThreads && TENSORS * sizeof(T) < 8 ? 2 : 1;
+
+// Turns whose rows have a place in shared memory: 64 KiB in flight besides the present one.
+template <typename T, int THREADS, int TENSORS>
+constexpr int kNormSlots = 65536 / (THREADS * TENSORS * kNormRows<T, THREADS, TENSORS> *
+                                    kNormValues * static_cast<int>(sizeof(T))) + 1;
+
+// shared memory of ``warps`` warps
+template <typename T, int THREADS, int TENSORS>
+constexpr uint32_t norm_smem(uint32_t warps) {
+  return warps * TENSORS * kNormSlots<T, THREADS, TENSORS> * kNormRows<T, THREADS, TENSORS> *
+         (kNormValues / kVec<T>)*kStripBytes;
+}
+
 struct NormFwdParams {
-  const void* x;
+  RowsOf x, y;
   const void* gamma;   // may be null (ones)
   const void* beta;    // may be null (zeros)
-  void* y;
+  uint32_t wide_params;   // both can be read in 16-byte vectors
   float* mean;         // may be null
   float* rstd;         // may be null
   uint8_t* q;          // checkpoint of y (KEEP)
   uint8_t* s;
   uint32_t rows, cols, blocks;
-  int64_t ld_x, ld_y;
   float eps;
 };
 
-// What one warp of a row's G threads holds of the row: vectors (k G + 32 w) .. + 32 for each k.
-template <int VE>
-__device__ __forceinline__ float warp_share(uint32_t g_threads, uint32_t w, int items,
-                                            uint32_t cols) {
+// The group's own barrier (id 0 is the CTA's); a group of one warp needs none.
+__device__ __forceinline__ void group_sync(uint32_t group, uint32_t g_threads) {
+  if (g_threads > 32u) asm volatile("bar.sync %0, %1;" ::"r"(group + 1u), "r"(g_threads) : "memory");
+}
+
+// How many of a row's values a warp of a group holds: strips w, w + g_warps, ... of 32 N values.
+template <int N>
+__device__ __forceinline__ float warp_share(uint32_t w, uint32_t g_warps, uint32_t cols) {
   uint32_t n = 0;
-  for (int k = 0; k < items; ++k) {
-    const uint32_t at = (k * g_threads + 32u * w) * VE;
-    n += at >= cols ? 0u : (cols - at < 32u * VE ? cols - at : 32u * VE);
+  for (uint32_t k = 0; k < kNormValues / N; ++k) {
+    const uint64_t at = static_cast<uint64_t>(k * g_warps + w) * (32u * N);
+    if (at < cols) n += cols - at < 32u * N ? static_cast<uint32_t>(cols - at) : 32u * N;
   }
   return static_cast<float>(n);
 }
 
-// y of VE values (and their checkpoint); ``col`` may lie past the row's end, all lanes call it.
-template <typename TX, typename TP, int VE, bool KEEP>
-__device__ __forceinline__ void norm_write(const NormFwdParams& p, uint32_t row, uint32_t col,
-                                           const float (&v)[VE], float mean, float rstd) {
-  const int64_t left = static_cast<int64_t>(p.cols) - col;
-  Raw<TX, VE> out;
-  float g[VE], b[VE];
+template <typename TP, int N>
+__device__ __forceinline__ void params_or(const void* p, uint32_t col, uint32_t cols, bool wide,
+                                          float none, float (&v)[N]) {
+  if (p) {
+    load_params<TP, N>(static_cast<const TP*>(p), col, cols, wide, v);
+  } else {
 #pragma unroll
-  for (int i = 0; i < VE; ++i) g[i] = 1.0f, b[i] = 0.0f;
-  if (p.gamma) {
-    const Raw<TP, VE> r = load_some<TP, VE>(static_cast<const TP*>(p.gamma) + col, left);
-#pragma unroll
-    for (int i = 0; i < VE; ++i) g[i] = to_f32(r.v[i]);
+    for (int i = 0; i < N; ++i) v[i] = none;
   }
-  if (p.beta) {
-    const Raw<TP, VE> r = load_some<TP, VE>(static_cast<const TP*>(p.beta) + col, left);
+}
+
+// y of the lane's N values at column ``col`` (and their checkpoint), of which ``left`` are in the
+// row; every lane of the warp calls it.
+template <typename TX, bool UNAL, bool KEEP>
+__device__ __forceinline__ void norm_write(const NormFwdParams& p, uint64_t row, uint32_t col,
+                                           int left, const float (&v)[kVec<TX>], float mean,
+                                           float rstd, const float (&g)[kVec<TX>],
+                                           const float (&b)[kVec<TX>]) {
+  constexpr int N = kVec<TX>;
+  float o[N];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) b[i] = to_f32(r.v[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < VE; ++i) out.v[i] = from_f32<TX>(fmaf((v[i] - mean) * rstd, g[i], b[i]));
-  store_some<TX, VE>(static_cast<TX*>(p.y) + static_cast<int64_t>(row) * p.ld_y + col, out, left);
+  for (int i = 0; i < N; ++i) o[i] = fmaf((v[i] - mean) * rstd, g[i], b[i]);
+  const V16 out = rounded<TX>(o);
+  store_vector<TX, UNAL>(p.y.base + static_cast<int64_t>(row) * p.y.pitch,
+                         static_cast<int64_t>(col) * static_cast<int>(sizeof(TX)), out, left);
   if constexpr (KEEP) {
-    float o[VE];
+    values<TX>(out, o);   // as rounded
+    if (left < N) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) o[i] = i < left ? to_f32(out.v[i]) : 0.0f;
-    Raw<uint8_t, VE> q;
-    const uint32_t s = ckpt8_quantise<VE>(o, q);
+      for (int i = 0; i < N; ++i) o[i] = i < left ? o[i] : 0.0f;
+    }
+    uint32_t q[N / 4];
+    const uint32_t s = ckpt8_quantise<N>(o, q);
     const uint32_t b32 = col / kCkptBlock;
     if (b32 < p.blocks) {
-      const uint64_t block = static_cast<uint64_t>(row) * p.blocks + b32;
-      *reinterpret_cast<Raw<uint8_t, VE>*>(p.q + block * kCkptBlock + col % kCkptBlock) = q;
+      const uint64_t block = row * p.blocks + b32;
+      store_kept<N>(p.q + block * kCkptBlock + col % kCkptBlock, q);
       if (col % kCkptBlock == 0) p.s[block] = static_cast<uint8_t>(s);
     }
   }
 }
 
-// A row in the registers of G threads: a warp (WARP_ROW, several rows per CTA), or the CTA.  Thread
-// t holds vectors t, t + G, ... of VE values, ITEMS of them, so G * ITEMS * VE >= cols.
-template <typename TX, typename TP, int VE, int ITEMS, bool WARP_ROW, bool KEEP>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : 1024) norm_fwd_kernel(const NormFwdParams p) {
-  __shared__ float2 part[32];
+// Row r belongs to CTA r % gridDim.x, and its turns there to the groups in turn.
+template <typename TX, typename TP, bool UNAL, bool KEEP, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
+    norm_fwd_kernel(const NormFwdParams p, const uint32_t g_threads) {
+  extern __shared__ uint8_t staged[];
+  __shared__ float2 part[2][kNormRows<TX, THREADS, 1>][32];
+  constexpr int N = kVec<TX>, kItems = kNormValues / N, R = kNormRows<TX, THREADS, 1>;
+  constexpr uint32_t kSlots = kNormSlots<TX, THREADS, 1>;
+  constexpr bool kHeld = THREADS == kNormThreads;   // parameters in registers
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-  const uint32_t g_threads = WARP_ROW ? 32u : blockDim.x;
-  const uint32_t t = WARP_ROW ? lane : threadIdx.x;
-  const uint32_t row = WARP_ROW ? blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
+  const uint32_t groups = blockDim.x / g_threads, group = threadIdx.x / g_threads;
+  const uint32_t g_warps = g_threads >> 5, wg = warp - group * g_warps;
+  const int64_t row_bytes = static_cast<int64_t>(p.cols) * static_cast<int>(sizeof(TX));
+  const uint32_t mine = smem_u32(staged) + warp * (kSlots * R * kItems * kStripBytes);
+  uint32_t col[kItems];
+  int left[kItems], n_mine = 0;
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const uint32_t v = (k * g_warps + wg) * 32u + lane;
+    col[k] = v * N;
+    left[k] = values_left<N>(v, p.cols);
+    n_mine += left[k] > 0 ? left[k] : 0;
+  }
+  // values of this thread, of this warp, of warp ``lane`` of the group, and of the row
+  const float n_t = static_cast<float>(n_mine);
+  const float n_w = warp_share<N>(wg, g_warps, p.cols);
+  const float n_l = lane < g_warps ? warp_share<N>(lane, g_warps, p.cols) : 0.0f;
+  const float n_row = static_cast<float>(p.cols);
   grid_dependency_wait();
   grid_launch_dependents();
-  if (row >= p.rows) return;   // whole warps (WARP_ROW), never part of a CTA otherwise
-  const TX* x = static_cast<const TX*>(p.x) + static_cast<int64_t>(row) * p.ld_x;
-  float v[ITEMS][VE];
+
+  float g[kHeld ? kItems : 1][N], b[kHeld ? kItems : 1][N];
+  if constexpr (kHeld) {
 #pragma unroll
-  for (int k = 0; k < ITEMS; ++k) {
-    const uint32_t col = (k * g_threads + t) * VE;
-    const Raw<TX, VE> r = load_some<TX, VE>(x + col, static_cast<int64_t>(p.cols) - col);
-#pragma unroll
-    for (int i = 0; i < VE; ++i) v[k][i] = to_f32(r.v[i]);
-  }
-  float sum = 0.0f;
-#pragma unroll
-  for (int k = 0; k < ITEMS; ++k)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) sum += v[k][i];   // values past the end are zero
-  sum = warp_sum(sum);
-  const uint32_t w = WARP_ROW ? 0u : warp;
-  const float n = warp_share<VE>(g_threads, w, ITEMS, p.cols);
-  const float m = n > 0.0f ? sum / n : 0.0f;
-  float m2 = 0.0f;
-#pragma unroll
-  for (int k = 0; k < ITEMS; ++k) {
-    const int64_t left = static_cast<int64_t>(p.cols) - (k * g_threads + t) * VE;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float d = v[k][i] - m;
-      m2 += i < left ? d * d : 0.0f;
+    for (int k = 0; k < kItems; ++k) {
+      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g[k]);
+      params_or<TP, N>(p.beta, col[k], p.cols, p.wide_params, 0.0f, b[k]);
     }
   }
-  m2 = warp_sum(m2);
-  float mean = m;
-  if constexpr (!WARP_ROW) {
-    const uint32_t warps = blockDim.x >> 5;
-    if (lane == 0) part[warp] = make_float2(sum, m2);
-    __syncthreads();
-    const float2 mine = lane < warps ? part[lane] : make_float2(0.0f, 0.0f);
-    mean = warp_sum(mine.x) / static_cast<float>(p.cols);
-    const float nl = lane < warps ? warp_share<VE>(g_threads, lane, ITEMS, p.cols) : 0.0f;
-    const float d = nl > 0.0f ? mine.x / nl - mean : 0.0f;
-    m2 = warp_sum(mine.y + nl * d * d);
-  }
-  const float rstd = 1.0f / sqrtf(m2 / static_cast<float>(p.cols) + p.eps);
-  if (t == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
-  }
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * groups;
+  auto stage = [&](uint64_t row, uint32_t slot) {   // rows row and row + step
 #pragma unroll
-  for (int k = 0; k < ITEMS; ++k)
-    norm_write<TX, TP, VE, KEEP>(p, row, (k * g_threads + t) * VE, v[k], mean, rstd);
+    for (int r = 0; r < R; ++r) {
+      if (row + r * step < p.rows) {
+        const char* at = p.x.base + static_cast<int64_t>(row + r * step) * p.x.pitch;
+#pragma unroll
+        for (int k = 0; k < kItems; ++k)
+          stage_vector<TX, UNAL>(mine + ((slot * R + r) * kItems + k) * kStripBytes, p.x, at,
+                                 static_cast<int64_t>(col[k]) * static_cast<int>(sizeof(TX)),
+                                 row_bytes);
+      }
+    }
+    cp_async_commit();
+  };
+  uint64_t row = blockIdx.x + static_cast<uint64_t>(gridDim.x) * group, ahead = row;
+  uint32_t slot = 0;
+#pragma unroll
+  for (uint32_t i = 0; i + 1 < kSlots; ++i, ahead += R * step) stage(ahead, i);
+  for (uint32_t turn = 0; row < p.rows; row += R * step, ++turn) {
+    stage(ahead, slot == 0u ? kSlots - 1u : slot - 1u);
+    ahead += R * step;
+    cp_async_wait<kSlots - 1>();
+    __syncwarp();
+    // a row past the end: what the slot holds, reduced and not written
+    float v[R][kItems][N], sum_a[R], sum_b[R], c[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t lead =
+          UNAL ? lead_of(p.x.base + static_cast<int64_t>(row + r * step) * p.x.pitch) : 0u;
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        values<TX>(staged_vector<TX, UNAL>(mine + ((slot * R + r) * kItems + k) * kStripBytes, lead),
+                   v[r][k]);
+        if (left[k] < N) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[r][k][i] = i < left[k] ? v[r][k][i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) s += v[r][k][i];
+      }
+      const float m = n_t > 0.0f ? s / n_t : 0.0f;
+      float m2 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        if (left[k] == N) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) m2 = fmaf(v[r][k][i] - m, v[r][k][i] - m, m2);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (i < left[k]) m2 = fmaf(v[r][k][i] - m, v[r][k][i] - m, m2);
+        }
+      }
+      c[r] = __shfl_sync(0xffffffffu, m, 0);   // lane 0 holds values wherever its warp holds any
+      const float d = n_t > 0.0f ? m - c[r] : 0.0f;
+      sum_b[r] = n_t * d;
+      sum_a[r] = fmaf(sum_b[r], d, m2);
+    }
+    __syncwarp();   // every lane has read the slot before it is filled again
+    slot = slot + 1u == kSlots ? 0u : slot + 1u;
+    float mean[R], rstd[R];
+    auto join = [&](float n) {   // sum_a, sum_b and c over the warp -> mean, sum_a = M2
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          sum_a[r] += __shfl_xor_sync(0xffffffffu, sum_a[r], o);
+          sum_b[r] += __shfl_xor_sync(0xffffffffu, sum_b[r], o);
+        }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float d = n > 0.0f ? sum_b[r] / n : 0.0f;
+        mean[r] = c[r] + d;
+        sum_a[r] = fmaxf(fmaf(-sum_b[r], d, sum_a[r]), sum_a[r] * 0.0f);   // NaN stays NaN
+      }
+    };
+    join(n_w);
+    if (g_warps > 1u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (lane == 0) part[turn & 1u][r][warp] = make_float2(mean[r], sum_a[r]);
+      group_sync(group, g_threads);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2 other = part[turn & 1u][r][warp - wg + (lane < g_warps ? lane : 0u)];
+        c[r] = __shfl_sync(0xffffffffu, other.x, 0);
+        const float d = n_l > 0.0f ? other.x - c[r] : 0.0f;
+        sum_b[r] = n_l * d;
+        sum_a[r] = n_l > 0.0f ? fmaf(sum_b[r], d, other.y) : 0.0f;
+      }
+      join(n_row);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) rstd[r] = 1.0f / sqrtf(sum_a[r] / n_row + p.eps);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t at = row + r * step;
+      if (at >= p.rows) break;
+      if (wg == 0u && lane == 0u) {
+        if (p.mean) p.mean[at] = mean[r];
+        if (p.rstd) p.rstd[at] = rstd[r];
+      }
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        if constexpr (kHeld) {
+          norm_write<TX, UNAL, KEEP>(p, at, col[k], left[k], v[r][k], mean[r], rstd[r], g[k], b[k]);
+        } else {
+          params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g[0]);
+          params_or<TP, N>(p.beta, col[k], p.cols, p.wide_params, 0.0f, b[0]);
+          norm_write<TX, UNAL, KEEP>(p, at, col[k], left[k], v[r][k], mean[r], rstd[r], g[0], b[0]);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
 }
 
 // Any width: the CTA walks its row three times; the second and third reads come from the L2.
-template <typename TX, typename TP, int VE, bool KEEP>
+template <typename TX, typename TP, bool UNAL, bool KEEP>
 __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const NormFwdParams p) {
   __shared__ float part[2][32];
+  constexpr int N = kVec<TX>;
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t row = blockIdx.x;
-  const TX* x = static_cast<const TX*>(p.x) + static_cast<int64_t>(row) * p.ld_x;
-  const uint32_t vecs = (p.cols + VE - 1) / VE;
-  float stat[2] = {0.0f, 0.0f};   // mean, then sum of squares about it
+  const char* x = p.x.base + static_cast<int64_t>(row) * p.x.pitch;
+  const int64_t row_bytes = static_cast<int64_t>(p.cols) * static_cast<int>(sizeof(TX));
+  const uint32_t end = ((p.cols + N - 1) / N + 31u) & ~31u;   // vectors, whole strips
+  float stat[2] = {0.0f, 0.0f};   // mean, then mean square about it
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     float a = 0.0f;
-    for (uint32_t j = threadIdx.x; j < vecs; j += blockDim.x) {
-      const int64_t left = static_cast<int64_t>(p.cols) - static_cast<int64_t>(j) * VE;
-      const Raw<TX, VE> r = load_some<TX, VE>(x + static_cast<int64_t>(j) * VE, left);
+    for (uint32_t j = threadIdx.x; j < end; j += blockDim.x) {
+      const int64_t left = static_cast<int64_t>(p.cols) - static_cast<int64_t>(j) * N;
+      float v[N];
+      values<TX>(load_vector<TX, UNAL>(p.x, x, static_cast<int64_t>(j) * 16, row_bytes), v);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float d = to_f32(r.v[i]) - stat[0];
+      for (int i = 0; i < N; ++i) {
+        const float d = v[i] - stat[0];
         a += i < left ? (pass ? d * d : d) : 0.0f;
       }
     }
@@ -177,289 +316,372 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const NormFwdParams
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;
   }
-  const uint32_t end = (vecs + 31u) & ~31u;   // whole warps, for the checkpoint's shuffles
   for (uint32_t j = threadIdx.x; j < end; j += blockDim.x) {
-    const int64_t left = static_cast<int64_t>(p.cols) - static_cast<int64_t>(j) * VE;
-    const Raw<TX, VE> r = load_some<TX, VE>(x + static_cast<int64_t>(j) * VE, left);
-    float v[VE];
-#pragma unroll
-    for (int i = 0; i < VE; ++i) v[i] = to_f32(r.v[i]);
-    norm_write<TX, TP, VE, KEEP>(p, row, j * VE, v, mean, rstd);
+    float v[N];
+    values<TX>(load_vector<TX, UNAL>(p.x, x, static_cast<int64_t>(j) * 16, row_bytes), v);
+    float g[N], b[N];
+    params_or<TP, N>(p.gamma, j * N, p.cols, p.wide_params, 1.0f, g);
+    params_or<TP, N>(p.beta, j * N, p.cols, p.wide_params, 0.0f, b);
+    norm_write<TX, UNAL, KEEP>(p, row, j * N, values_left<N>(j, p.cols), v, mean, rstd, g, b);
   }
 }
 
 // ---------------------------------------------------------------- backward
 struct NormBwdParams {
-  const void* dy;
-  const void* x;         // the tensor, or (KEPT) null
+  RowsOf dy, dx;
+  RowsOf x;              // the tensor (not KEPT)
   const uint8_t* q;      // the checkpoint of x (KEPT)
   const uint8_t* s;
   const void* gamma;     // may be null (ones)
+  uint32_t wide_params;
   const float* mean;
   const float* rstd;
-  void* dx;
-  float* partials;       // [parts][2][cols] sums of dy xh and of dy; null: not wanted
+  float* partials;       // [parts][2][part_cols] sums of dy xh and of dy; null: not wanted
+  uint32_t part_cols;    // cols rounded up to 4
   uint32_t rows, cols, blocks;
-  int64_t ld_dy, ld_x, ld_dx;
 };
 
-// Where a row's x comes from: VE values at ``col``, as they lie in memory.
-template <typename TX, int VE, bool KEPT>
-struct XSource {
-  using Held = Raw<TX, VE>;
-  static __device__ __forceinline__ Held load(const NormBwdParams& p, uint32_t row, uint32_t col,
-                                              int64_t left) {
-    return load_some<TX, VE>(
-        static_cast<const TX*>(p.x) + static_cast<int64_t>(row) * p.ld_x + col, left);
-  }
-  static __device__ __forceinline__ void values(const Held& h, float (&v)[VE]) {
-#pragma unroll
-    for (int i = 0; i < VE; ++i) v[i] = to_f32(h.v[i]);
-  }
-};
-template <typename TX, int VE>
-struct XSource<TX, VE, true> {
-  using Held = Kept<VE>;
-  static __device__ __forceinline__ Held load(const NormBwdParams& p, uint32_t row, uint32_t col,
-                                              int64_t left) {
-    Held h = {};
-    if (left > 0) {
-      const uint64_t block = static_cast<uint64_t>(row) * p.blocks + col / kCkptBlock;
-      h.q = load_raw<uint8_t, VE>(p.q + block * kCkptBlock + col % kCkptBlock);
-      h.s = p.s[block];
+// The lane's N values of x at vector ``v`` of the row, straight from memory (every lane calls it).
+template <typename TX, bool UNAL, bool KEPT>
+__device__ __forceinline__ void x_values(const NormBwdParams& p, uint32_t row, uint32_t v,
+                                         int64_t row_bytes, float (&out)[kVec<TX>]) {
+  constexpr int N = kVec<TX>;
+  if constexpr (KEPT) {
+    uint32_t q[N / 4] = {}, s = 127u;
+    const uint64_t col = static_cast<uint64_t>(v) * N;
+    if (col < p.cols) {
+      const uint64_t b = static_cast<uint64_t>(row) * p.blocks + col / kCkptBlock;
+      load_kept<N>(p.q + b * kCkptBlock + col % kCkptBlock, q);
+      s = p.s[b];
     }
-    return h;
+    kept_values<N>(q, s, out);
+  } else {
+    const char* at = p.x.base + static_cast<int64_t>(row) * p.x.pitch;
+    values<TX>(load_vector<TX, UNAL>(p.x, at, static_cast<int64_t>(v) * 16, row_bytes), out);
   }
-  static __device__ __forceinline__ void values(const Held& h, float (&v)[VE]) {
-    kept_values<VE>(h, v);
-  }
-};
+}
 
-// Rows go to groups of G threads (a CTA holds blockDim.x / G of them, G a multiple of 32), each
-// thread keeping the sums of dy xh and dy of its own columns in registers over all its rows.  The
-// next row is read while the present one is reduced.  At the end the groups of a CTA add up, and
-// the CTA writes one row of partial sums; norm_bwd_join_kernel adds those in a fixed order, so the
-// result does not depend on timing.
-template <typename TX, typename TP, int VE, int ITEMS, bool KEPT>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdParams p, uint32_t g_threads) {
-  extern __shared__ float shared_cols[];    // [2][cols], used when a CTA holds several groups
-  __shared__ float2 part[2][16];
-  using X = XSource<TX, VE, KEPT>;
+// As the forward kernel; each thread keeps the sums of dy xh and dy of its own columns in registers
+// over all its rows.  At the end the groups of a CTA add up in order, the CTA writes one row of
+// partial sums, and norm_bwd_join_kernel adds those in a fixed order, so the result does not depend
+// on timing.  A staged vector of a checkpoint: N bytes, and at byte 8 the 4-byte word that holds
+// its scale.
+template <typename TX, typename TP, bool UNAL, bool KEPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
+    norm_bwd_kernel(const NormBwdParams p, const uint32_t g_threads) {
+  extern __shared__ uint8_t staged[];
+  __shared__ float2 part[2][kNormRows<TX, THREADS, 2>][32];
+  constexpr int N = kVec<TX>, kItems = kNormValues / N, R = kNormRows<TX, THREADS, 2>;
+  constexpr uint32_t kSlots = kNormSlots<TX, THREADS, 2>;
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t groups = blockDim.x / g_threads, group = threadIdx.x / g_threads;
-  const uint32_t t = threadIdx.x - group * g_threads;
-  const uint32_t g_warps = g_threads >> 5, first_warp = group * g_warps;
+  const uint32_t g_warps = g_threads >> 5, wg = warp - group * g_warps;
+  const int64_t row_bytes = static_cast<int64_t>(p.cols) * static_cast<int>(sizeof(TX));
+  // per warp, slot and row: kItems strips of dy, then of x
+  const uint32_t mine = smem_u32(staged) + warp * (kSlots * R * 2 * kItems * kStripBytes);
+  const float inv_cols = 1.0f / static_cast<float>(p.cols);
+  uint32_t col[kItems];
+  int left[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const uint32_t v = (k * g_warps + wg) * 32u + lane;
+    col[k] = v * N;
+    left[k] = values_left<N>(v, p.cols);
+  }
   grid_dependency_wait();
   grid_launch_dependents();
-  float gamma[ITEMS][VE], dg[ITEMS][VE], db[ITEMS][VE];
+
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * groups;
+  auto stage = [&](uint64_t first, uint32_t slot) {   // rows first and first + step
 #pragma unroll
-  for (int k = 0; k < ITEMS; ++k) {
-    const uint32_t col = (k * g_threads + t) * VE;
+    for (int r = 0; r < R; ++r) {
+      const uint64_t row = first + r * step;
+      const uint32_t at = mine + (slot * R + r) * (2 * kItems * kStripBytes);
+      if (row < p.rows) {
+        const char* dy = p.dy.base + static_cast<int64_t>(row) * p.dy.pitch;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) gamma[k][i] = 1.0f, dg[k][i] = 0.0f, db[k][i] = 0.0f;
-    if (p.gamma) {
-      const Raw<TP, VE> r = load_some<TP, VE>(static_cast<const TP*>(p.gamma) + col,
-                                              static_cast<int64_t>(p.cols) - col);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) gamma[k][i] = to_f32(r.v[i]);
-    }
-  }
-  const float inv_cols = 1.0f / static_cast<float>(p.cols);
-  const uint32_t step = gridDim.x * groups;
-  uint32_t row = blockIdx.x * groups + group;
-  typename X::Held xr[ITEMS];
-  Raw<TX, VE> dyr[ITEMS];
-  float mean = 0.0f, rstd = 0.0f;
-  auto fetch = [&](uint32_t r) {
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const uint32_t col = (k * g_threads + t) * VE;
-      const int64_t left = static_cast<int64_t>(p.cols) - col;
-      xr[k] = X::load(p, r, col, left);
-      dyr[k] = load_some<TX, VE>(
-          static_cast<const TX*>(p.dy) + static_cast<int64_t>(r) * p.ld_dy + col, left);
-    }
-    mean = p.mean[r];
-    rstd = p.rstd[r];
-  };
-  if (row < p.rows) fetch(row);
-  uint32_t turn = 0;
-  while (row < p.rows) {
-    float dy[ITEMS][VE], xh[ITEMS][VE];
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const int64_t left = static_cast<int64_t>(p.cols) - (k * g_threads + t) * VE;
-      float xv[VE];
-      X::values(xr[k], xv);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        dy[k][i] = to_f32(dyr[k].v[i]);             // zero past the row's end
-        xh[k][i] = i < left ? (xv[i] - mean) * rstd : 0.0f;
-        const float g = dy[k][i] * gamma[k][i];
-        s1 += g;
-        s2 = fmaf(g, xh[k][i], s2);
-      }
-    }
-    const float scale = rstd;
-    const uint32_t here = row;
-    row += step;
-    if (row < p.rows) fetch(row);
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (g_warps > 1) {
-      if (lane == 0) part[turn & 1u][warp] = make_float2(s1, s2);
-      // the group's own barrier: other groups of the CTA are on other rows
-      asm volatile("bar.sync %0, %1;" ::"r"(group + 1u), "r"(g_threads) : "memory");
-      const float2 mine =
-          lane < g_warps ? part[turn & 1u][first_warp + lane] : make_float2(0.0f, 0.0f);
-      s1 = warp_sum(mine.x);
-      s2 = warp_sum(mine.y);
-      ++turn;   // the other half of ``part``: a slower warp may still read this one
-    }
-    const float c1 = s1 * inv_cols, c2 = s2 * inv_cols;
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-      const uint32_t col = (k * g_threads + t) * VE;
-      Raw<TX, VE> out;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        dg[k][i] = fmaf(dy[k][i], xh[k][i], dg[k][i]);
-        db[k][i] += dy[k][i];
-        out.v[i] = from_f32<TX>(scale * (fmaf(dy[k][i], gamma[k][i], -c1) - xh[k][i] * c2));
-      }
-      store_some<TX, VE>(static_cast<TX*>(p.dx) + static_cast<int64_t>(here) * p.ld_dx + col, out,
-                         static_cast<int64_t>(p.cols) - col);
-    }
-  }
-  if (p.partials == nullptr) return;
-  float* mine = p.partials + static_cast<uint64_t>(blockIdx.x) * 2u * p.cols;
-  for (uint32_t turn_of = 0; turn_of < groups; ++turn_of) {   // the groups add up one by one
-    if (group == turn_of) {
-      const bool first = turn_of == 0, last = turn_of + 1 == groups;
-#pragma unroll
-      for (int k = 0; k < ITEMS; ++k) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          const uint32_t col = (k * g_threads + t) * VE + i;
-          if (col >= p.cols) continue;
-          float a = dg[k][i], b = db[k][i];
-          if (!first) a += shared_cols[col], b += shared_cols[p.cols + col];
-          if (last) {
-            mine[col] = a;
-            mine[p.cols + col] = b;
+        for (int k = 0; k < kItems; ++k) {
+          const int64_t byte = static_cast<int64_t>(col[k]) * static_cast<int>(sizeof(TX));
+          stage_vector<TX, UNAL>(at + k * kStripBytes, p.dy, dy, byte, row_bytes);
+          const uint32_t xs = at + (kItems + k) * kStripBytes;
+          if constexpr (KEPT) {
+            if (left[k] > 0) {
+              const uint64_t b = row * p.blocks + col[k] / kCkptBlock;
+              cp_async<N>(xs + lane * 16u, p.q + b * kCkptBlock + col[k] % kCkptBlock);
+              const uint8_t* s = p.s + b;
+              const uint8_t* word = s - (reinterpret_cast<uintptr_t>(s) & 3u);
+              if (word >= p.s && word + 4 <= p.s + static_cast<uint64_t>(p.rows) * p.blocks)
+                cp_async<4>(xs + lane * 16u + 8u, word);
+              else
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(xs + lane * 16u + 8u +
+                                                             static_cast<uint32_t>(s - word)),
+                             "r"(static_cast<uint32_t>(*s))
+                             : "memory");
+            }
           } else {
-            shared_cols[col] = a;
-            shared_cols[p.cols + col] = b;
+            stage_vector<TX, UNAL>(xs, p.x, p.x.base + static_cast<int64_t>(row) * p.x.pitch, byte,
+                                   row_bytes);
           }
         }
       }
     }
-    if (turn_of + 1 < groups) __syncthreads();
+    cp_async_commit();
+  };
+  // the lane's dy and xh of its k-th vector, from the row's place in the slot; zero past the row's
+  // end, and for a row past the matrix's
+  auto values_at = [&](uint64_t row, uint32_t slot, int r, int k, float mean, float rstd,
+                       float (&dy)[N], float (&xh)[N]) {
+    const uint32_t at = mine + (slot * R + r) * (2 * kItems * kStripBytes);
+    const uint32_t lead_dy =
+        UNAL ? lead_of(p.dy.base + static_cast<int64_t>(row) * p.dy.pitch) : 0u;
+    values<TX>(staged_vector<TX, UNAL>(at + k * kStripBytes, lead_dy), dy);
+    const uint32_t xs = at + (kItems + k) * kStripBytes;
+    if constexpr (KEPT) {
+      const V16 w = ld_shared_v16(xs + lane * 16u);
+      const uint8_t* s = p.s + row * p.blocks + col[k] / kCkptBlock;
+      const uint32_t byte = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s) & 3u);
+      kept_values<N>(w.w, (w.w[2] >> (8u * byte)) & 0xFFu, xh);
+    } else {
+      const uint32_t lead_x = UNAL ? lead_of(p.x.base + static_cast<int64_t>(row) * p.x.pitch) : 0u;
+      values<TX>(staged_vector<TX, UNAL>(xs, lead_x), xh);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) xh[i] = (xh[i] - mean) * rstd;
+    const int n = row < p.rows ? left[k] : 0;
+    if (n < N) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        dy[i] = i < n ? dy[i] : 0.0f;
+        xh[i] = i < n ? xh[i] : 0.0f;
+      }
+    }
+  };
+
+  float dg[kItems][N], db[kItems][N];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) dg[k][i] = db[k][i] = 0.0f;
+  uint64_t row = blockIdx.x + static_cast<uint64_t>(gridDim.x) * group, ahead = row;
+  uint32_t slot = 0;
+  float mean[R], rstd[R];
+  auto stats = [&](uint64_t first, float (&m)[R], float (&s)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t at = first + r * step;
+      m[r] = at < p.rows ? p.mean[at] : 0.0f;
+      s[r] = at < p.rows ? p.rstd[at] : 0.0f;
+    }
+  };
+  stats(row, mean, rstd);
+#pragma unroll
+  for (uint32_t i = 0; i + 1 < kSlots; ++i, ahead += R * step) stage(ahead, i);
+  for (uint32_t turn = 0; row < p.rows; row += R * step, ++turn) {
+    stage(ahead, slot == 0u ? kSlots - 1u : slot - 1u);
+    ahead += R * step;
+    float next_mean[R], next_rstd[R];
+    stats(row + R * step, next_mean, next_rstd);
+    cp_async_wait<kSlots - 1>();
+    __syncwarp();
+    float s1[R], s2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s1[r] = s2[r] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      float g[N];
+      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float dy[N], xh[N];
+        values_at(row + r * step, slot, r, k, mean[r], rstd[r], dy, xh);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float gd = dy[i] * g[i];
+          s1[r] += gd;
+          s2[r] = fmaf(gd, xh[i], s2[r]);
+          dg[k][i] = fmaf(dy[i], xh[i], dg[k][i]);
+          db[k][i] += dy[i];
+        }
+      }
+    }
+    auto join = [&]() {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          s1[r] += __shfl_xor_sync(0xffffffffu, s1[r], o);
+          s2[r] += __shfl_xor_sync(0xffffffffu, s2[r], o);
+        }
+    };
+    join();
+    if (g_warps > 1u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (lane == 0) part[turn & 1u][r][warp] = make_float2(s1[r], s2[r]);
+      group_sync(group, g_threads);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2 other = lane < g_warps ? part[turn & 1u][r][warp - wg + lane]
+                                            : make_float2(0.0f, 0.0f);
+        s1[r] = other.x;
+        s2[r] = other.y;
+      }
+      join();
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {   // the rows again, from shared memory
+      float g[N];
+      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint64_t at = row + r * step;
+        const float c1 = s1[r] * inv_cols, c2 = s2[r] * inv_cols;
+        float dy[N], xh[N];
+        values_at(at, slot, r, k, mean[r], rstd[r], dy, xh);
+#pragma unroll
+        for (int i = 0; i < N; ++i) dy[i] = rstd[r] * (fmaf(dy[i], g[i], -c1) - xh[i] * c2);
+        if (at < p.rows)
+          store_vector<TX, UNAL>(p.dx.base + static_cast<int64_t>(at) * p.dx.pitch,
+                                 static_cast<int64_t>(col[k]) * static_cast<int>(sizeof(TX)),
+                                 rounded<TX>(dy), left[k]);
+      }
+    }
+    __syncwarp();   // every lane has read the slot before it is filled again
+    slot = slot + 1u == kSlots ? 0u : slot + 1u;
+#pragma unroll
+    for (int r = 0; r < R; ++r) mean[r] = next_mean[r], rstd[r] = next_rstd[r];
+  }
+  cp_async_wait<0>();
+  if (p.partials == nullptr) return;
+  float* out = p.partials + static_cast<uint64_t>(blockIdx.x) * 2u * p.part_cols;
+  float* sums = reinterpret_cast<float*>(staged);   // [2][part_cols], once staging is over
+  if (groups > 1u) __syncthreads();
+  for (uint32_t g = 0; g < groups; ++g) {           // the groups add up one by one
+    if (group == g) {
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          const uint32_t col = ((k * g_warps + wg) * 32u + lane) * N + i;
+          if (col >= p.part_cols) continue;
+          float4 a = make_float4(dg[k][i], dg[k][i + 1], dg[k][i + 2], dg[k][i + 3]);
+          float4 b = make_float4(db[k][i], db[k][i + 1], db[k][i + 2], db[k][i + 3]);
+          float4* sa = reinterpret_cast<float4*>(sums + col);
+          float4* sb = reinterpret_cast<float4*>(sums + p.part_cols + col);
+          if (g > 0u) {
+            const float4 c = *sa, d = *sb;
+            a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
+            b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+          }
+          if (g + 1u == groups) {
+            *reinterpret_cast<float4*>(out + col) = a;
+            *reinterpret_cast<float4*>(out + p.part_cols + col) = b;
+          } else {
+            *sa = a;
+            *sb = b;
+          }
+        }
+      }
+    }
+    if (g + 1u < groups) __syncthreads();
   }
 }
 
 // Any width: a CTA walks its row twice (sums, then dx; the second read comes from the L2), and
 // norm_bwd_cols_kernel reads x and dy once more for the sums over rows.
-template <typename TX, typename TP, int VE, bool KEPT>
+template <typename TX, typename TP, bool UNAL, bool KEPT>
 __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormBwdParams p) {
   __shared__ float2 part[32];
-  using X = XSource<TX, VE, KEPT>;
+  constexpr int N = kVec<TX>;
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t row = blockIdx.x;
   const float mean = p.mean[row], rstd = p.rstd[row];
-  const uint32_t vecs = (p.cols + VE - 1) / VE;
+  const int64_t row_bytes = static_cast<int64_t>(p.cols) * static_cast<int>(sizeof(TX));
+  const char* dy_row = p.dy.base + static_cast<int64_t>(row) * p.dy.pitch;
+  const uint32_t end = ((p.cols + N - 1) / N + 31u) & ~31u;   // vectors, whole strips
   float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    for (uint32_t j = threadIdx.x; j < vecs; j += blockDim.x) {
-      const uint32_t col = j * VE;
-      const int64_t left = static_cast<int64_t>(p.cols) - col;
-      const typename X::Held h = X::load(p, row, col, left);
-      const Raw<TX, VE> d = load_some<TX, VE>(
-          static_cast<const TX*>(p.dy) + static_cast<int64_t>(row) * p.ld_dy + col, left);
-      float xv[VE], gamma[VE];
-      X::values(h, xv);
+    for (uint32_t j = threadIdx.x; j < end; j += blockDim.x) {
+      const int64_t left = static_cast<int64_t>(p.cols) - static_cast<int64_t>(j) * N;
+      float x[N], dy[N], g[N];
+      x_values<TX, UNAL, KEPT>(p, row, j, row_bytes, x);
+      values<TX>(load_vector<TX, UNAL>(p.dy, dy_row, static_cast<int64_t>(j) * 16, row_bytes), dy);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) gamma[i] = 1.0f;
-      if (p.gamma) {
-        const Raw<TP, VE> r = load_some<TP, VE>(static_cast<const TP*>(p.gamma) + col, left);
+      for (int i = 0; i < N; ++i) g[i] = 1.0f;
+      if (p.gamma)
+        load_params<TP, N>(static_cast<const TP*>(p.gamma), j * N, p.cols, p.wide_params, g);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) gamma[i] = to_f32(r.v[i]);
-      }
-      Raw<TX, VE> out;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float dy = to_f32(d.v[i]);
-        const float xh = i < left ? (xv[i] - mean) * rstd : 0.0f;
+      for (int i = 0; i < N; ++i) {
+        const float xh = i < left ? (x[i] - mean) * rstd : 0.0f;
+        const float d = i < left ? dy[i] : 0.0f;
         if (pass == 0) {
-          c1 = fmaf(dy, gamma[i], c1);
-          c2 = fmaf(dy * gamma[i], xh, c2);
-        } else {
-          out.v[i] = from_f32<TX>(rstd * (fmaf(dy, gamma[i], -c1) - xh * c2));
+          c1 = fmaf(d, g[i], c1);
+          c2 = fmaf(d * g[i], xh, c2);
         }
+        dy[i] = rstd * (fmaf(d, g[i], -c1) - xh * c2);
       }
       if (pass == 1)
-        store_some<TX, VE>(static_cast<TX*>(p.dx) + static_cast<int64_t>(row) * p.ld_dx + col, out,
-                           left);
+        store_vector<TX, UNAL>(p.dx.base + static_cast<int64_t>(row) * p.dx.pitch,
+                               static_cast<int64_t>(j) * 16, rounded<TX>(dy),
+                               values_left<N>(j, p.cols));
     }
     if (pass == 0) {
       c1 = warp_sum(c1);
       c2 = warp_sum(c2);
       if (lane == 0) part[warp] = make_float2(c1, c2);
       __syncthreads();
-      const float2 mine = lane < warps ? part[lane] : make_float2(0.0f, 0.0f);
-      c1 = warp_sum(mine.x) / static_cast<float>(p.cols);
-      c2 = warp_sum(mine.y) / static_cast<float>(p.cols);
+      const float2 other = lane < warps ? part[lane] : make_float2(0.0f, 0.0f);
+      c1 = warp_sum(other.x) / static_cast<float>(p.cols);
+      c2 = warp_sum(other.y) / static_cast<float>(p.cols);
     }
   }
 }
 
-// Sums over rows for any width: thread t of block (i, j) takes VE columns and rows j, j + parts, ...
-template <typename TX, int VE, bool KEPT>
+// Sums over rows for any width: thread t of block (i, j) takes N columns and rows j, j + parts, ...
+template <typename TX, bool UNAL, bool KEPT>
 __global__ void __launch_bounds__(128) norm_bwd_cols_kernel(const NormBwdParams p) {
-  using X = XSource<TX, VE, KEPT>;
+  constexpr int N = kVec<TX>;
   grid_dependency_wait();
   grid_launch_dependents();
-  const uint64_t at = (static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * VE;
-  if (at >= p.cols) return;
-  const uint32_t col = static_cast<uint32_t>(at);
-  const int64_t left = static_cast<int64_t>(p.cols) - col;
-  float dg[VE], db[VE];
+  const uint32_t v = blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t row_bytes = static_cast<int64_t>(p.cols) * static_cast<int>(sizeof(TX));
+  float dg[N], db[N];
 #pragma unroll
-  for (int i = 0; i < VE; ++i) dg[i] = 0.0f, db[i] = 0.0f;
+  for (int i = 0; i < N; ++i) dg[i] = db[i] = 0.0f;
 #pragma unroll 4
   for (uint32_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
-    const typename X::Held h = X::load(p, row, col, left);
-    const Raw<TX, VE> d = load_some<TX, VE>(
-        static_cast<const TX*>(p.dy) + static_cast<int64_t>(row) * p.ld_dy + col, left);
+    float x[N], dy[N];
+    x_values<TX, UNAL, KEPT>(p, row, v, row_bytes, x);
+    values<TX>(load_vector<TX, UNAL>(p.dy, p.dy.base + static_cast<int64_t>(row) * p.dy.pitch,
+                                     static_cast<int64_t>(v) * 16, row_bytes),
+               dy);
     const float mean = p.mean[row], rstd = p.rstd[row];
-    float xv[VE];
-    X::values(h, xv);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float dy = to_f32(d.v[i]);
-      dg[i] = fmaf(dy, (xv[i] - mean) * rstd, dg[i]);
-      db[i] += dy;
+    for (int i = 0; i < N; ++i) {
+      dg[i] = fmaf(dy[i], (x[i] - mean) * rstd, dg[i]);
+      db[i] += dy[i];
     }
   }
-  float* mine = p.partials + static_cast<uint64_t>(blockIdx.y) * 2u * p.cols;
+  float* out = p.partials + static_cast<uint64_t>(blockIdx.y) * 2u * p.part_cols;
 #pragma unroll
-  for (int i = 0; i < VE; ++i)
-    if (i < left) {
-      mine[col + i] = dg[i];
-      mine[p.cols + col + i] = db[i];
-    }
+  for (int i = 0; i < N; i += 4) {
+    const uint64_t col = static_cast<uint64_t>(v) * N + i;
+    if (col >= p.part_cols) continue;
+    *reinterpret_cast<float4*>(out + col) = make_float4(dg[i], dg[i + 1], dg[i + 2], dg[i + 3]);
+    *reinterpret_cast<float4*>(out + p.part_cols + col) =
+        make_float4(db[i], db[i + 1], db[i + 2], db[i + 3]);
+  }
 }
 
 // dgamma and dbeta from ``parts`` rows of partial sums (none: zeros).  A block takes 32 columns of
 // one of the two; warp w adds rows w, w + 8, ..., then the eight warps' sums are added in order.
 template <typename TP>
 __global__ void __launch_bounds__(256)
-    norm_bwd_join_kernel(const float* __restrict__ partials, uint32_t parts, uint32_t cols,
-                         TP* __restrict__ dgamma, TP* __restrict__ dbeta) {
+    norm_bwd_join_kernel(const float* __restrict__ partials, uint32_t parts, uint32_t part_cols,
+                         uint32_t cols, TP* __restrict__ dgamma, TP* __restrict__ dbeta) {
   __shared__ float sums[8][32];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -469,9 +691,9 @@ __global__ void __launch_bounds__(256)
   if (out == nullptr) return;
   float a = 0.0f;
   if (col < cols) {
-    const float* src = partials + static_cast<uint64_t>(blockIdx.y) * cols + col;
+    const float* src = partials + static_cast<uint64_t>(blockIdx.y) * part_cols + col;
 #pragma unroll 8
-    for (uint32_t i = warp; i < parts; i += 8u) a += src[static_cast<uint64_t>(i) * 2u * cols];
+    for (uint32_t i = warp; i < parts; i += 8u) a += src[static_cast<uint64_t>(i) * 2u * part_cols];
   }
   sums[warp][lane] = a;
   __syncthreads();

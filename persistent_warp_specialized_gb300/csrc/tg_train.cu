@@ -12,24 +12,27 @@ namespace tg {
 
 namespace {
 
-bool aligned(const void* p, uint64_t bytes) {
-  return reinterpret_cast<uintptr_t>(p) % bytes == 0;
-}
-
 uint32_t round_up(uint64_t n, uint32_t to) { return static_cast<uint32_t>((n + to - 1) / to * to); }
 
-// A row (or a whole parameter vector: ld 0) can be read in 16-byte vectors of its type.
+// Every row starts on a 16-byte boundary (a null matrix has no say).
 bool rows_aligned(const void* p, int64_t ld, uint32_t elem) {
-  return aligned(p, 16) && static_cast<uint64_t>(ld) * elem % 16 == 0;
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 &&
+                          static_cast<uint64_t>(ld) * elem % 16 == 0);
 }
 
-// Names a type (or a number) as an argument of a generic lambda.
+RowsOf rows_of(const void* p, int64_t rows, int64_t cols, int64_t ld, uint32_t elem) {
+  RowsOf r;
+  r.base = static_cast<char*>(const_cast<void*>(p));
+  r.end = p ? r.base + ((rows - 1) * ld + cols) * static_cast<int64_t>(elem) : r.base;
+  r.pitch = ld * static_cast<int64_t>(elem);
+  return r;
+}
+
+// Names a type as an argument of a generic lambda.
 template <typename T>
 struct Of {
   using type = T;
 };
-template <int N>
-using Num = std::integral_constant<int, N>;
 
 // Calls f(Of<TX>, Of<TP>) for the element type and the parameters' type.
 template <typename F>
@@ -47,202 +50,227 @@ cudaError_t with_type(int dtype, F&& f) {
   return dtype == TG_F16 ? f(Of<__half>()) : f(Of<__nv_bfloat16>());
 }
 
-// ---------------------------------------------------------------- layer norm, forward
-constexpr int64_t kWarpRowCols = 1024;    // a row held by one warp, 32 values a lane
-constexpr int64_t kCtaRowCols = 16384;    // a row held by one CTA, 16 values a thread
+// ---------------------------------------------------------------- layer norm
+// columns that one group of threads holds
+constexpr int64_t kNormCols = kNormValues * kNormThreads;
+constexpr int64_t kNormWideCols = kNormValues * kNormWideThreads;
+constexpr uint32_t kLongParts = 64;
 
-template <typename TX, typename TP, int VE, bool KEEP>
-cudaError_t norm_fwd_ve(const NormLaunch& l, const NormFwdParams& p, cudaStream_t stream) {
-  if (l.cols <= kWarpRowCols) {
-    const dim3 grid(static_cast<uint32_t>((l.rows + 3) / 4));
-    if (l.cols <= 256)
-      return launch_pdl(norm_fwd_kernel<TX, TP, VE, 8 / VE, true, KEEP>, grid, 128, 0, stream, p);
-    return launch_pdl(norm_fwd_kernel<TX, TP, VE, 32 / VE, true, KEEP>, grid, 128, 0, stream, p);
-  }
-  const dim3 grid(static_cast<uint32_t>(l.rows));
-  if (l.cols <= kCtaRowCols)
-    return launch_pdl(norm_fwd_kernel<TX, TP, VE, 16 / VE, false, KEEP>, grid,
-                      round_up((l.cols + 15) / 16, 32), 0, stream, p);
-  return launch_pdl(norm_fwd_long_kernel<TX, TP, VE, KEEP>, grid, 1024, 0, stream, p);
+// Threads of a group, 16 columns each.
+uint32_t group_threads(int64_t cols) { return round_up((cols + kNormValues - 1) / kNormValues, 32); }
+
+// CTAs, and groups in each: as many groups as ``threads`` hold, no more than there are rows.
+struct NormGrid {
+  uint32_t g_threads, groups, ctas;
+};
+NormGrid norm_grid(int64_t rows, int64_t cols, int threads, int sms) {
+  NormGrid g;
+  g.g_threads = group_threads(cols);
+  g.ctas = static_cast<uint32_t>(rows < sms ? rows : sms);
+  const int64_t per_cta = (rows + g.ctas - 1) / g.ctas;
+  uint32_t most = threads / g.g_threads;
+  if (most > kNormMaxGroups && g.g_threads > 32) most = kNormMaxGroups;
+  g.groups = static_cast<uint32_t>(per_cta < most ? per_cta : most);
+  return g;
 }
 
-// ---------------------------------------------------------------- layer norm, backward
-constexpr int64_t kBwdGroupCols = 8192;   // 16 columns a thread, 512 threads
-constexpr uint32_t kBwdThreads = 512;
-constexpr uint32_t kBwdLongParts = 64;
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+  return bytes <= 48 * 1024 ? cudaSuccess
+                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(bytes));
+}
 
-uint32_t bwd_group_threads(int64_t cols) { return round_up((cols + 15) / 16, 32); }
+bool wide(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream) {
-  NormFwdParams p;
-  p.x = l.x;
-  p.gamma = l.gamma;
-  p.beta = l.beta;
-  p.y = l.y;
-  p.mean = l.mean;
-  p.rstd = l.rstd;
-  p.q = static_cast<uint8_t*>(l.q);
-  p.s = static_cast<uint8_t*>(l.s);
-  p.rows = static_cast<uint32_t>(l.rows);
-  p.cols = static_cast<uint32_t>(l.cols);
-  p.blocks = round_up(l.cols, kCkptBlock) / kCkptBlock;
-  p.ld_x = l.ld_x;
-  p.ld_y = l.ld_y;
-  p.eps = l.eps;
-  return with_types(l.dtype, l.param_dtype, [&](auto tx, auto tp) -> cudaError_t {
+  auto run = [&](auto tx, auto tp, auto unal, auto keep) -> cudaError_t {
     using TX = typename decltype(tx)::type;
     using TP = typename decltype(tp)::type;
-    constexpr int kVec = 16 / sizeof(TX);
-    const bool vec = rows_aligned(l.x, l.ld_x, sizeof(TX)) &&
-                     rows_aligned(l.y, l.ld_y, sizeof(TX)) && aligned(l.gamma, 16) &&
-                     aligned(l.beta, 16);
-    if (vec)
-      return l.q ? norm_fwd_ve<TX, TP, kVec, true>(l, p, stream)
-                 : norm_fwd_ve<TX, TP, kVec, false>(l, p, stream);
-    return l.q ? norm_fwd_ve<TX, TP, 1, true>(l, p, stream)
-               : norm_fwd_ve<TX, TP, 1, false>(l, p, stream);
+    constexpr bool UNAL = decltype(unal)::value, KEEP = decltype(keep)::value;
+    NormFwdParams p;
+    p.x = rows_of(l.x, l.rows, l.cols, l.ld_x, sizeof(TX));
+    p.y = rows_of(l.y, l.rows, l.cols, l.ld_y, sizeof(TX));
+    p.gamma = l.gamma;
+    p.beta = l.beta;
+    p.wide_params = wide(l.gamma) && wide(l.beta) ? 1u : 0u;
+    p.mean = l.mean;
+    p.rstd = l.rstd;
+    p.q = static_cast<uint8_t*>(l.q);
+    p.s = static_cast<uint8_t*>(l.s);
+    p.rows = static_cast<uint32_t>(l.rows);
+    p.cols = static_cast<uint32_t>(l.cols);
+    p.blocks = round_up(l.cols, kCkptBlock) / kCkptBlock;
+    p.eps = l.eps;
+    auto grouped = [&](auto n) -> cudaError_t {
+      constexpr int kThreads = decltype(n)::value;
+      const NormGrid g = norm_grid(l.rows, l.cols, kThreads, l.sms);
+      const uint32_t threads = g.groups * g.g_threads;
+      const size_t smem = norm_smem<TX, kThreads, 1>(threads / 32);
+      auto kernel = norm_fwd_kernel<TX, TP, UNAL, KEEP, kThreads>;
+      cudaError_t e = allow_smem(kernel, smem);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(kernel, dim3(g.ctas), threads, smem, stream, p, g.g_threads);
+    };
+    if (l.cols <= kNormCols) return grouped(std::integral_constant<int, kNormThreads>());
+    if (l.cols <= kNormWideCols) return grouped(std::integral_constant<int, kNormWideThreads>());
+    return launch_pdl(norm_fwd_long_kernel<TX, TP, UNAL, KEEP>,
+                      dim3(static_cast<uint32_t>(l.rows)), 1024, 0, stream, p);
+  };
+  return with_types(l.dtype, l.param_dtype, [&](auto tx, auto tp) -> cudaError_t {
+    constexpr uint32_t kElem = sizeof(typename decltype(tx)::type);
+    const bool unal = !rows_aligned(l.x, l.ld_x, kElem) || !rows_aligned(l.y, l.ld_y, kElem);
+    if (l.q) return unal ? run(tx, tp, std::true_type(), std::true_type())
+                         : run(tx, tp, std::false_type(), std::true_type());
+    return unal ? run(tx, tp, std::true_type(), std::false_type())
+                : run(tx, tp, std::false_type(), std::false_type());
   });
 }
 
-uint32_t norm_bwd_parts(int64_t rows, int64_t cols, int sms) {
+namespace {
+
+// Rows of partial sums: one a CTA, or the row ranges of norm_bwd_cols_kernel.
+uint32_t norm_bwd_parts(int64_t rows, int64_t cols, int dtype, int sms) {
   if (rows == 0) return 0;
-  if (cols > kBwdGroupCols)
-    return static_cast<uint32_t>(rows < kBwdLongParts ? rows : kBwdLongParts);
-  const uint32_t groups = kBwdThreads / bwd_group_threads(cols);
-  const int64_t ctas = (rows + groups - 1) / groups;
-  return static_cast<uint32_t>(ctas < sms ? ctas : sms);
+  if (cols > (dtype == TG_F32 ? kNormCols : kNormWideCols))
+    return static_cast<uint32_t>(rows < kLongParts ? rows : kLongParts);
+  return static_cast<uint32_t>(rows < sms ? rows : sms);
+}
+
+}  // namespace
+
+int64_t norm_bwd_workspace(int64_t rows, int64_t cols, int sms) {
+  const uint32_t a = norm_bwd_parts(rows, cols, TG_F32, sms);
+  const uint32_t b = norm_bwd_parts(rows, cols, TG_F16, sms);
+  return static_cast<int64_t>(a > b ? a : b) * 2 * round_up(cols, 4) * 4;
 }
 
 cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
-  const uint32_t parts = norm_bwd_parts(l.rows, l.cols, l.sms);
+  const uint32_t parts = norm_bwd_parts(l.rows, l.cols, l.dtype, l.sms);
   const bool sums = l.dgamma != nullptr || l.dbeta != nullptr;
-  NormBwdParams p;
-  p.dy = l.dy;
-  p.x = l.x;
-  p.q = static_cast<const uint8_t*>(l.q);
-  p.s = static_cast<const uint8_t*>(l.s);
-  p.gamma = l.gamma;
-  p.mean = l.mean;
-  p.rstd = l.rstd;
-  p.dx = l.dx;
-  p.partials = sums ? l.partials : nullptr;
-  p.rows = static_cast<uint32_t>(l.rows);
-  p.cols = static_cast<uint32_t>(l.cols);
-  p.blocks = round_up(l.cols, kCkptBlock) / kCkptBlock;
-  p.ld_dy = l.ld_dy;
-  p.ld_x = l.ld_x;
-  p.ld_dx = l.ld_dx;
-  auto rows_pass = [&](auto tx, auto tp, auto ve, auto kept) -> cudaError_t {
+  auto rows_pass = [&](auto tx, auto tp, auto unal, auto kept) -> cudaError_t {
     using TX = typename decltype(tx)::type;
     using TP = typename decltype(tp)::type;
-    constexpr int VE = decltype(ve)::value;
-    constexpr bool KEPT = decltype(kept)::value;
-    if (l.cols <= kBwdGroupCols) {
-      const uint32_t g = bwd_group_threads(l.cols), groups = kBwdThreads / g;
-      const size_t smem = groups > 1 ? 2 * sizeof(float) * static_cast<size_t>(l.cols) : 0;
-      return launch_pdl(norm_bwd_kernel<TX, TP, VE, 16 / VE, KEPT>, dim3(parts), groups * g, smem,
-                        stream, p, g);
-    }
-    cudaError_t e = launch_pdl(norm_bwd_long_kernel<TX, TP, VE, KEPT>,
+    constexpr bool UNAL = decltype(unal)::value, KEPT = decltype(kept)::value;
+    NormBwdParams p;
+    p.dy = rows_of(l.dy, l.rows, l.cols, l.ld_dy, sizeof(TX));
+    p.dx = rows_of(l.dx, l.rows, l.cols, l.ld_dx, sizeof(TX));
+    p.x = rows_of(l.x, l.rows, l.cols, l.ld_x, sizeof(TX));
+    p.q = static_cast<const uint8_t*>(l.q);
+    p.s = static_cast<const uint8_t*>(l.s);
+    p.gamma = l.gamma;
+    p.wide_params = wide(l.gamma) ? 1u : 0u;
+    p.mean = l.mean;
+    p.rstd = l.rstd;
+    p.partials = sums ? l.partials : nullptr;
+    p.part_cols = round_up(l.cols, 4);
+    p.rows = static_cast<uint32_t>(l.rows);
+    p.cols = static_cast<uint32_t>(l.cols);
+    p.blocks = round_up(l.cols, kCkptBlock) / kCkptBlock;
+    auto grouped = [&](auto n) -> cudaError_t {
+      constexpr int kThreads = decltype(n)::value;
+      const NormGrid g = norm_grid(l.rows, l.cols, kThreads, l.sms);
+      const uint32_t threads = g.groups * g.g_threads;
+      const size_t smem = norm_smem<TX, kThreads, 2>(threads / 32);
+      auto kernel = norm_bwd_kernel<TX, TP, UNAL, KEPT, kThreads>;
+      cudaError_t e = allow_smem(kernel, smem);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(kernel, dim3(g.ctas), threads, smem, stream, p, g.g_threads);
+    };
+    if (l.cols <= kNormCols) return grouped(std::integral_constant<int, kNormThreads>());
+    if constexpr (sizeof(TX) == 2)
+      if (l.cols <= kNormWideCols)
+        return grouped(std::integral_constant<int, kNormWideThreads>());
+    cudaError_t e = launch_pdl(norm_bwd_long_kernel<TX, TP, UNAL, KEPT>,
                                dim3(static_cast<uint32_t>(l.rows)), 1024, 0, stream, p);
     if (e != cudaSuccess || !sums) return e;
-    const dim3 grid(round_up(l.cols, 128 * VE) / (128 * VE), parts);
-    return launch_pdl(norm_bwd_cols_kernel<TX, VE, KEPT>, grid, 128, 0, stream, p);
+    constexpr uint32_t kCols = 128 * kVec<TX>;
+    return launch_pdl(norm_bwd_cols_kernel<TX, UNAL, KEPT>,
+                      dim3(round_up(l.cols, kCols) / kCols, parts), 128, 0, stream, p);
   };
   return with_types(l.dtype, l.param_dtype, [&](auto tx, auto tp) -> cudaError_t {
-    using TX = typename decltype(tx)::type;
     using TP = typename decltype(tp)::type;
-    constexpr int kVec = 16 / sizeof(TX);
-    const bool vec = rows_aligned(l.dy, l.ld_dy, sizeof(TX)) &&
-                     rows_aligned(l.dx, l.ld_dx, sizeof(TX)) && aligned(l.gamma, 16) &&
-                     (l.x == nullptr || rows_aligned(l.x, l.ld_x, sizeof(TX)));
+    constexpr uint32_t kElem = sizeof(typename decltype(tx)::type);
+    const bool unal = !rows_aligned(l.dy, l.ld_dy, kElem) ||
+                      !rows_aligned(l.dx, l.ld_dx, kElem) || !rows_aligned(l.x, l.ld_x, kElem);
     cudaError_t e = cudaSuccess;
     if (l.rows > 0) {
       if (l.x)
-        e = vec ? rows_pass(tx, tp, Num<kVec>(), std::false_type())
-                : rows_pass(tx, tp, Num<1>(), std::false_type());
+        e = unal ? rows_pass(tx, tp, std::true_type(), std::false_type())
+                 : rows_pass(tx, tp, std::false_type(), std::false_type());
       else
-        e = vec ? rows_pass(tx, tp, Num<kVec>(), std::true_type())
-                : rows_pass(tx, tp, Num<1>(), std::true_type());
+        e = unal ? rows_pass(tx, tp, std::true_type(), std::true_type())
+                 : rows_pass(tx, tp, std::false_type(), std::true_type());
     }
     if (e != cudaSuccess || !sums) return e;
     const dim3 grid(round_up(l.cols, 32) / 32, 2);
     return launch_pdl(norm_bwd_join_kernel<TP>, grid, 256, 0, stream,
-                      static_cast<const float*>(l.partials), parts, p.cols,
-                      static_cast<TP*>(l.dgamma), static_cast<TP*>(l.dbeta));
+                      static_cast<const float*>(l.partials), parts, round_up(l.cols, 4),
+                      static_cast<uint32_t>(l.cols), static_cast<TP*>(l.dgamma),
+                      static_cast<TP*>(l.dbeta));
   });
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoints
 namespace {
 
-// Rows in one launch, so that its units fit in 31 bits.
-int64_t rows_per_launch(int64_t blocks, int per) {
-  const int64_t most = (int64_t(1) << 30) / (blocks * per);
-  return most < 1 ? 1 : most;
-}
-
-uint32_t ckpt8_grid(uint64_t units, int sms) {
-  const uint64_t want = (units + 255) / 256, most = static_cast<uint64_t>(sms) * 32;
-  return static_cast<uint32_t>(want < most ? want : most);
-}
-
-template <typename TX, int VE, bool PACK>
-cudaError_t ckpt8_run(void* x, uint8_t* q, uint8_t* s, int64_t rows, int64_t cols, int64_t ld,
+template <typename TX, bool UNAL, bool PACK>
+cudaError_t ckpt8_run(char* x, uint8_t* q, uint8_t* s, int64_t rows, int64_t cols, int64_t ld,
                       int sms, cudaStream_t stream) {
+  constexpr int kN = kVec<TX>;
   Ckpt8Params p;
   p.cols = static_cast<uint32_t>(cols);
   p.blocks = round_up(cols, kCkptBlock) / kCkptBlock;
-  p.ld = ld;
-  constexpr int kPer = kCkptBlock / VE;
-  const int64_t chunk = rows_per_launch(p.blocks, kPer);
+  p.per_row = UNAL ? round_up(cols, 32 * kN) / kN : p.blocks * (kCkptBlock / kN);
+  p.div_shift = 0;
+  while ((uint64_t(1) << p.div_shift) < p.per_row) ++p.div_shift;
+  p.div_mul = static_cast<uint32_t>(
+      ((uint64_t(1) << 32) * ((uint64_t(1) << p.div_shift) - p.per_row)) / p.per_row + 1);
+  // rows of one launch: its units are numbered in 31 bits
+  const int64_t most = (int64_t(1) << 30) / p.per_row, chunk = most < 1 ? 1 : most;
   for (int64_t r = 0; r < rows; r += chunk) {
     const int64_t n = rows - r < chunk ? rows - r : chunk;
-    TX* at = static_cast<TX*>(x) + r * ld;
-    p.src = at;
-    p.dst = at;
+    const int64_t elem = sizeof(TX);
+    p.x = rows_of(x + r * ld * elem, n, cols, ld, sizeof(TX));
     p.q = q + r * p.blocks * kCkptBlock;
     p.s = s + r * p.blocks;
-    p.units = static_cast<uint32_t>(n * p.blocks * kPer);
-    cudaError_t e;
-    if constexpr (PACK)
-      e = launch_pdl(ckpt8_pack_kernel<TX, VE>, dim3(ckpt8_grid(p.units, sms)), 256, 0, stream, p);
-    else
-      e = launch_pdl(ckpt8_unpack_kernel<TX, VE>, dim3(ckpt8_grid(p.units, sms)), 256, 0, stream,
-                     p);
+    p.units = static_cast<uint32_t>(n * p.per_row);
+    const uint64_t want = (static_cast<uint64_t>(p.units) + 255) / 256;
+    const uint64_t cap = static_cast<uint64_t>(sms) * 8;
+    const cudaError_t e =
+        launch_pdl(ckpt8_kernel<TX, UNAL, PACK>, dim3(static_cast<uint32_t>(want < cap ? want : cap)),
+                   256, 0, stream, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+template <bool PACK>
+cudaError_t ckpt8_any(void* x, void* q, void* s, int64_t rows, int64_t cols, int64_t ld, int dtype,
+                      int sms, cudaStream_t stream) {
+  return with_type(dtype, [&](auto tx) -> cudaError_t {
+    using TX = typename decltype(tx)::type;
+    char* src = static_cast<char*>(x);
+    uint8_t *q8 = static_cast<uint8_t*>(q), *s8 = static_cast<uint8_t*>(s);
+    return rows_aligned(x, ld, sizeof(TX))
+               ? ckpt8_run<TX, false, PACK>(src, q8, s8, rows, cols, ld, sms, stream)
+               : ckpt8_run<TX, true, PACK>(src, q8, s8, rows, cols, ld, sms, stream);
+  });
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt8_pack(const void* x, void* q, void* s, int64_t rows, int64_t cols,
                               int64_t ld_x, int dtype, int sms, cudaStream_t stream) {
-  return with_type(dtype, [&](auto tx) -> cudaError_t {
-    using TX = typename decltype(tx)::type;
-    constexpr int kVec = 16 / sizeof(TX);
-    void* src = const_cast<void*>(x);
-    uint8_t *q8 = static_cast<uint8_t*>(q), *s8 = static_cast<uint8_t*>(s);
-    return rows_aligned(x, ld_x, sizeof(TX))
-               ? ckpt8_run<TX, kVec, true>(src, q8, s8, rows, cols, ld_x, sms, stream)
-               : ckpt8_run<TX, 1, true>(src, q8, s8, rows, cols, ld_x, sms, stream);
-  });
+  return ckpt8_any<true>(const_cast<void*>(x), q, s, rows, cols, ld_x, dtype, sms, stream);
 }
 
 cudaError_t launch_ckpt8_unpack(const void* q, const void* s, void* out, int64_t rows, int64_t cols,
                                 int64_t ld_out, int dtype, int sms, cudaStream_t stream) {
-  return with_type(dtype, [&](auto tx) -> cudaError_t {
-    using TX = typename decltype(tx)::type;
-    constexpr int kVec = 16 / sizeof(TX);
-    uint8_t* q8 = const_cast<uint8_t*>(static_cast<const uint8_t*>(q));
-    uint8_t* s8 = const_cast<uint8_t*>(static_cast<const uint8_t*>(s));
-    return rows_aligned(out, ld_out, sizeof(TX))
-               ? ckpt8_run<TX, kVec, false>(out, q8, s8, rows, cols, ld_out, sms, stream)
-               : ckpt8_run<TX, 1, false>(out, q8, s8, rows, cols, ld_out, sms, stream);
-  });
+  return ckpt8_any<false>(out, const_cast<void*>(q), const_cast<void*>(s), rows, cols, ld_out,
+                          dtype, sms, stream);
 }
 
 }  // namespace tg

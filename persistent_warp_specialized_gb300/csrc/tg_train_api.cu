@@ -274,8 +274,10 @@ int tg_layernorm_fwd(const void* x_dev, const void* gamma_dev, const void* beta_
                       {gamma_dev, param, "gamma"},
                       {beta_dev, param, "beta"}};
   TG_TRY(check_apart(r, 5, 8));
-  TG_TRY(device_ready(nullptr, nullptr));
+  int sms = 0;
+  TG_TRY(device_ready(&sms, nullptr));
   tg::NormLaunch l;
+  l.sms = sms;
   l.x = x_dev;
   l.gamma = gamma_dev;
   l.beta = beta_dev;
@@ -300,7 +302,7 @@ int64_t tg_layernorm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows == 0 || cols == 0) return 0;
   int sms = 0;
   TG_TRY(device_ready(&sms, nullptr));
-  return static_cast<int64_t>(tg::norm_bwd_parts(rows, cols, sms)) * 2 * cols * 4;
+  return tg::norm_bwd_workspace(rows, cols, sms);
 }
 
 int tg_layernorm_bwd(const void* dy_dev, const void* x_dev, const void* xq_dev, const void* xs_dev,
@@ -337,8 +339,7 @@ int tg_layernorm_bwd(const void* dy_dev, const void* x_dev, const void* xq_dev, 
   int sms = 0;
   TG_TRY(device_ready(&sms, nullptr));
   const bool sums = dgamma_dev || dbeta_dev;
-  const int64_t need =
-      sums ? static_cast<int64_t>(tg::norm_bwd_parts(rows, cols, sms)) * 2 * cols * 4 : 0;
+  const int64_t need = sums && rows > 0 ? tg::norm_bwd_workspace(rows, cols, sms) : 0;
   if (need > 0) {
     if (!workspace_dev || workspace_bytes < need)
       return fail(TG_ERR_ARG, "workspace of %lld bytes; dgamma and dbeta need %lld",

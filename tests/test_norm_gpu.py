@@ -261,3 +261,38 @@ def test_another_stream():
         side.synchronize()
         check_forward(x, gamma, beta, got, "bf16")
         check_backward(dy, f64(x), got[1], got[2], gamma, grads, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(2, 31), (3, 7), (5, 255), (4, 257), (7, 1001), (3, 4099),
+                                       (2, 9001), (2, 16387)])
+@pytest.mark.parametrize("offset", [0, 1, 5])
+def test_nothing_is_written_outside(rows, cols, dtype, offset):
+    # y, dx and unpacked values inside larger buffers: the 300 values before and after stay
+    x, gamma, beta, dy = make(rows, cols, dtype, seed=cols)
+    dev = [t.cuda() for t in (x, gamma, beta, dy)]
+    n = rows * cols
+
+    def guarded():
+        buf = torch.full((n + 600 + offset,), 7.0, dtype=DT[dtype], device="cuda")
+        return buf, buf[300 + offset:300 + offset + n].view(rows, cols)
+
+    def intact(buf):
+        return (buf[:300 + offset] == 7).all() and (buf[300 + offset + n:] == 7).all()
+
+    buf, y = guarded()
+    got = tg.layer_norm(*dev[:3], out=y)
+    check_forward(x, gamma, beta, got, dtype)
+    assert intact(buf)
+    buf, dx = guarded()
+    dgamma, dbeta = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    ws = torch.empty(tg.tg_layernorm_bwd_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    tg.tg_layernorm_bwd(dev[3], dev[0], None, None, dev[1], got[1], got[2], dx, dgamma, dbeta, rows,
+                        cols, cols, cols, cols, dtype, "f32", ws)
+    check_backward(dy, f64(x), got[1], got[2], gamma, (dx, dgamma, dbeta), dtype)
+    assert intact(buf)
+    buf, out = guarded()
+    kept = tg.ckpt8_pack(dev[0])
+    tg.ckpt8_unpack(kept, DT[dtype], out=out)
+    v = train.unpack(kept.q.cpu().numpy(), kept.s.cpu().numpy(), cols)
+    assert torch.equal(out.cpu(), torch.from_numpy(v).to(DT[dtype])) and intact(buf)
