@@ -175,11 +175,22 @@ def _dtype(d):
     return DTYPES[d] if isinstance(d, str) else int(d)
 
 
+_raw_stream = None      # torch's raw handle of a device's current stream, once torch is in
+
+
 def _stream(s):
     if s is None:
-        import torch
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
 
-        return torch.cuda.current_stream().cuda_stream
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            if raw is None:
+                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream   # noqa: E731
+            else:                # without the Stream object: 0.5 us a call instead of 3
+                device = torch.cuda.current_device
+                _raw_stream = lambda: raw(device())                            # noqa: E731
+        return _raw_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -500,80 +511,96 @@ class Checkpoint8:
         import torch
 
         nb = (cols + 31) // 32
-        return cls(torch.empty((rows, 32 * nb), dtype=torch.uint8, device=device),
-                   torch.empty((rows, nb), dtype=torch.uint8, device=device), cols)
+        kept = cls.__new__(cls)
+        kept.q = torch.empty((rows, 32 * nb), dtype=torch.uint8, device=device)
+        kept.s = torch.empty((rows, nb), dtype=torch.uint8, device=device)
+        kept.cols = cols
+        return kept
 
 
 def _allocating_on(stream):
     """Context in which torch allocates for ``stream``, so that memory freed after the call returns
     is handed out again only to work that follows on it."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _NO_CONTEXT
     import torch
 
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
                              else stream)
 
 
-_TYPE_NAMES = None
+_NO_CONTEXT = contextlib.nullcontext()
+_TYPE_CODES = None
 
 
-def _type_name(dtype):
-    global _TYPE_NAMES
-    if _TYPE_NAMES is None:
+def _type_code(dtype):
+    """TG_F16, TG_BF16 or TG_F32 of a torch dtype."""
+    global _TYPE_CODES
+    if _TYPE_CODES is None:
         import torch
 
-        _TYPE_NAMES = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}
-    if dtype not in _TYPE_NAMES:
+        _TYPE_CODES = {torch.float16: TG_F16, torch.bfloat16: TG_BF16, torch.float32: TG_F32}
+    code = _TYPE_CODES.get(dtype)
+    if code is None:
         raise TypeError(f"{dtype} is not float16, bfloat16 or float32")
-    return _TYPE_NAMES[dtype]
+    return code
 
 
 def _rows_of(x, name):
     """(rows, cols, row stride) of a 2-D tensor with unit stride along its rows."""
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"{name} must be a 2-D tensor with unit stride along its rows")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
     rows, cols = x.shape
-    ld = x.stride(0) if rows > 1 else cols
-    if ld < cols:
+    ld, unit = x.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
         raise ValueError(f"the rows of {name} overlap")
     return rows, cols, ld
 
 
-def _param_type(dtype, cols, **params):
-    """The common type name of the parameters given (f32 if none), each [cols] and contiguous."""
-    found = set()
-    for name, p in params.items():
-        if p is None:
-            continue
-        if tuple(p.shape) != (cols,) or not p.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor of {cols} values")
-        found.add(_type_name(p.dtype))
-    if len(found) > 1 or (found and not found <= {"f32", dtype}):
-        raise TypeError("parameters must all be float32, or all of the values' type")
-    return found.pop() if found else "f32"
+def _param(p, dtype, cols, name):
+    """(pointer, type code) of a parameter vector [cols]: float32 or the values' type ``dtype``."""
+    code = _type_code(p.dtype)
+    if code != TG_F32 and code != dtype:
+        raise TypeError(f"{name} must be float32 or of the values' type")
+    if p.dim() != 1 or p.shape[0] != cols or not p.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {cols} values")
+    return p.data_ptr(), code
 
 
 def layer_norm(x, gamma=None, beta=None, eps=1e-5, out=None, checkpoint=False, stream=None):
     """torch convenience: (y, mean, rstd) of a CUDA tensor x [rows, cols] (float16, bfloat16 or
     float32), normalised along its rows; with ``checkpoint`` also y's Checkpoint8, made in the same
-    pass.  gamma, beta: [cols] of float32 or x's type, or None."""
+    pass.  gamma, beta: [cols], both float32 or both of x's type, or None."""
     import torch
 
-    dtype = _type_name(x.dtype)
+    dtype = _type_code(x.dtype)
     rows, cols, ld_x = _rows_of(x, "x")
-    params = _param_type(dtype, cols, gamma=gamma, beta=beta)
+    g, params = _param(gamma, dtype, cols, "gamma") if gamma is not None else (None, TG_F32)
+    b = None
+    if beta is not None:
+        b, beta_type = _param(beta, dtype, cols, "beta")
+        if gamma is not None and beta_type != params:
+            raise TypeError("gamma and beta must be of one type")
+        params = beta_type
     if out is not None and (out.dtype != x.dtype or out.shape != x.shape):
         raise ValueError("out must have x's shape and type")
     with _allocating_on(stream):
         if out is None:
             out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+            ld_y = cols
+        else:
+            ld_y = _rows_of(out, "out")[2]
         mean = torch.empty(rows, dtype=torch.float32, device=x.device)
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
         kept = Checkpoint8.empty(rows, cols, x.device) if checkpoint else None
-    ld_y = _rows_of(out, "out")[2]
-    tg_layernorm_fwd(x, gamma, beta, out, mean, rstd, kept.q if kept else None,
-                     kept.s if kept else None, rows, cols, ld_x, ld_y, dtype, params, eps, stream)
+    _check(load_library().tg_layernorm_fwd(
+        x.data_ptr(), g, b, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        kept.q.data_ptr() if kept else None, kept.s.data_ptr() if kept else None, rows, cols, ld_x,
+        ld_y, dtype, params, eps, _stream(stream)))
     return (out, mean, rstd, kept) if checkpoint else (out, mean, rstd)
 
 
@@ -583,41 +610,44 @@ def layer_norm_backward(dy, x, mean, rstd, gamma=None, stream=None):
     without gamma)."""
     import torch
 
-    dtype = _type_name(dy.dtype)
+    dtype = _type_code(dy.dtype)
     rows, cols, ld_dy = _rows_of(dy, "dy")
-    params = _param_type(dtype, cols, gamma=gamma)
-    kept = x if isinstance(x, Checkpoint8) else None
-    if kept is not None:
-        if (kept.rows, kept.cols) != (rows, cols):
+    g, params = _param(gamma, dtype, cols, "gamma") if gamma is not None else (None, TG_F32)
+    if isinstance(x, Checkpoint8):
+        if x.rows != rows or x.cols != cols:
             raise ValueError("the checkpoint and dy differ in shape")
-        ld_x = cols
+        xp, qp, sp, ld_x = None, x.q.data_ptr(), x.s.data_ptr(), cols
     else:
         if x.dtype != dy.dtype or x.shape != dy.shape:
             raise ValueError("x and dy must have the same shape and type")
-        ld_x = _rows_of(x, "x")[2]
+        xp, qp, sp, ld_x = x.data_ptr(), None, None, _rows_of(x, "x")[2]
     for name, t in (("mean", mean), ("rstd", rstd)):
-        if t.dtype != torch.float32 or tuple(t.shape) != (rows,) or not t.is_contiguous():
+        if (t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != rows
+                or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous float32 tensor of {rows} values")
-    nbytes = tg_layernorm_bwd_workspace_bytes(rows, cols)
+    lib = load_library()
+    nbytes = _check(lib.tg_layernorm_bwd_workspace_bytes(rows, cols))
     pt = gamma.dtype if gamma is not None else torch.float32
     with _allocating_on(stream):
         dx = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
         dgamma = torch.empty(cols, dtype=pt, device=dy.device)
         dbeta = torch.empty(cols, dtype=pt, device=dy.device)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes else None
-    tg_layernorm_bwd(dy, None if kept else x, kept.q if kept else None, kept.s if kept else None,
-                     gamma, mean, rstd, dx, dgamma, dbeta, rows, cols, ld_dy, ld_x, cols, dtype,
-                     params, ws, stream)
+    _check(lib.tg_layernorm_bwd(
+        dy.data_ptr(), xp, qp, sp, g, mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
+        dgamma.data_ptr(), dbeta.data_ptr(), rows, cols, ld_dy, ld_x, cols, dtype, params,
+        ws.data_ptr() if nbytes else None, nbytes, _stream(stream)))
     return dx, dgamma, dbeta
 
 
 def ckpt8_pack(x, stream=None):
     """torch convenience: the Checkpoint8 of a CUDA tensor x [rows, cols]."""
-    dtype = _type_name(x.dtype)
+    dtype = _type_code(x.dtype)
     rows, cols, ld = _rows_of(x, "x")
     with _allocating_on(stream):
         kept = Checkpoint8.empty(rows, cols, x.device)
-    tg_ckpt8_pack(x, kept.q, kept.s, rows, cols, ld, dtype, stream)
+    _check(load_library().tg_ckpt8_pack(x.data_ptr(), kept.q.data_ptr(), kept.s.data_ptr(), rows,
+                                        cols, ld, dtype, _stream(stream)))
     return kept
 
 
@@ -625,14 +655,19 @@ def ckpt8_unpack(kept, dtype, out=None, stream=None):
     """torch convenience: the values of a Checkpoint8 as a tensor of ``dtype``."""
     import torch
 
-    name = _type_name(dtype)
+    code = _type_code(dtype)
+    q, cols = kept.q, kept.cols
+    rows = q.shape[0]
     if out is None:
         with _allocating_on(stream):
-            out = torch.empty((kept.rows, kept.cols), dtype=dtype, device=kept.q.device)
-    elif out.dtype != dtype or tuple(out.shape) != (kept.rows, kept.cols):
+            out = torch.empty((rows, cols), dtype=dtype, device=q.device)
+        ld = cols
+    elif out.dtype != dtype or tuple(out.shape) != (rows, cols):
         raise ValueError("out must have the checkpoint's shape and the type asked for")
-    tg_ckpt8_unpack(kept.q, kept.s, out, kept.rows, kept.cols, _rows_of(out, "out")[2], name,
-                    stream)
+    else:
+        ld = _rows_of(out, "out")[2]
+    _check(load_library().tg_ckpt8_unpack(q.data_ptr(), kept.s.data_ptr(), out.data_ptr(), rows,
+                                          cols, ld, code, _stream(stream)))
     return out
 
 
@@ -641,17 +676,23 @@ def ckpt8_wgrad(kept, dy, out=None, stream=None):
     whose input x is the Checkpoint8 ``kept``; dy [rows, outs] is float16 or bfloat16."""
     import torch
 
-    dtype = _type_name(dy.dtype)
+    dtype = _type_code(dy.dtype)
     rows, outs, ld_dy = _rows_of(dy, "dy")
+    cols = kept.cols
     if kept.rows != rows:
         raise ValueError(f"the checkpoint has {kept.rows} rows and dy {rows}")
-    if out is not None and (out.dtype != dy.dtype or tuple(out.shape) != (kept.cols, outs)):
-        raise ValueError(f"out must be [{kept.cols}, {outs}] of dy's type")
-    nbytes = tg_ckpt8_wgrad_workspace_bytes(rows, kept.cols, outs)
+    if out is not None and (out.dtype != dy.dtype or tuple(out.shape) != (cols, outs)):
+        raise ValueError(f"out must be [{cols}, {outs}] of dy's type")
+    lib = load_library()
+    nbytes = _check(lib.tg_ckpt8_wgrad_workspace_bytes(rows, cols, outs))
     with _allocating_on(stream):
         if out is None:
-            out = torch.empty((kept.cols, outs), dtype=dy.dtype, device=dy.device)
+            out = torch.empty((cols, outs), dtype=dy.dtype, device=dy.device)
+            ld_dw = outs
+        else:
+            ld_dw = _rows_of(out, "out")[2]
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes else None
-    tg_ckpt8_wgrad(kept.q, kept.s, dy, out, rows, kept.cols, outs, ld_dy, _rows_of(out, "out")[2],
-                   dtype, ws, stream)
+    _check(lib.tg_ckpt8_wgrad(kept.q.data_ptr(), kept.s.data_ptr(), dy.data_ptr(), out.data_ptr(),
+                              rows, cols, outs, ld_dy, ld_dw, dtype,
+                              ws.data_ptr() if nbytes else None, nbytes, _stream(stream)))
     return out

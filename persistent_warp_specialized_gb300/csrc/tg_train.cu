@@ -1,5 +1,6 @@
 // tg_train.cu -- instantiations and launchers of the operators around the GEMM in training: layer
 // norm forward and backward, and activation checkpoints in 8 bits.
+#include <atomic>
 #include <type_traits>
 
 #include "../../include/tg.h"
@@ -59,6 +60,8 @@ constexpr uint32_t kLongParts = 64;
 // Threads of a group, 16 columns each.
 uint32_t group_threads(int64_t cols) { return round_up((cols + kNormValues - 1) / kNormValues, 32); }
 
+constexpr int kMostSmem = 226 * 1024;   // dynamic; the kernels' static share is below 1 KiB
+
 // CTAs, and groups in each: as many groups as ``threads`` hold, no more than there are rows.
 struct NormGrid {
   uint32_t g_threads, groups, ctas;
@@ -74,11 +77,19 @@ NormGrid norm_grid(int64_t rows, int64_t cols, int threads, int sms) {
   return g;
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ? cudaSuccess
-                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(bytes));
+// Lets kernel K use ``bytes`` of dynamic shared memory on the current device; asked of the driver
+// once per device (it takes about a microsecond), as the GEMM kernels' limits are.
+template <auto K>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || bytes <= 48 * 1024) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 bool wide(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -109,8 +120,8 @@ cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream) {
       const NormGrid g = norm_grid(l.rows, l.cols, kThreads, l.sms);
       const uint32_t threads = g.groups * g.g_threads;
       const size_t smem = norm_smem<TX, kThreads, 1>(threads / 32);
-      auto kernel = norm_fwd_kernel<TX, TP, UNAL, KEEP, kThreads>;
-      cudaError_t e = allow_smem(kernel, smem);
+      constexpr auto kernel = norm_fwd_kernel<TX, TP, UNAL, KEEP, kThreads>;
+      cudaError_t e = allow_smem<kernel>(smem);
       if (e != cudaSuccess) return e;
       return launch_pdl(kernel, dim3(g.ctas), threads, smem, stream, p, g.g_threads);
     };
@@ -174,8 +185,8 @@ cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
       const NormGrid g = norm_grid(l.rows, l.cols, kThreads, l.sms);
       const uint32_t threads = g.groups * g.g_threads;
       const size_t smem = norm_smem<TX, kThreads, 2>(threads / 32);
-      auto kernel = norm_bwd_kernel<TX, TP, UNAL, KEPT, kThreads>;
-      cudaError_t e = allow_smem(kernel, smem);
+      constexpr auto kernel = norm_bwd_kernel<TX, TP, UNAL, KEPT, kThreads>;
+      cudaError_t e = allow_smem<kernel>(smem);
       if (e != cudaSuccess) return e;
       return launch_pdl(kernel, dim3(g.ctas), threads, smem, stream, p, g.g_threads);
     };
