@@ -9,8 +9,8 @@
 // Both are bound by memory: a row stays on the SM from its one read to the result's write.
 //
 // Rows go to groups of G threads, 16 values a thread (G a multiple of 32); a CTA, one per SM, holds
-// as many groups as its threads allow.  A group takes two rows a turn: one barrier, and one chain of
-// shuffles, serves both.  Each thread copies its own values of the rows ahead to shared memory
+// as many groups as its threads allow.  In the forward pass a group takes two rows a turn: one
+// barrier, and one chain of shuffles, serves both.  Each thread copies its own values of the rows ahead to shared memory
 // (cp.async), so that 64 KiB are on their way to an SM at any time.  Rows of any alignment are read
 // and written in whole 16-byte granules (UNAL, tg_rows.cuh).
 //
@@ -27,26 +27,26 @@ namespace tg {
 
 constexpr int kNormValues = 16;      // of a thread
 constexpr int kNormMaxGroups = 15;   // one named barrier each
-// Threads of a CTA: 512 with 128 registers hold the parameters (forward) or the sums over rows
-// (backward) and two rows a turn.  Rows of more than 8192 values take 1024 threads of 64 registers,
-// one row a turn, parameters read again for each row (backward: 16-bit values only, and some of the
-// sums spill; 32-bit values would need more shared memory than there is).
+// Threads of a CTA: 512 with 128 registers hold the parameters, the row's values and (backward) the
+// sums over rows.  Rows of more than 8192 values take 1024 threads of 64 registers: one row a turn,
+// parameters read again for each row, and (backward, 16-bit values only: 32-bit ones would need more
+// shared memory than there is) the row's values taken from shared memory twice, some sums spilled.
 constexpr int kNormThreads = 512;
 constexpr int kNormWideThreads = 1024;
 
-// Rows a turn: two, unless two turns of them are too much for shared memory (backward, 32 bits).
-template <typename T, int THREADS, int TENSORS>
-constexpr int kNormRows = THREADS == kNormThreads && TENSORS * sizeof(T) < 8 ? 2 : 1;
+// Rows a turn
+template <int THREADS, int TENSORS>
+constexpr int kNormRows = THREADS == kNormThreads && TENSORS == 1 ? 2 : 1;
 
 // Turns whose rows have a place in shared memory: 64 KiB in flight besides the present one.
 template <typename T, int THREADS, int TENSORS>
-constexpr int kNormSlots = 65536 / (THREADS * TENSORS * kNormRows<T, THREADS, TENSORS> *
+constexpr int kNormSlots = 65536 / (THREADS * TENSORS * kNormRows<THREADS, TENSORS> *
                                     kNormValues * static_cast<int>(sizeof(T))) + 1;
 
 // shared memory of ``warps`` warps
 template <typename T, int THREADS, int TENSORS>
 constexpr uint32_t norm_smem(uint32_t warps) {
-  return warps * TENSORS * kNormSlots<T, THREADS, TENSORS> * kNormRows<T, THREADS, TENSORS> *
+  return warps * TENSORS * kNormSlots<T, THREADS, TENSORS> * kNormRows<THREADS, TENSORS> *
          (kNormValues / kVec<T>)*kStripBytes;
 }
 
@@ -126,10 +126,10 @@ template <typename TX, typename TP, bool UNAL, bool KEEP, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_fwd_kernel(const NormFwdParams p, const uint32_t g_threads) {
   extern __shared__ uint8_t staged[];
-  __shared__ float2 part[2][kNormRows<TX, THREADS, 1>][32];
-  constexpr int N = kVec<TX>, kItems = kNormValues / N, R = kNormRows<TX, THREADS, 1>;
+  constexpr int N = kVec<TX>, kItems = kNormValues / N, R = kNormRows<THREADS, 1>;
   constexpr uint32_t kSlots = kNormSlots<TX, THREADS, 1>;
   constexpr bool kHeld = THREADS == kNormThreads;   // parameters in registers
+  __shared__ float part[2][R][3][32];               // c, A and B of each warp
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t groups = blockDim.x / g_threads, group = threadIdx.x / g_threads;
   const uint32_t g_warps = g_threads >> 5, wg = warp - group * g_warps;
@@ -137,18 +137,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t mine = smem_u32(staged) + warp * (kSlots * R * kItems * kStripBytes);
   uint32_t col[kItems];
   int left[kItems], n_mine = 0;
+  bool inner[kItems];
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const uint32_t v = (k * g_warps + wg) * 32u + lane;
     col[k] = v * N;
     left[k] = values_left<N>(v, p.cols);
+    inner[k] = inner_vector<UNAL>(v * 16u, row_bytes);
     n_mine += left[k] > 0 ? left[k] : 0;
   }
-  // values of this thread, of this warp, of warp ``lane`` of the group, and of the row
+  // values of this thread, of warp ``lane`` of the group, and of the row
   const float n_t = static_cast<float>(n_mine);
-  const float n_w = warp_share<N>(wg, g_warps, p.cols);
   const float n_l = lane < g_warps ? warp_share<N>(lane, g_warps, p.cols) : 0.0f;
-  const float n_row = static_cast<float>(p.cols);
+  const float inv_l = n_l > 0.0f ? 1.0f / n_l : 0.0f;
+  const float inv_row = 1.0f / static_cast<float>(p.cols);
   grid_dependency_wait();
   grid_launch_dependents();
 
@@ -169,8 +171,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int k = 0; k < kItems; ++k)
           stage_vector<TX, UNAL>(mine + ((slot * R + r) * kItems + k) * kStripBytes, p.x, at,
-                                 static_cast<int64_t>(col[k]) * static_cast<int>(sizeof(TX)),
-                                 row_bytes);
+                                 col[k] * static_cast<uint32_t>(sizeof(TX)), row_bytes, inner[k]);
       }
     }
     cp_async_commit();
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     cp_async_wait<kSlots - 1>();
     __syncwarp();
     // a row past the end: what the slot holds, reduced and not written
-    float v[R][kItems][N], sum_a[R], sum_b[R], c[R];
+    float v[R][kItems][N], c[R], ab[2 * R];   // ab: A and B of each row
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const uint32_t lead =
@@ -202,60 +203,59 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int i = 0; i < N; ++i) s += v[r][k][i];
       }
-      const float m = n_t > 0.0f ? s / n_t : 0.0f;
-      float m2 = 0.0f;
+      // exact where all values are one (a constant row has variance 0)
+      float m = s * (1.0f / kNormValues), m2 = 0.0f;
+      if (n_mine == kNormValues) {
 #pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        if (left[k] == N) {
+        for (int k = 0; k < kItems; ++k)
 #pragma unroll
           for (int i = 0; i < N; ++i) m2 = fmaf(v[r][k][i] - m, v[r][k][i] - m, m2);
-        } else {
+      } else {
+        m = n_mine > 0 ? s / n_t : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kItems; ++k)
 #pragma unroll
           for (int i = 0; i < N; ++i)
             if (i < left[k]) m2 = fmaf(v[r][k][i] - m, v[r][k][i] - m, m2);
-        }
       }
       c[r] = __shfl_sync(0xffffffffu, m, 0);   // lane 0 holds values wherever its warp holds any
-      const float d = n_t > 0.0f ? m - c[r] : 0.0f;
-      sum_b[r] = n_t * d;
-      sum_a[r] = fmaf(sum_b[r], d, m2);
+      const float d = n_mine > 0 ? m - c[r] : 0.0f;
+      ab[2 * r + 1] = n_t * d;
+      ab[2 * r] = fmaf(ab[2 * r + 1], d, m2);
     }
     __syncwarp();   // every lane has read the slot before it is filled again
     slot = slot + 1u == kSlots ? 0u : slot + 1u;
-    float mean[R], rstd[R];
-    auto join = [&](float n) {   // sum_a, sum_b and c over the warp -> mean, sum_a = M2
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          sum_a[r] += __shfl_xor_sync(0xffffffffu, sum_a[r], o);
-          sum_b[r] += __shfl_xor_sync(0xffffffffu, sum_b[r], o);
-        }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float d = n > 0.0f ? sum_b[r] / n : 0.0f;
-        mean[r] = c[r] + d;
-        sum_a[r] = fmaxf(fmaf(-sum_b[r], d, sum_a[r]), sum_a[r] * 0.0f);   // NaN stays NaN
-      }
-    };
-    join(n_w);
+    float sums = warp_sums(ab);
     if (g_warps > 1u) {
+      if (lane % (16 / R) == 0u) part[turn & 1u][lane / (32 / R)][1 + lane / (16 / R) % 2][warp] = sums;
+      if (lane == 0u) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (lane == 0) part[turn & 1u][r][warp] = make_float2(mean[r], sum_a[r]);
+        for (int r = 0; r < R; ++r) part[turn & 1u][r][0][warp] = c[r];
+      }
       group_sync(group, g_threads);
+      const uint32_t w = warp - wg + (lane < g_warps ? lane : 0u);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float2 other = part[turn & 1u][r][warp - wg + (lane < g_warps ? lane : 0u)];
-        c[r] = __shfl_sync(0xffffffffu, other.x, 0);
-        const float d = n_l > 0.0f ? other.x - c[r] : 0.0f;
-        sum_b[r] = n_l * d;
-        sum_a[r] = n_l > 0.0f ? fmaf(sum_b[r], d, other.y) : 0.0f;
+        const float bw = part[turn & 1u][r][2][w], dw = bw * inv_l;
+        const float mw = part[turn & 1u][r][0][w] + dw;
+        const float m2 = fmaf(-bw, dw, part[turn & 1u][r][1][w]);
+        c[r] = __shfl_sync(0xffffffffu, mw, 0);
+        const float d = n_l > 0.0f ? mw - c[r] : 0.0f;
+        ab[2 * r + 1] = n_l * d;
+        ab[2 * r] = n_l > 0.0f ? fmaf(ab[2 * r + 1], d, m2) : 0.0f;
       }
-      join(n_row);
+      sums = warp_sums(ab);
     }
+    float mean[R], rstd[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) rstd[r] = 1.0f / sqrtf(sum_a[r] / n_row + p.eps);
+    for (int r = 0; r < R; ++r) {
+      const float sa = sum_of<2 * R>(sums, 2 * r), sb = sum_of<2 * R>(sums, 2 * r + 1);
+      const float d = sb * inv_row;
+      mean[r] = c[r] + d;
+      // rsqrtf: within 2 ulp, and 1 / sqrt(0) = infinity; the difference may round below zero
+      const float m2 = fmaf(-sb, d, sa);
+      rstd[r] = rsqrtf((m2 < 0.0f ? 0.0f : m2) * inv_row + p.eps);
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const uint64_t at = row + r * step;
@@ -370,68 +370,80 @@ template <typename TX, typename TP, bool UNAL, bool KEPT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_bwd_kernel(const NormBwdParams p, const uint32_t g_threads) {
   extern __shared__ uint8_t staged[];
-  __shared__ float2 part[2][kNormRows<TX, THREADS, 2>][32];
-  constexpr int N = kVec<TX>, kItems = kNormValues / N, R = kNormRows<TX, THREADS, 2>;
+  constexpr int N = kVec<TX>, kItems = kNormValues / N;
   constexpr uint32_t kSlots = kNormSlots<TX, THREADS, 2>;
+  constexpr bool kHeld = THREADS == kNormThreads;   // gamma and the row's values in registers
+  __shared__ float part[2][2][32];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t groups = blockDim.x / g_threads, group = threadIdx.x / g_threads;
   const uint32_t g_warps = g_threads >> 5, wg = warp - group * g_warps;
   const int64_t row_bytes = static_cast<int64_t>(p.cols) * static_cast<int>(sizeof(TX));
-  // per warp, slot and row: kItems strips of dy, then of x
-  const uint32_t mine = smem_u32(staged) + warp * (kSlots * R * 2 * kItems * kStripBytes);
+  // per warp and slot: kItems strips of dy, then of x
+  const uint32_t mine = smem_u32(staged) + warp * (kSlots * 2 * kItems * kStripBytes);
   const float inv_cols = 1.0f / static_cast<float>(p.cols);
   uint32_t col[kItems];
   int left[kItems];
+  bool inner[kItems];
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const uint32_t v = (k * g_warps + wg) * 32u + lane;
     col[k] = v * N;
     left[k] = values_left<N>(v, p.cols);
+    inner[k] = inner_vector<UNAL>(v * 16u, row_bytes);
   }
   grid_dependency_wait();
   grid_launch_dependents();
 
+  float held_g[kHeld ? kItems : 1][N];
+  if constexpr (kHeld) {
+#pragma unroll
+    for (int k = 0; k < kItems; ++k)
+      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, held_g[k]);
+  }
+  auto gamma_at = [&](int k, float (&g)[N]) {
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[i] = held_g[k][i];
+    } else {
+      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g);
+    }
+  };
   const uint64_t step = static_cast<uint64_t>(gridDim.x) * groups;
-  auto stage = [&](uint64_t first, uint32_t slot) {   // rows first and first + step
+  auto stage = [&](uint64_t row, uint32_t slot) {
+    const uint32_t at = mine + slot * (2 * kItems * kStripBytes);
+    if (row < p.rows) {
+      const char* dy = p.dy.base + static_cast<int64_t>(row) * p.dy.pitch;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint64_t row = first + r * step;
-      const uint32_t at = mine + (slot * R + r) * (2 * kItems * kStripBytes);
-      if (row < p.rows) {
-        const char* dy = p.dy.base + static_cast<int64_t>(row) * p.dy.pitch;
-#pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-          const int64_t byte = static_cast<int64_t>(col[k]) * static_cast<int>(sizeof(TX));
-          stage_vector<TX, UNAL>(at + k * kStripBytes, p.dy, dy, byte, row_bytes);
-          const uint32_t xs = at + (kItems + k) * kStripBytes;
-          if constexpr (KEPT) {
-            if (left[k] > 0) {
-              const uint64_t b = row * p.blocks + col[k] / kCkptBlock;
-              cp_async<N>(xs + lane * 16u, p.q + b * kCkptBlock + col[k] % kCkptBlock);
-              const uint8_t* s = p.s + b;
-              const uint8_t* word = s - (reinterpret_cast<uintptr_t>(s) & 3u);
-              if (word >= p.s && word + 4 <= p.s + static_cast<uint64_t>(p.rows) * p.blocks)
-                cp_async<4>(xs + lane * 16u + 8u, word);
-              else
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"(xs + lane * 16u + 8u +
-                                                             static_cast<uint32_t>(s - word)),
-                             "r"(static_cast<uint32_t>(*s))
-                             : "memory");
-            }
-          } else {
-            stage_vector<TX, UNAL>(xs, p.x, p.x.base + static_cast<int64_t>(row) * p.x.pitch, byte,
-                                   row_bytes);
+      for (int k = 0; k < kItems; ++k) {
+        const uint32_t byte = col[k] * static_cast<uint32_t>(sizeof(TX));
+        stage_vector<TX, UNAL>(at + k * kStripBytes, p.dy, dy, byte, row_bytes, inner[k]);
+        const uint32_t xs = at + (kItems + k) * kStripBytes;
+        if constexpr (KEPT) {
+          if (left[k] > 0) {
+            const uint64_t b = row * p.blocks + col[k] / kCkptBlock;
+            cp_async<N>(xs + lane * 16u, p.q + b * kCkptBlock + col[k] % kCkptBlock);
+            const uint8_t* s = p.s + b;
+            const uint8_t* word = s - (reinterpret_cast<uintptr_t>(s) & 3u);
+            if (word >= p.s && word + 4 <= p.s + static_cast<uint64_t>(p.rows) * p.blocks)
+              cp_async<4>(xs + lane * 16u + 8u, word);
+            else
+              asm volatile("st.shared.u8 [%0], %1;" ::"r"(xs + lane * 16u + 8u +
+                                                           static_cast<uint32_t>(s - word)),
+                           "r"(static_cast<uint32_t>(*s))
+                           : "memory");
           }
+        } else {
+          stage_vector<TX, UNAL>(xs, p.x, p.x.base + static_cast<int64_t>(row) * p.x.pitch, byte,
+                                 row_bytes, inner[k]);
         }
       }
     }
     cp_async_commit();
   };
-  // the lane's dy and xh of its k-th vector, from the row's place in the slot; zero past the row's
-  // end, and for a row past the matrix's
-  auto values_at = [&](uint64_t row, uint32_t slot, int r, int k, float mean, float rstd,
-                       float (&dy)[N], float (&xh)[N]) {
-    const uint32_t at = mine + (slot * R + r) * (2 * kItems * kStripBytes);
+  // the lane's dy and xh of its k-th vector, from the row's slot; zero past the row's end
+  auto values_at = [&](uint64_t row, uint32_t slot, int k, float mean, float rstd, float (&dy)[N],
+                       float (&xh)[N]) {
+    const uint32_t at = mine + slot * (2 * kItems * kStripBytes);
     const uint32_t lead_dy =
         UNAL ? lead_of(p.dy.base + static_cast<int64_t>(row) * p.dy.pitch) : 0u;
     values<TX>(staged_vector<TX, UNAL>(at + k * kStripBytes, lead_dy), dy);
@@ -447,12 +459,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) xh[i] = (xh[i] - mean) * rstd;
-    const int n = row < p.rows ? left[k] : 0;
-    if (n < N) {
+    if (left[k] < N) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        dy[i] = i < n ? dy[i] : 0.0f;
-        xh[i] = i < n ? xh[i] : 0.0f;
+        dy[i] = i < left[k] ? dy[i] : 0.0f;
+        xh[i] = i < left[k] ? xh[i] : 0.0f;
       }
     }
   };
@@ -464,92 +475,70 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < N; ++i) dg[k][i] = db[k][i] = 0.0f;
   uint64_t row = blockIdx.x + static_cast<uint64_t>(gridDim.x) * group, ahead = row;
   uint32_t slot = 0;
-  float mean[R], rstd[R];
-  auto stats = [&](uint64_t first, float (&m)[R], float (&s)[R]) {
+  float mean = 0.0f, rstd = 0.0f;
+  if (row < p.rows) mean = p.mean[row], rstd = p.rstd[row];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint64_t at = first + r * step;
-      m[r] = at < p.rows ? p.mean[at] : 0.0f;
-      s[r] = at < p.rows ? p.rstd[at] : 0.0f;
-    }
-  };
-  stats(row, mean, rstd);
-#pragma unroll
-  for (uint32_t i = 0; i + 1 < kSlots; ++i, ahead += R * step) stage(ahead, i);
-  for (uint32_t turn = 0; row < p.rows; row += R * step, ++turn) {
+  for (uint32_t i = 0; i + 1 < kSlots; ++i, ahead += step) stage(ahead, i);
+  for (uint32_t turn = 0; row < p.rows; row += step, ++turn) {
     stage(ahead, slot == 0u ? kSlots - 1u : slot - 1u);
-    ahead += R * step;
-    float next_mean[R], next_rstd[R];
-    stats(row + R * step, next_mean, next_rstd);
+    ahead += step;
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    if (row + step < p.rows) next_mean = p.mean[row + step], next_rstd = p.rstd[row + step];
     cp_async_wait<kSlots - 1>();
     __syncwarp();
-    float s1[R], s2[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) s1[r] = s2[r] = 0.0f;
+    float s[2] = {0.0f, 0.0f};   // sums of dy gamma, and of it times xh
+    float hold_g[kHeld ? kItems : 1][N], hold_x[kHeld ? kItems : 1][N];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      float g[N];
-      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g);
+      float dy[N], xh[N], g[N];
+      gamma_at(k, g);
+      values_at(row, slot, k, mean, rstd, dy, xh);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float dy[N], xh[N];
-        values_at(row + r * step, slot, r, k, mean[r], rstd[r], dy, xh);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float gd = dy[i] * g[i];
-          s1[r] += gd;
-          s2[r] = fmaf(gd, xh[i], s2[r]);
-          dg[k][i] = fmaf(dy[i], xh[i], dg[k][i]);
-          db[k][i] += dy[i];
+      for (int i = 0; i < N; ++i) {
+        const float gd = dy[i] * g[i];
+        s[0] += gd;
+        s[1] = fmaf(gd, xh[i], s[1]);
+        dg[k][i] = fmaf(dy[i], xh[i], dg[k][i]);
+        db[k][i] += dy[i];
+        if constexpr (kHeld) {
+          hold_g[k][i] = gd;
+          hold_x[k][i] = xh[i];
         }
       }
     }
-    auto join = [&]() {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          s1[r] += __shfl_xor_sync(0xffffffffu, s1[r], o);
-          s2[r] += __shfl_xor_sync(0xffffffffu, s2[r], o);
-        }
-    };
-    join();
+    float sums = warp_sums(s);
     if (g_warps > 1u) {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (lane == 0) part[turn & 1u][r][warp] = make_float2(s1[r], s2[r]);
+      if (lane % 16u == 0u) part[turn & 1u][lane / 16u][warp] = sums;
       group_sync(group, g_threads);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float2 other = lane < g_warps ? part[turn & 1u][r][warp - wg + lane]
-                                            : make_float2(0.0f, 0.0f);
-        s1[r] = other.x;
-        s2[r] = other.y;
-      }
-      join();
+      s[0] = lane < g_warps ? part[turn & 1u][0][warp - wg + lane] : 0.0f;
+      s[1] = lane < g_warps ? part[turn & 1u][1][warp - wg + lane] : 0.0f;
+      sums = warp_sums(s);
     }
+    // dx = rstd gd - rstd c1 - xh rstd c2
+    const float c1 = sum_of<2>(sums, 0) * inv_cols * rstd;
+    const float c2 = sum_of<2>(sums, 1) * inv_cols * rstd;
+    char* out = p.dx.base + static_cast<int64_t>(row) * p.dx.pitch;
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {   // the rows again, from shared memory
-      float g[N];
-      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g);
+    for (int k = 0; k < kItems; ++k) {
+      float dx[N];
+      if constexpr (kHeld) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const uint64_t at = row + r * step;
-        const float c1 = s1[r] * inv_cols, c2 = s2[r] * inv_cols;
-        float dy[N], xh[N];
-        values_at(at, slot, r, k, mean[r], rstd[r], dy, xh);
+        for (int i = 0; i < N; ++i)
+          dx[i] = fmaf(-hold_x[k][i], c2, fmaf(hold_g[k][i], rstd, -c1));
+      } else {   // the row again, from shared memory
+        float xh[N], g[N];
+        values_at(row, slot, k, mean, rstd, dx, xh);
+        gamma_at(k, g);
 #pragma unroll
-        for (int i = 0; i < N; ++i) dy[i] = rstd[r] * (fmaf(dy[i], g[i], -c1) - xh[i] * c2);
-        if (at < p.rows)
-          store_vector<TX, UNAL>(p.dx.base + static_cast<int64_t>(at) * p.dx.pitch,
-                                 static_cast<int64_t>(col[k]) * static_cast<int>(sizeof(TX)),
-                                 rounded<TX>(dy), left[k]);
+        for (int i = 0; i < N; ++i) dx[i] = fmaf(-xh[i], c2, fmaf(dx[i] * g[i], rstd, -c1));
       }
+      store_vector<TX, UNAL>(out, static_cast<int64_t>(col[k]) * static_cast<int>(sizeof(TX)),
+                             rounded<TX>(dx), left[k]);
     }
     __syncwarp();   // every lane has read the slot before it is filled again
     slot = slot + 1u == kSlots ? 0u : slot + 1u;
-#pragma unroll
-    for (int r = 0; r < R; ++r) mean[r] = next_mean[r], rstd[r] = next_rstd[r];
+    mean = next_mean;
+    rstd = next_rstd;
   }
   cp_async_wait<0>();
   if (p.partials == nullptr) return;

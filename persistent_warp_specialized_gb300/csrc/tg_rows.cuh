@@ -264,24 +264,33 @@ __device__ __forceinline__ V16 ld_shared_v16(uint32_t addr) {
 constexpr uint32_t kStripBytes = 33 * 16;   // a strip's granules in shared memory
 
 // Starts the copy of the lane's granule of a strip (and, from lane 31 with UNAL, of the 33rd) to
-// ``strip``; granules past the row's end are zero.
+// ``strip``; what lies past the row's end is not copied.  ``inner``: the granules lie within the
+// row whatever its lead, so nothing needs to be checked (see inner_vector).
 template <typename T, bool UNAL>
 __device__ __forceinline__ void stage_vector(uint32_t strip, const RowsOf& m, const char* row,
-                                             int64_t at, int64_t row_bytes) {
+                                             uint32_t at, int64_t row_bytes, bool inner) {
   const uint32_t lane = threadIdx.x & 31u;
   const uint32_t lead = UNAL ? lead_of(row) : 0u;
-  auto one = [&](uint32_t dst, int64_t o) {
-    const char* p = row - lead + o;
-    if (o < row_bytes + lead && p >= m.base && p + 16 <= m.end) {
-      cp_async<16>(dst, p);
-    } else {
-      V16 r = {{0u, 0u, 0u, 0u}};
-      if (o < row_bytes + lead) r = load_granule<T>(p, m.base, m.end);
-      st_shared_v4(dst, r.w[0], r.w[1], r.w[2], r.w[3]);
-    }
-  };
-  one(strip + lane * 16u, at);
-  if (UNAL && lane == 31u) one(strip + 32u * 16u, at + 16);
+  const char* p = row - lead + at;
+  if (inner) {
+    cp_async<16>(strip + lane * 16u, p);
+    if (UNAL && lane == 31u) cp_async<16>(strip + 32u * 16u, p + 16);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < (UNAL ? 2 : 1); ++j) {
+    if (j == 1 && lane != 31u) break;
+    if (at + 16u * j >= row_bytes + lead) break;
+    const V16 r = load_granule<T>(p + 16 * j, m.base, m.end);
+    st_shared_v4(strip + (lane + j) * 16u, r.w[0], r.w[1], r.w[2], r.w[3]);
+  }
+}
+
+// Whether a vector's granules lie within every row: not the first (with a lead it begins before the
+// row) nor one of the last.
+template <bool UNAL>
+__device__ __forceinline__ bool inner_vector(uint32_t at, int64_t row_bytes) {
+  return UNAL ? at >= 16u && at + 32u <= row_bytes : at + 16u <= row_bytes;
 }
 
 // The lane's vector of a staged strip (the warp's copies have landed).
@@ -323,6 +332,34 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Sums of V (2 or 4) values over a warp at once: the lanes share the values out as they add, in
+// V - 1 + log2(32 / V) shuffles instead of 5 V.  Returns the sum of value lane / (32 / V).
+template <int V>
+__device__ __forceinline__ float warp_sums(const float (&v)[V]) {
+  const uint32_t lane = threadIdx.x & 31u;
+  float u[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) u[i] = v[i];
+  int o = 16;
+#pragma unroll
+  for (int n = V; n > 1; n /= 2, o /= 2) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float keep = upper ? u[i + n / 2] : u[i], give = upper ? u[i] : u[i + n / 2];
+      u[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+#pragma unroll
+  for (; o > 0; o /= 2) u[0] += __shfl_xor_sync(0xffffffffu, u[0], o);
+  return u[0];
+}
+// the sum of value i of warp_sums, from the lanes that have it
+template <int V>
+__device__ __forceinline__ float sum_of(float sums, int i) {
+  return __shfl_sync(0xffffffffu, sums, i * (32 / V));
 }
 
 // ---------------------------------------------------------------- E4M3 and E8M0
