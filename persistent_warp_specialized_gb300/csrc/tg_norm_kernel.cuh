@@ -364,8 +364,8 @@ __device__ __forceinline__ void x_values(const NormBwdParams& p, uint32_t row, u
 // As the forward kernel; each thread keeps the sums of dy xh and dy of its own columns in registers
 // over all its rows.  At the end the groups of a CTA add up in order, the CTA writes one row of
 // partial sums, and norm_bwd_join_kernel adds those in a fixed order, so the result does not depend
-// on timing.  A staged vector of a checkpoint: N bytes, and at byte 8 the 4-byte word that holds
-// its scale.
+// on timing.  A staged strip of a checkpoint: N bytes a lane, then for each block of 32 values the
+// 4-byte word that holds its scale.
 template <typename TX, typename TP, bool UNAL, bool KEPT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_bwd_kernel(const NormBwdParams p, const uint32_t g_threads) {
@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int N = kVec<TX>, kItems = kNormValues / N;
   constexpr uint32_t kSlots = kNormSlots<TX, THREADS, 2>;
   constexpr bool kHeld = THREADS == kNormThreads;   // gamma and the row's values in registers
+  constexpr uint32_t kPer = kCkptBlock / N;         // lanes per block of 32 values
   __shared__ float part[2][2][32];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t groups = blockDim.x / g_threads, group = threadIdx.x / g_threads;
@@ -421,16 +422,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         if constexpr (KEPT) {
           if (left[k] > 0) {
             const uint64_t b = row * p.blocks + col[k] / kCkptBlock;
-            cp_async<N>(xs + lane * 16u, p.q + b * kCkptBlock + col[k] % kCkptBlock);
-            const uint8_t* s = p.s + b;
-            const uint8_t* word = s - (reinterpret_cast<uintptr_t>(s) & 3u);
-            if (word >= p.s && word + 4 <= p.s + static_cast<uint64_t>(p.rows) * p.blocks)
-              cp_async<4>(xs + lane * 16u + 8u, word);
-            else
-              asm volatile("st.shared.u8 [%0], %1;" ::"r"(xs + lane * 16u + 8u +
-                                                           static_cast<uint32_t>(s - word)),
-                           "r"(static_cast<uint32_t>(*s))
-                           : "memory");
+            cp_async<N>(xs + lane * N, p.q + b * kCkptBlock + col[k] % kCkptBlock);
+            if (lane % kPer == 0u) {
+              const uint8_t* s = p.s + b;
+              const uint8_t* word = s - (reinterpret_cast<uintptr_t>(s) & 3u);
+              const uint32_t dst = xs + 32u * N + lane / kPer * 4u;
+              if (word >= p.s && word + 4 <= p.s + static_cast<uint64_t>(p.rows) * p.blocks)
+                cp_async<4>(dst, word);
+              else
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(s - word)),
+                             "r"(static_cast<uint32_t>(*s))
+                             : "memory");
+            }
           }
         } else {
           stage_vector<TX, UNAL>(xs, p.x, p.x.base + static_cast<int64_t>(row) * p.x.pitch, byte,
@@ -449,10 +452,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     values<TX>(staged_vector<TX, UNAL>(at + k * kStripBytes, lead_dy), dy);
     const uint32_t xs = at + (kItems + k) * kStripBytes;
     if constexpr (KEPT) {
-      const V16 w = ld_shared_v16(xs + lane * 16u);
-      const uint8_t* s = p.s + row * p.blocks + col[k] / kCkptBlock;
-      const uint32_t byte = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s) & 3u);
-      kept_values<N>(w.w, (w.w[2] >> (8u * byte)) & 0xFFu, xh);
+      uint32_t q[N / 4];
+      if constexpr (N == 8)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q[0]), "=r"(q[1]) : "r"(xs + lane * 8u) : "memory");
+      else
+        q[0] = ld_shared_u32(xs + lane * 4u);
+      const uint32_t byte = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.s)) +
+                             static_cast<uint32_t>(row) * p.blocks + col[k] / kCkptBlock) & 3u;
+      kept_values<N>(q, (ld_shared_u32(xs + 32u * N + lane / kPer * 4u) >> (8u * byte)) & 0xFFu, xh);
     } else {
       const uint32_t lead_x = UNAL ? lead_of(p.x.base + static_cast<int64_t>(row) * p.x.pitch) : 0u;
       values<TX>(staged_vector<TX, UNAL>(xs, lead_x), xh);

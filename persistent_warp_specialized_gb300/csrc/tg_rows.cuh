@@ -221,17 +221,20 @@ __device__ __forceinline__ void store_vector(char* row, int64_t at, const V16& r
     char* p = row + at - lead;
     const int first = lane == 0u ? ahead : 0;
     const int limit = ahead + left;   // where left < 0, -left of the lane before's are missing too
-    if (first == 0 && limit >= kN) {
-      store16(p, g);
-    } else {
+    // lane 0 begins its granule at its own first value, lane 31 also ends the next one: its values
+    // from kN - ahead on.  Both ends share the stores: value i of lane 0's granule, or of lane 31's
+    // vector.
+    if (first == 0 && limit >= kN) store16(p, g);
+    const bool tail = lane == 31u && limit >= kN;
+    if (tail || first != 0 || limit < kN) {
+      const int lo = tail ? kN - ahead : first, hi = tail ? left : limit;
+      char* q = tail ? row + at : p;
+      V16 e;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e.w[i] = tail ? r.w[i] : g.w[i];
 #pragma unroll
       for (int i = 0; i < kN; ++i)
-        if (i >= first && i < limit) store_one<T>(p, g, i);
-    }
-    if (lane == 31u) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if (i >= kN - ahead && i < left) store_one<T>(row + at, r, i);
+        if (i >= lo && i < hi) store_one<T>(q, e, i);
     }
   }
 }
@@ -261,6 +264,12 @@ __device__ __forceinline__ V16 ld_shared_v16(uint32_t addr) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 constexpr uint32_t kStripBytes = 33 * 16;   // a strip's granules in shared memory
 
 // Starts the copy of the lane's granule of a strip (and, from lane 31 with UNAL, of the 33rd) to
@@ -281,8 +290,14 @@ __device__ __forceinline__ void stage_vector(uint32_t strip, const RowsOf& m, co
   for (int j = 0; j < (UNAL ? 2 : 1); ++j) {
     if (j == 1 && lane != 31u) break;
     if (at + 16u * j >= row_bytes + lead) break;
-    const V16 r = load_granule<T>(p + 16 * j, m.base, m.end);
-    st_shared_v4(strip + (lane + j) * 16u, r.w[0], r.w[1], r.w[2], r.w[3]);
+    const char* q = p + 16 * j;
+    const uint32_t dst = strip + (lane + j) * 16u;
+    if (q >= m.base && q + 16 <= m.end) {
+      cp_async<16>(dst, q);
+    } else {   // at the matrix's ends
+      const V16 r = load_granule<T>(q, m.base, m.end);
+      st_shared_v4(dst, r.w[0], r.w[1], r.w[2], r.w[3]);
+    }
   }
 }
 
