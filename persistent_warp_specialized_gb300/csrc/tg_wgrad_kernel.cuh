@@ -111,6 +111,20 @@ __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// umma_f16_pair with the descriptors given as two words each.
+__device__ __forceinline__ void umma_f16_pair_words(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                                    uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // A position in a ring of N slots and the parity of its present turn.
 template <uint32_t N>
 struct RingPos {
@@ -418,17 +432,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
       bool ok = true;
       RingPos<kStages> ring;
       uint32_t uses[2] = {0, 0};      // units that have used each accumulator
-      // MMAs of N-half h into accumulator ``acc`` for the k-block in ring slot s
+      // MMAs of N-half h into accumulator ``acc`` for the k-block in ring slot s.  One thread issues
+      // eight MMAs in 1024 cycles, so a descriptor is one addition to the low word of a constant one
+      // (the address field: 16-byte units, below 2^14); built whole for each MMA, issuing was what
+      // the kernel's time went to.
+      const uint64_t a0 = smem_desc_sw128(sA0, kWgChunkBytes, 1024);
+      const uint64_t b0 = smem_desc_sw128(sB0, kWgChunkBytes, 1024);
+      const uint32_t a_lo = static_cast<uint32_t>(a0), b_lo = static_cast<uint32_t>(b0);
+      const uint32_t a_hi = static_cast<uint32_t>(a0 >> 32), b_hi = static_cast<uint32_t>(b0 >> 32);
       auto issue_half = [&](uint32_t s, uint32_t h, uint32_t acc, bool first, uint32_t idesc) {
+        const uint32_t at = s * (kStageBytes >> 4), d = tmem_base + acc * kBN;
+        const uint32_t a = a_lo + at, b = b_lo + at + h * (2u * kWgChunkBytes >> 4);
 #pragma unroll
-        for (uint32_t kk = 0; kk < kWgBK / kUmmaK; ++kk) {
-          // both operands: 16 tokens = 2048 bytes on; LBO = the next 64 columns
-          const uint32_t off = s * kStageBytes + kk * kUmmaK * 128u;
-          const uint64_t a_desc = smem_desc_sw128(sA0 + off, kWgChunkBytes, 1024);
-          const uint64_t b_desc =
-              smem_desc_sw128(sB0 + off + h * 2u * kWgChunkBytes, kWgChunkBytes, 1024);
-          umma_f16_pair(tmem_base + acc * kBN, a_desc, b_desc, idesc, !first || kk != 0u ? 1u : 0u);
-        }
+        for (uint32_t kk = 0; kk < kWgBK / kUmmaK; ++kk)   // 16 tokens = 2048 bytes on
+          umma_f16_pair_words(d, a + kk * 128u, a_hi, b + kk * 128u, b_hi, idesc,
+                              !first || kk != 0u ? 1u : 0u);
       };
       auto acc_free = [&](uint32_t acc) {   // both CTAs' epilogues have read its last unit out
         const bool got = pair_wait_or_abort<true>(bar_tmem_empty + 8u * acc, (uses[acc] & 1u) ^ 1u,
