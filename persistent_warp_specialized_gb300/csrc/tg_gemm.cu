@@ -179,11 +179,12 @@ WgradParams wgrad_params_of(const WgradLaunch& l) {
 
 template <int DT, int NH, bool SPLIT, bool DEBUG>
 cudaError_t launch_wgrad_pair(const WgradLaunch& l, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(wgrad_pair_kernel<DT, NH, SPLIT, DEBUG>, l.grid, kWgThreads,
+  cudaError_t e = launch_pdl(wgrad_pair_kernel<DT, NH, SPLIT, DEBUG>, l.grid,
+                             WgradConfig<NH>::kThreads,
                              WgradConfig<NH>::kSmemBytes, stream, l.tmQ, l.tmB, l.tmC,
                              l.tmS, wgrad_params_of(l));
   if (e != cudaSuccess || !SPLIT) return e;
-  const uint64_t vecs = static_cast<uint64_t>(l.cols) * (l.outs / 8u);
+  const uint64_t vecs = static_cast<uint64_t>(l.cols) * (l.outs / 4u);
   const uint64_t want = (vecs + 255) / 256, most = static_cast<uint64_t>(l.sms) * 8;
   return launch_pdl(wgrad_join_kernel<DT>, static_cast<uint32_t>(want < most ? want : most), 256, 0,
                     stream, static_cast<const float*>(l.partials), l.splits,
@@ -266,7 +267,7 @@ cudaError_t prepare_gemm_kernels(int* max_pairs) {
   if (e != cudaSuccess) return e;
   if (mx_clusters < clusters) clusters = mx_clusters;
   int wgrad_clusters = 0;
-  cfg.blockDim = dim3(kWgThreads, 1, 1);
+  cfg.blockDim = dim3(WgradConfig<2>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = WgradConfig<2>::kSmemBytes;
   e = cudaOccupancyMaxActiveClusters(&wgrad_clusters, wgrad_pair_kernel<1, 2, false, false>, &cfg);
   if (e != cudaSuccess) return e;

@@ -11,7 +11,7 @@
 // The pair structure is that of tg_gemm_pair_kernel.cuh and, for tiles of two N-halves (256 x 512),
 // of tg_gemm_pair_wide_kernel.cuh: CTA r holds columns 128 r .. of x as its rows of A, and half of
 // each N-half's columns of dY.  One more role: per k-block of 64 tokens warp 3 loads 64 x 128 bytes
-// of q and their scales into a ring of their own, and the eight warps 8..15, four to a k-block,
+// of q and their scales into a ring of their own, and warps 8.., four to a k-block,
 // turn them into the A operand (two chunks of 64 columns x 64 tokens, 128-byte swizzle) and report
 // to the even CTA's ``made`` barrier (there also for the dY bytes of both CTAs), which the MMA
 // thread waits for.
@@ -80,7 +80,7 @@ struct __align__(8) WgradCtl {
   uint64_t drain;
   uint64_t odd_done;
   PairFills<Cfg::kStages> fills;
-  uint32_t sink[kEpiWarps + kWgMakeGroups * kWgMakeWarps];
+  uint32_t sink[kEpiWarps + Cfg::kGroups * kWgMakeWarps];
   uint32_t tmem_base;
   int abort;
 };
@@ -125,6 +125,17 @@ __device__ __forceinline__ void umma_f16_pair_words(uint32_t d_tmem, uint32_t a_
       : "memory");
 }
 
+// One lane of the warp, the same at every call; every lane calls it.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t leader;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(leader));
+  return leader != 0;
+}
+
 // A position in a ring of N slots and the parity of its present turn.
 template <uint32_t N>
 struct RingPos {
@@ -150,45 +161,48 @@ __device__ __forceinline__ void widen_any(const uint32_t (&in)[4], uint32_t s, u
   }
 }
 
-// Whether the short way below is exact for these bytes: no NaN among them and a scale under which
-// its factor is a number of the type.
-template <int DT>
-__device__ __forceinline__ bool widens_short(const uint32_t (&in)[4], uint32_t s) {
-  uint32_t nan = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) nan |= (in[i] & 0x7F7F7F7Fu) + 0x01010101u;
-  return (nan & 0x80808080u) == 0u && s <= 134u && (DT == 1 || s >= 95u);
-}
-
 // The same by moving bits: E4M3's exponent and fraction put in the place of the 16-bit type's read
 // as the value times 2^-120 (bf16) or 2^-8 (fp16), subnormals included, and one multiplication by
-// 2^(s - 7) or 2^(s - 119) sets that right with one rounding.
+// 2^(s - 7) or 2^(s - 119) sets that right with one rounding.  Right unless a byte is NaN or the
+// factor is not a number of the type (s > 134; fp16 also s < 95): ``top`` gathers the largest
+// magnitudes as they were moved, in both halves, for widened_right.
 template <int DT>
-__device__ __forceinline__ void widen_short(const uint32_t (&in)[4], uint32_t s,
-                                            uint32_t (&out)[8]) {
+__device__ __forceinline__ void widen_short(const uint32_t (&in)[4], uint32_t s, uint32_t (&out)[8],
+                                            uint32_t& top) {
   uint32_t factor;   // the power of two in both halves
   if constexpr (DT == 1) {
     factor = (s + 120u) << 7;
   } else {
     factor = s >= 105u ? (s - 104u) << 10 : 1u << (s - 95u);
   }
-  factor |= factor << 16;
+  factor = __byte_perm(factor, 0u, 0x1010u);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     // bytes 2 (i % 2) and + 1 of the word to the high bytes of the two halves
     const uint32_t t = __byte_perm(in[i / 2], 0u, i & 1 ? 0x3424u : 0x1404u);
     if constexpr (DT == 1) {
-      const uint32_t b = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
+      const uint32_t m = (t >> 4) & 0x07F007F0u;
+      const uint32_t b = (t & 0x80008000u) | m;
+      top = __vmaxu2(top, m);
       const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b),
                                        *reinterpret_cast<const __nv_bfloat162*>(&factor));
       out[i] = *reinterpret_cast<const uint32_t*>(&r);
     } else {
-      const uint32_t b = (t & 0x80008000u) | ((t >> 1) & 0x3F803F80u);
+      const uint32_t m = (t >> 1) & 0x3F803F80u;
+      const uint32_t b = (t & 0x80008000u) | m;
+      top = __vmaxu2(top, m);
       const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&b),
                                 *reinterpret_cast<const __half2*>(&factor));
       out[i] = *reinterpret_cast<const uint32_t*>(&r);
     }
   }
+}
+
+// Whether widen_short was right for all that went into ``top`` and for scales s_min .. s_max.
+template <int DT>
+__device__ __forceinline__ bool widened_right(uint32_t top, uint32_t s_min, uint32_t s_max) {
+  constexpr uint32_t nan = DT == 1 ? 0x07F0u : 0x3F80u;   // E4M3 NaN, moved
+  return (top & 0xFFFFu) < nan && (top >> 16) < nan && s_max <= 134u && (DT == 1 || s_min >= 95u);
 }
 
 // Stores one 64-column chunk of the accumulator (v: lane = row, fp32 bits) as fp32 partial sums,
@@ -220,7 +234,7 @@ __device__ __forceinline__ void wgrad_store_partial(const uint32_t (&v)[64], uin
 // DT: 0 = fp16, 1 = bf16 (dY and dW).  NH: N-halves per tile.  SPLIT: partial sums to the workspace
 // (tmC is then the workspace's map).  DEBUG adds fault injection.
 template <int DT, int NH, bool SPLIT, bool DEBUG>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WgradConfig<NH>::kThreads, 1)
     wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmC,
@@ -426,31 +440,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (lane == 0 && rank == 0) {
+    // The whole warp walks the loop and one elected lane issues: control flow and operands are then
+    // uniform, which the instruction wants; a single lane on its own copied each operand over, and
+    // its 90 cycles an MMA bounded the kernel (k-blocks of four MMAs took 810 cycles).
+    if (rank == 0) {
       constexpr uint32_t idesc_full = idesc_f16(DT, kPairBM, kBN, /*A M-major*/ 1, /*B N-major*/ 1);
       constexpr uint32_t idesc_half = idesc_f16(DT, kPairBM, kBN / 2, 1, 1);
+      const bool leader = elect_one();
       bool ok = true;
       RingPos<kStages> ring;
       uint32_t uses[2] = {0, 0};      // units that have used each accumulator
-      // MMAs of N-half h into accumulator ``acc`` for the k-block in ring slot s.  One thread issues
-      // eight MMAs in 1024 cycles, so a descriptor is one addition to the low word of a constant one
-      // (the address field: 16-byte units, below 2^14); built whole for each MMA, issuing was what
-      // the kernel's time went to.
+      // a descriptor is an addition to the low word of a constant one (the address field: 16-byte
+      // units, below 2^14)
       const uint64_t a0 = smem_desc_sw128(sA0, kWgChunkBytes, 1024);
       const uint64_t b0 = smem_desc_sw128(sB0, kWgChunkBytes, 1024);
       const uint32_t a_lo = static_cast<uint32_t>(a0), b_lo = static_cast<uint32_t>(b0);
       const uint32_t a_hi = static_cast<uint32_t>(a0 >> 32), b_hi = static_cast<uint32_t>(b0 >> 32);
+      // MMAs of N-half h into accumulator ``acc`` for the k-block in ring slot s
       auto issue_half = [&](uint32_t s, uint32_t h, uint32_t acc, bool first, uint32_t idesc) {
         const uint32_t at = s * (kStageBytes >> 4), d = tmem_base + acc * kBN;
         const uint32_t a = a_lo + at, b = b_lo + at + h * (2u * kWgChunkBytes >> 4);
+        if (leader) {
 #pragma unroll
-        for (uint32_t kk = 0; kk < kWgBK / kUmmaK; ++kk)   // 16 tokens = 2048 bytes on
-          umma_f16_pair_words(d, a + kk * 128u, a_hi, b + kk * 128u, b_hi, idesc,
-                              !first || kk != 0u ? 1u : 0u);
+          for (uint32_t kk = 0; kk < kWgBK / kUmmaK; ++kk)   // 16 tokens = 2048 bytes on
+            umma_f16_pair_words(d, a + kk * 128u, a_hi, b + kk * 128u, b_hi, idesc,
+                                !first || kk != 0u ? 1u : 0u);
+        }
+      };
+      auto commit = [&](uint32_t bar) {
+        if (leader) umma_commit_pair_multicast(bar, 0x3);
+        __syncwarp();
+      };
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool got = pair_wait_or_abort<true>(bar, parity, abort_flag, peer_abort, limit,
+                                                  kRoleMma);
+        return __all_sync(0xffffffffu, got) != 0;
       };
       auto acc_free = [&](uint32_t acc) {   // both CTAs' epilogues have read its last unit out
-        const bool got = pair_wait_or_abort<true>(bar_tmem_empty + 8u * acc, (uses[acc] & 1u) ^ 1u,
-                                                  abort_flag, peer_abort, limit, kRoleMma);
+        const bool got = wait(bar_tmem_empty + 8u * acc, (uses[acc] & 1u) ^ 1u);
         ++uses[acc];
         tcgen05_fence_after_sync();
         return got;
@@ -466,10 +493,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
         const uint32_t defer = halves == 2u && nk > 1u ? 1u : 0u;
         const uint32_t s0 = ring.slot;
         for (uint32_t k = 0; k < nk; ++k, ring.advance(1)) {
-          const uint32_t s = ring.slot, par = ring.parity;
-          if (!pair_wait_or_abort<true>(bar_made + 8u * s, par, abort_flag, peer_abort, limit,
-                                        kRoleMma) ||
-              (k == 0 && !acc_free(acc0))) {
+          const uint32_t s = ring.slot;
+          if (!wait(bar_made + 8u * s, ring.parity) || (k == 0 && !acc_free(acc0))) {
             ok = false;
             break;
           }
@@ -484,19 +509,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
               }
               if (defer) {   // catch N-half 1 up
                 issue_half(s0, 1, 1, true, idesc);
-                umma_commit_pair_multicast(bar_consumed + 8u * s0, 0x3);
+                commit(bar_consumed + 8u * s0);
               }
             }
             issue_half(s, 1, 1, k == 0, idesc);
           }
-          umma_commit_pair_multicast(bar_consumed + 8u * s, 0x3);
+          commit(bar_consumed + 8u * s);
         }
         if (!ok) break;
-        umma_commit_pair_multicast(bar_tmem_full + 8u * acc0, 0x3);
-        if (halves == 2u) umma_commit_pair_multicast(bar_tmem_full + 8u, 0x3);
+        commit(bar_tmem_full + 8u * acc0);
+        if (halves == 2u) commit(bar_tmem_full + 8u);
       }
-      umma_commit_pair_multicast(bar_drain, 0x1);
-      wait_bounded(bar_drain, 0, limit, kRoleDrain);
+      if (leader) {
+        umma_commit_pair_multicast(bar_drain, 0x1);
+        wait_bounded(bar_drain, 0, limit, kRoleDrain);
+      }
     }
     __syncwarp();
   } else if (warp >= kWgFirstMakeWarp) {
@@ -529,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
       const uint32_t scale_at = sS0 + r0 * kWgScalePitch + c / 2u +
                                 (p.tma_scales ? sc & 15u : (r0 * p.scale_cols) & 3u);
       uint32_t k = skip;
-      for (; k < nk; k += kWgMakeGroups, ring.advance(kWgMakeGroups), raw.advance(kWgMakeGroups)) {
+      for (; k < nk; k += Cfg::kGroups, ring.advance(Cfg::kGroups), raw.advance(Cfg::kGroups)) {
         const uint32_t r = raw.slot, s = ring.slot;
         bool got = pair_wait_or_abort(bar_raw_full + 8u * r, raw.parity, abort_flag, peer_abort,
                                       limit, kRoleProducer) &&
@@ -547,10 +574,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
                        in[i][2], in[i][3]);
           scale[i] = ld_shared_u8(scale_at + r * kWgScaleBytes + i * 16u * kWgScalePitch);
         }
-        bool is_short = true;
 #pragma unroll
         for (uint32_t i = 0; i < kWgPasses; ++i) {
-          is_short = is_short && widens_short<DT>(in[i], scale[i]);
           // the half that is written first comes first
           const uint32_t w0 = in[i][0], w1 = in[i][1];
           in[i][0] = swap ? in[i][2] : w0;
@@ -571,14 +596,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
           st_shared_v4(a + at0 + i * 2048u, out[0], out[1], out[2], out[3]);
           st_shared_v4(a + at1 + i * 2048u, out[4], out[5], out[6], out[7]);
         };
-        if (__all_sync(0xffffffffu, is_short)) {
+        uint32_t top = 0, s_min = 255, s_max = 0;
 #pragma unroll
-          for (uint32_t i = 0; i < kWgPasses; ++i) {
-            uint32_t out[8];
-            widen_short<DT>(in[i], scale[i], out);
-            put(i, out);
-          }
-        } else {
+        for (uint32_t i = 0; i < kWgPasses; ++i) {
+          uint32_t out[8];
+          widen_short<DT>(in[i], scale[i], out, top);
+          put(i, out);
+          s_min = min(s_min, scale[i]);
+          s_max = max(s_max, scale[i]);
+        }
+        if (!widened_right<DT>(top, s_min, s_max)) {   // rare: again, the long way
 #pragma unroll
           for (uint32_t i = 0; i < kWgPasses; ++i) {
             uint32_t out[8];
@@ -586,6 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
             put(i, out);
           }
         }
+        __syncwarp();
         fence_proxy_async_shared();
         // the report of the even CTA's first warp of the group also says that dY has landed, so
         // the MMA thread has one barrier to wait for (two took it 100 cycles more a k-block)
@@ -666,34 +694,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
   }
 }
 
-// dW = the sum of the splits' partial sums [splits][part_rows][outs], rounded once.  A thread takes
-// 8 neighbouring columns of a row (outs is a multiple of 8).
+// dW = the sum of the splits' partial sums [splits][part_rows][outs], in order, rounded once.  A
+// thread takes 4 neighbouring columns of a row (outs is a multiple of 8) and reads four splits at a
+// time, so that what bounds it is the L2's bandwidth and not a chain of reads.
 template <int DT>
 __global__ void __launch_bounds__(256)
     wgrad_join_kernel(const float* __restrict__ partials, uint32_t splits, uint64_t split_stride,
                       uint32_t rows, uint32_t outs, void* __restrict__ dw, int64_t ld_dw) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const uint32_t vecs = outs / 8u;
-  const uint64_t total = static_cast<uint64_t>(rows) * vecs;
+  const uint32_t vecs = outs / 4u;
+  const uint64_t total = static_cast<uint64_t>(rows) * vecs, stride4 = split_stride / 4u;
   for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
        i += static_cast<uint64_t>(gridDim.x) * blockDim.x) {
     const uint32_t row = static_cast<uint32_t>(i / vecs), v = static_cast<uint32_t>(i % vecs);
-    const float4* src = reinterpret_cast<const float4*>(partials + static_cast<uint64_t>(row) * outs) + 2u * v;
-    float4 a = src[0], b = src[1];
-    for (uint32_t s = 1; s < splits; ++s) {
-      src += split_stride / 4u;
-      const float4 c = src[0], d = src[1];
-      a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
-      b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+    const float4* src = reinterpret_cast<const float4*>(partials) + i;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    uint32_t s = 0;
+    for (; s + 4u <= splits; s += 4u, src += 4u * stride4) {
+      float4 c[4];
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) c[j] = __ldcg(src + j * stride4);
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) a.x += c[j].x, a.y += c[j].y, a.z += c[j].z, a.w += c[j].w;
     }
-    uint4 o;
+    for (; s < splits; ++s, src += stride4) {
+      const float4 c = __ldcg(src);
+      a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
+    }
+    uint2 o;
     o.x = pack_out<DT>(__float_as_uint(a.x), __float_as_uint(a.y));
     o.y = pack_out<DT>(__float_as_uint(a.z), __float_as_uint(a.w));
-    o.z = pack_out<DT>(__float_as_uint(b.x), __float_as_uint(b.y));
-    o.w = pack_out<DT>(__float_as_uint(b.z), __float_as_uint(b.w));
-    *reinterpret_cast<uint4*>(static_cast<char*>(dw) +
-                              (static_cast<int64_t>(row) * ld_dw + 8 * v) * 2) = o;
+    *reinterpret_cast<uint2*>(static_cast<char*>(dw) +
+                              (static_cast<int64_t>(row) * ld_dw + 4 * v) * 2) = o;
   }
 }
 
