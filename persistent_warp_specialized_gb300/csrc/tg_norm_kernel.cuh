@@ -90,6 +90,13 @@ __device__ __forceinline__ void params_or(const void* p, uint32_t col, uint32_t 
   }
 }
 
+// Zeroes a warp's strips: those past a row's end stay so, and the values there count for nothing.
+__device__ __forceinline__ void clear_strips(uint32_t at, uint32_t strips) {
+  for (uint32_t o = (threadIdx.x & 31u) * 16u; o < strips * kStripBytes; o += 512u)
+    st_shared_v4(at + o, 0u, 0u, 0u, 0u);
+  __syncwarp();
+}
+
 // y of the lane's N values at column ``col`` (and their checkpoint), of which ``left`` are in the
 // row; every lane of the warp calls it.
 template <typename TX, bool UNAL, bool KEEP>
@@ -178,6 +185,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
   uint64_t row = blockIdx.x + static_cast<uint64_t>(gridDim.x) * group, ahead = row;
   uint32_t slot = 0;
+  clear_strips(mine, kSlots * R * kItems);
 #pragma unroll
   for (uint32_t i = 0; i + 1 < kSlots; ++i, ahead += R * step) stage(ahead, i);
   for (uint32_t turn = 0; row < p.rows; row += R * step, ++turn) {
@@ -196,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int k = 0; k < kItems; ++k) {
         values<TX>(staged_vector<TX, UNAL>(mine + ((slot * R + r) * kItems + k) * kStripBytes, lead),
                    v[r][k]);
-        if (left[k] < N) {
+        if constexpr (UNAL) {
 #pragma unroll
           for (int i = 0; i < N; ++i) v[r][k][i] = i < left[k] ? v[r][k][i] : 0.0f;
         }
@@ -204,19 +212,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < N; ++i) s += v[r][k][i];
       }
       // exact where all values are one (a constant row has variance 0)
-      float m = s * (1.0f / kNormValues), m2 = 0.0f;
-      if (n_mine == kNormValues) {
+      const float m = n_mine == kNormValues ? s * (1.0f / kNormValues)
+                                            : (n_mine > 0 ? s / n_t : 0.0f);
+      float m2 = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kItems; ++k)
+      for (int k = 0; k < kItems; ++k) {
+        float q = 0.0f;
 #pragma unroll
-          for (int i = 0; i < N; ++i) m2 = fmaf(v[r][k][i] - m, v[r][k][i] - m, m2);
-      } else {
-        m = n_mine > 0 ? s / n_t : 0.0f;
-#pragma unroll
-        for (int k = 0; k < kItems; ++k)
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (i < left[k]) m2 = fmaf(v[r][k][i] - m, v[r][k][i] - m, m2);
+        for (int i = 0; i < N; ++i) {
+          const float d = !UNAL || i < left[k] ? v[r][k][i] - m : 0.0f;
+          q = fmaf(d, d, q);
+        }
+        m2 += UNAL || left[k] > 0 ? q : 0.0f;
       }
       c[r] = __shfl_sync(0xffffffffu, m, 0);   // lane 0 holds values wherever its warp holds any
       const float d = n_mine > 0 ? m - c[r] : 0.0f;
@@ -443,7 +450,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     cp_async_commit();
   };
-  // the lane's dy and xh of its k-th vector, from the row's slot; zero past the row's end
+  // the lane's dy and xh of its k-th vector, from the row's slot; past the row's end dy is zero, and
+  // xh a number
   auto values_at = [&](uint64_t row, uint32_t slot, int k, float mean, float rstd, float (&dy)[N],
                        float (&xh)[N]) {
     const uint32_t at = mine + slot * (2 * kItems * kStripBytes);
@@ -459,14 +467,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         q[0] = ld_shared_u32(xs + lane * 4u);
       const uint32_t byte = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.s)) +
                              static_cast<uint32_t>(row) * p.blocks + col[k] / kCkptBlock) & 3u;
-      kept_values<N>(q, (ld_shared_u32(xs + 32u * N + lane / kPer * 4u) >> (8u * byte)) & 0xFFu, xh);
+      kept_less<N>(q, (ld_shared_u32(xs + 32u * N + lane / kPer * 4u) >> (8u * byte)) & 0xFFu, mean,
+                   xh);
+#pragma unroll
+      for (int i = 0; i < N; ++i) xh[i] *= rstd;
     } else {
       const uint32_t lead_x = UNAL ? lead_of(p.x.base + static_cast<int64_t>(row) * p.x.pitch) : 0u;
       values<TX>(staged_vector<TX, UNAL>(xs, lead_x), xh);
-    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) xh[i] = (xh[i] - mean) * rstd;
-    if (left[k] < N) {
+      for (int i = 0; i < N; ++i) xh[i] = (xh[i] - mean) * rstd;
+    }
+    if constexpr (UNAL) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         dy[i] = i < left[k] ? dy[i] : 0.0f;
@@ -484,6 +495,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t slot = 0;
   float mean = 0.0f, rstd = 0.0f;
   if (row < p.rows) mean = p.mean[row], rstd = p.rstd[row];
+  clear_strips(mine, kSlots * 2 * kItems);
 #pragma unroll
   for (uint32_t i = 0; i + 1 < kSlots; ++i, ahead += step) stage(ahead, i);
   for (uint32_t turn = 0; row < p.rows; row += step, ++turn) {

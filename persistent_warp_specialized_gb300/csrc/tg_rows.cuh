@@ -116,8 +116,10 @@ struct RowsOf {
 };
 
 // A row starts ``lead`` bytes into a 16-byte granule.  A warp takes 32 neighbouring vectors of 16
-// bytes from it (a strip); with lead != 0 (UNAL) vector j lies in granules j and j + 1, so a strip
-// needs 33 granules, all read as they lie, and each lane shifts its vector out of two of them.
+// bytes from it (a strip); with lead != 0 vector j lies in granules j and j + 1, so a strip needs 33
+// granules, all read as they lie, and each lane shifts its vector out of two of them.  UNAL: some
+// row has a lead, or rows are not whole vectors; without it every vector is a granule in the row, or
+// past its end.
 
 // Value i of the 16 bytes (i a constant), stored alone.
 template <typename T>
@@ -273,36 +275,39 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
 constexpr uint32_t kStripBytes = 33 * 16;   // a strip's granules in shared memory
 
 // Starts the copy of the lane's granule of a strip (and, from lane 31 with UNAL, of the 33rd) to
-// ``strip``; what lies past the row's end is not copied.  ``inner``: the granules lie within the
-// row whatever its lead, so nothing needs to be checked (see inner_vector).
+// ``strip``; what lies past the row's end is not copied.  ``inner``: inner_vector of the vector.
 template <typename T, bool UNAL>
 __device__ __forceinline__ void stage_vector(uint32_t strip, const RowsOf& m, const char* row,
                                              uint32_t at, int64_t row_bytes, bool inner) {
   const uint32_t lane = threadIdx.x & 31u;
-  const uint32_t lead = UNAL ? lead_of(row) : 0u;
-  const char* p = row - lead + at;
-  if (inner) {
-    cp_async<16>(strip + lane * 16u, p);
-    if (UNAL && lane == 31u) cp_async<16>(strip + 32u * 16u, p + 16);
-    return;
-  }
+  if constexpr (!UNAL) {
+    if (inner) cp_async<16>(strip + lane * 16u, row + at);
+  } else {
+    const uint32_t lead = lead_of(row);
+    const char* p = row - lead + at;
+    if (inner) {
+      cp_async<16>(strip + lane * 16u, p);
+      if (lane == 31u) cp_async<16>(strip + 32u * 16u, p + 16);
+      return;
+    }
 #pragma unroll
-  for (int j = 0; j < (UNAL ? 2 : 1); ++j) {
-    if (j == 1 && lane != 31u) break;
-    if (at + 16u * j >= row_bytes + lead) break;
-    const char* q = p + 16 * j;
-    const uint32_t dst = strip + (lane + j) * 16u;
-    if (q >= m.base && q + 16 <= m.end) {
-      cp_async<16>(dst, q);
-    } else {   // at the matrix's ends
-      const V16 r = load_granule<T>(q, m.base, m.end);
-      st_shared_v4(dst, r.w[0], r.w[1], r.w[2], r.w[3]);
+    for (int j = 0; j < 2; ++j) {
+      if (j == 1 && lane != 31u) break;
+      if (at + 16u * j >= row_bytes + lead) break;
+      const char* q = p + 16 * j;
+      const uint32_t dst = strip + (lane + j) * 16u;
+      if (q >= m.base && q + 16 <= m.end) {
+        cp_async<16>(dst, q);
+      } else {   // at the matrix's ends
+        const V16 r = load_granule<T>(q, m.base, m.end);
+        st_shared_v4(dst, r.w[0], r.w[1], r.w[2], r.w[3]);
+      }
     }
   }
 }
 
-// Whether a vector's granules lie within every row: not the first (with a lead it begins before the
-// row) nor one of the last.
+// Whether a vector's granules lie within every row, so that nothing has to be checked: with UNAL
+// not the first (with a lead it begins before the row) nor the last ones.
 template <bool UNAL>
 __device__ __forceinline__ bool inner_vector(uint32_t at, int64_t row_bytes) {
   return UNAL ? at >= 16u && at + 32u <= row_bytes : at + 16u <= row_bytes;
@@ -420,6 +425,19 @@ __device__ __forceinline__ void kept_values(const uint32_t* q, uint32_t s, float
     const float2 f = e4m3x2_value(q[i / 4] >> (8 * (i & 2)));
     v[i] = f.x * scale;
     v[i + 1] = f.y * scale;
+  }
+}
+
+// kept_values less ``mean``, rounded once (a byte times its scale is exact)
+template <int N>
+__device__ __forceinline__ void kept_less(const uint32_t* q, uint32_t s, float mean,
+                                          float (&v)[N]) {
+  const float scale = e8m0_value(s);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 f = e4m3x2_value(q[i / 4] >> (8 * (i & 2)));
+    v[i] = fmaf(f.x, scale, -mean);
+    v[i + 1] = fmaf(f.y, scale, -mean);
   }
 }
 

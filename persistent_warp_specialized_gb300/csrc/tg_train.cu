@@ -132,7 +132,8 @@ cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream) {
   };
   return with_types(l.dtype, l.param_dtype, [&](auto tx, auto tp) -> cudaError_t {
     constexpr uint32_t kElem = sizeof(typename decltype(tx)::type);
-    const bool unal = !rows_aligned(l.x, l.ld_x, kElem) || !rows_aligned(l.y, l.ld_y, kElem);
+    const bool unal = l.cols * kElem % 16 != 0 || !rows_aligned(l.x, l.ld_x, kElem) ||
+                      !rows_aligned(l.y, l.ld_y, kElem);
     if (l.q) return unal ? run(tx, tp, std::true_type(), std::true_type())
                          : run(tx, tp, std::false_type(), std::true_type());
     return unal ? run(tx, tp, std::true_type(), std::false_type())
@@ -204,7 +205,7 @@ cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
   return with_types(l.dtype, l.param_dtype, [&](auto tx, auto tp) -> cudaError_t {
     using TP = typename decltype(tp)::type;
     constexpr uint32_t kElem = sizeof(typename decltype(tx)::type);
-    const bool unal = !rows_aligned(l.dy, l.ld_dy, kElem) ||
+    const bool unal = l.cols * kElem % 16 != 0 || !rows_aligned(l.dy, l.ld_dy, kElem) ||
                       !rows_aligned(l.dx, l.ld_dx, kElem) || !rows_aligned(l.x, l.ld_x, kElem);
     cudaError_t e = cudaSuccess;
     if (l.rows > 0) {
