@@ -371,8 +371,8 @@ __device__ __forceinline__ void x_values(const NormBwdParams& p, uint32_t row, u
 // As the forward kernel; each thread keeps the sums of dy xh and dy of its own columns in registers
 // over all its rows.  At the end the groups of a CTA add up in order, the CTA writes one row of
 // partial sums, and norm_bwd_join_kernel adds those in a fixed order, so the result does not depend
-// on timing.  A staged strip of a checkpoint: N bytes a lane, then for each block of 32 values the
-// 4-byte word that holds its scale.
+// on timing.  A staged strip of a checkpoint holds N bytes a lane; scales, like the statistics, are
+// read into registers a row ahead.
 template <typename TX, typename TP, bool UNAL, bool KEPT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_bwd_kernel(const NormBwdParams p, const uint32_t g_threads) {
@@ -380,7 +380,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int N = kVec<TX>, kItems = kNormValues / N;
   constexpr uint32_t kSlots = kNormSlots<TX, THREADS, 2>;
   constexpr bool kHeld = THREADS == kNormThreads;   // gamma and the row's values in registers
-  constexpr uint32_t kPer = kCkptBlock / N;         // lanes per block of 32 values
   __shared__ float part[2][2][32];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t groups = blockDim.x / g_threads, group = threadIdx.x / g_threads;
@@ -427,21 +426,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         stage_vector<TX, UNAL>(at + k * kStripBytes, p.dy, dy, byte, row_bytes, inner[k]);
         const uint32_t xs = at + (kItems + k) * kStripBytes;
         if constexpr (KEPT) {
-          if (left[k] > 0) {
-            const uint64_t b = row * p.blocks + col[k] / kCkptBlock;
-            cp_async<N>(xs + lane * N, p.q + b * kCkptBlock + col[k] % kCkptBlock);
-            if (lane % kPer == 0u) {
-              const uint8_t* s = p.s + b;
-              const uint8_t* word = s - (reinterpret_cast<uintptr_t>(s) & 3u);
-              const uint32_t dst = xs + 32u * N + lane / kPer * 4u;
-              if (word >= p.s && word + 4 <= p.s + static_cast<uint64_t>(p.rows) * p.blocks)
-                cp_async<4>(dst, word);
-              else
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(s - word)),
-                             "r"(static_cast<uint32_t>(*s))
-                             : "memory");
-            }
-          }
+          if (left[k] > 0)
+            cp_async<N>(xs + lane * N, p.q + row * p.blocks * kCkptBlock + col[k]);
         } else {
           stage_vector<TX, UNAL>(xs, p.x, p.x.base + static_cast<int64_t>(row) * p.x.pitch, byte,
                                  row_bytes, inner[k]);
@@ -449,6 +435,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     cp_async_commit();
+  };
+  uint32_t scale[kItems];
+  auto scales_of = [&](uint64_t row, uint32_t (&to)[kItems]) {
+#pragma unroll
+    for (int k = 0; k < kItems; ++k)
+      to[k] = KEPT && left[k] > 0 ? p.s[row * p.blocks + col[k] / kCkptBlock] : 127u;
   };
   // the lane's dy and xh of its k-th vector, from the row's slot; past the row's end dy is zero, and
   // xh a number
@@ -465,10 +457,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q[0]), "=r"(q[1]) : "r"(xs + lane * 8u) : "memory");
       else
         q[0] = ld_shared_u32(xs + lane * 4u);
-      const uint32_t byte = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.s)) +
-                             static_cast<uint32_t>(row) * p.blocks + col[k] / kCkptBlock) & 3u;
-      kept_less<N>(q, (ld_shared_u32(xs + 32u * N + lane / kPer * 4u) >> (8u * byte)) & 0xFFu, mean,
-                   xh);
+      kept_less<N>(q, scale[k], mean, xh);
 #pragma unroll
       for (int i = 0; i < N; ++i) xh[i] *= rstd;
     } else {
@@ -494,7 +483,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t row = blockIdx.x + static_cast<uint64_t>(gridDim.x) * group, ahead = row;
   uint32_t slot = 0;
   float mean = 0.0f, rstd = 0.0f;
-  if (row < p.rows) mean = p.mean[row], rstd = p.rstd[row];
+  if (row < p.rows) {
+    mean = p.mean[row];
+    rstd = p.rstd[row];
+    scales_of(row, scale);
+  }
   clear_strips(mine, kSlots * 2 * kItems);
 #pragma unroll
   for (uint32_t i = 0; i + 1 < kSlots; ++i, ahead += step) stage(ahead, i);
@@ -502,7 +495,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     stage(ahead, slot == 0u ? kSlots - 1u : slot - 1u);
     ahead += step;
     float next_mean = 0.0f, next_rstd = 0.0f;
-    if (row + step < p.rows) next_mean = p.mean[row + step], next_rstd = p.rstd[row + step];
+    uint32_t next_scale[kItems];
+    if (row + step < p.rows) {
+      next_mean = p.mean[row + step];
+      next_rstd = p.rstd[row + step];
+      scales_of(row + step, next_scale);
+    }
     cp_async_wait<kSlots - 1>();
     __syncwarp();
     float s[2] = {0.0f, 0.0f};   // sums of dy gamma, and of it times xh
@@ -558,6 +556,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     slot = slot + 1u == kSlots ? 0u : slot + 1u;
     mean = next_mean;
     rstd = next_rstd;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) scale[k] = next_scale[k];
   }
   cp_async_wait<0>();
   if (p.partials == nullptr) return;
