@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     cp_async_commit();
   };
-  uint32_t scale[kItems];
+  uint32_t scale[kItems] = {};
   auto scales_of = [&](uint64_t row, uint32_t (&to)[kItems]) {
 #pragma unroll
     for (int k = 0; k < kItems; ++k)
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     stage(ahead, slot == 0u ? kSlots - 1u : slot - 1u);
     ahead += step;
     float next_mean = 0.0f, next_rstd = 0.0f;
-    uint32_t next_scale[kItems];
+    uint32_t next_scale[kItems] = {};
     if (row + step < p.rows) {
       next_mean = p.mean[row + step];
       next_rstd = p.rstd[row + step];

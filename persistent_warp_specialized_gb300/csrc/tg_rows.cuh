@@ -149,19 +149,29 @@ __device__ __forceinline__ V16 load_granule(const char* p, const char* from, con
   return r;
 }
 
-// 16 bytes from byte ``lead`` (a multiple of the value's size, below 16) of a and b put together.
+// 16 bytes from byte ``lead`` (a multiple of the value's size, below 16; the same in every lane) of
+// a and b put together: one of four word offsets, then a shift by half a word.
 template <typename T>
 __device__ __forceinline__ V16 window(const V16& a, const V16& b, uint32_t lead) {
-  uint32_t w[8] = {a.w[0], a.w[1], a.w[2], a.w[3], b.w[0], b.w[1], b.w[2], b.w[3]};
-  const bool by8 = lead & 8u, by4 = lead & 4u;
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = by8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = by4 ? w[i + 1] : w[i];
+  const uint32_t bits = sizeof(T) == 4 ? 0u : (lead & 2u) * 8u;
   V16 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r.w[i] = sizeof(T) == 4 ? w[i] : __funnelshift_r(w[i], w[i + 1], (lead & 2u) * 8u);
+  switch (lead >> 2) {
+    case 0:
+      r = V16{{__funnelshift_r(a.w[0], a.w[1], bits), __funnelshift_r(a.w[1], a.w[2], bits),
+               __funnelshift_r(a.w[2], a.w[3], bits), __funnelshift_r(a.w[3], b.w[0], bits)}};
+      break;
+    case 1:
+      r = V16{{__funnelshift_r(a.w[1], a.w[2], bits), __funnelshift_r(a.w[2], a.w[3], bits),
+               __funnelshift_r(a.w[3], b.w[0], bits), __funnelshift_r(b.w[0], b.w[1], bits)}};
+      break;
+    case 2:
+      r = V16{{__funnelshift_r(a.w[2], a.w[3], bits), __funnelshift_r(a.w[3], b.w[0], bits),
+               __funnelshift_r(b.w[0], b.w[1], bits), __funnelshift_r(b.w[1], b.w[2], bits)}};
+      break;
+    default:
+      r = V16{{__funnelshift_r(a.w[3], b.w[0], bits), __funnelshift_r(b.w[0], b.w[1], bits),
+               __funnelshift_r(b.w[1], b.w[2], bits), __funnelshift_r(b.w[2], b.w[3], bits)}};
+  }
   return r;
 }
 

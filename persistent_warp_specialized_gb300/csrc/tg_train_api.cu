@@ -213,8 +213,12 @@ int wgrad_impl(const void* q, const void* sc, const void* dy, void* dw, int64_t 
   l.m_blocks = w.m_tiles;
   l.n_blocks = w.n_tiles;
   l.k_blocks = w.k_blocks;
-  l.group = tg::kGroup;
-  l.column_major = 0;
+  // Whole columns of tiles in turn: a wave reads few columns of dY and all of x, which is half of
+  // dY's size a value and stays in the L2.  Measured (us, bf16, whole columns / groups of 8 in row
+  // order): 8192^3 566 / 580, 32768 x 8192 x 4096 1138 / 1191, 16384 x 2048 x 16384 623 / 648,
+  // 4000 x 2048 x 7000 84.6 / 84.6, 16384 x 16384 x 2048 591 / 586.
+  l.group = w.m_tiles < 255u ? w.m_tiles : 255u;
+  l.column_major = 1;
   l.split_from = w.split_from;
   l.total_units = w.units;
   l.splits = w.splits;
