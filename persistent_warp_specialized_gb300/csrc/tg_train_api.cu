@@ -79,50 +79,71 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 // How the weight gradient [cols, outs] over ``tokens`` tokens is cut into units.
 struct WgradPlan {
-  uint32_t halves, m_tiles, n_tiles, k_blocks, splits, blocks_per_split, split_from, units, pairs;
+  uint32_t halves;      // N-halves of 256 columns in a tile of dW
+  uint32_t m_tiles, n_tiles, k_blocks, splits, blocks_per_split, split_from, units, pairs;
   uint64_t workspace;   // bytes of partial sums (0: one split)
+  double us;            // what the plan is expected to take
 };
 
-// Tiles that fill a wave of CTA pairs are each one unit over all tokens.  Fewer tiles: the tokens
-// are split so that every pair has a unit, as long as a unit keeps kWgMinBlocks k-blocks.
-constexpr uint64_t kWgMinBlocks = 8;
+// Microseconds on GB300 that the choice of a plan goes by: a k-block of a whole tile and of its
+// half-width unit; what a unit's epilogue keeps the MMAs waiting (two accumulators overlap it); the
+// join, and bytes of partial sums a microsecond, written and read.
+constexpr double kWgBlockUs[2] = {0.40, 0.56}, kWgHalfBlockUs[2] = {0.33, 0.40};
+constexpr double kWgDrainUs[2] = {0.2, 2.0}, kWgJoinUs = 2.5;
+constexpr double kWgWriteBytes = 5e6, kWgReadBytes = 4e6;
+constexpr uint64_t kWgMinBlocks = 8;   // k-blocks of a unit, when the tokens are split
 
-// N-halves of 256 columns in a tile of dW.  Two halve the bytes that have to be widened for each
-// multiplication, and give the MMA thread eight MMAs a k-block instead of four; one leaves smaller
-// units when there are few.  Measured (GB300, bf16, one / two halves, us, L2 flushed): tokens x
-// cols x outs 8192^3 861 / 615, 4096^3 134 / 99, 1024 x 4096 x 4096 43.6 / 37.5, 16384 x 2048 x
-// 2048 132 / 103 (32 wide tiles), 32768 x 1000 x 512 49.8 / 51.8 and 2048 x 512 x 512 19.1 / 21.1
-// (4 and 2 wide tiles).
-constexpr uint64_t kWgWideTiles = 16;
-
-uint32_t wgrad_halves(int64_t cols, int64_t outs) {
-  const uint64_t wide = ceil_div(cols, tg::kPairBM) * ceil_div(outs, 2 * tg::kBN);
-  return outs > tg::kBN && wide >= kWgWideTiles ? 2 : 1;
-}
-
-WgradPlan wgrad_plan(int64_t tokens, int64_t cols, int64_t outs, int max_pairs) {
+// The plan with tiles of ``halves`` N-halves and the tokens in about ``splits`` ranges.
+WgradPlan wgrad_plan_of(int64_t tokens, int64_t cols, int64_t outs, uint64_t pairs,
+                        uint32_t halves, uint64_t splits) {
   WgradPlan w;
+  w.halves = halves;
   w.m_tiles = static_cast<uint32_t>(ceil_div(cols, tg::kPairBM));
-  w.halves = wgrad_halves(cols, outs);
-  w.n_tiles = static_cast<uint32_t>(ceil_div(outs, w.halves * tg::kBN));
+  w.n_tiles = static_cast<uint32_t>(ceil_div(outs, halves * tg::kBN));
   w.k_blocks = static_cast<uint32_t>(ceil_div(tokens, tg::kWgBK));
-  const uint64_t tiles = static_cast<uint64_t>(w.m_tiles) * w.n_tiles;
-  const uint64_t pairs = static_cast<uint64_t>(max_pairs);
-  uint64_t splits = tiles < pairs ? pairs / tiles : 1;
-  if (splits > w.k_blocks / kWgMinBlocks) splits = w.k_blocks / kWgMinBlocks;
-  if (splits < 1) splits = 1;
+  const uint32_t tiles = w.m_tiles * w.n_tiles;
   w.blocks_per_split = static_cast<uint32_t>(ceil_div(w.k_blocks, splits));
   w.splits = w.k_blocks ? static_cast<uint32_t>(ceil_div(w.k_blocks, w.blocks_per_split)) : 1;
   w.workspace = 0;
-  w.split_from = w.units = static_cast<uint32_t>(tiles);
-  if (w.splits > 1)
-    w.workspace = static_cast<uint64_t>(w.splits) * w.m_tiles * tg::kPairBM * outs * 4;
-  else
-    tg::PersistentTileScheduler::tail_split(static_cast<uint32_t>(tiles), max_pairs, w.split_from,
+  w.split_from = w.units = tiles;
+  if (w.splits == 1)
+    tg::PersistentTileScheduler::tail_split(tiles, static_cast<uint32_t>(pairs), w.split_from,
                                             w.units);
   const uint64_t all = static_cast<uint64_t>(w.units) * w.splits;
   w.pairs = static_cast<uint32_t>(all < pairs ? all : pairs);
+  const uint32_t h = halves - 1;
+  const double whole = static_cast<double>(ceil_div(w.split_from * uint64_t(w.splits), pairs));
+  w.us = whole * (w.blocks_per_split * kWgBlockUs[h] + kWgDrainUs[h]);
+  if (w.units > w.split_from) w.us += w.k_blocks * kWgHalfBlockUs[h];
+  if (w.splits > 1) {
+    w.workspace = static_cast<uint64_t>(w.splits) * w.m_tiles * tg::kPairBM * outs * 4;
+    const double sums = static_cast<double>(w.splits) * cols * outs * 4.0;
+    w.us += sums / kWgWriteBytes + kWgJoinUs + sums / kWgReadBytes;
+  }
   return w;
+}
+
+// Tiles of two N-halves halve the bytes that have to be widened for each multiplication, and have
+// eight MMAs a k-block where one half has four and is bound by shared memory; tiles of one make
+// smaller units, which fill the pairs when there are few.  Fewer tiles than pairs: the tokens may
+// also be split, so that every pair has a unit, at the price of partial sums in fp32.  The least
+// expected time decides.  Measured (bf16, us back to back; one half / two halves, splits in
+// brackets): 8192^3 760 / 558, 1024 x 4096 x 4096 36 / 30, 32768 x 1000
+// x 512 36.5 [9] / 36.6 [19], 65536 x 512 x 512 38.6 [19] / 44.8 [38]; two halves, whole / split:
+// 2048^3 19.4 / 26.3 [2], 16384 x 2048 x 1024 - / 53 [4].
+WgradPlan wgrad_plan(int64_t tokens, int64_t cols, int64_t outs, int max_pairs) {
+  const uint64_t pairs = static_cast<uint64_t>(max_pairs);
+  WgradPlan best = wgrad_plan_of(tokens, cols, outs, pairs, 1, 1);
+  for (uint32_t halves = 1; halves <= (outs > tg::kBN ? 2u : 1u); ++halves) {
+    const WgradPlan whole = wgrad_plan_of(tokens, cols, outs, pairs, halves, 1);
+    if (whole.us < best.us) best = whole;
+    uint64_t splits = pairs / (uint64_t(whole.m_tiles) * whole.n_tiles);
+    if (splits > whole.k_blocks / kWgMinBlocks) splits = whole.k_blocks / kWgMinBlocks;
+    if (splits < 2) continue;
+    const WgradPlan cut = wgrad_plan_of(tokens, cols, outs, pairs, halves, splits);
+    if (cut.us < best.us) best = cut;
+  }
+  return best;
 }
 
 int check_wgrad_sizes(int64_t tokens, int64_t cols, int64_t outs) {
