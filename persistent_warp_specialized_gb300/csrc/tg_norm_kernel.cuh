@@ -90,6 +90,16 @@ __device__ __forceinline__ void params_or(const void* p, uint32_t col, uint32_t 
   }
 }
 
+// 1 / sqrt(a): rsqrtf is within 2 ulp, and one Newton step, r + r (1 - a r^2) / 2, takes that to
+// about half of one.  Every value of a row is multiplied by it, so its error would move results to
+// the other side of a rounding, a whole step of 1/16 in an 8-bit checkpoint.  0 gives infinity,
+// infinity 0.
+__device__ __forceinline__ float inverse_root(float a) {
+  const float r = rsqrtf(a);
+  const float e = fmaf(-a * r, r, 1.0f);
+  return a > 0.0f && a < INFINITY ? fmaf(0.5f * r, e, r) : r;
+}
+
 // Zeroes a warp's strips: those past a row's end stay so, and the values there count for nothing.
 __device__ __forceinline__ void clear_strips(uint32_t at, uint32_t strips) {
   for (uint32_t o = (threadIdx.x & 31u) * 16u; o < strips * kStripBytes; o += 512u)
@@ -259,9 +269,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float sa = sum_of<2 * R>(sums, 2 * r), sb = sum_of<2 * R>(sums, 2 * r + 1);
       const float d = sb * inv_row;
       mean[r] = c[r] + d;
-      // rsqrtf: within 2 ulp, and 1 / sqrt(0) = infinity; the difference may round below zero
-      const float m2 = fmaf(-sb, d, sa);
-      rstd[r] = rsqrtf((m2 < 0.0f ? 0.0f : m2) * inv_row + p.eps);
+      const float m2 = fmaf(-sb, d, sa);   // may round below zero
+      rstd[r] = inverse_root((m2 < 0.0f ? 0.0f : m2) * inv_row + p.eps);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const NormFwdParams
     a = warp_sum(lane < warps ? part[pass][lane] : 0.0f);
     stat[pass] = a / static_cast<float>(p.cols);
   }
-  const float mean = stat[0], rstd = 1.0f / sqrtf(stat[1] + p.eps);
+  const float mean = stat[0], rstd = inverse_root(stat[1] + p.eps);
   if (threadIdx.x == 0) {
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;
