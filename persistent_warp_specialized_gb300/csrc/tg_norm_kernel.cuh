@@ -8,11 +8,11 @@
 //   dbeta = sum_rows dy;  x is the tensor, or its 8-bit checkpoint.
 // Both are bound by memory: a row stays on the SM from its one read to the result's write.
 //
-// Rows go to groups of G threads, 16 values a thread (G a multiple of 32); a CTA, one per SM, holds
-// as many groups as its threads allow.  In the forward pass a group takes two rows a turn: one
-// barrier, and one chain of shuffles, serves both.  Each thread copies its own values of the rows ahead to shared memory
-// (cp.async), so that 64 KiB are on their way to an SM at any time.  Rows of any alignment are read
-// and written in whole 16-byte granules (UNAL, tg_rows.cuh).
+// Rows go to groups of G threads (G a multiple of 32), 16 values a thread (or 32, below); a CTA, one
+// per SM, holds as many groups as its threads allow.  In the forward pass a group takes two rows a turn: one
+// barrier, and one chain of shuffles, serves both.  Each thread copies its own values of the rows
+// ahead to shared memory (cp.async), so that 64 KiB are on their way to an SM at any time.  Rows of
+// any alignment are read and written in whole 16-byte granules (UNAL, tg_rows.cuh).
 //
 // The variance: each thread takes the mean of its own values and their squares about that mean
 // (n, m, M2); lanes, and then warps, are joined about the mean c of the first of them,
@@ -25,36 +25,51 @@
 
 namespace tg {
 
-constexpr int kNormValues = 16;      // of a thread
 constexpr int kNormMaxGroups = 15;   // one named barrier each
+constexpr int kNormValues = 16;      // of a thread
 // Threads of a CTA: 512 with 128 registers hold the parameters, the row's values and (backward) the
 // sums over rows.  Rows of more than 8192 values take 1024 threads of 64 registers: one row a turn,
 // parameters read again for each row, and (backward, 16-bit values only: 32-bit ones would need more
 // shared memory than there is) the row's values taken from shared memory twice, some sums spilled.
 constexpr int kNormThreads = 512;
 constexpr int kNormWideThreads = 1024;
+// Forward, 16-bit values: 512 threads of 32 values halve the shuffles, joins and barriers a value;
+// the parameters come from shared memory up to 8192 columns and are read again above.  Taken for
+// rows of more than 2048 values from 96 Ki values an SM on, else the start costs more: 8192 x 8192
+// 53 us against 56 with 16 values a thread, 4000 x 7000 31 against 33, 4096 x 16384 70 against 85
+// (1024 threads), but 100 x 8192 10.9 against 8.8.  fp32 rows would have one row a turn: 4800 x 16384
+// 156 against 134.
+constexpr int kFwdLongValues = 32;
+constexpr int kFwdLongCols = 2048, kFwdParamCols = 8192;
+constexpr int64_t kFwdLongWork = 96 * 1024;   // values an SM
 
-// Rows a turn
-template <int THREADS, int TENSORS>
-constexpr int kNormRows = THREADS == kNormThreads && TENSORS == 1 ? 2 : 1;
+// Forward: rows a turn
+template <int THREADS>
+constexpr int kFwdRows = THREADS == kNormThreads ? 2 : 1;
 
 // Turns whose rows have a place in shared memory: 64 KiB in flight besides the present one.
-template <typename T, int THREADS, int TENSORS>
-constexpr int kNormSlots = 65536 / (THREADS * TENSORS * kNormRows<THREADS, TENSORS> *
-                                    kNormValues * static_cast<int>(sizeof(T))) + 1;
+template <typename T, int THREADS, int VALUES>
+constexpr int kFwdSlots =
+    65536 / (THREADS * kFwdRows<THREADS> * VALUES * static_cast<int>(sizeof(T))) + 1;
+template <typename T, int THREADS>
+constexpr int kBwdSlots = 65536 / (THREADS * 2 * kNormValues * static_cast<int>(sizeof(T))) + 1;
 
-// shared memory of ``warps`` warps
-template <typename T, int THREADS, int TENSORS>
-constexpr uint32_t norm_smem(uint32_t warps) {
-  return warps * TENSORS * kNormSlots<T, THREADS, TENSORS> * kNormRows<THREADS, TENSORS> *
-         (kNormValues / kVec<T>)*kStripBytes;
+// shared memory of ``warps`` warps for rows
+template <typename T, int THREADS, int VALUES>
+constexpr uint32_t norm_fwd_smem(uint32_t warps) {
+  return warps * kFwdSlots<T, THREADS, VALUES> * kFwdRows<THREADS> * (VALUES / kVec<T>)*kStripBytes;
+}
+template <typename T, int THREADS>
+constexpr uint32_t norm_bwd_smem(uint32_t warps) {
+  return warps * 2 * kBwdSlots<T, THREADS> * (kNormValues / kVec<T>)*kStripBytes;
 }
 
 struct NormFwdParams {
   RowsOf x, y;
   const void* gamma;   // may be null (ones)
   const void* beta;    // may be null (zeros)
-  uint32_t wide_params;   // both can be read in 16-byte vectors
+  uint32_t wide_params;     // both can be read in 16-byte vectors
+  uint32_t shared_params;   // byte offset of their fp32 copies in shared memory; 0: none
   float* mean;         // may be null
   float* rstd;         // may be null
   uint8_t* q;          // checkpoint of y (KEEP)
@@ -69,10 +84,10 @@ __device__ __forceinline__ void group_sync(uint32_t group, uint32_t g_threads) {
 }
 
 // How many of a row's values a warp of a group holds: strips w, w + g_warps, ... of 32 N values.
-template <int N>
+template <int N, int VALUES>
 __device__ __forceinline__ float warp_share(uint32_t w, uint32_t g_warps, uint32_t cols) {
   uint32_t n = 0;
-  for (uint32_t k = 0; k < kNormValues / N; ++k) {
+  for (uint32_t k = 0; k < VALUES / N; ++k) {
     const uint64_t at = static_cast<uint64_t>(k * g_warps + w) * (32u * N);
     if (at < cols) n += cols - at < 32u * N ? static_cast<uint32_t>(cols - at) : 32u * N;
   }
@@ -139,13 +154,15 @@ __device__ __forceinline__ void norm_write(const NormFwdParams& p, uint64_t row,
 }
 
 // Row r belongs to CTA r % gridDim.x, and its turns there to the groups in turn.
-template <typename TX, typename TP, bool UNAL, bool KEEP, int THREADS>
+template <typename TX, typename TP, bool UNAL, bool KEEP, int THREADS, int VALUES>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_fwd_kernel(const NormFwdParams p, const uint32_t g_threads) {
   extern __shared__ uint8_t staged[];
-  constexpr int N = kVec<TX>, kItems = kNormValues / N, R = kNormRows<THREADS, 1>;
-  constexpr uint32_t kSlots = kNormSlots<TX, THREADS, 1>;
-  constexpr bool kHeld = THREADS == kNormThreads;   // parameters in registers
+  constexpr int N = kVec<TX>, kItems = VALUES / N, R = kFwdRows<THREADS>;
+  constexpr uint32_t kSlots = kFwdSlots<TX, THREADS, VALUES>;
+  // parameters in registers, or in shared memory, or read again for each row
+  constexpr bool kHeld = THREADS == kNormThreads && VALUES == kNormValues;
+  constexpr bool kShared = VALUES == kFwdLongValues;
   __shared__ float part[2][R][3][32];               // c, A and B of each warp
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t groups = blockDim.x / g_threads, group = threadIdx.x / g_threads;
@@ -165,7 +182,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   // values of this thread, of warp ``lane`` of the group, and of the row
   const float n_t = static_cast<float>(n_mine);
-  const float n_l = lane < g_warps ? warp_share<N>(lane, g_warps, p.cols) : 0.0f;
+  const float n_l = lane < g_warps ? warp_share<N, VALUES>(lane, g_warps, p.cols) : 0.0f;
   const float inv_l = n_l > 0.0f ? 1.0f / n_l : 0.0f;
   const float inv_row = 1.0f / static_cast<float>(p.cols);
   grid_dependency_wait();
@@ -179,6 +196,44 @@ __global__ void __launch_bounds__(THREADS, 1)
       params_or<TP, N>(p.beta, col[k], p.cols, p.wide_params, 0.0f, b[k]);
     }
   }
+  // fp32 copies for every vector of the row, four columns of each of 32 lanes' vectors after
+  // the other, so that a warp reads them without meeting in a bank: gamma, then beta
+  const uint32_t shared_g = smem_u32(staged) + p.shared_params;
+  const uint32_t shared_b = shared_g + g_threads * VALUES * 4u;
+  if (kShared && p.shared_params) {
+    for (uint32_t v = threadIdx.x; v < kItems * g_threads; v += blockDim.x) {
+      float t[2][N];
+      params_or<TP, N>(p.gamma, v * N, p.cols, p.wide_params, 1.0f, t[0]);
+      params_or<TP, N>(p.beta, v * N, p.cols, p.wide_params, 0.0f, t[1]);
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j) {
+        const uint32_t at = ((v / 32u * (N / 4) + j) * 32u + v % 32u) * 16u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          st_shared_v4((h ? shared_b : shared_g) + at, __float_as_uint(t[h][4 * j]),
+                       __float_as_uint(t[h][4 * j + 1]), __float_as_uint(t[h][4 * j + 2]),
+                       __float_as_uint(t[h][4 * j + 3]));
+      }
+    }
+    __syncthreads();
+  }
+  auto params_of = [&](int k, float (&gg)[N], float (&bb)[N]) {   // not held
+    if (kShared && p.shared_params) {
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j) {
+        const uint32_t at = (((k * g_warps + wg) * (N / 4) + j) * 32u + lane) * 16u;
+        const V16 x = ld_shared_v16(shared_g + at), y = ld_shared_v16(shared_b + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          gg[4 * j + i] = __uint_as_float(x.w[i]);
+          bb[4 * j + i] = __uint_as_float(y.w[i]);
+        }
+      }
+    } else {
+      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, gg);
+      params_or<TP, N>(p.beta, col[k], p.cols, p.wide_params, 0.0f, bb);
+    }
+  };
   const uint64_t step = static_cast<uint64_t>(gridDim.x) * groups;
   auto stage = [&](uint64_t row, uint32_t slot) {   // rows row and row + step
 #pragma unroll
@@ -222,8 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < N; ++i) s += v[r][k][i];
       }
       // exact where all values are one (a constant row has variance 0)
-      const float m = n_mine == kNormValues ? s * (1.0f / kNormValues)
-                                            : (n_mine > 0 ? s / n_t : 0.0f);
+      const float m = n_mine == VALUES ? s * (1.0f / VALUES) : (n_mine > 0 ? s / n_t : 0.0f);
       float m2 = 0.0f;
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
@@ -272,23 +326,24 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float m2 = fmaf(-sb, d, sa);   // may round below zero
       rstd[r] = inverse_root((m2 < 0.0f ? 0.0f : m2) * inv_row + p.eps);
     }
+    if (wg == 0u && lane == 0u) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint64_t at = row + r * step;
-      if (at >= p.rows) break;
-      if (wg == 0u && lane == 0u) {
+      for (int r = 0; r < R; ++r) {
+        const uint64_t at = row + r * step;
+        if (at >= p.rows) break;
         if (p.mean) p.mean[at] = mean[r];
         if (p.rstd) p.rstd[at] = rstd[r];
       }
+    }
+    __syncwarp();
 #pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        if constexpr (kHeld) {
-          norm_write<TX, UNAL, KEEP>(p, at, col[k], left[k], v[r][k], mean[r], rstd[r], g[k], b[k]);
-        } else {
-          params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g[0]);
-          params_or<TP, N>(p.beta, col[k], p.cols, p.wide_params, 0.0f, b[0]);
-          norm_write<TX, UNAL, KEEP>(p, at, col[k], left[k], v[r][k], mean[r], rstd[r], g[0], b[0]);
-        }
+    for (int k = 0; k < kItems; ++k) {
+      if constexpr (!kHeld) params_of(k, g[0], b[0]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (row + r * step >= p.rows) break;
+        norm_write<TX, UNAL, KEEP>(p, row + r * step, col[k], left[k], v[r][k], mean[r], rstd[r],
+                                   g[kHeld ? k : 0], b[kHeld ? k : 0]);
       }
     }
   }
@@ -387,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     norm_bwd_kernel(const NormBwdParams p, const uint32_t g_threads) {
   extern __shared__ uint8_t staged[];
   constexpr int N = kVec<TX>, kItems = kNormValues / N;
-  constexpr uint32_t kSlots = kNormSlots<TX, THREADS, 2>;
+  constexpr uint32_t kSlots = kBwdSlots<TX, THREADS>;
   constexpr bool kHeld = THREADS == kNormThreads;   // gamma and the row's values in registers
   __shared__ float part[2][2][32];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;

@@ -57,8 +57,8 @@ constexpr int64_t kNormCols = kNormValues * kNormThreads;
 constexpr int64_t kNormWideCols = kNormValues * kNormWideThreads;
 constexpr uint32_t kLongParts = 64;
 
-// Threads of a group, 16 columns each.
-uint32_t group_threads(int64_t cols) { return round_up((cols + kNormValues - 1) / kNormValues, 32); }
+// Threads of a group, ``values`` columns each.
+uint32_t group_threads(int64_t cols, int values) { return round_up((cols + values - 1) / values, 32); }
 
 constexpr int kMostSmem = 224 * 1024;   // dynamic; the kernels' static share is below 3 KiB
 
@@ -66,9 +66,9 @@ constexpr int kMostSmem = 224 * 1024;   // dynamic; the kernels' static share is
 struct NormGrid {
   uint32_t g_threads, groups, ctas;
 };
-NormGrid norm_grid(int64_t rows, int64_t cols, int threads, int sms) {
+NormGrid norm_grid(int64_t rows, int64_t cols, int values, int threads, int sms) {
   NormGrid g;
-  g.g_threads = group_threads(cols);
+  g.g_threads = group_threads(cols, values);
   g.ctas = static_cast<uint32_t>(rows < sms ? rows : sms);
   const int64_t per_cta = (rows + g.ctas - 1) / g.ctas;
   uint32_t most = threads / g.g_threads;
@@ -115,18 +115,31 @@ cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream) {
     p.cols = static_cast<uint32_t>(l.cols);
     p.blocks = round_up(l.cols, kCkptBlock) / kCkptBlock;
     p.eps = l.eps;
-    auto grouped = [&](auto n) -> cudaError_t {
-      constexpr int kThreads = decltype(n)::value;
-      const NormGrid g = norm_grid(l.rows, l.cols, kThreads, l.sms);
+    p.shared_params = 0;
+    auto grouped = [&](auto n, auto m) -> cudaError_t {
+      constexpr int kThreads = decltype(n)::value, kValues = decltype(m)::value;
+      const NormGrid g = norm_grid(l.rows, l.cols, kValues, kThreads, l.sms);
       const uint32_t threads = g.groups * g.g_threads;
-      const size_t smem = norm_smem<TX, kThreads, 1>(threads / 32);
-      constexpr auto kernel = norm_fwd_kernel<TX, TP, UNAL, KEEP, kThreads>;
+      size_t smem = norm_fwd_smem<TX, kThreads, kValues>(threads / 32);
+      if (kValues == kFwdLongValues && l.cols <= kFwdParamCols) {
+        p.shared_params = static_cast<uint32_t>(smem);
+        smem += 2 * sizeof(float) * static_cast<size_t>(g.g_threads) * kValues;
+      }
+      constexpr auto kernel = norm_fwd_kernel<TX, TP, UNAL, KEEP, kThreads, kValues>;
       cudaError_t e = allow_smem<kernel>(smem);
       if (e != cudaSuccess) return e;
       return launch_pdl(kernel, dim3(g.ctas), threads, smem, stream, p, g.g_threads);
     };
-    if (l.cols <= kNormCols) return grouped(std::integral_constant<int, kNormThreads>());
-    if (l.cols <= kNormWideCols) return grouped(std::integral_constant<int, kNormWideThreads>());
+    constexpr std::integral_constant<int, kNormThreads> kOne;
+    constexpr std::integral_constant<int, kNormWideThreads> kWide;
+    constexpr std::integral_constant<int, kNormValues> kFew;
+    constexpr std::integral_constant<int, kFwdLongValues> kMany;
+    if constexpr (sizeof(TX) == 2)
+      if (l.cols > kFwdLongCols && l.cols <= kNormWideCols &&
+          l.rows * l.cols >= kFwdLongWork * l.sms)
+        return grouped(kOne, kMany);
+    if (l.cols <= kNormCols) return grouped(kOne, kFew);
+    if (l.cols <= kNormWideCols) return grouped(kWide, kFew);
     return launch_pdl(norm_fwd_long_kernel<TX, TP, UNAL, KEEP>,
                       dim3(static_cast<uint32_t>(l.rows)), 1024, 0, stream, p);
   };
@@ -183,9 +196,9 @@ cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
     p.blocks = round_up(l.cols, kCkptBlock) / kCkptBlock;
     auto grouped = [&](auto n) -> cudaError_t {
       constexpr int kThreads = decltype(n)::value;
-      const NormGrid g = norm_grid(l.rows, l.cols, kThreads, l.sms);
+      const NormGrid g = norm_grid(l.rows, l.cols, kNormValues, kThreads, l.sms);
       const uint32_t threads = g.groups * g.g_threads;
-      const size_t smem = norm_smem<TX, kThreads, 2>(threads / 32);
+      const size_t smem = norm_bwd_smem<TX, kThreads>(threads / 32);
       constexpr auto kernel = norm_bwd_kernel<TX, TP, UNAL, KEPT, kThreads>;
       cudaError_t e = allow_smem<kernel>(smem);
       if (e != cudaSuccess) return e;

@@ -296,3 +296,32 @@ def test_nothing_is_written_outside(rows, cols, dtype, offset):
     tg.ckpt8_unpack(kept, DT[dtype], out=out)
     v = train.unpack(kept.q.cpu().numpy(), kept.s.cpu().numpy(), cols)
     assert torch.equal(out.cpu(), torch.from_numpy(v).to(DT[dtype])) and intact(buf)
+
+
+# From 96 Ki values an SM on, 16-bit rows of 2049 to 16384 values go 32 to a thread.
+@pytest.mark.parametrize("dtype,param", [("f16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,cols,pad", [(7400, 2049, 0), (5001, 3001, 3), (3700, 4096, 0),
+                                           (2200, 7000, 8), (1900, 8192, 0), (1830, 8199, 0),
+                                           (950, 16383, 1), (950, 16384, 0)])
+def test_many_long_rows(rows, cols, pad, dtype, param):
+    part, gamma, beta, _ = make(61, cols, dtype, seed=cols)
+    gamma, beta = gamma.to(DT[param]), beta.to(DT[param])
+    at = torch.arange(rows) * 7 % 61                       # row r holds row at[r] of ``part``
+    x = torch.zeros((rows, cols + pad), dtype=DT[dtype], device="cuda")[:, :cols]
+    x.copy_(part[at].cuda())
+    buf = torch.full((rows * cols + 602,), 7.0, dtype=DT[dtype], device="cuda")
+    y = buf[301:-301].view(rows, cols)
+    _, mean, rstd = tg.layer_norm(x, gamma.cuda(), beta.cuda(), out=y)
+    assert (buf[:301] == 7).all() and (buf[-301:] == 7).all()
+    again = tg.layer_norm(x, gamma.cuda(), beta.cuda(), checkpoint=True)
+    first = torch.tensor([(at == r).nonzero()[0].item() for r in range(61)])
+    check_forward(part, gamma, beta, (y[first], mean[first], rstd[first]), dtype)
+    same = first[at].cuda()
+    for got in (y, mean, rstd):
+        assert torch.equal(got, got[same])
+    assert all(torch.equal(a, b) for a, b in zip(again[:3], (y, mean, rstd)))
+    kept = again[3]
+    q, s = train.pack(f64(y[first]))
+    np.testing.assert_array_equal(kept.q[first].cpu().numpy(), q)
+    np.testing.assert_array_equal(kept.s[first].cpu().numpy(), s)
+    assert torch.equal(kept.q, kept.q[same]) and torch.equal(kept.s, kept.s[same])
