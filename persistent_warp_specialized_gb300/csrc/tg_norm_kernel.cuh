@@ -9,10 +9,11 @@
 // Both are bound by memory: a row stays on the SM from its one read to the result's write.
 //
 // Rows go to groups of G threads (G a multiple of 32), 16 values a thread (or 32, below); a CTA, one
-// per SM, holds as many groups as its threads allow.  In the forward pass a group takes two rows a turn: one
-// barrier, and one chain of shuffles, serves both.  Each thread copies its own values of the rows
-// ahead to shared memory (cp.async), so that 64 KiB are on their way to an SM at any time.  Rows of
-// any alignment are read and written in whole 16-byte granules (UNAL, tg_rows.cuh).
+// per SM, holds as many groups as its threads allow.  In the forward pass a group takes two rows a
+// turn: one barrier, and one chain of shuffles, serves both.  Each thread copies its own values of
+// the rows ahead to shared memory (cp.async), so that 64 KiB are on their way to an SM at any time.
+// Rows of any alignment are read and written in whole 16-byte granules (UNAL, tg_rows.cuh).  Rows
+// that a warp holds are left to tg_norm_short_kernel.cuh.
 //
 // The variance: each thread takes the mean of its own values and their squares about that mean
 // (n, m, M2); lanes, and then warps, are joined about the mean c of the first of them,

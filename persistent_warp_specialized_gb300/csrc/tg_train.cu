@@ -8,6 +8,7 @@
 #include "tg_internal.h"
 #include "tg_launch.cuh"
 #include "tg_norm_kernel.cuh"
+#include "tg_norm_short_kernel.cuh"
 
 namespace tg {
 
@@ -56,6 +57,7 @@ cudaError_t with_type(int dtype, F&& f) {
 constexpr int64_t kNormCols = kNormValues * kNormThreads;
 constexpr int64_t kNormWideCols = kNormValues * kNormWideThreads;
 constexpr uint32_t kLongParts = 64;
+constexpr int64_t kShortBytes = 512;   // of a row that a warp holds
 
 // Threads of a group, ``values`` columns each.
 uint32_t group_threads(int64_t cols, int values) { return round_up((cols + values - 1) / values, 32); }
@@ -92,21 +94,39 @@ cudaError_t allow_smem(size_t bytes) {
   return e;
 }
 
+// log2 of the lanes that a short row takes: one vector each, and a checkpoint's block at least.
+template <typename TX>
+uint32_t short_shift(int64_t cols) {
+  uint32_t shift = kVec<TX> == 8 ? 2u : 3u;
+  while ((int64_t(kVec<TX>) << shift) < cols) ++shift;
+  return shift;
+}
+
+// The largest of 16, 4 and the value's size that the bases, row pitches and the row's length are all
+// multiples of (null matrices are zeros): passed to f as a constant.
+template <typename TX, typename F>
+cudaError_t with_access(int64_t cols, const RowsOf& a, const RowsOf& b, const RowsOf& c, F&& f) {
+  uint64_t bits = static_cast<uint64_t>(cols) * sizeof(TX);
+  for (const RowsOf* m : {&a, &b, &c})
+    bits |= reinterpret_cast<uintptr_t>(m->base) | static_cast<uint64_t>(m->pitch);
+  if (bits % 16 == 0) return f(std::integral_constant<int, 16>());
+  if (bits % 4 == 0) return f(std::integral_constant<int, 4>());
+  return f(std::integral_constant<int, static_cast<int>(sizeof(TX))>());
+}
+
 bool wide(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream) {
-  auto run = [&](auto tx, auto tp, auto unal, auto keep) -> cudaError_t {
-    using TX = typename decltype(tx)::type;
-    using TP = typename decltype(tp)::type;
-    constexpr bool UNAL = decltype(unal)::value, KEEP = decltype(keep)::value;
+  auto params = [&](size_t elem) {
     NormFwdParams p;
-    p.x = rows_of(l.x, l.rows, l.cols, l.ld_x, sizeof(TX));
-    p.y = rows_of(l.y, l.rows, l.cols, l.ld_y, sizeof(TX));
+    p.x = rows_of(l.x, l.rows, l.cols, l.ld_x, elem);
+    p.y = rows_of(l.y, l.rows, l.cols, l.ld_y, elem);
     p.gamma = l.gamma;
     p.beta = l.beta;
     p.wide_params = wide(l.gamma) && wide(l.beta) ? 1u : 0u;
+    p.shared_params = 0;
     p.mean = l.mean;
     p.rstd = l.rstd;
     p.q = static_cast<uint8_t*>(l.q);
@@ -115,7 +135,29 @@ cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream) {
     p.cols = static_cast<uint32_t>(l.cols);
     p.blocks = round_up(l.cols, kCkptBlock) / kCkptBlock;
     p.eps = l.eps;
-    p.shared_params = 0;
+    return p;
+  };
+  auto run_short = [&](auto tx, auto tp, auto keep) -> cudaError_t {
+    using TX = typename decltype(tx)::type;
+    using TP = typename decltype(tp)::type;
+    const NormFwdParams p = params(sizeof(TX));
+    const uint32_t shift = short_shift<TX>(l.cols), per_warp = 32u >> shift;
+    const int64_t turns = (l.rows + per_warp - 1) / per_warp;   // of a warp
+    const int64_t most = static_cast<int64_t>(l.sms) * kShortFwdCtas;
+    const int64_t ctas = turns < most ? turns : most, warps = (turns + ctas - 1) / ctas;
+    constexpr int64_t kWarps = kShortFwdThreads / 32;
+    const uint32_t threads = static_cast<uint32_t>(32 * (warps < kWarps ? warps : kWarps));
+    return with_access<TX>(l.cols, p.x, p.y, p.y, [&](auto access) {
+      return launch_pdl(
+          norm_fwd_short_kernel<TX, TP, decltype(keep)::value, decltype(access)::value>,
+          dim3(static_cast<uint32_t>(ctas)), threads, 0, stream, p, shift);
+    });
+  };
+  auto run = [&](auto tx, auto tp, auto unal, auto keep) -> cudaError_t {
+    using TX = typename decltype(tx)::type;
+    using TP = typename decltype(tp)::type;
+    constexpr bool UNAL = decltype(unal)::value, KEEP = decltype(keep)::value;
+    NormFwdParams p = params(sizeof(TX));
     auto grouped = [&](auto n, auto m) -> cudaError_t {
       constexpr int kThreads = decltype(n)::value, kValues = decltype(m)::value;
       const NormGrid g = norm_grid(l.rows, l.cols, kValues, kThreads, l.sms);
@@ -145,6 +187,8 @@ cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream) {
   };
   return with_types(l.dtype, l.param_dtype, [&](auto tx, auto tp) -> cudaError_t {
     constexpr uint32_t kElem = sizeof(typename decltype(tx)::type);
+    if (l.cols * kElem <= kShortBytes)
+      return l.q ? run_short(tx, tp, std::true_type()) : run_short(tx, tp, std::false_type());
     const bool unal = l.cols * kElem % 16 != 0 || !rows_aligned(l.x, l.ld_x, kElem) ||
                       !rows_aligned(l.y, l.ld_y, kElem);
     if (l.q) return unal ? run(tx, tp, std::true_type(), std::true_type())
@@ -175,14 +219,11 @@ int64_t norm_bwd_workspace(int64_t rows, int64_t cols, int sms) {
 cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
   const uint32_t parts = norm_bwd_parts(l.rows, l.cols, l.dtype, l.sms);
   const bool sums = l.dgamma != nullptr || l.dbeta != nullptr;
-  auto rows_pass = [&](auto tx, auto tp, auto unal, auto kept) -> cudaError_t {
-    using TX = typename decltype(tx)::type;
-    using TP = typename decltype(tp)::type;
-    constexpr bool UNAL = decltype(unal)::value, KEPT = decltype(kept)::value;
+  auto params = [&](size_t elem) {
     NormBwdParams p;
-    p.dy = rows_of(l.dy, l.rows, l.cols, l.ld_dy, sizeof(TX));
-    p.dx = rows_of(l.dx, l.rows, l.cols, l.ld_dx, sizeof(TX));
-    p.x = rows_of(l.x, l.rows, l.cols, l.ld_x, sizeof(TX));
+    p.dy = rows_of(l.dy, l.rows, l.cols, l.ld_dy, elem);
+    p.dx = rows_of(l.dx, l.rows, l.cols, l.ld_dx, elem);
+    p.x = rows_of(l.x, l.rows, l.cols, l.x ? l.ld_x : 0, elem);
     p.q = static_cast<const uint8_t*>(l.q);
     p.s = static_cast<const uint8_t*>(l.s);
     p.gamma = l.gamma;
@@ -194,6 +235,28 @@ cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
     p.rows = static_cast<uint32_t>(l.rows);
     p.cols = static_cast<uint32_t>(l.cols);
     p.blocks = round_up(l.cols, kCkptBlock) / kCkptBlock;
+    return p;
+  };
+  auto run_short = [&](auto tx, auto tp, auto kept) -> cudaError_t {
+    using TX = typename decltype(tx)::type;
+    using TP = typename decltype(tp)::type;
+    const NormBwdParams p = params(sizeof(TX));
+    const uint32_t shift = short_shift<TX>(l.cols), per_warp = 32u >> shift;
+    // ``parts`` CTAs, each of as many warps (a power of two) as have rows
+    const int64_t turns = (l.rows + per_warp - 1) / per_warp;
+    uint32_t threads = 32;
+    while (threads < kShortBwdThreads && int64_t(threads / 32) * parts < turns) threads *= 2;
+    return with_access<TX>(l.cols, p.dy, p.dx, p.x, [&](auto access) {
+      return launch_pdl(
+          norm_bwd_short_kernel<TX, TP, decltype(kept)::value, decltype(access)::value>,
+          dim3(parts), threads, 0, stream, p, shift);
+    });
+  };
+  auto rows_pass = [&](auto tx, auto tp, auto unal, auto kept) -> cudaError_t {
+    using TX = typename decltype(tx)::type;
+    using TP = typename decltype(tp)::type;
+    constexpr bool UNAL = decltype(unal)::value, KEPT = decltype(kept)::value;
+    NormBwdParams p = params(sizeof(TX));
     auto grouped = [&](auto n) -> cudaError_t {
       constexpr int kThreads = decltype(n)::value;
       const NormGrid g = norm_grid(l.rows, l.cols, kNormValues, kThreads, l.sms);
@@ -222,7 +285,9 @@ cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
                       !rows_aligned(l.dx, l.ld_dx, kElem) || !rows_aligned(l.x, l.ld_x, kElem);
     cudaError_t e = cudaSuccess;
     if (l.rows > 0) {
-      if (l.x)
+      if (l.cols * kElem <= kShortBytes)
+        e = l.x ? run_short(tx, tp, std::false_type()) : run_short(tx, tp, std::true_type());
+      else if (l.x)
         e = unal ? rows_pass(tx, tp, std::true_type(), std::false_type())
                  : rows_pass(tx, tp, std::false_type(), std::false_type());
       else

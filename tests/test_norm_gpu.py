@@ -325,3 +325,48 @@ def test_many_long_rows(rows, cols, pad, dtype, param):
     np.testing.assert_array_equal(kept.q[first].cpu().numpy(), q)
     np.testing.assert_array_equal(kept.s[first].cpu().numpy(), s)
     assert torch.equal(kept.q, kept.q[same]) and torch.equal(kept.s, kept.s[same])
+
+
+# Rows of at most 512 bytes, several to a warp: full and partial turns, each access width (16 bytes, 4,
+# one value), x and dy with gaps between rows.
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 3, 0), (37, 17, 1), (5003, 20, 0), (4999, 24, 8),
+                                           (5001, 33, 0), (9001, 64, 0), (3001, 90, 2),
+                                           (4003, 128, 0), (2501, 129, 3), (5003, 200, 0),
+                                           (3000, 254, 4), (5003, 256, 0)])
+def test_short_rows(rows, cols, pad, dtype):
+    x, gamma, beta, dy = make(rows, cols, dtype, seed=cols)
+    xd, dyd = (torch.full((rows, cols + pad), 9.0, dtype=DT[dtype], device="cuda")[:, :cols]
+               for _ in range(2))
+    xd.copy_(x.cuda())
+    dyd.copy_(dy.cuda())
+    gd, bd = gamma.cuda(), beta.cuda()
+    buf = torch.full((rows * cols + 600,), 7.0, dtype=DT[dtype], device="cuda")
+    y = buf[300:-300].view(rows, cols)
+    _, mean, rstd = tg.layer_norm(xd, gd, bd, out=y)
+    assert (buf[:300] == 7).all() and (buf[-300:] == 7).all()
+    check_forward(x, gamma, beta, (y, mean, rstd), dtype)
+    y2, mean2, rstd2, kept = tg.layer_norm(xd, gd, bd, checkpoint=True)
+    assert torch.equal(y2, y) and torch.equal(mean2, mean) and torch.equal(rstd2, rstd)
+    q, s = train.pack(f64(y))
+    np.testing.assert_array_equal(kept.s.cpu().numpy(), s)
+    np.testing.assert_array_equal(kept.q.cpu().numpy(), q)
+    grads = tg.layer_norm_backward(dyd, xd, mean, rstd, gd)
+    check_backward(dy, f64(x), mean, rstd, gamma, grads, dtype)
+    again = tg.layer_norm_backward(dyd, xd, mean, rstd, gd)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    kept = tg.ckpt8_pack(xd)
+    grads = tg.layer_norm_backward(dyd, kept, mean, rstd, gd)
+    x64 = train.unpack(kept.q.cpu().numpy(), kept.s.cpu().numpy(), cols)
+    check_backward(dy, x64, mean, rstd, gamma, grads, dtype)
+
+
+def test_what_is_not_finite_stays_in_its_short_row():
+    x, gamma, beta, _ = make(2000, 72, "bf16", seed=9)
+    x[7, 3] = float("nan")
+    x[40, 71] = float("-inf")
+    xd = x.cuda()
+    y, mean, rstd = tg.layer_norm(xd, gamma.cuda(), beta.cuda())
+    fine = [r for r in range(2000) if r not in (7, 40)]
+    assert torch.isnan(y[[7, 40]]).all()
+    check_forward(x[fine], gamma, beta, (y[fine], mean[fine], rstd[fine]), "bf16")
