@@ -65,6 +65,19 @@ constexpr uint32_t norm_bwd_smem(uint32_t warps) {
   return warps * 2 * kBwdSlots<T, THREADS> * (kNormValues / kVec<T>)*kStripBytes;
 }
 
+// How the rows lie.  kWholeRows: in whole 16-byte granules.  kAnyRows: anyhow; vectors are shifted
+// out of two granules when they are read, and shifted back when they are written (tg_rows.cuh).
+// kOneLead: anyhow, but in all the tensors alike, so that row r starts ``lead`` bytes into a granule
+// in each; the rows of a CTA are a multiple of 8 apart and have one lead.  Backward, a thread takes
+// granules instead of vectors: its columns begin lead values earlier, nothing is shifted, and only a
+// row's first and last granule hold values that are not the row's.  (The sums' order, and with it the
+// last bits of dx, then depends on the lead.)  Forward, the statistics are taken over vectors as ever,
+// so that a row gives the same bits wherever it lies, and only y is written in granules; not with a
+// checkpoint, whose blocks lie otherwise.
+// Against kAnyRows, caches cold: forward 8000 x 4099 bf16 51 us instead of 87, 2000 x 4099 fp32 26
+// instead of 36; backward 77 instead of 111, and 34 instead of 48; few rows alike.
+enum Rows : int { kWholeRows, kOneLead, kAnyRows };
+
 struct NormFwdParams {
   RowsOf x, y;
   const void* gamma;   // may be null (ones)
@@ -103,6 +116,40 @@ __device__ __forceinline__ void params_or(const void* p, uint32_t col, uint32_t 
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = none;
+  }
+}
+
+// kOneLead: parameters of columns col + i, skip <= i < left (others: zero).
+template <typename TP, int N>
+__device__ __forceinline__ void params_between(const void* p, int col, int skip, int left, float none,
+                                               float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    v[i] = !p ? none : i >= skip && i < left ? to_f32(static_cast<const TP*>(p)[col + i]) : 0.0f;
+}
+
+// kOneLead: starts the copy of the lane's granule at p to shared memory.  ``inner``: all of it is
+// the row's.
+template <typename T>
+__device__ __forceinline__ void stage_granule(uint32_t dst, const RowsOf& m, const char* p, int left,
+                                              bool inner) {
+  if (inner || (left > 0 && p >= m.base && p + 16 <= m.end)) {
+    cp_async<16>(dst, p);
+  } else if (left > 0) {   // at the matrix's ends
+    const V16 r = load_granule<T>(p, m.base, m.end);
+    st_shared_v4(dst, r.w[0], r.w[1], r.w[2], r.w[3]);
+  }
+}
+
+// kOneLead: stores values skip to left - 1 of the granule at p.
+template <typename T>
+__device__ __forceinline__ void store_between(char* p, const V16& r, int skip, int left, bool inner) {
+  if (inner) {
+    store16(p, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec<T>; ++i)
+      if (i >= skip && i < left) store_one<T>(p, r, i);
   }
 }
 
@@ -155,21 +202,25 @@ __device__ __forceinline__ void norm_write(const NormFwdParams& p, uint64_t row,
 }
 
 // Row r belongs to CTA r % gridDim.x, and its turns there to the groups in turn.
-template <typename TX, typename TP, bool UNAL, bool KEEP, int THREADS, int VALUES>
+template <typename TX, typename TP, int ROWS, bool KEEP, int THREADS, int VALUES>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_fwd_kernel(const NormFwdParams p, const uint32_t g_threads) {
   extern __shared__ uint8_t staged[];
   constexpr int N = kVec<TX>, kItems = VALUES / N, R = kFwdRows<THREADS>;
+  constexpr bool LEAD = ROWS == kOneLead, UNAL = ROWS == kAnyRows || LEAD;
   constexpr uint32_t kSlots = kFwdSlots<TX, THREADS, VALUES>;
   // parameters in registers, or in shared memory, or read again for each row
   constexpr bool kHeld = THREADS == kNormThreads && VALUES == kNormValues;
   constexpr bool kShared = VALUES == kFwdLongValues;
+  static_assert(!LEAD || (THREADS == kNormThreads && !KEEP));
   __shared__ float part[2][R][3][32];               // c, A and B of each warp
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t groups = blockDim.x / g_threads, group = threadIdx.x / g_threads;
   const uint32_t g_warps = g_threads >> 5, wg = warp - group * g_warps;
   const int64_t row_bytes = static_cast<int64_t>(p.cols) * static_cast<int>(sizeof(TX));
   const uint32_t mine = smem_u32(staged) + warp * (kSlots * R * kItems * kStripBytes);
+  // The statistics are always taken over vectors from the row's start, shifted out of their granules,
+  // so that a row's have the same bits wherever it lies.
   uint32_t col[kItems];
   int left[kItems], n_mine = 0;
   bool inner[kItems];
@@ -181,6 +232,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     inner[k] = inner_vector<UNAL>(v * 16u, row_bytes);
     n_mine += left[k] > 0 ? left[k] : 0;
   }
+  // kOneLead: y is written in granules, the thread's k-th of which holds columns col[k] - lead_n on
+  const uint32_t lead =
+      UNAL ? lead_of(p.x.base + static_cast<int64_t>(blockIdx.x) * p.x.pitch) : 0u;
+  const int lead_n = static_cast<int>(lead / sizeof(TX));
+  const int skip_0 = wg == 0u && lane == 0u ? lead_n : 0;
+  auto skip = [=](int k) { return k == 0 ? skip_0 : 0; };   // values before the row's first
+  auto end = [&](int k) { return values_left<N>(col[k] / N, p.cols + lead_n); };
   // values of this thread, of warp ``lane`` of the group, and of the row
   const float n_t = static_cast<float>(n_mine);
   const float n_l = lane < g_warps ? warp_share<N, VALUES>(lane, g_warps, p.cols) : 0.0f;
@@ -193,8 +251,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   if constexpr (kHeld) {
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g[k]);
-      params_or<TP, N>(p.beta, col[k], p.cols, p.wide_params, 0.0f, b[k]);
+      if constexpr (LEAD) {
+        const int at = static_cast<int>(col[k]) - lead_n;
+        params_between<TP, N>(p.gamma, at, skip(k), end(k), 1.0f, g[k]);
+        params_between<TP, N>(p.beta, at, skip(k), end(k), 0.0f, b[k]);
+      } else {
+        params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, g[k]);
+        params_or<TP, N>(p.beta, col[k], p.cols, p.wide_params, 0.0f, b[k]);
+      }
     }
   }
   // fp32 copies for every vector of the row, four columns of each of 32 lanes' vectors after
@@ -204,8 +268,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (kShared && p.shared_params) {
     for (uint32_t v = threadIdx.x; v < kItems * g_threads; v += blockDim.x) {
       float t[2][N];
-      params_or<TP, N>(p.gamma, v * N, p.cols, p.wide_params, 1.0f, t[0]);
-      params_or<TP, N>(p.beta, v * N, p.cols, p.wide_params, 0.0f, t[1]);
+      if constexpr (LEAD) {
+        const int at = static_cast<int>(v * N) - lead_n, n = values_left<N>(v, p.cols + lead_n);
+        params_between<TP, N>(p.gamma, at, v == 0u ? lead_n : 0, n, 1.0f, t[0]);
+        params_between<TP, N>(p.beta, at, v == 0u ? lead_n : 0, n, 0.0f, t[1]);
+      } else {
+        params_or<TP, N>(p.gamma, v * N, p.cols, p.wide_params, 1.0f, t[0]);
+        params_or<TP, N>(p.beta, v * N, p.cols, p.wide_params, 0.0f, t[1]);
+      }
 #pragma unroll
       for (int j = 0; j < N / 4; ++j) {
         const uint32_t at = ((v / 32u * (N / 4) + j) * 32u + v % 32u) * 16u;
@@ -263,14 +333,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     float v[R][kItems][N], c[R], ab[2 * R];   // ab: A and B of each row
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint32_t lead =
-          UNAL ? lead_of(p.x.base + static_cast<int64_t>(row + r * step) * p.x.pitch) : 0u;
       float s = 0.0f;
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
         values<TX>(staged_vector<TX, UNAL>(mine + ((slot * R + r) * kItems + k) * kStripBytes, lead),
                    v[r][k]);
-        if constexpr (UNAL) {
+        if (UNAL && left[k] < N) {
 #pragma unroll
           for (int i = 0; i < N; ++i) v[r][k][i] = i < left[k] ? v[r][k][i] : 0.0f;
         }
@@ -283,20 +351,22 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
         float q = 0.0f;
+        if (UNAL && left[k] < N) {   // what is not the row's deviates by nothing
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[r][k][i] = i < left[k] ? v[r][k][i] : m;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float d = !UNAL || i < left[k] ? v[r][k][i] - m : 0.0f;
+          const float d = v[r][k][i] - m;
           q = fmaf(d, d, q);
         }
-        m2 += UNAL || left[k] > 0 ? q : 0.0f;
+        m2 += left[k] > 0 ? q : 0.0f;
       }
       c[r] = __shfl_sync(0xffffffffu, m, 0);   // lane 0 holds values wherever its warp holds any
       const float d = n_mine > 0 ? m - c[r] : 0.0f;
       ab[2 * r + 1] = n_t * d;
       ab[2 * r] = fmaf(ab[2 * r + 1], d, m2);
     }
-    __syncwarp();   // every lane has read the slot before it is filled again
-    slot = slot + 1u == kSlots ? 0u : slot + 1u;
     float sums = warp_sums(ab);
     if (g_warps > 1u) {
       if (lane % (16 / R) == 0u) part[turn & 1u][lane / (32 / R)][1 + lane / (16 / R) % 2][warp] = sums;
@@ -343,10 +413,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (row + r * step >= p.rows) break;
-        norm_write<TX, UNAL, KEEP>(p, row + r * step, col[k], left[k], v[r][k], mean[r], rstd[r],
-                                   g[kHeld ? k : 0], b[kHeld ? k : 0]);
+        if constexpr (LEAD) {
+          float o[N];
+          values<TX>(ld_shared_v16(mine + ((slot * R + r) * kItems + k) * kStripBytes + lane * 16u),
+                     o);
+#pragma unroll
+          for (int i = 0; i < N; ++i) o[i] = fmaf((o[i] - mean[r]) * rstd[r], g[kHeld ? k : 0][i], b[kHeld ? k : 0][i]);
+          const int n = end(k);
+          store_between<TX>(p.y.base + static_cast<int64_t>(row + r * step) * p.y.pitch - lead +
+                                col[k] * static_cast<uint32_t>(sizeof(TX)),
+                            rounded<TX>(o), skip(k), n, n == N && skip(k) == 0);
+        } else {
+          norm_write<TX, UNAL, KEEP>(p, row + r * step, col[k], left[k], v[r][k], mean[r], rstd[r],
+                                     g[kHeld ? k : 0], b[kHeld ? k : 0]);
+        }
       }
     }
+    __syncwarp();   // every lane has read the slot before it is filled again
+    slot = slot + 1u == kSlots ? 0u : slot + 1u;
   }
   cp_async_wait<0>();
 }
@@ -409,7 +493,7 @@ struct NormBwdParams {
   const float* mean;
   const float* rstd;
   float* partials;       // [parts][2][part_cols] sums of dy xh and of dy; null: not wanted
-  uint32_t part_cols;    // cols rounded up to 4
+  uint32_t part_cols;    // a multiple of 32, at least cols (kOneLead: and the largest lead)
   uint32_t rows, cols, blocks;
 };
 
@@ -438,12 +522,13 @@ __device__ __forceinline__ void x_values(const NormBwdParams& p, uint32_t row, u
 // partial sums, and norm_bwd_join_kernel adds those in a fixed order, so the result does not depend
 // on timing.  A staged strip of a checkpoint holds N bytes a lane; scales, like the statistics, are
 // read into registers a row ahead.
-template <typename TX, typename TP, bool UNAL, bool KEPT, int THREADS>
+template <typename TX, typename TP, int ROWS, bool KEPT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
     norm_bwd_kernel(const NormBwdParams p, const uint32_t g_threads) {
   extern __shared__ uint8_t staged[];
   constexpr int N = kVec<TX>, kItems = kNormValues / N;
   constexpr uint32_t kSlots = kBwdSlots<TX, THREADS>;
+  constexpr bool UNAL = ROWS == kAnyRows, LEAD = ROWS == kOneLead;
   constexpr bool kHeld = THREADS == kNormThreads;   // gamma and the row's values in registers
   __shared__ float part[2][2][32];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -453,15 +538,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   // per warp and slot: kItems strips of dy, then of x
   const uint32_t mine = smem_u32(staged) + warp * (kSlots * 2 * kItems * kStripBytes);
   const float inv_cols = 1.0f / static_cast<float>(p.cols);
-  uint32_t col[kItems];
+  static_assert(!LEAD || (kHeld && !KEPT));
+  const uint32_t lead =   // kOneLead: bytes, and values
+      LEAD ? lead_of(p.dy.base + static_cast<int64_t>(blockIdx.x) * p.dy.pitch) : 0u;
+  const int lead_n = static_cast<int>(lead / sizeof(TX));
+  uint32_t col[kItems];   // kOneLead: counted from the row's first granule
   int left[kItems];
   bool inner[kItems];
+  const int skip_0 = wg == 0u && lane == 0u ? lead_n : 0;
+  auto skip = [=](int k) { return k == 0 ? skip_0 : 0; };   // values before the row's first
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const uint32_t v = (k * g_warps + wg) * 32u + lane;
     col[k] = v * N;
-    left[k] = values_left<N>(v, p.cols);
-    inner[k] = inner_vector<UNAL>(v * 16u, row_bytes);
+    left[k] = values_left<N>(v, p.cols + lead_n);
+    inner[k] = LEAD ? left[k] == N && skip(k) == 0 : inner_vector<UNAL>(v * 16u, row_bytes);
   }
   grid_dependency_wait();
   grid_launch_dependents();
@@ -469,8 +560,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   float held_g[kHeld ? kItems : 1][N];
   if constexpr (kHeld) {
 #pragma unroll
-    for (int k = 0; k < kItems; ++k)
-      params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, held_g[k]);
+    for (int k = 0; k < kItems; ++k) {
+      if constexpr (LEAD)
+        params_between<TP, N>(p.gamma, static_cast<int>(col[k]) - lead_n, skip(k), left[k], 1.0f,
+                              held_g[k]);
+      else
+        params_or<TP, N>(p.gamma, col[k], p.cols, p.wide_params, 1.0f, held_g[k]);
+    }
   }
   auto gamma_at = [&](int k, float (&g)[N]) {
     if constexpr (kHeld) {
@@ -488,14 +584,21 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
         const uint32_t byte = col[k] * static_cast<uint32_t>(sizeof(TX));
-        stage_vector<TX, UNAL>(at + k * kStripBytes, p.dy, dy, byte, row_bytes, inner[k]);
+        if constexpr (LEAD)
+          stage_granule<TX>(at + k * kStripBytes + lane * 16u, p.dy, dy - lead + byte, left[k],
+                            inner[k]);
+        else
+          stage_vector<TX, UNAL>(at + k * kStripBytes, p.dy, dy, byte, row_bytes, inner[k]);
         const uint32_t xs = at + (kItems + k) * kStripBytes;
         if constexpr (KEPT) {
           if (left[k] > 0)
             cp_async<N>(xs + lane * N, p.q + row * p.blocks * kCkptBlock + col[k]);
         } else {
-          stage_vector<TX, UNAL>(xs, p.x, p.x.base + static_cast<int64_t>(row) * p.x.pitch, byte,
-                                 row_bytes, inner[k]);
+          const char* x = p.x.base + static_cast<int64_t>(row) * p.x.pitch;
+          if constexpr (LEAD)
+            stage_granule<TX>(xs + lane * 16u, p.x, x - lead + byte, left[k], inner[k]);
+          else
+            stage_vector<TX, UNAL>(xs, p.x, x, byte, row_bytes, inner[k]);
         }
       }
     }
@@ -531,11 +634,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int i = 0; i < N; ++i) xh[i] = (xh[i] - mean) * rstd;
     }
-    if constexpr (UNAL) {
+    if (UNAL || (LEAD && !inner[k])) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        dy[i] = i < left[k] ? dy[i] : 0.0f;
-        xh[i] = i < left[k] ? xh[i] : 0.0f;
+        dy[i] = i >= skip(k) && i < left[k] ? dy[i] : 0.0f;
+        xh[i] = i >= skip(k) && i < left[k] ? xh[i] : 0.0f;
       }
     }
   };
@@ -614,8 +717,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int i = 0; i < N; ++i) dx[i] = fmaf(-xh[i], c2, fmaf(dx[i] * g[i], rstd, -c1));
       }
-      store_vector<TX, UNAL>(out, static_cast<int64_t>(col[k]) * static_cast<int>(sizeof(TX)),
-                             rounded<TX>(dx), left[k]);
+      const int64_t byte = static_cast<int64_t>(col[k]) * static_cast<int>(sizeof(TX));
+      if constexpr (LEAD)
+        store_between<TX>(out - lead + byte, rounded<TX>(dx), skip(k), left[k], inner[k]);
+      else
+        store_vector<TX, UNAL>(out, byte, rounded<TX>(dx), left[k]);
     }
     __syncwarp();   // every lane has read the slot before it is filled again
     slot = slot + 1u == kSlots ? 0u : slot + 1u;
@@ -628,6 +734,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (p.partials == nullptr) return;
   float* out = p.partials + static_cast<uint64_t>(blockIdx.x) * 2u * p.part_cols;
   float* sums = reinterpret_cast<float*>(staged);   // [2][part_cols], once staging is over
+  // kOneLead: columns counted from the first granule here too; the join knows each CTA's lead
   if (groups > 1u) __syncthreads();
   for (uint32_t g = 0; g < groups; ++g) {           // the groups add up one by one
     if (group == g) {
@@ -751,10 +858,12 @@ __global__ void __launch_bounds__(128) norm_bwd_cols_kernel(const NormBwdParams 
 
 // dgamma and dbeta from ``parts`` rows of partial sums (none: zeros).  A block takes 32 columns of
 // one of the two; warp w adds rows w, w + 8, ..., then the eight warps' sums are added in order.
+// Row i's columns begin (first + i * apart) % 16 / size values in (kOneLead; else first = apart = 0).
 template <typename TP>
 __global__ void __launch_bounds__(256)
     norm_bwd_join_kernel(const float* __restrict__ partials, uint32_t parts, uint32_t part_cols,
-                         uint32_t cols, TP* __restrict__ dgamma, TP* __restrict__ dbeta) {
+                         uint32_t cols, uint32_t first, uint32_t apart, uint32_t size_log2,
+                         TP* __restrict__ dgamma, TP* __restrict__ dbeta) {
   __shared__ float sums[8][32];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -764,7 +873,9 @@ __global__ void __launch_bounds__(256)
   if (out == nullptr) return;
   float a = 0.0f;
   if (col < cols) {
-    const float* src = partials + static_cast<uint64_t>(blockIdx.y) * part_cols + col;
+    // the same for a warp's rows, 8 apart
+    const uint32_t lead = (first + warp * apart) % 16u >> size_log2;
+    const float* src = partials + static_cast<uint64_t>(blockIdx.y) * part_cols + col + lead;
 #pragma unroll 8
     for (uint32_t i = warp; i < parts; i += 8u) a += src[static_cast<uint64_t>(i) * 2u * part_cols];
   }

@@ -114,6 +114,16 @@ cudaError_t with_access(int64_t cols, const RowsOf& a, const RowsOf& b, const Ro
   return f(std::integral_constant<int, static_cast<int>(sizeof(TX))>());
 }
 
+// kOneLead: every row starts as far into a granule in ``b`` as in ``a``.  The rows of a CTA are a
+// multiple of the grid apart; where that is a multiple of 8 they start alike.
+bool one_lead(const RowsOf& a, const RowsOf& b) {
+  return (reinterpret_cast<uintptr_t>(a.base) - reinterpret_cast<uintptr_t>(b.base)) % 16 == 0 &&
+         (a.pitch - b.pitch) % 16 == 0;
+}
+
+// Columns of a row of partial sums, in whole 128-byte lines; those of a lead, at most 7, come before.
+uint32_t part_cols(int64_t cols, bool lead) { return round_up(cols + (lead ? 7 : 0), 32); }
+
 bool wide(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
@@ -158,30 +168,40 @@ cudaError_t launch_norm_fwd(const NormLaunch& l, cudaStream_t stream) {
     using TP = typename decltype(tp)::type;
     constexpr bool UNAL = decltype(unal)::value, KEEP = decltype(keep)::value;
     NormFwdParams p = params(sizeof(TX));
-    auto grouped = [&](auto n, auto m) -> cudaError_t {
+    auto grouped = [&](auto lie, auto n, auto m) -> cudaError_t {
       constexpr int kThreads = decltype(n)::value, kValues = decltype(m)::value;
-      const NormGrid g = norm_grid(l.rows, l.cols, kValues, kThreads, l.sms);
+      const NormGrid g = norm_grid(l.rows, l.cols, kValues, kThreads, UNAL ? l.sms & ~7 : l.sms);
       const uint32_t threads = g.groups * g.g_threads;
       size_t smem = norm_fwd_smem<TX, kThreads, kValues>(threads / 32);
       if (kValues == kFwdLongValues && l.cols <= kFwdParamCols) {
         p.shared_params = static_cast<uint32_t>(smem);
         smem += 2 * sizeof(float) * static_cast<size_t>(g.g_threads) * kValues;
       }
-      constexpr auto kernel = norm_fwd_kernel<TX, TP, UNAL, KEEP, kThreads, kValues>;
+      constexpr auto kernel =
+          norm_fwd_kernel<TX, TP, decltype(lie)::value, KEEP, kThreads, kValues>;
       cudaError_t e = allow_smem<kernel>(smem);
       if (e != cudaSuccess) return e;
       return launch_pdl(kernel, dim3(g.ctas), threads, smem, stream, p, g.g_threads);
     };
+    constexpr std::integral_constant<int, UNAL ? kAnyRows : kWholeRows> kLie;
     constexpr std::integral_constant<int, kNormThreads> kOne;
     constexpr std::integral_constant<int, kNormWideThreads> kWide;
-    constexpr std::integral_constant<int, kNormValues> kFew;
-    constexpr std::integral_constant<int, kFwdLongValues> kMany;
+    // kOneLead where a row's last granule is still the group's
+    auto held = [&](auto m) -> cudaError_t {
+      constexpr int kValues = decltype(m)::value;
+      if constexpr (UNAL && !KEEP)
+        if (l.cols <= kNormCols && one_lead(p.x, p.y) &&
+            group_threads(l.cols + kVec<TX> - 1, kValues) == group_threads(l.cols, kValues))
+          return grouped(std::integral_constant<int, kOneLead>(), kOne, m);
+      return grouped(kLie, kOne, m);
+    };
     if constexpr (sizeof(TX) == 2)
       if (l.cols > kFwdLongCols && l.cols <= kNormWideCols &&
           l.rows * l.cols >= kFwdLongWork * l.sms)
-        return grouped(kOne, kMany);
-    if (l.cols <= kNormCols) return grouped(kOne, kFew);
-    if (l.cols <= kNormWideCols) return grouped(kWide, kFew);
+        return held(std::integral_constant<int, kFwdLongValues>());
+    constexpr std::integral_constant<int, kNormValues> kFew;
+    if (l.cols <= kNormCols) return held(kFew);
+    if (l.cols <= kNormWideCols) return grouped(kLie, kWide, kFew);
     return launch_pdl(norm_fwd_long_kernel<TX, TP, UNAL, KEEP>,
                       dim3(static_cast<uint32_t>(l.rows)), 1024, 0, stream, p);
   };
@@ -213,12 +233,14 @@ uint32_t norm_bwd_parts(int64_t rows, int64_t cols, int dtype, int sms) {
 int64_t norm_bwd_workspace(int64_t rows, int64_t cols, int sms) {
   const uint32_t a = norm_bwd_parts(rows, cols, TG_F32, sms);
   const uint32_t b = norm_bwd_parts(rows, cols, TG_F16, sms);
-  return static_cast<int64_t>(a > b ? a : b) * 2 * round_up(cols, 4) * 4;
+  return static_cast<int64_t>(a > b ? a : b) * 2 * part_cols(cols, true) * 4;
 }
 
 cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
   const uint32_t parts = norm_bwd_parts(l.rows, l.cols, l.dtype, l.sms);
   const bool sums = l.dgamma != nullptr || l.dbeta != nullptr;
+  uint32_t first = 0, apart = 0;   // kOneLead: of the rows
+  uint32_t columns = part_cols(l.cols, false);
   auto params = [&](size_t elem) {
     NormBwdParams p;
     p.dy = rows_of(l.dy, l.rows, l.cols, l.ld_dy, elem);
@@ -231,7 +253,7 @@ cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
     p.mean = l.mean;
     p.rstd = l.rstd;
     p.partials = sums ? l.partials : nullptr;
-    p.part_cols = round_up(l.cols, 4);
+    p.part_cols = part_cols(l.cols, false);
     p.rows = static_cast<uint32_t>(l.rows);
     p.cols = static_cast<uint32_t>(l.cols);
     p.blocks = round_up(l.cols, kCkptBlock) / kCkptBlock;
@@ -258,15 +280,30 @@ cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
     constexpr bool UNAL = decltype(unal)::value, KEPT = decltype(kept)::value;
     NormBwdParams p = params(sizeof(TX));
     auto grouped = [&](auto n) -> cudaError_t {
-      constexpr int kThreads = decltype(n)::value;
+      constexpr int kThreads = decltype(n)::value, kRows = UNAL ? kAnyRows : kWholeRows;
       const NormGrid g = norm_grid(l.rows, l.cols, kNormValues, kThreads, l.sms);
       const uint32_t threads = g.groups * g.g_threads;
       const size_t smem = norm_bwd_smem<TX, kThreads>(threads / 32);
-      constexpr auto kernel = norm_bwd_kernel<TX, TP, UNAL, KEPT, kThreads>;
+      constexpr auto kernel = norm_bwd_kernel<TX, TP, kRows, KEPT, kThreads>;
       cudaError_t e = allow_smem<kernel>(smem);
       if (e != cudaSuccess) return e;
       return launch_pdl(kernel, dim3(g.ctas), threads, smem, stream, p, g.g_threads);
     };
+    if constexpr (UNAL && !KEPT)
+      if (l.cols + kVec<TX> - 1 <= kNormCols && one_lead(p.dy, p.x) && one_lead(p.dy, p.dx) &&
+          (l.rows <= l.sms || l.sms % 8 == 0)) {
+        first = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.dy.base) % 16);
+        apart = static_cast<uint32_t>(p.dy.pitch % 16);
+        p.part_cols = columns = part_cols(l.cols, true);
+        const NormGrid g =
+            norm_grid(l.rows, l.cols + kVec<TX> - 1, kNormValues, kNormThreads, l.sms);
+        const uint32_t threads = g.groups * g.g_threads;
+        const size_t smem = norm_bwd_smem<TX, kNormThreads>(threads / 32);
+        constexpr auto kernel = norm_bwd_kernel<TX, TP, kOneLead, KEPT, kNormThreads>;
+        cudaError_t e = allow_smem<kernel>(smem);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3(g.ctas), threads, smem, stream, p, g.g_threads);
+      }
     if (l.cols <= kNormCols) return grouped(std::integral_constant<int, kNormThreads>());
     if constexpr (sizeof(TX) == 2)
       if (l.cols <= kNormWideCols)
@@ -297,9 +334,9 @@ cudaError_t launch_norm_bwd(const NormBwdLaunch& l, cudaStream_t stream) {
     if (e != cudaSuccess || !sums) return e;
     const dim3 grid(round_up(l.cols, 32) / 32, 2);
     return launch_pdl(norm_bwd_join_kernel<TP>, grid, 256, 0, stream,
-                      static_cast<const float*>(l.partials), parts, round_up(l.cols, 4),
-                      static_cast<uint32_t>(l.cols), static_cast<TP*>(l.dgamma),
-                      static_cast<TP*>(l.dbeta));
+                      static_cast<const float*>(l.partials), parts, columns,
+                      static_cast<uint32_t>(l.cols), first, apart, kElem == 4 ? 2u : 1u,
+                      static_cast<TP*>(l.dgamma), static_cast<TP*>(l.dbeta));
   });
 }
 

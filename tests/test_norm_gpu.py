@@ -370,3 +370,45 @@ def test_what_is_not_finite_stays_in_its_short_row():
     fine = [r for r in range(2000) if r not in (7, 40)]
     assert torch.isnan(y[[7, 40]]).all()
     check_forward(x[fine], gamma, beta, (y[fine], mean[fine], rstd[fine]), "bf16")
+
+
+# Rows that start inside a 16-byte granule, equally in all tensors; every tensor inside a larger
+# buffer whose other values (NaN among the inputs, 7 among the outputs) must not matter and stay.
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad,offset", [(1, 301, 0, 1), (3, 1023, 0, 0), (700, 517, 0, 3),
+                                                  (1001, 2047, 0, 0), (2003, 1030, 3, 5),
+                                                  (153, 4099, 0, 7), (500, 7001, 1, 2),
+                                                  (305, 8185, 0, 1), (5003, 264, 1, 0)])
+def test_rows_with_one_lead(rows, cols, pad, offset, dtype):
+    x, gamma, beta, dy = make(rows, cols, dtype, seed=cols)
+    ld, n = cols + pad, rows * (cols + pad)
+
+    def inside(t, fill):
+        buf = torch.full((n + 64 + offset,), fill, dtype=DT[dtype], device="cuda")
+        m = buf[32 + offset:32 + offset + n].view(rows, ld)[:, :cols]
+        if t is not None:
+            m.copy_(t.cuda())
+        return buf, m
+
+    def intact(buf):
+        gaps = buf[32 + offset:32 + offset + n].view(rows, ld)[:, cols:]
+        return all((v == 7).all() for v in (buf[:32 + offset], buf[32 + offset + n:], gaps))
+
+    gd, bd = gamma.cuda(), beta.cuda()
+    xd, dyd = inside(x, float("nan"))[1], inside(dy, float("nan"))[1]
+    buf, y = inside(None, 7.0)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    tg.tg_layernorm_fwd(xd, gd, bd, y, mean, rstd, None, None, rows, cols, ld, ld, dtype)
+    check_forward(x, gamma, beta, (y, mean, rstd), dtype)
+    assert intact(buf)
+    ws = torch.empty(tg.tg_layernorm_bwd_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    grads = []
+    for _ in range(2):
+        buf, dx = inside(None, 7.0)
+        dgamma, dbeta = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+        tg.tg_layernorm_bwd(dyd, xd, None, None, gd, mean, rstd, dx, dgamma, dbeta, rows, cols, ld,
+                            ld, ld, dtype, "f32", ws)
+        check_backward(dy, f64(x), mean, rstd, gamma, (dx, dgamma, dbeta), dtype)
+        assert intact(buf)
+        grads.append((dx, dgamma, dbeta))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
