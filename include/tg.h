@@ -428,10 +428,10 @@ int tg_ckpt8_unpack(const void* q_dev, const void* s_dev, void* out_dev, int64_t
  *   exact, sums fp32, and each result is rounded once.  outs, ld_dy and ld_dw are multiples of 8;
  *   q, dY and dW are 16-byte aligned; rows and cols are any.  rows == 0: dW is zero-filled.
  *   cols == 0 or outs == 0: nothing is done.
- * One CTA pair per 256 x 256 tile of dW, persistent.  When the tiles do not fill the device, the
- * rows are split into ranges whose fp32 sums go through workspace_dev (256-byte aligned,
- * tg_ckpt8_wgrad_workspace_bytes bytes, in use until the call's work is done; NULL if that is 0)
- * and are added in a fixed order.
+ * One CTA pair per tile of dW, persistent; tiles are 256 x 256 or 256 x 512, whichever is expected to
+ * take less time.  When the tiles do not fill the device, the rows may be split into ranges whose
+ * fp32 sums go through workspace_dev (256-byte aligned, tg_ckpt8_wgrad_workspace_bytes bytes, in use
+ * until the call's work is done; NULL if that is 0) and are added in a fixed order.
  */
 int tg_ckpt8_wgrad(const void* q_dev, const void* s_dev, const void* dY_dev, void* dW_dev,
                    int64_t rows, int64_t cols, int64_t outs, int64_t ld_dy, int64_t ld_dw,

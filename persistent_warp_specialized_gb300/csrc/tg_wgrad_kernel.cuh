@@ -16,9 +16,11 @@
 // to the even CTA's ``made`` barrier (there also for the dY bytes of both CTAs), which the MMA
 // thread waits for.
 //
-// What bounds it, at 8192^3 with two N-halves: shared memory and the MMA thread's hand-over.  The
-// MMAs of a k-block take 1024 cycles; with the widening left out (in a copy) the kernel ran at the
-// dense GEMM's 1980 TFLOP/s, its reads and writes of 8 + 16 KiB a k-block cost 12 %.
+// What bounds it: with two N-halves the tensor pipe and the power cap, 8192^3 at 1882 to 1971 TFLOP/s
+// (the dense GEMM reaches 1980); the MMAs of a k-block take 1024 cycles, and the widening's reads and
+// writes of 8 + 16 KiB go on behind them.  With one N-half shared memory: a k-block moves about 656
+// wavefronts for 512 cycles of MMAs (32768 x 1000 x 512, 37 us).
+//
 // Few tiles: the tokens are split into ``splits`` ranges, (tile, range) units write fp32 partial
 // sums to a workspace [splits][m_blocks * 256][outs], and wgrad_join_kernel adds them in order.
 //
