@@ -382,7 +382,8 @@ int tg_gemm_mxfp8_debug(const void* A_dev, const void* SFA_dev, const void* B_de
  *   x_dev, y_dev: [rows, cols] of ``dtype`` (TG_F16, TG_BF16 or TG_F32).  gamma_dev, beta_dev:
  *   [cols] of ``param_dtype`` (TG_F32 or dtype); NULL: ones, zeros.  mean_dev, rstd_dev: [rows]
  *   fp32, either may be NULL.  yq_dev, ys_dev: NULL, or a checkpoint of the rounded y, made in the
- *   same pass.  rows == 0 or cols == 0: nothing is done.  A row with a NaN or an infinity gives NaN.
+ *   same pass.  rows == 0: nothing is done.  cols == 0: mean and rstd are NaN.  A row with a NaN or
+ *   an infinity gives NaN.
  */
 int tg_layernorm_fwd(const void* x_dev, const void* gamma_dev, const void* beta_dev, void* y_dev,
                      float* mean_dev, float* rstd_dev, void* yq_dev, void* ys_dev, int64_t rows,

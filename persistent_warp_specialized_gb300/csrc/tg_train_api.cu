@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/tg.h"
 #include "tg_api_common.h"
@@ -279,8 +280,19 @@ int tg_layernorm_fwd(const void* x_dev, const void* gamma_dev, const void* beta_
   if (!(eps >= 0.0f)) return fail(TG_ERR_ARG, "eps must not be negative");
   if ((yq_dev == nullptr) != (ys_dev == nullptr))
     return fail(TG_ERR_ARG, "a checkpoint of y needs both yq and ys");
-  if (rows == 0 || cols == 0) return TG_OK;
+  if (rows == 0) return TG_OK;
   const uint64_t e = elem_bytes(dtype), pe = elem_bytes(param_dtype), kb = kept_blocks(cols);
+  const uint64_t stat = 4 * static_cast<uint64_t>(rows), param = pe * cols;
+  if (cols == 0) {   // the mean of no values: 0 / 0
+    for (float* out : {mean_dev, rstd_dev}) {
+      if (!out) continue;
+      TG_TRY(check_array(out, 4, out == mean_dev ? "mean" : "rstd"));
+      const cudaError_t err =   // every byte 255: NaN
+          cudaMemsetAsync(out, 0xFF, stat, static_cast<cudaStream_t>(stream));
+      if (err != cudaSuccess) return fail_cuda("filling the statistics", err);
+    }
+    return TG_OK;
+  }
   TG_TRY(check_array(x_dev, e, "x"));
   TG_TRY(check_array(y_dev, e, "y"));
   TG_TRY(check_optional(gamma_dev, pe, "gamma"));
@@ -289,7 +301,6 @@ int tg_layernorm_fwd(const void* x_dev, const void* gamma_dev, const void* beta_
   TG_TRY(check_optional(rstd_dev, 4, "rstd"));
   TG_TRY(check_optional(yq_dev, 16, "yq"));
   TG_TRY(check_optional(ys_dev, 1, "ys"));
-  const uint64_t stat = 4 * static_cast<uint64_t>(rows), param = pe * cols;
   const Region r[] = {{y_dev, span(rows, cols, ld_y, e), "y"},
                       {mean_dev, stat, "mean"},
                       {rstd_dev, stat, "rstd"},
