@@ -610,8 +610,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int k = 0; k < kItems; ++k)
       to[k] = KEPT && left[k] > 0 ? p.s[row * p.blocks + col[k] / kCkptBlock] : 127u;
   };
-  // the lane's dy and xh of its k-th vector, from the row's slot; past the row's end dy is zero, and
-  // xh a number
+  // the lane's dy and xh of its k-th vector, from the row's slot; past the row's end both are
+  // zero (!kHeld and kWholeRows: dy alone)
   auto values_at = [&](uint64_t row, uint32_t slot, int k, float mean, float rstd, float (&dy)[N],
                        float (&xh)[N]) {
     const uint32_t at = mine + slot * (2 * kItems * kStripBytes);
@@ -619,20 +619,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         UNAL ? lead_of(p.dy.base + static_cast<int64_t>(row) * p.dy.pitch) : 0u;
     values<TX>(staged_vector<TX, UNAL>(at + k * kStripBytes, lead_dy), dy);
     const uint32_t xs = at + (kItems + k) * kStripBytes;
+    // A lane past the row's end has zeros in its strips.  kWholeRows: it takes them about zero, since
+    // mean * rstd may be infinite and zero times that would not be zero (!kHeld: it skips its sums).
+    const float about = !kHeld || ROWS != kWholeRows || left[k] > 0 ? mean : 0.0f;
     if constexpr (KEPT) {
       uint32_t q[N / 4];
       if constexpr (N == 8)
         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q[0]), "=r"(q[1]) : "r"(xs + lane * 8u) : "memory");
       else
         q[0] = ld_shared_u32(xs + lane * 4u);
-      kept_less<N>(q, scale[k], mean, xh);
+      kept_less<N>(q, scale[k], about, xh);
 #pragma unroll
       for (int i = 0; i < N; ++i) xh[i] *= rstd;
     } else {
       const uint32_t lead_x = UNAL ? lead_of(p.x.base + static_cast<int64_t>(row) * p.x.pitch) : 0u;
       values<TX>(staged_vector<TX, UNAL>(xs, lead_x), xh);
 #pragma unroll
-      for (int i = 0; i < N; ++i) xh[i] = (xh[i] - mean) * rstd;
+      for (int i = 0; i < N; ++i) xh[i] = (xh[i] - about) * rstd;
     }
     if (UNAL || (LEAD && !inner[k])) {
 #pragma unroll
@@ -675,6 +678,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     float hold_g[kHeld ? kItems : 1][N], hold_x[kHeld ? kItems : 1][N];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
+      if (!kHeld && ROWS == kWholeRows && left[k] <= 0) continue;
       float dy[N], xh[N], g[N];
       gamma_at(k, g);
       values_at(row, slot, k, mean, rstd, dy, xh);

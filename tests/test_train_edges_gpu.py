@@ -35,3 +35,19 @@ def test_rows_without_columns(dtype):
     assert torch.isnan(mean).all() and torch.isnan(rstd).all()
     dx, dgamma, dbeta = tg.layer_norm_backward(x, kept, mean, rstd)
     assert dx.shape == (300, 0) and dgamma.shape == dbeta.shape == (0,)
+
+
+# A group's last lanes have no values at these widths.  The rows are constant and so large that
+# mean * rstd is infinite, while every value's (x - mean) rstd is zero.
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("cols", [40, 136, 264, 520, 1000, 4104, 8200, 12296, 16392])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_lanes_without_values_count_for_nothing(dtype, cols, kept):
+    _, gamma, _, dy = make(5, cols, dtype, seed=cols)
+    x = torch.full((5, cols), 2.0 ** 120, dtype=DT[dtype])
+    mean, rstd = torch.full((5,), 2.0 ** 120), torch.full((5,), 2.0 ** 10)
+    xd = tg.ckpt8_pack(x.cuda()) if kept else x.cuda()
+    got = tg.layer_norm_backward(dy.cuda(), xd, mean.cuda(), rstd.cuda(), gamma.cuda())
+    assert torch.isfinite(got[0]).all()
+    check_backward(dy, f64(x), mean, rstd, gamma, got, dtype)
+    assert (got[1] == 0).all()
