@@ -364,8 +364,10 @@ int tg_gemm_mxfp8_debug(const void* A_dev, const void* SFA_dev, const void* B_de
  * the backward pass takes from them.  Matrices are [rows, cols] with unit stride along a row and
  * a row stride ``ld`` >= cols given in elements; rows and cols are >= 0 and < 2^31.  Any element
  * alignment is accepted; rows that start on 16-byte boundaries are moved in wider accesses.  No
- * output may overlap an input or another output.  Asynchronous on ``stream``, deterministic, no
- * allocation; errors as for tg_gemm_persistent.
+ * output may overlap an input or another output; matrices of one row stride may lie in each other's
+ * gaps, as column slices of one buffer do (of different strides they may not, even where no element
+ * is shared).  Asynchronous on ``stream``, deterministic, no allocation; errors as for
+ * tg_gemm_persistent.
  *
  * A checkpoint of x [rows, cols] is two arrays: q [rows, 32 ceil(cols / 32)] of E4M3 bytes, 16-byte
  * aligned, zero past column ``cols``, and s [rows, ceil(cols / 32)] of E8M0 bytes; it stands for

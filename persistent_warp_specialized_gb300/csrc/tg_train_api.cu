@@ -53,17 +53,37 @@ int check_optional(const void* p, uint64_t elem, const char* name) {
   return p ? check_array(p, elem, name) : TG_OK;
 }
 
+// A device array: ``bytes`` from its first element to past its last.  pitch != 0: a matrix whose
+// rows are ``row`` bytes, ``pitch`` bytes apart.
 struct Region {
   const void* p;
   uint64_t bytes;
   const char* name;
+  uint64_t row = 0, pitch = 0;
 };
+
+Region matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, uint64_t elem,
+              const char* name) {
+  return {p, span(rows, cols, ld, elem), name, cols * elem, ld * elem};
+}
+
+// Whether two arrays share no byte.  Matrices of one pitch may lie in each other's gaps, as column
+// slices of one buffer do: their rows then take separate parts of every ``pitch`` bytes.  Anything
+// else is told apart by where it begins and ends.
+bool apart(const Region& a, const Region& b) {
+  if (!overlaps(a.p, a.bytes, b.p, b.bytes)) return true;
+  if (a.pitch == 0 || a.pitch != b.pitch) return false;
+  const uint64_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  // how far into a's rows b's begin
+  const uint64_t at = b0 >= a0 ? (b0 - a0) % a.pitch : a.pitch - 1 - (a0 - b0 - 1) % a.pitch;
+  return at >= a.row && at + b.row <= a.pitch;
+}
 
 // No output may overlap an input or another output (regions [0, outs) are the outputs).
 int check_apart(const Region* r, int outs, int n) {
   for (int i = 0; i < outs; ++i)
     for (int j = i + 1; j < n; ++j)
-      if (r[i].p && r[j].p && overlaps(r[i].p, r[i].bytes, r[j].p, r[j].bytes))
+      if (r[i].p && r[j].p && !apart(r[i], r[j]))
         return fail(TG_ERR_ARG, "%s overlaps %s", r[i].name, r[j].name);
   return TG_OK;
 }
@@ -194,11 +214,11 @@ int wgrad_impl(const void* q, const void* sc, const void* dy, void* dw, int64_t 
                   (long long)(ws ? ws_bytes : 0), (unsigned long long)w.workspace);
     TG_TRY(check_array(ws, 256, "workspace"));
   }
-  const Region r[] = {{dw, span(cols, outs, ld_dw, 2), "dW"},
+  const Region r[] = {matrix(dw, cols, outs, ld_dw, 2, "dW"),
                       {w.workspace ? ws : nullptr, w.workspace, "workspace"},
                       {q, tokens * kb * 32, "q"},
                       {sc, tokens * kb, "s"},
-                      {dy, span(tokens, outs, ld_dy, 2), "dY"}};
+                      matrix(dy, tokens, outs, ld_dy, 2, "dY")};
   TG_TRY(check_apart(r, 2, 5));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -301,12 +321,12 @@ int tg_layernorm_fwd(const void* x_dev, const void* gamma_dev, const void* beta_
   TG_TRY(check_optional(rstd_dev, 4, "rstd"));
   TG_TRY(check_optional(yq_dev, 16, "yq"));
   TG_TRY(check_optional(ys_dev, 1, "ys"));
-  const Region r[] = {{y_dev, span(rows, cols, ld_y, e), "y"},
+  const Region r[] = {matrix(y_dev, rows, cols, ld_y, e, "y"),
                       {mean_dev, stat, "mean"},
                       {rstd_dev, stat, "rstd"},
                       {yq_dev, rows * kb * 32, "yq"},
                       {ys_dev, rows * kb, "ys"},
-                      {x_dev, span(rows, cols, ld_x, e), "x"},
+                      matrix(x_dev, rows, cols, ld_x, e, "x"),
                       {gamma_dev, param, "gamma"},
                       {beta_dev, param, "beta"}};
   TG_TRY(check_apart(r, 5, 8));
@@ -383,12 +403,12 @@ int tg_layernorm_bwd(const void* dy_dev, const void* x_dev, const void* xq_dev, 
     TG_TRY(check_array(workspace_dev, 256, "workspace"));
   }
   const uint64_t stat = 4 * static_cast<uint64_t>(rows), param = pe * cols;
-  const Region r[] = {{rows > 0 ? dx_dev : nullptr, span(rows, cols, ld_dx, e), "dx"},
+  const Region r[] = {matrix(rows > 0 ? dx_dev : nullptr, rows, cols, ld_dx, e, "dx"),
                       {dgamma_dev, param, "dgamma"},
                       {dbeta_dev, param, "dbeta"},
                       {need > 0 ? workspace_dev : nullptr, static_cast<uint64_t>(need), "workspace"},
-                      {dy_dev, span(rows, cols, ld_dy, e), "dy"},
-                      {x_dev, span(rows, cols, ld_x, e), "x"},
+                      matrix(dy_dev, rows, cols, ld_dy, e, "dy"),
+                      matrix(x_dev, rows, cols, ld_x, e, "x"),
                       {xq_dev, rows * kb * 32, "xq"},
                       {xs_dev, rows * kb, "xs"},
                       {mean_dev, stat, "mean"},
@@ -431,7 +451,7 @@ int tg_ckpt8_pack(const void* x_dev, void* q_dev, void* s_dev, int64_t rows, int
   const uint64_t kb = kept_blocks(cols);
   const Region r[] = {{q_dev, rows * kb * 32, "q"},
                       {s_dev, rows * kb, "s"},
-                      {x_dev, span(rows, cols, ld_x, elem_bytes(dtype)), "x"}};
+                      matrix(x_dev, rows, cols, ld_x, elem_bytes(dtype), "x")};
   TG_TRY(check_apart(r, 2, 3));
   int sms = 0;
   TG_TRY(device_ready(&sms, nullptr));
@@ -450,7 +470,7 @@ int tg_ckpt8_unpack(const void* q_dev, const void* s_dev, void* out_dev, int64_t
   TG_TRY(check_array(s_dev, 1, "s"));
   TG_TRY(check_array(out_dev, elem_bytes(dtype), "out"));
   const uint64_t kb = kept_blocks(cols);
-  const Region r[] = {{out_dev, span(rows, cols, ld_out, elem_bytes(dtype)), "out"},
+  const Region r[] = {matrix(out_dev, rows, cols, ld_out, elem_bytes(dtype), "out"),
                       {q_dev, rows * kb * 32, "q"},
                       {s_dev, rows * kb, "s"}};
   TG_TRY(check_apart(r, 1, 3));

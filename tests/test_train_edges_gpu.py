@@ -51,3 +51,75 @@ def test_lanes_without_values_count_for_nothing(dtype, cols, kept):
     assert torch.isfinite(got[0]).all()
     check_backward(dy, f64(x), mean, rstd, gamma, got, dtype)
     assert (got[1] == 0).all()
+
+
+# Column slices of one buffer: they share no element, whichever comes first.
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("cols,gap,lead", [(48, 0, 0), (264, 3, 5), (700, 0, 8), (4096, 8, 0)])
+def test_outputs_between_the_inputs_rows(cols, gap, lead, dtype):
+    rows, ld = 37, lead + 2 * cols + gap
+    x, gamma, beta, dy = make(rows, cols, dtype, seed=cols)
+    gd, bd = gamma.cuda(), beta.cuda()
+    for first in (0, 1):
+        def slices():
+            buf = torch.full((rows, ld), 7.0, dtype=DT[dtype], device="cuda")
+            halves = buf[:, lead:lead + cols], buf[:, lead + cols:lead + 2 * cols]
+            return buf, halves[first], halves[1 - first]
+
+        def intact(buf):
+            return (buf[:, :lead] == 7).all() and (buf[:, lead + 2 * cols:] == 7).all()
+
+        buf, xs, y = slices()
+        xs.copy_(x)
+        got = tg.layer_norm(xs, gd, bd, out=y)
+        check_forward(x, gamma, beta, got, dtype)
+        assert torch.equal(xs.cpu(), x) and intact(buf)
+        buf, dys, dx = slices()
+        dys.copy_(dy)
+        dgamma, dbeta = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+        nbytes = tg.tg_layernorm_bwd_workspace_bytes(rows, cols)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        tg.tg_layernorm_bwd(dys, x.cuda(), None, None, gd, got[1], got[2], dx, dgamma, dbeta, rows,
+                            cols, ld, cols, ld, dtype, "f32", ws)
+        check_backward(dy, f64(x), got[1], got[2], gamma, (dx, dgamma, dbeta), dtype)
+        assert torch.equal(dys.cpu(), dy) and intact(buf)
+
+
+def test_a_weight_gradient_between_its_inputs_rows():
+    buf = torch.zeros((200, 256), dtype=torch.bfloat16, device="cuda")
+    dy, dw = buf[:, :120], buf[:96, 136:]
+    gen = torch.Generator().manual_seed(1)
+    dy.copy_(torch.randint(-2, 3, (200, 120), generator=gen))
+    x = torch.randint(-4, 5, (200, 96), generator=gen).float()
+    tg.ckpt8_wgrad(tg.ckpt8_pack(x.cuda()), dy, out=dw)
+    assert torch.equal(dw.cpu().double(), (x.double().T @ dy.cpu().double()).bfloat16().double())
+    assert (buf[96:, 136:] == 0).all() and (buf[:, 120:136] == 0).all()
+
+
+def test_outputs_that_do_overlap_are_refused():
+    buf = torch.zeros((40, 256), dtype=torch.float16, device="cuda")
+    flat = buf.view(-1)
+
+    def refused(x, out):
+        with pytest.raises(tg.TgError) as e:
+            tg.layer_norm(x, out=out)
+        assert e.value.code == tg.TG_ERR_ARG and "overlaps" in str(e.value)
+
+    refused(buf[:, :128], buf[:, :128])
+    refused(buf[:, :128], buf[:, 127:255])                     # one column
+    refused(buf[:, 127:255], buf[:, :128])
+    wrapped = flat[200:].as_strided((39, 100), (256, 1))       # columns 200 .. 255 and 0 .. 43
+    refused(buf[:39, :100], wrapped)
+    refused(wrapped, buf[:39, :100])
+    refused(wrapped, buf[:39, 101:201])
+    tg.layer_norm(buf[:39, 60:160], out=wrapped)               # between 44 and 199
+    tg.layer_norm(wrapped, out=buf[:39, 60:160])
+    refused(buf[:20, :64], flat[64:].as_strided((20, 64), (512, 1)))      # rows of another pitch
+    refused(buf[:, :64], flat[64:64 + 40 * 64].view(40, 64))
+    tg.layer_norm(buf[:20, :128], out=buf[20:, :128])          # one after the other
+    tg.layer_norm(flat[:256].view(1, 256), out=flat[256:512].view(1, 256))
+    mean = torch.zeros(40, device="cuda")
+    y = torch.empty((40, 128), dtype=torch.float16, device="cuda")
+    with pytest.raises(tg.TgError):
+        tg.tg_layernorm_fwd(buf[:, :128], None, None, y, y.view(torch.float32)[0], mean, None, None,
+                            40, 128, 256, 128, "f16")
