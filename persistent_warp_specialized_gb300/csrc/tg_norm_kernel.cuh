@@ -16,11 +16,14 @@
 // that a warp holds are left to tg_norm_short_kernel.cuh.
 //
 // The variance: each thread takes the mean of its own values and their squares about that mean
-// (n, m, M2); lanes, and then warps, are joined about the mean c of the first of them,
+// (n, m, M2; fp32: about the mean of its first four, corrected for the rest); lanes, and then warps,
+// are joined about the mean c of the first of them,
 //   A = sum [M2 + n (m - c)^2],  B = sum n (m - c);  mean = c + B / n,  M2 = A - B^2 / n,
 // two sums that run side by side.  No difference of large sums is formed, so a large mean costs no
 // digits: B^2 / n <= (1 - 1 / k) sum n (m - c)^2 for k equal parts, at most 5 bits for 32.
 #pragma once
+
+#include <type_traits>
 
 #include "tg_rows.cuh"
 
@@ -163,6 +166,18 @@ __device__ __forceinline__ float inverse_root(float a) {
   return a > 0.0f && a < INFINITY ? fmaf(0.5f * r, e, r) : r;
 }
 
+// Adds ``rest``, the mean of the deviations from ``mean``, to it, and makes ``square``, the mean square
+// about it, that about the new one.  Equal values so give their value, whatever the first sum lost.
+// Only where the mean outweighs the deviations: they are rounded as the values are, all alike where
+// the values have one exponent, which is more than a small mean's own sum loses.
+__device__ __forceinline__ bool mean_outweighs(float mean, float square) {
+  return square < mean * mean;
+}
+__device__ __forceinline__ void correct_mean(float& mean, float& square, float rest) {
+  mean += rest;
+  square = fmaxf(fmaf(-rest, rest, square), 0.0f);   // may round below zero
+}
+
 // Zeroes a warp's strips: those past a row's end stay so, and the values there count for nothing.
 __device__ __forceinline__ void clear_strips(uint32_t at, uint32_t strips) {
   for (uint32_t o = (threadIdx.x & 31u) * 16u; o < strips * kStripBytes; o += 512u)
@@ -213,6 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr bool kHeld = THREADS == kNormThreads && VALUES == kNormValues;
   constexpr bool kShared = VALUES == kFwdLongValues;
   static_assert(!LEAD || (THREADS == kNormThreads && !KEEP));
+  constexpr bool kExact = sizeof(TX) == 4;   // sums that fp32 would round: below
   __shared__ float part[2][R][3][32];               // c, A and B of each warp
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t groups = blockDim.x / g_threads, group = threadIdx.x / g_threads;
@@ -338,19 +354,27 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int k = 0; k < kItems; ++k) {
         values<TX>(staged_vector<TX, UNAL>(mine + ((slot * R + r) * kItems + k) * kStripBytes, lead),
                    v[r][k]);
-        if (UNAL && left[k] < N) {
+        if (UNAL && left[k] < N && (!kExact || k == 0)) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) v[r][k][i] = i < left[k] ? v[r][k][i] : 0.0f;
+          for (int i = 0; i < N; ++i) v[r][k][i] = i < left[k] ? v[r][k][i] : kExact ? v[r][0][0] : 0.0f;
         }
+        if constexpr (!kExact) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) s += v[r][k][i];
+          for (int i = 0; i < N; ++i) s += v[r][k][i];
+        }
       }
-      // exact where all values are one (a constant row has variance 0)
-      const float m = n_mine == VALUES ? s * (1.0f / VALUES) : (n_mine > 0 ? s / n_t : 0.0f);
-      float m2 = 0.0f;
+      // Where all values are one, so is their mean.  32 values of 16 bits add up exactly; of fp32 ones,
+      // which do not, four do, in pairs: squares are taken about the first vector's mean, and ``low`` is
+      // what the thread's mean has beyond it.
+      auto over_n = [&](float a) { return n_mine == VALUES ? a * (1.0f / VALUES) : a / n_t; };
+      float m, m2 = 0.0f, off = 0.0f, low = 0.0f;
+      if constexpr (kExact)
+        m = 0.25f * ((v[r][0][0] + v[r][0][1]) + (v[r][0][2] + v[r][0][3]));
+      else
+        m = n_mine > 0 ? over_n(s) : 0.0f;
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
-        float q = 0.0f;
+        float q = 0.0f, e = 0.0f;
         if (UNAL && left[k] < N) {   // what is not the row's deviates by nothing
 #pragma unroll
           for (int i = 0; i < N; ++i) v[r][k][i] = i < left[k] ? v[r][k][i] : m;
@@ -359,11 +383,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < N; ++i) {
           const float d = v[r][k][i] - m;
           q = fmaf(d, d, q);
+          if constexpr (kExact) e += d;
         }
         m2 += left[k] > 0 ? q : 0.0f;
+        if constexpr (kExact) off += left[k] > 0 ? e : 0.0f;
       }
-      c[r] = __shfl_sync(0xffffffffu, m, 0);   // lane 0 holds values wherever its warp holds any
-      const float d = n_mine > 0 ? m - c[r] : 0.0f;
+      if (kExact && n_mine > 0) {
+        low = over_n(off);
+        m2 = fmaf(-off, low, m2);
+      }
+      // lane 0 holds values wherever its warp holds any
+      c[r] = __shfl_sync(0xffffffffu, kExact ? m + low : m, 0);
+      const float d = n_mine > 0 ? (kExact ? (m - c[r]) + low : m - c[r]) : 0.0f;
       ab[2 * r + 1] = n_t * d;
       ab[2 * r] = fmaf(ab[2 * r + 1], d, m2);
     }
@@ -379,10 +410,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float bw = part[turn & 1u][r][2][w], dw = bw * inv_l;
-        const float mw = part[turn & 1u][r][0][w] + dw;
+        const float cw = part[turn & 1u][r][0][w], mw = cw + dw;
         const float m2 = fmaf(-bw, dw, part[turn & 1u][r][1][w]);
         c[r] = __shfl_sync(0xffffffffu, mw, 0);
-        const float d = n_l > 0.0f ? mw - c[r] : 0.0f;
+        const float d = n_l > 0.0f ? (kExact ? (cw - c[r]) + dw : mw - c[r]) : 0.0f;
         ab[2 * r + 1] = n_l * d;
         ab[2 * r] = n_l > 0.0f ? fmaf(ab[2 * r + 1], d, m2) : 0.0f;
       }
@@ -435,10 +466,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   cp_async_wait<0>();
 }
 
-// Any width: the CTA walks its row three times; the second and third reads come from the L2.
+// Any width: the CTA walks its row three times (mean; squares about it, and what the mean lacks; y);
+// the second and third reads come from the L2.
 template <typename TX, typename TP, bool UNAL, bool KEEP>
 __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const NormFwdParams p) {
-  __shared__ float part[2][32];
+  __shared__ float part[2][2][32];
   constexpr int N = kVec<TX>;
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   grid_dependency_wait();
@@ -447,27 +479,37 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const NormFwdParams
   const char* x = p.x.base + static_cast<int64_t>(row) * p.x.pitch;
   const int64_t row_bytes = static_cast<int64_t>(p.cols) * static_cast<int>(sizeof(TX));
   const uint32_t end = ((p.cols + N - 1) / N + 31u) & ~31u;   // vectors, whole strips
-  float stat[2] = {0.0f, 0.0f};   // mean, then mean square about it
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    float a = 0.0f;
+  float mean = 0.0f;
+  auto walk = [&](auto which, float& sum, float& squares) {   // of deviations from ``mean``
+    constexpr int pass = decltype(which)::value;
+    float a = 0.0f, q = 0.0f;
     for (uint32_t j = threadIdx.x; j < end; j += blockDim.x) {
       const int64_t left = static_cast<int64_t>(p.cols) - static_cast<int64_t>(j) * N;
       float v[N];
       values<TX>(load_vector<TX, UNAL>(p.x, x, static_cast<int64_t>(j) * 16, row_bytes), v);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float d = v[i] - stat[0];
-        a += i < left ? (pass ? d * d : d) : 0.0f;
+        const float d = i < left ? v[i] - mean : 0.0f;
+        a += d;
+        if constexpr (pass) q = fmaf(d, d, q);
       }
     }
     a = warp_sum(a);
-    if (lane == 0) part[pass][warp] = a;
+    if constexpr (pass) q = warp_sum(q);
+    if (lane == 0) {
+      part[pass][0][warp] = a;
+      part[pass][1][warp] = q;
+    }
     __syncthreads();
-    a = warp_sum(lane < warps ? part[pass][lane] : 0.0f);
-    stat[pass] = a / static_cast<float>(p.cols);
-  }
-  const float mean = stat[0], rstd = inverse_root(stat[1] + p.eps);
+    sum = warp_sum(lane < warps ? part[pass][0][lane] : 0.0f) / static_cast<float>(p.cols);
+    squares = warp_sum(lane < warps ? part[pass][1][lane] : 0.0f) / static_cast<float>(p.cols);
+  };
+  float first, rest, square;
+  walk(std::integral_constant<int, 0>(), first, square);
+  mean = first;
+  walk(std::integral_constant<int, 1>(), rest, square);
+  if (mean_outweighs(mean, square)) correct_mean(mean, square, rest);
+  const float rstd = inverse_root(square + p.eps);
   if (threadIdx.x == 0) {
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;

@@ -99,14 +99,23 @@ __global__ void __launch_bounds__(kShortFwdThreads, kShortFwdCtas)
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) s += x[i];
-    const float mean = row_sum(s, shift) / cols;
+    float mean = row_sum(s, shift) / cols;
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float d = i < left ? x[i] - mean : 0.0f;
       q = fmaf(d, d, q);
     }
-    const float rstd = inverse_root(row_sum(q, shift) / cols + p.eps);
+    float square = row_sum(q, shift) / cols;
+    // 16-bit values add up exactly over a short row, so equal ones have their value as mean
+    if (sizeof(TX) == 4 && __any_sync(0xffffffffu, mean_outweighs(mean, square))) {
+      float e = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) e += i < left ? x[i] - mean : 0.0f;
+      e = row_sum(e, shift) / cols;
+      if (mean_outweighs(mean, square)) correct_mean(mean, square, e);
+    }
+    const float rstd = inverse_root(square + p.eps);
     const bool valid = row < p.rows;
     if (v == 0u && valid) {
       if (p.mean) p.mean[row] = mean;

@@ -53,6 +53,36 @@ def test_lanes_without_values_count_for_nothing(dtype, cols, kept):
     assert (got[1] == 0).all()
 
 
+# The sum of equal values is rounded where they take all of a float's bits; their mean is the value.
+@pytest.mark.parametrize("cols", [1, 3, 31, 100, 128, 129, 700, 1001, 4099, 5000, 8192, 9000, 16384,
+                                  20000, 40001])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_constant_rows_of_any_value(cols, dtype):
+    values = torch.tensor([0.1, 1.1, 1000.3, 1 / 3, -7.7, 1.0009765625]).to(DT[dtype])
+    x = values[:, None].repeat(1, cols).cuda()
+    y, mean, rstd = tg.layer_norm(x, eps=1e-5)
+    assert torch.equal(mean.cpu(), values.float()) and (y == 0).all()
+    torch.testing.assert_close(rstd.cpu(), torch.full((6,), 1e-5 ** -0.5), rtol=1e-6, atol=0)
+    y, mean, _ = tg.layer_norm(x, eps=0.0)       # 0 times whatever the root's inverse is
+    assert torch.equal(mean.cpu(), values.float()) and ((y == 0) | torch.isnan(y)).all()
+    beta = torch.linspace(-2, 2, cols, device="cuda")
+    y = tg.layer_norm(x, beta=beta, eps=1e-5)[0]
+    assert torch.equal(y, beta.to(DT[dtype])[None].expand(6, cols))
+
+
+# Deviations far below the mean: what is left of them is what the mean's own rounding leaves.
+@pytest.mark.parametrize("cols", [100, 1000, 4099, 8192, 20000])
+def test_small_deviations_about_a_large_mean(cols):
+    gen = torch.Generator().manual_seed(cols)
+    steps = torch.randint(-8, 9, (7, cols), generator=gen)
+    x = 1000.3 + steps * 2.0 ** -14              # one to eight units in the last place
+    _, mean, rstd = tg.layer_norm(x.float().cuda(), eps=1e-12)
+    _, rm, rr = train.norm(f64(x.float()), None, None, 1e-12)
+    # the mean to a unit in the last place, and the variance about it to one part in 100
+    assert (np.abs(f64(mean) - rm) <= 2.0 ** -14).all()
+    assert (np.abs(f64(rstd) / rr - 1) < 0.005).all()
+
+
 # Column slices of one buffer: they share no element, whichever comes first.
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("cols,gap,lead", [(48, 0, 0), (264, 3, 5), (700, 0, 8), (4096, 8, 0)])
