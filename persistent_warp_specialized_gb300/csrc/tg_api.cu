@@ -63,7 +63,8 @@ EncodeTiledFn encode_fn() {
 struct DeviceInfo {
   int state = 0;  // 0 unknown, 1 ready, -1 unsupported
   int sms = 0;
-  int max_pairs = 0;  // CTA pairs of the pair kernel resident at once
+  int max_pairs = 0;  // CTA pairs of the pair kernels resident at once
+  int wgrad_pairs = 0;  // and of the weight gradient's; 0: not set up yet
   char why[256] = "";
 };
 constexpr int kMaxDevices = 64;
@@ -97,6 +98,25 @@ int device_ready(int* sms_out, int* max_pairs_out) {
   if (d.state < 0) return fail(TG_ERR_CUDA, "%s", d.why);
   if (sms_out) *sms_out = d.sms;
   if (max_pairs_out) *max_pairs_out = d.max_pairs;
+  return TG_OK;
+}
+
+int wgrad_ready(int* sms_out, int* max_pairs_out) {
+  if (const int rc = device_ready(sms_out, nullptr)) return rc;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail_cuda("cudaGetDevice", e);
+  std::lock_guard<std::mutex> lock(g_dev_mu);
+  int& pairs = g_dev[dev].wgrad_pairs;
+  if (pairs == 0) {
+    int n = 0;
+    if ((e = tg::prepare_wgrad_kernels(&n)) != cudaSuccess)
+      return fail_cuda("preparing the weight gradient (shared memory limit, cluster occupancy)", e);
+    if (n < 1)
+      return fail(TG_ERR_CUDA, "no CTA pair of the weight-gradient kernel fits on this device");
+    pairs = n;
+  }
+  *max_pairs_out = pairs;
   return TG_OK;
 }
 

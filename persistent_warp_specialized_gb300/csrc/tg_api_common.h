@@ -20,6 +20,11 @@ int fail_cuda(const char* what, cudaError_t e);
 // may be null: the SM count, and the CTA pairs of the pair kernels that are resident at once.
 int device_ready(int* sms_out, int* max_pairs_out);
 
+// device_ready, and the weight gradient's kernels set up on the device's first weight gradient (the
+// other calls neither wait for them nor depend on their occupancy).  max_pairs_out: its own CTA pairs
+// that are resident at once, at least one.
+int wgrad_ready(int* sms_out, int* max_pairs_out);
+
 // TG_OK if ``p`` is device memory of the current device (TMA reads it directly).
 int check_device_ptr(const void* p, const char* name);
 

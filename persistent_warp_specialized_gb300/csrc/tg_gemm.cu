@@ -240,10 +240,6 @@ cudaError_t prepare_gemm_kernels(int* max_pairs) {
   if ((e = set_mx_smem_attr<1, false>()) != cudaSuccess) return e;
   if ((e = set_mx_smem_attr<0, true>()) != cudaSuccess) return e;
   if ((e = set_mx_smem_attr<1, true>()) != cudaSuccess) return e;
-  if ((e = set_wgrad_smem_attr<0, 1>()) != cudaSuccess) return e;
-  if ((e = set_wgrad_smem_attr<1, 1>()) != cudaSuccess) return e;
-  if ((e = set_wgrad_smem_attr<0, 2>()) != cudaSuccess) return e;
-  if ((e = set_wgrad_smem_attr<1, 2>()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -255,7 +251,7 @@ cudaError_t prepare_gemm_kernels(int* max_pairs) {
   cfg.dynamicSmemBytes = kPairSmemBytes;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int clusters = 0, mx_clusters = 0, wide_clusters = 0;   // the least of all pair kernels counts
+  int clusters = 0, mx_clusters = 0, wide_clusters = 0;   // the least of the three counts
   e = cudaOccupancyMaxActiveClusters(&clusters, gemm_pair_ws_kernel<1, false>, &cfg);
   if (e != cudaSuccess) return e;
   cfg.dynamicSmemBytes = kWideSmemBytes;
@@ -265,13 +261,35 @@ cudaError_t prepare_gemm_kernels(int* max_pairs) {
   cfg.dynamicSmemBytes = kMxPairSmemBytes;
   e = cudaOccupancyMaxActiveClusters(&mx_clusters, gemm_mxfp8_pair_ws_kernel<1, false>, &cfg);
   if (e != cudaSuccess) return e;
-  if (mx_clusters < clusters) clusters = mx_clusters;
-  int wgrad_clusters = 0;
+  *max_pairs = clusters < mx_clusters ? clusters : mx_clusters;
+  return cudaSuccess;
+}
+
+cudaError_t prepare_wgrad_kernels(int* max_pairs) {
+  cudaError_t e;
+  if ((e = set_wgrad_smem_attr<0, 1>()) != cudaSuccess) return e;
+  if ((e = set_wgrad_smem_attr<1, 1>()) != cudaSuccess) return e;
+  if ((e = set_wgrad_smem_attr<0, 2>()) != cudaSuccess) return e;
+  if ((e = set_wgrad_smem_attr<1, 2>()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(WgradConfig<1>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = WgradConfig<1>::kSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int one = 0, two = 0;   // of one and of two N-halves a tile; the plan has one count for both
+  e = cudaOccupancyMaxActiveClusters(&one, wgrad_pair_kernel<1, 1, false, false>, &cfg);
+  if (e != cudaSuccess) return e;
   cfg.blockDim = dim3(WgradConfig<2>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = WgradConfig<2>::kSmemBytes;
-  e = cudaOccupancyMaxActiveClusters(&wgrad_clusters, wgrad_pair_kernel<1, 2, false, false>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&two, wgrad_pair_kernel<1, 2, false, false>, &cfg);
   if (e != cudaSuccess) return e;
-  *max_pairs = wgrad_clusters < clusters ? wgrad_clusters : clusters;
+  *max_pairs = one < two ? one : two;
   return cudaSuccess;
 }
 

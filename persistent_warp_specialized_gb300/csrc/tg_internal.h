@@ -123,6 +123,8 @@ struct WgradLaunch {
   int64_t inject_skip_phase;
   int sms;
 };
+// Sets the kernels' shared memory limits; *max_pairs: how many of their CTA pairs are resident at once.
+cudaError_t prepare_wgrad_kernels(int* max_pairs);
 cudaError_t launch_wgrad(int dtype, bool debug, const WgradLaunch& l, cudaStream_t stream);
 
 cudaError_t clear_watchdog_status(cudaStream_t stream);

@@ -204,9 +204,7 @@ int wgrad_impl(const void* q, const void* sc, const void* dy, void* dw, int64_t 
     TG_TRY(check_array(dy, 16, "dY"));
   }
   int sms = 0, max_pairs = 0;
-  TG_TRY(device_ready(&sms, &max_pairs));
-  if (max_pairs < 1)
-    return fail(TG_ERR_CUDA, "no CTA pair of the weight-gradient kernel fits on this device");
+  TG_TRY(wgrad_ready(&sms, &max_pairs));
   const WgradPlan w = wgrad_plan(tokens, cols, outs, max_pairs);
   if (w.workspace > 0) {
     if (!ws || static_cast<uint64_t>(ws_bytes) < w.workspace)
@@ -485,9 +483,7 @@ int64_t tg_ckpt8_wgrad_workspace_bytes(int64_t rows, int64_t cols, int64_t outs)
   TG_TRY(check_wgrad_sizes(rows, cols, outs));
   if (rows == 0 || cols == 0 || outs == 0) return 0;
   int max_pairs = 0;
-  TG_TRY(device_ready(nullptr, &max_pairs));
-  if (max_pairs < 1)
-    return fail(TG_ERR_CUDA, "no CTA pair of the weight-gradient kernel fits on this device");
+  TG_TRY(wgrad_ready(nullptr, &max_pairs));
   return static_cast<int64_t>(wgrad_plan(rows, cols, outs, max_pairs).workspace);
 }
 
