@@ -8,6 +8,7 @@ import subprocess
 import pytest
 
 from persistent_warp_specialized_gb300 import _build
+from wgrad_shapes import PAIRS, WAYS
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -60,3 +61,25 @@ def test_without_the_weight_gradient_the_gemm_still_runs(driver, wgrad_pairs):
     gemm, _, wgrad = run(driver, 512, 512, 512, wgrad_pairs=wgrad_pairs)
     assert gemm == (0, 76)
     assert wgrad["rc"] == -3 and wgrad["halves"] == 0    # TG_ERR_CUDA, and no launch
+
+
+@pytest.mark.parametrize("shape", WAYS)
+def test_what_is_launched(driver, shape):
+    halves, splits, half_units, most, tma = WAYS[shape]
+    _, _, w = run(driver, *shape)
+    assert w["rc"] == 0 and (w["halves"], w["splits"]) == (halves, splits)
+    assert w["units"] - w["split_from"] == half_units
+    assert -(-w["units"] * w["splits"] // (w["grid"] // 2)) == most
+    assert bool(w["tma_scales"]) == tma
+    # scales off the 16-byte grid are copied word by word
+    assert run(driver, *shape, scale_offset=4)[2]["tma_scales"] == 0
+
+
+def test_ranges_cover_the_tokens(driver):
+    for rows in (9000, 10369, 16000, 20000, 30000, 65536):
+        for cols, outs in ((40, 16), (512, 1024), (2000, 1000), (300, 520)):
+            _, _, w = run(driver, rows, cols, outs)
+            assert w["k_blocks"] == -(-rows // 64)
+            assert (w["splits"] - 1) * w["blocks_per_split"] < w["k_blocks"]
+            assert w["splits"] * w["blocks_per_split"] >= w["k_blocks"]
+            assert w["units"] * w["splits"] <= PAIRS or w["splits"] == 1
