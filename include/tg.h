@@ -385,7 +385,9 @@ int tg_gemm_mxfp8_debug(const void* A_dev, const void* SFA_dev, const void* B_de
  *   [cols] of ``param_dtype`` (TG_F32 or dtype); NULL: ones, zeros.  mean_dev, rstd_dev: [rows]
  *   fp32, either may be NULL.  yq_dev, ys_dev: NULL, or a checkpoint of the rounded y, made in the
  *   same pass.  rows == 0: nothing is done.  cols == 0: mean and rstd are NaN.  A row with a NaN or
- *   an infinity gives NaN.
+ *   an infinity gives NaN.  The last bits of a row's results depend on the number of rows (16-bit rows
+ *   of 2049 to 16384 values are summed in another order from 96 Ki values an SM on), but neither on
+ *   where the rows lie nor on what lies beside them, nor on whether a checkpoint is made.
  */
 int tg_layernorm_fwd(const void* x_dev, const void* gamma_dev, const void* beta_dev, void* y_dev,
                      float* mean_dev, float* rstd_dev, void* yq_dev, void* ys_dev, int64_t rows,

@@ -42,7 +42,7 @@ constexpr int kNormWideThreads = 1024;
 // rows of more than 2048 values from 96 Ki values an SM on, else the start costs more: 8192 x 8192
 // 53 us against 56 with 16 values a thread, 4000 x 7000 31 against 33, 4096 x 16384 70 against 85
 // (1024 threads), but 100 x 8192 10.9 against 8.8.  fp32 rows would have one row a turn: 4800 x 16384
-// 156 against 134.
+// 156 against 134.  (A row's last bits so depend on the number of rows.)
 constexpr int kFwdLongValues = 32;
 constexpr int kFwdLongCols = 2048, kFwdParamCols = 8192;
 constexpr int64_t kFwdLongWork = 96 * 1024;   // values an SM

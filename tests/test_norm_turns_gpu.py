@@ -171,3 +171,18 @@ def test_steps_from_several_threads():
     for t in threads:
         t.join()
     assert not failed and tg.tg_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(700, 24), (700, 99), (900, 520), (900, 1001), (400, 4096),
+                                       (400, 4099), (300, 8192), (200, 9001), (60, 16400),
+                                       (3700, 4096)])
+def test_a_row_gives_the_same_bits_wherever_it_lies(rows, cols, dtype):
+    x, gamma, beta, _ = make(rows, cols, dtype, seed=cols)
+    gd, bd = gamma.cuda(), beta.cuda()
+    want = tg.layer_norm(x.cuda(), gd, bd, checkpoint=True)
+    for n, pad in ((0, 8), (0, 3), (1, 0), (5, 2)):
+        got = tg.layer_norm(offset_by(x, n, pad), gd, bd, checkpoint=n != 1)
+        assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3])), (n, pad)
+        if n != 1:
+            assert torch.equal(got[3].q, want[3].q) and torch.equal(got[3].s, want[3].s)
