@@ -42,6 +42,10 @@ extern "C" {
    operators only */
 enum { TG_F16 = 0, TG_BF16 = 1, TG_F32 = 2 };
 
+/* activations of the gated feed-forward projections: g s(g), and GELU in its tanh form,
+   g s(2 sqrt(2 / pi) (g + 0.044715 g^3)), with s the logistic function */
+enum { TG_ACT_SILU = 0, TG_ACT_GELU = 1 };
+
 /* kernel variants (tg_gemm_persistent_ex, tg_gemm_persistent_debug, tg_gemm_launch_shape) */
 enum {
   TG_VARIANT_AUTO = 0,    /* the library's choice for the problem (what tg_gemm_persistent runs) */
@@ -451,6 +455,95 @@ int tg_ckpt8_wgrad_debug(const void* q_dev, const void* s_dev, const void* dY_de
                          int64_t rows, int64_t cols, int64_t outs, int64_t ld_dy, int64_t ld_dw,
                          int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream,
                          uint64_t watchdog_ns, int64_t inject_skip_phase);
+
+/*
+ * ---- Products with fused epilogues: what stands between the norm and the loss of a training step.
+ * fp16 or bf16 matrices (``dtype``), fp32 accumulation, each result rounded once.  Sizes are >= 0 and
+ * < 2^31; ``cols`` and ``outs`` are multiples of 8, rows and vocab are any.  Row strides ``ld`` (in
+ * elements) are multiples of 8 and at least a row's values; matrices are 16-byte aligned.  Overlap as
+ * for the training operators above.  Asynchronous on ``stream``, no allocation; every sum is added in
+ * an order that the sizes and the device determine, so equal calls give equal bits.  workspace_dev
+ * (256-byte aligned): as many bytes as the call's _workspace_bytes says for these sizes, contents
+ * scratch, in use until the call's work is done; calls that may run at the same time (two streams, two
+ * graphs) need one each.  NULL if that is 0.  Errors as for tg_gemm_persistent.
+ */
+
+/*
+ * tg_input_grad -- what a linear layer y = x W hands back to x:  dX = dY W^T
+ *   dY_dev [rows, outs], W_dev [cols, outs], dX_dev [rows, cols].  W is read as it lies.  Where the tiles
+ *   of dX are few, outs is split into ranges whose fp32 sums go through the workspace.
+ *   rows == 0 or cols == 0: nothing is done.  outs == 0: dX is zero-filled.
+ */
+int tg_input_grad(const void* dY_dev, const void* W_dev, void* dX_dev, int64_t rows, int64_t cols,
+                  int64_t outs, int64_t ld_dy, int64_t ld_w, int64_t ld_dx, int dtype,
+                  void* workspace_dev, int64_t workspace_bytes, void* stream);
+int64_t tg_input_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t outs);
+
+/* tg_input_grad, synchronously, with the watchdog limit and the injected missing fill of
+   tg_gemm_persistent_debug (its CTA-pair form). */
+int tg_input_grad_debug(const void* dY_dev, const void* W_dev, void* dX_dev, int64_t rows,
+                        int64_t cols, int64_t outs, int64_t ld_dy, int64_t ld_w, int64_t ld_dx,
+                        int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream,
+                        uint64_t watchdog_ns, int64_t inject_skip_phase);
+
+/*
+ * tg_gated_fwd -- the gated feed-forward projections:  h = act(g) u,  g = x Wg,  u = x Wu
+ *   x_dev [rows, cols]; wg_dev, wu_dev [cols, outs]; h_dev [rows, outs].  g_dev, u_dev: NULL, or
+ *   [rows, outs] each, kept for the backward pass; h is made from g and u before they are rounded.
+ *   act: TG_ACT_*.  rows == 0 or outs == 0: nothing is done.  cols == 0: the outputs are zero-filled.
+ *   Wg and Wu may be column slices of one [cols, 2 outs] matrix.
+ */
+int tg_gated_fwd(const void* x_dev, const void* wg_dev, const void* wu_dev, void* h_dev,
+                 void* g_dev, void* u_dev, int64_t rows, int64_t cols, int64_t outs, int64_t ld_x,
+                 int64_t ld_wg, int64_t ld_wu, int64_t ld_h, int64_t ld_g, int64_t ld_u, int act,
+                 int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream);
+int64_t tg_gated_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t outs);
+
+/*
+ * tg_gated_bwd -- the gradients of tg_gated_fwd from dh, with g and u as it kept them:
+ *     dg = dh u act'(g),  du = dh act(g);   dx = dg Wg^T + du Wu^T,  dWg = x^T dg,  dWu = x^T du
+ *   dg and du are rounded to ``dtype`` before the products.  dx_dev may be NULL (Wg and Wu are then
+ *   not read), or dwg_dev and dwu_dev (x is then not read).  cols == 0: nothing is done.  rows == 0 or
+ *   outs == 0: what is asked for is zero-filled.
+ */
+int tg_gated_bwd(const void* dh_dev, const void* g_dev, const void* u_dev, const void* x_dev,
+                 const void* wg_dev, const void* wu_dev, void* dx_dev, void* dwg_dev, void* dwu_dev,
+                 int64_t rows, int64_t cols, int64_t outs, int64_t ld_dh, int64_t ld_g,
+                 int64_t ld_u, int64_t ld_x, int64_t ld_wg, int64_t ld_wu, int64_t ld_dx,
+                 int64_t ld_dwg, int64_t ld_dwu, int act, int dtype, void* workspace_dev,
+                 int64_t workspace_bytes, void* stream);
+int64_t tg_gated_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t outs);
+
+/*
+ * tg_xent_fwd -- softmax cross entropy of a vocabulary projection, row by row, without keeping the logits:
+ *     l = x W^T,   lse = log sum_v exp l[v],   loss = lse - l[target]
+ *   x_dev [rows, cols]; w_dev [vocab, cols], one row a word; targets_dev [rows] int64; loss_dev, lse_dev
+ *   [rows] fp32.  A row whose target is ignore_index has loss 0; one whose target is outside
+ *   [0, vocab) and not ignore_index has loss NaN.  A row with a NaN or +infinite logit gives NaN.
+ *   vocab and cols are at least 1 and 8.  rows == 0: nothing is done.
+ */
+int tg_xent_fwd(const void* x_dev, const void* w_dev, const int64_t* targets_dev, float* loss_dev,
+                float* lse_dev, int64_t rows, int64_t cols, int64_t vocab, int64_t ld_x,
+                int64_t ld_w, int64_t ignore_index, int dtype, void* workspace_dev,
+                int64_t workspace_bytes, void* stream);
+int64_t tg_xent_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab);
+
+/*
+ * tg_xent_bwd -- the gradients of tg_xent_fwd.  With dl[r, v] = dloss[r] (exp(l[r, v] - lse[r]) - [v is
+ * r's target]), 0 in ignored rows:   dx = dl W,   dW = dl^T x
+ *   dloss_dev [rows] fp32: the gradient of each row's loss (1 / n in every row for the mean of n
+ *   losses); lse_dev: what tg_xent_fwd wrote; dx_dev [rows, cols], dw_dev [vocab, cols], either may be
+ *   NULL.  The logits are computed again, a piece of the vocabulary at a time (at most 256 MiB of
+ *   their gradients, or 2048 words' where that is more); dl is rounded to ``dtype`` before the products
+ *   (scaled by a power of two in fp16, so that small probabilities keep their bits).  Rows with a wrong
+ *   target give NaN.  An ignored row's x adds zero times itself to dW.  rows == 0: dW is zero-filled.
+ */
+int tg_xent_bwd(const float* dloss_dev, const void* x_dev, const void* w_dev,
+                const int64_t* targets_dev, const float* lse_dev, void* dx_dev, void* dw_dev,
+                int64_t rows, int64_t cols, int64_t vocab, int64_t ld_x, int64_t ld_w,
+                int64_t ld_dx, int64_t ld_dw, int64_t ignore_index, int dtype,
+                void* workspace_dev, int64_t workspace_bytes, void* stream);
+int64_t tg_xent_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab);
 
 #ifdef __cplusplus
 }

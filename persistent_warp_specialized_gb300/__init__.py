@@ -40,6 +40,10 @@ TG_SCHEDULE_NOALLOC_MAX_UNITS = 65536   # scratch rows of tg_tile_schedule_noall
 VARIANTS = {"auto": TG_VARIANT_AUTO, "single": TG_VARIANT_SINGLE, "pair": TG_VARIANT_PAIR,
             "wide": TG_VARIANT_PAIR_WIDE}
 
+TG_ACT_SILU = 0
+TG_ACT_GELU = 1
+ACTIVATIONS = {"silu": TG_ACT_SILU, "gelu": TG_ACT_GELU}   # GELU in its tanh form
+
 DTYPES = {"f16": TG_F16, "bf16": TG_BF16, "f32": TG_F32}
 
 EXPORTED = (
@@ -69,6 +73,17 @@ EXPORTED = (
     "tg_ckpt8_wgrad",
     "tg_ckpt8_wgrad_workspace_bytes",
     "tg_ckpt8_wgrad_debug",
+    "tg_input_grad",
+    "tg_input_grad_workspace_bytes",
+    "tg_input_grad_debug",
+    "tg_gated_fwd",
+    "tg_gated_fwd_workspace_bytes",
+    "tg_gated_bwd",
+    "tg_gated_bwd_workspace_bytes",
+    "tg_xent_fwd",
+    "tg_xent_fwd_workspace_bytes",
+    "tg_xent_bwd",
+    "tg_xent_bwd_workspace_bytes",
 )
 
 
@@ -149,6 +164,22 @@ def load_library(path=LIB_PATH):
     lib.tg_ckpt8_wgrad_workspace_bytes.restype = i64
     lib.tg_ckpt8_wgrad_debug.argtypes = [vp] * 4 + [i64] * 5 + [i32, vp, i64, vp, u64, i64]
     lib.tg_ckpt8_wgrad_debug.restype = i32
+    lib.tg_input_grad.argtypes = [vp] * 3 + [i64] * 6 + [i32, vp, i64, vp]
+    lib.tg_input_grad.restype = i32
+    lib.tg_input_grad_debug.argtypes = [vp] * 3 + [i64] * 6 + [i32, vp, i64, vp, u64, i64]
+    lib.tg_input_grad_debug.restype = i32
+    lib.tg_gated_fwd.argtypes = [vp] * 6 + [i64] * 9 + [i32, i32, vp, i64, vp]
+    lib.tg_gated_fwd.restype = i32
+    lib.tg_gated_bwd.argtypes = [vp] * 9 + [i64] * 12 + [i32, i32, vp, i64, vp]
+    lib.tg_gated_bwd.restype = i32
+    lib.tg_xent_fwd.argtypes = [vp] * 5 + [i64] * 6 + [i32, vp, i64, vp]
+    lib.tg_xent_fwd.restype = i32
+    lib.tg_xent_bwd.argtypes = [vp] * 7 + [i64] * 8 + [i32, vp, i64, vp]
+    lib.tg_xent_bwd.restype = i32
+    for name in ("input_grad", "gated_fwd", "gated_bwd", "xent_fwd", "xent_bwd"):
+        nbytes = getattr(lib, f"tg_{name}_workspace_bytes")
+        nbytes.argtypes = [i64] * 3
+        nbytes.restype = i64
     _lib = lib
     return lib
 
@@ -696,3 +727,229 @@ def ckpt8_wgrad(kept, dy, out=None, stream=None):
                               rows, cols, outs, ld_dy, ld_dw, dtype,
                               ws.data_ptr() if nbytes else None, nbytes, _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- products with fused epilogues
+def tg_input_grad(dY, W, dX, rows, cols, outs, ld_dy, ld_w, ld_dx, dtype, workspace=None,
+                  stream=None, workspace_bytes=None):
+    """dX [rows, cols] = dY [rows, outs] W^T for W [cols, outs]."""
+    return _check(load_library().tg_input_grad(
+        _ptr(dY), _ptr(W), _ptr(dX), rows, cols, outs, ld_dy, ld_w, ld_dx, _dtype(dtype),
+        _ptr(workspace), _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def tg_input_grad_workspace_bytes(rows, cols, outs):
+    return _check(load_library().tg_input_grad_workspace_bytes(rows, cols, outs))
+
+
+def tg_input_grad_debug(dY, W, dX, rows, cols, outs, ld_dy, ld_w, ld_dx, dtype, workspace=None,
+                        stream=None, watchdog_ns=0, inject_skip_phase=-1, workspace_bytes=None):
+    return _check(load_library().tg_input_grad_debug(
+        _ptr(dY), _ptr(W), _ptr(dX), rows, cols, outs, ld_dy, ld_w, ld_dx, _dtype(dtype),
+        _ptr(workspace), _nbytes(workspace, workspace_bytes), _stream(stream), watchdog_ns,
+        inject_skip_phase))
+
+
+def _act(act):
+    if isinstance(act, str):
+        if act not in ACTIVATIONS:
+            raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, not {act!r}")
+        return ACTIVATIONS[act]
+    return int(act)
+
+
+def tg_gated_fwd(x, wg, wu, h, g, u, rows, cols, outs, ld_x, ld_wg, ld_wu, ld_h, ld_g, ld_u, act,
+                 dtype, workspace=None, stream=None, workspace_bytes=None):
+    """h = act(x wg) (x wu); g = x wg and u = x wu are kept where they are not None."""
+    return _check(load_library().tg_gated_fwd(
+        _ptr(x), _ptr(wg), _ptr(wu), _ptr(h), _ptr(g), _ptr(u), rows, cols, outs, ld_x, ld_wg,
+        ld_wu, ld_h, ld_g, ld_u, _act(act), _dtype(dtype), _ptr(workspace),
+        _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def tg_gated_fwd_workspace_bytes(rows, cols, outs):
+    return _check(load_library().tg_gated_fwd_workspace_bytes(rows, cols, outs))
+
+
+def tg_gated_bwd(dh, g, u, x, wg, wu, dx, dwg, dwu, rows, cols, outs, ld_dh, ld_g, ld_u, ld_x, ld_wg,
+                 ld_wu, ld_dx, ld_dwg, ld_dwu, act, dtype, workspace=None, stream=None,
+                 workspace_bytes=None):
+    """The gradients of tg_gated_fwd; dx, or dwg and dwu, may be None."""
+    return _check(load_library().tg_gated_bwd(
+        _ptr(dh), _ptr(g), _ptr(u), _ptr(x), _ptr(wg), _ptr(wu), _ptr(dx), _ptr(dwg), _ptr(dwu),
+        rows, cols, outs, ld_dh, ld_g, ld_u, ld_x, ld_wg, ld_wu, ld_dx, ld_dwg, ld_dwu, _act(act),
+        _dtype(dtype), _ptr(workspace), _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def tg_gated_bwd_workspace_bytes(rows, cols, outs):
+    return _check(load_library().tg_gated_bwd_workspace_bytes(rows, cols, outs))
+
+
+def tg_xent_fwd(x, w, targets, loss, lse, rows, cols, vocab, ld_x, ld_w, ignore_index, dtype,
+                workspace=None, stream=None, workspace_bytes=None):
+    """The cross entropy and log-sum-exp of each row of x w^T, w [vocab, cols]."""
+    return _check(load_library().tg_xent_fwd(
+        _ptr(x), _ptr(w), _ptr(targets), _ptr(loss), _ptr(lse), rows, cols, vocab, ld_x, ld_w,
+        ignore_index, _dtype(dtype), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+        _stream(stream)))
+
+
+def tg_xent_fwd_workspace_bytes(rows, cols, vocab):
+    return _check(load_library().tg_xent_fwd_workspace_bytes(rows, cols, vocab))
+
+
+def tg_xent_bwd(dloss, x, w, targets, lse, dx, dw, rows, cols, vocab, ld_x, ld_w, ld_dx, ld_dw,
+                ignore_index, dtype, workspace=None, stream=None, workspace_bytes=None):
+    """The gradients of tg_xent_fwd; dx or dw may be None."""
+    return _check(load_library().tg_xent_bwd(
+        _ptr(dloss), _ptr(x), _ptr(w), _ptr(targets), _ptr(lse), _ptr(dx), _ptr(dw), rows, cols,
+        vocab, ld_x, ld_w, ld_dx, ld_dw, ignore_index, _dtype(dtype), _ptr(workspace),
+        _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+def tg_xent_bwd_workspace_bytes(rows, cols, vocab):
+    return _check(load_library().tg_xent_bwd_workspace_bytes(rows, cols, vocab))
+
+
+def _matrix16(x, name, like=None, shape=None):
+    """(type code, rows, cols, row stride) of a float16 or bfloat16 matrix; of ``like``'s type and of
+    ``shape``, where they are given."""
+    code = _type_code(x.dtype)
+    if code == TG_F32 or (like is not None and x.dtype != like.dtype):
+        raise TypeError(f"{name} must be float16 or bfloat16"
+                        + (", the other matrices' type" if like is not None else ""))
+    rows, cols, ld = _rows_of(x, name)
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} must be [{shape[0]}, {shape[1]}], not [{rows}, {cols}]")
+    return code, rows, cols, ld
+
+
+def _row_values(x, name, dtype, rows):
+    if x.dtype != dtype or x.dim() != 1 or x.shape[0] != rows or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {rows} values")
+    return x.data_ptr()
+
+
+def _workspace(nbytes, like):
+    """(tensor, pointer) of ``nbytes`` on like's device."""
+    import torch
+
+    if nbytes == 0:
+        return None, None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return ws, ws.data_ptr()
+
+
+def input_grad(dy, w, out=None, stream=None):
+    """torch convenience: dx = dy w^T [rows, cols], what a linear layer y = x w hands back to x, of dy
+    [rows, outs] and w [cols, outs], both float16 or both bfloat16.  w is not transposed in memory."""
+    dtype, rows, outs, ld_dy = _matrix16(dy, "dy")
+    _, cols, w_outs, ld_w = _matrix16(w, "w", dy)
+    if w_outs != outs:
+        raise ValueError(f"dy has {outs} columns and w {w_outs}")
+    ld_dx = cols if out is None else _matrix16(out, "out", dy, (rows, cols))[3]
+    lib = load_library()
+    nbytes = _check(lib.tg_input_grad_workspace_bytes(rows, cols, outs))
+    with _allocating_on(stream):
+        if out is None:
+            out = dy.new_empty((rows, cols))
+        ws, wsp = _workspace(nbytes, dy)
+    _check(lib.tg_input_grad(dy.data_ptr(), w.data_ptr(), out.data_ptr(), rows, cols, outs, ld_dy,
+                             ld_w, ld_dx, dtype, wsp, nbytes, _stream(stream)))
+    return out
+
+
+def gated_forward(x, w_gate, w_up, act="silu", keep=False, out=None, stream=None):
+    """torch convenience: h = act(x w_gate) (x w_up) of x [rows, cols] and weights [cols, outs], all
+    float16 or all bfloat16; act is "silu" or "gelu" (tanh form).  keep: (h, g, u), with g = x w_gate
+    and u = x w_up for gated_backward."""
+    dtype, rows, cols, ld_x = _matrix16(x, "x")
+    outs = w_gate.shape[-1]
+    ld_wg = _matrix16(w_gate, "w_gate", x, (cols, outs))[3]
+    ld_wu = _matrix16(w_up, "w_up", x, (cols, outs))[3]
+    ld_h = outs if out is None else _matrix16(out, "out", x, (rows, outs))[3]
+    code = _act(act)
+    lib = load_library()
+    nbytes = _check(lib.tg_gated_fwd_workspace_bytes(rows, cols, outs))
+    with _allocating_on(stream):
+        if out is None:
+            out = x.new_empty((rows, outs))
+        g = x.new_empty((rows, outs)) if keep else None
+        u = x.new_empty((rows, outs)) if keep else None
+        ws, wsp = _workspace(nbytes, x)
+    _check(lib.tg_gated_fwd(
+        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(),
+        g.data_ptr() if keep else None, u.data_ptr() if keep else None, rows, cols, outs, ld_x,
+        ld_wg, ld_wu, ld_h, outs, outs, code, dtype, wsp, nbytes, _stream(stream)))
+    return (out, g, u) if keep else out
+
+
+def gated_backward(dh, g, u, x, w_gate, w_up, act="silu", stream=None):
+    """torch convenience: (dx, dw_gate, dw_up) of gated_forward from dh [rows, outs] and the g and u
+    that it kept."""
+    dtype, rows, outs, ld_dh = _matrix16(dh, "dh")
+    ld_g = _matrix16(g, "g", dh, (rows, outs))[3]
+    ld_u = _matrix16(u, "u", dh, (rows, outs))[3]
+    cols = x.shape[-1]
+    ld_x = _matrix16(x, "x", dh, (rows, cols))[3]
+    ld_wg = _matrix16(w_gate, "w_gate", dh, (cols, outs))[3]
+    ld_wu = _matrix16(w_up, "w_up", dh, (cols, outs))[3]
+    code = _act(act)
+    lib = load_library()
+    nbytes = _check(lib.tg_gated_bwd_workspace_bytes(rows, cols, outs))
+    with _allocating_on(stream):
+        dx = dh.new_empty((rows, cols))
+        dwg = dh.new_empty((cols, outs))
+        dwu = dh.new_empty((cols, outs))
+        ws, wsp = _workspace(nbytes, dh)
+    _check(lib.tg_gated_bwd(
+        dh.data_ptr(), g.data_ptr(), u.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
+        w_up.data_ptr(), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), rows, cols, outs, ld_dh,
+        ld_g, ld_u, ld_x, ld_wg, ld_wu, cols, outs, outs, code, dtype, wsp, nbytes,
+        _stream(stream)))
+    return dx, dwg, dwu
+
+
+def linear_cross_entropy(x, w, targets, ignore_index=-100, stream=None):
+    """torch convenience: (loss, lse), float32 [rows], of the logits x w^T, which are not kept: x
+    [rows, cols] and w [vocab, cols] float16 or bfloat16, targets int64 [rows].  Rows whose target is
+    ignore_index have loss 0; other targets outside the vocabulary give NaN."""
+    import torch
+
+    dtype, rows, cols, ld_x = _matrix16(x, "x")
+    vocab = w.shape[0]
+    ld_w = _matrix16(w, "w", x, (vocab, cols))[3]
+    at = _row_values(targets, "targets", torch.int64, rows)
+    lib = load_library()
+    nbytes = _check(lib.tg_xent_fwd_workspace_bytes(rows, cols, vocab))
+    with _allocating_on(stream):
+        loss = torch.empty(rows, dtype=torch.float32, device=x.device)
+        lse = torch.empty(rows, dtype=torch.float32, device=x.device)
+        ws, wsp = _workspace(nbytes, x)
+    _check(lib.tg_xent_fwd(x.data_ptr(), w.data_ptr(), at, loss.data_ptr(), lse.data_ptr(), rows,
+                           cols, vocab, ld_x, ld_w, ignore_index, dtype, wsp, nbytes,
+                           _stream(stream)))
+    return loss, lse
+
+
+def linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index=-100, stream=None):
+    """torch convenience: (dx, dw) of linear_cross_entropy from the gradient of each row's loss,
+    float32 [rows], and the lse that it returned."""
+    import torch
+
+    dtype, rows, cols, ld_x = _matrix16(x, "x")
+    vocab = w.shape[0]
+    ld_w = _matrix16(w, "w", x, (vocab, cols))[3]
+    at = _row_values(targets, "targets", torch.int64, rows)
+    dp = _row_values(dloss, "dloss", torch.float32, rows)
+    lp = _row_values(lse, "lse", torch.float32, rows)
+    lib = load_library()
+    nbytes = _check(lib.tg_xent_bwd_workspace_bytes(rows, cols, vocab))
+    with _allocating_on(stream):
+        dx = x.new_empty((rows, cols))
+        dw = x.new_empty((vocab, cols))
+        ws, wsp = _workspace(nbytes, x)
+    _check(lib.tg_xent_bwd(dp, x.data_ptr(), w.data_ptr(), at, lp, dx.data_ptr(), dw.data_ptr(),
+                           rows, cols, vocab, ld_x, ld_w, cols, cols, ignore_index, dtype, wsp,
+                           nbytes, _stream(stream)))
+    return dx, dw

@@ -65,6 +65,7 @@ struct DeviceInfo {
   int sms = 0;
   int max_pairs = 0;  // CTA pairs of the pair kernels resident at once
   int wgrad_pairs = 0;  // and of the weight gradient's; 0: not set up yet
+  int linear_pairs = 0;  // and of the products with fused epilogues
   char why[256] = "";
 };
 constexpr int kMaxDevices = 64;
@@ -101,23 +102,39 @@ int device_ready(int* sms_out, int* max_pairs_out) {
   return TG_OK;
 }
 
-int wgrad_ready(int* sms_out, int* max_pairs_out) {
+namespace {
+
+// device_ready, and one family of kernels set up on the device's first call of it: ``prepare`` gives
+// their resident CTA pairs, kept in the device's ``member``.
+int family_ready(int* sms_out, int* max_pairs_out, int DeviceInfo::*member,
+                 cudaError_t (*prepare)(int*), const char* what) {
   if (const int rc = device_ready(sms_out, nullptr)) return rc;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail_cuda("cudaGetDevice", e);
   std::lock_guard<std::mutex> lock(g_dev_mu);
-  int& pairs = g_dev[dev].wgrad_pairs;
+  int& pairs = g_dev[dev].*member;
   if (pairs == 0) {
     int n = 0;
-    if ((e = tg::prepare_wgrad_kernels(&n)) != cudaSuccess)
-      return fail_cuda("preparing the weight gradient (shared memory limit, cluster occupancy)", e);
-    if (n < 1)
-      return fail(TG_ERR_CUDA, "no CTA pair of the weight-gradient kernel fits on this device");
+    if ((e = prepare(&n)) != cudaSuccess) return fail_cuda(what, e);
+    if (n < 1) return fail(TG_ERR_CUDA, "%s: no CTA pair fits on this device", what);
     pairs = n;
   }
   *max_pairs_out = pairs;
   return TG_OK;
+}
+
+}  // namespace
+
+int wgrad_ready(int* sms_out, int* max_pairs_out) {
+  return family_ready(sms_out, max_pairs_out, &DeviceInfo::wgrad_pairs, tg::prepare_wgrad_kernels,
+                      "preparing the weight gradient (shared memory limit, cluster occupancy)");
+}
+
+int linear_ready(int* sms_out, int* max_pairs_out) {
+  return family_ready(sms_out, max_pairs_out, &DeviceInfo::linear_pairs,
+                      tg::prepare_linear_kernels,
+                      "preparing the fused products (shared memory limit, cluster occupancy)");
 }
 
 int check_device_ptr(const void* p, const char* name) {

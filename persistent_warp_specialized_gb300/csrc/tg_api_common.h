@@ -25,6 +25,9 @@ int device_ready(int* sms_out, int* max_pairs_out);
 // that are resident at once, at least one.
 int wgrad_ready(int* sms_out, int* max_pairs_out);
 
+// The same for the products with fused epilogues, on the device's first of them.
+int linear_ready(int* sms_out, int* max_pairs_out);
+
 // TG_OK if ``p`` is device memory of the current device (TMA reads it directly).
 int check_device_ptr(const void* p, const char* name);
 

@@ -1,0 +1,125 @@
+// tg_gated_kernel.cuh -- what the gated feed-forward projections do outside the tensor core:
+//
+//   the backward pass of h = act(g) u:   dg = dh u act'(g),   du = dh act(g)
+//   and h from partial sums of g and u when K was split.
+//
+// Both are bound by memory: 8 values a thread and tensor in one 16-byte access each, two vectors ahead.
+#pragma once
+
+#include "tg_linear_kernel.cuh"
+
+namespace tg {
+
+template <int DT>
+__device__ __forceinline__ float2 unpack_in(uint32_t w) {
+  if constexpr (DT == 1) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  } else {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+}
+
+struct GatedGradParams {
+  const void *dh, *g, *u;
+  void* dgu;                       // [rows][2 vecs x 8]: dg, then du
+  int64_t ld_dh, ld_g, ld_u;       // elements
+  uint32_t rows, vecs;             // vectors of 8 values in a row
+  uint32_t act;
+};
+
+// A block walks vectors of its rows: blockIdx.y strides over rows, blockIdx.x over a row's vectors.
+template <int DT>
+__global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint64_t total = static_cast<uint64_t>(p.rows) * p.vecs;
+  const uint64_t stride = static_cast<uint64_t>(gridDim.x) * blockDim.x;
+  auto at = [](const void* base, uint64_t row, int64_t ld, uint32_t v) {
+    return reinterpret_cast<const uint4*>(static_cast<const char*>(base) +
+                                          (static_cast<int64_t>(row) * ld + 8ll * v) * 2);
+  };
+  auto work = [&](uint64_t row, uint32_t v, const uint4& dh4, const uint4& g4, const uint4& u4) {
+    const uint32_t dhw[4] = {dh4.x, dh4.y, dh4.z, dh4.w}, gw[4] = {g4.x, g4.y, g4.z, g4.w},
+                   uw[4] = {u4.x, u4.y, u4.z, u4.w};
+    uint32_t dgw[4], duw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 dh = unpack_in<DT>(dhw[i]), g = unpack_in<DT>(gw[i]), u = unpack_in<DT>(uw[i]);
+      const Gate a = gate_of(g.x, p.act), b = gate_of(g.y, p.act);
+      const float ax = g.x * a.s, bx = g.y * b.s;
+      dgw[i] = pack_out<DT>(
+          __float_as_uint(dh.x * u.x * fmaf(ax * (1.0f - a.s), a.slope, a.s)),
+          __float_as_uint(dh.y * u.y * fmaf(bx * (1.0f - b.s), b.slope, b.s)));
+      duw[i] = pack_out<DT>(__float_as_uint(dh.x * ax), __float_as_uint(dh.y * bx));
+    }
+    char* to = static_cast<char*>(p.dgu) + (row * 2u * p.vecs + v) * 16u;
+    st_global_v4(to, dgw[0], dgw[1], dgw[2], dgw[3]);
+    st_global_v4(to + static_cast<uint64_t>(p.vecs) * 16u, duw[0], duw[1], duw[2], duw[3]);
+  };
+  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += 2u * stride) {
+    const uint64_t i1 = i + stride;
+    const bool two = i1 < total;
+    const uint64_t r0 = i / p.vecs, r1 = two ? i1 / p.vecs : r0;
+    const uint32_t v0 = static_cast<uint32_t>(i - r0 * p.vecs);
+    const uint32_t v1 = two ? static_cast<uint32_t>(i1 - r1 * p.vecs) : v0;
+    const uint4 dh0 = __ldcs(at(p.dh, r0, p.ld_dh, v0)), g0 = __ldcs(at(p.g, r0, p.ld_g, v0)),
+                u0 = __ldcs(at(p.u, r0, p.ld_u, v0));
+    uint4 dh1 = dh0, g1 = g0, u1 = u0;
+    if (two) {
+      dh1 = __ldcs(at(p.dh, r1, p.ld_dh, v1));
+      g1 = __ldcs(at(p.g, r1, p.ld_g, v1));
+      u1 = __ldcs(at(p.u, r1, p.ld_u, v1));
+    }
+    work(r0, v0, dh0, g0, u0);
+    if (two) work(r1, v1, dh1, g1, u1);
+  }
+}
+
+struct GatedJoinParams {
+  const float *g_parts, *u_parts;
+  uint64_t split_stride;           // values between splits
+  uint32_t splits, rows, outs;
+  uint32_t act;
+  void *h, *g, *u;                 // g and u together, or neither
+  int64_t ld_h, ld_g, ld_u;
+};
+
+// A thread takes 4 neighbouring columns and adds the splits in order.
+template <int DT>
+__global__ void __launch_bounds__(256) gated_join_kernel(const GatedJoinParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t vecs = p.outs / 4u;
+  const uint64_t total = static_cast<uint64_t>(p.rows) * vecs, stride4 = p.split_stride / 4u;
+  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += static_cast<uint64_t>(gridDim.x) * blockDim.x) {
+    const uint64_t row = i / vecs;
+    const uint32_t v = static_cast<uint32_t>(i - row * vecs);
+    float g[4] = {}, u[4] = {};
+#pragma unroll 4
+    for (uint32_t s = 0; s < p.splits; ++s) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(p.g_parts) + i + s * stride4);
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(p.u_parts) + i + s * stride4);
+      g[0] += a.x, g[1] += a.y, g[2] += a.z, g[3] += a.w;
+      u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
+    }
+    auto put = [&](void* base, int64_t ld, const float (&f)[4]) {
+      uint2 o;
+      o.x = pack_out<DT>(__float_as_uint(f[0]), __float_as_uint(f[1]));
+      o.y = pack_out<DT>(__float_as_uint(f[2]), __float_as_uint(f[3]));
+      *reinterpret_cast<uint2*>(static_cast<char*>(base) +
+                                (static_cast<int64_t>(row) * ld + 4ll * v) * 2) = o;
+    };
+    if (p.g != nullptr) {
+      put(p.g, p.ld_g, g);
+      put(p.u, p.ld_u, u);
+    }
+    float h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = g[j] * gate_of(g[j], p.act).s * u[j];
+    put(p.h, p.ld_h, h);
+  }
+}
+
+}  // namespace tg

@@ -1,13 +1,15 @@
 // tg_gemm.cu -- instantiations and launchers of the sm_103a kernels behind the C ABI:
 // the persistent warp-specialized GEMM (fp16 and bf16, product and debug builds; single CTA,
 // CTA pair and wide CTA pair), the
-// block-scaled MXFP8 GEMM (single CTA and CTA pair), the weight gradient from an 8-bit checkpoint,
+// block-scaled MXFP8 GEMM (single CTA and CTA pair), the weight gradient from an 8-bit checkpoint, the
+// products with fused epilogues (tg_linear_launch.cuh),
 // the tile-schedule inspection kernel, and the zero fill used when K == 0.  All kernels share this translation unit's watchdog status word.
 #include "tg_gemm_kernel.cuh"
 #include "tg_gemm_pair_kernel.cuh"
 #include "tg_gemm_pair_wide_kernel.cuh"
 #include "tg_internal.h"
 #include "tg_launch.cuh"
+#include "tg_linear_launch.cuh"
 #include "tg_mx_kernel.cuh"
 #include "tg_mx_pack.cuh"
 #include "tg_mx_pair_kernel.cuh"

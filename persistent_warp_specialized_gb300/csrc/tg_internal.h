@@ -1,5 +1,6 @@
-// tg_internal.h -- interface between the C-ABI translation units (tg_api.cu, tg_train_api.cu) and
-// those that hold the kernels (tg_gemm.cu, tg_train.cu).  Not installed, not part of the ABI.
+// tg_internal.h -- interface between the C-ABI translation units (tg_api.cu, tg_train_api.cu,
+// tg_linear_api.cu) and those that hold the kernels (tg_gemm.cu, tg_train.cu).  Not installed, not
+// part of the ABI.
 #pragma once
 
 #include <cuda.h>
@@ -126,6 +127,85 @@ struct WgradLaunch {
 // Sets the kernels' shared memory limits; *max_pairs: how many of their CTA pairs are resident at once.
 cudaError_t prepare_wgrad_kernels(int* max_pairs);
 cudaError_t launch_wgrad(int dtype, bool debug, const WgradLaunch& l, cudaStream_t stream);
+
+// Products with fused epilogues (tg_linear_kernel.cuh).  Matrices, tile counts and segments as
+// LinearParams has them.
+struct LinearLaunch {
+  CUtensorMap a[2], b[2], c[3];
+  int dtype;
+  bool a_mn, b_mn;              // the operand lies with m (n) contiguous
+  int epi;                      // LinearEpi
+  uint32_t M, N;
+  uint32_t m_blocks, n_blocks, k_blocks, n_seg, k_seg, group, column_major;
+  uint32_t split_from, total_units, splits, blocks_per_split;   // units: per split
+  uint32_t partial, part_rows;
+  const float* alpha;
+  uint32_t act, keep;
+  const int64_t* targets;
+  uint32_t first_col, slots;
+  void* stats;
+  float* hit;
+  const float *lse, *weight;
+  uint32_t grid;                // CTAs
+  uint64_t watchdog_ns;
+  int64_t inject_skip_phase;
+};
+// Sets the kernels' shared memory limits; *max_pairs: how many of their CTA pairs are resident at once.
+cudaError_t prepare_linear_kernels(int* max_pairs);
+cudaError_t launch_linear(const LinearLaunch& l, cudaStream_t stream);
+
+// out [rows, cols] = alpha (null: 1) times the sum over splits of partials [splits][part_rows][cols]
+struct LinearJoin {
+  const float* partials;
+  uint32_t splits, part_rows, rows, cols;
+  const float* alpha;
+  void* out;
+  int64_t ld_out;
+  int dtype, sms;
+};
+cudaError_t launch_linear_join(const LinearJoin& l, cudaStream_t stream);
+
+// h = act(g) u of partial sums of g and u, each [splits][part_rows][outs]; g and u too where given
+struct GatedJoin {
+  const float *g_parts, *u_parts;
+  uint32_t splits, part_rows, rows, outs;
+  uint32_t act;
+  void *h, *g, *u;
+  int64_t ld_h, ld_g, ld_u;
+  int dtype, sms;
+};
+cudaError_t launch_gated_join(const GatedJoin& l, cudaStream_t stream);
+
+// dgu [rows, 2 outs] = (dh u act'(g), dh act(g)), side by side (tg_gated_kernel.cuh)
+struct GatedGrad {
+  const void *dh, *g, *u;
+  void* dgu;
+  int64_t rows, outs, ld_dh, ld_g, ld_u;
+  uint32_t act;
+  int dtype, sms;
+};
+cudaError_t launch_gated_grad(const GatedGrad& l, cudaStream_t stream);
+
+// Cross entropy (tg_xent_kernel.cuh): loss and lse of each row from its statistics; and the weight of
+// each row's gradient relative to the largest, with the factor that undoes that.
+struct XentJoin {
+  const void* stats;     // float2 [rows][slots]
+  const float* hit;
+  const int64_t* targets;
+  int64_t ignore;
+  float *loss, *lse;
+  uint32_t rows, slots, vocab;
+};
+cudaError_t launch_xent_join(const XentJoin& l, cudaStream_t stream);
+struct XentWeights {
+  const float* dloss;
+  const int64_t* targets;
+  int64_t ignore;
+  float *weight, *alpha;
+  uint32_t rows, vocab;
+  int dtype;
+};
+cudaError_t launch_xent_weights(const XentWeights& l, cudaStream_t stream);
 
 cudaError_t clear_watchdog_status(cudaStream_t stream);
 // synchronises ``stream``, returns the status word in *out and clears it

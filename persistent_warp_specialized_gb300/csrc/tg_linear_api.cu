@@ -1,0 +1,837 @@
+// tg_linear_api.cu -- the C ABI of the operators between the norm and the loss (include/tg.h): the
+// gated feed-forward projections, the cross entropy of a vocabulary projection, a linear layer's input
+// gradient.  Argument checks, plans of the products, workspaces and launches.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <initializer_list>
+
+#include "../../include/tg.h"
+#include "tg_api_checks.h"
+#include "tg_api_common.h"
+#include "tg_internal.h"
+#include "tg_linear_config.h"
+#include "tg_tile_scheduler.cuh"
+
+using namespace tg::abi;
+
+namespace {
+
+// A matrix as it lies in memory: ``rows`` rows of ``cols`` values, ``ld`` values apart.
+struct Mat {
+  const void* p = nullptr;
+  int64_t rows = 0, cols = 0, ld = 0;
+  const char* name = "";
+};
+
+// D[M, N] = A B, before its plan.  Two matrices may stand in an operand's place (tg_linear_kernel.cuh):
+// segs_n: N columns each of b[0], b[1] to c[0], c[1]; segs_k: K values each of a[i], b[i].
+struct Product {
+  int epi = tg::kEpiStore;
+  int dtype = 0;
+  bool a_mn = false, b_mn = false;
+  int64_t M = 0, N = 0, K = 0;
+  int segs_n = 1, segs_k = 1;
+  Mat a[2], b[2], c[3];
+  const float* alpha = nullptr;
+  // kEpiStore over several launches: 0 alone, 1 the first, 2 a later one, whose fp32 sums are added to
+  // the first's; the caller joins them after the last
+  int accumulate = 0;
+  uint32_t act = 0, keep = 0;
+  const int64_t* targets = nullptr;
+  uint32_t first_col = 0, slots = 0;
+  void* stats = nullptr;
+  float* hit = nullptr;
+  const float *lse = nullptr, *weight = nullptr;
+};
+
+// How a product is cut into units.
+struct Plan {
+  uint32_t m_tiles, n_tiles, n_seg, k_blocks, k_seg, splits, blocks_per_split, split_from, units,
+      pairs;
+  uint32_t part_rows;
+  uint64_t partial_bytes;   // fp32 sums of one N segment (0: results are stored rounded)
+  double us;                // what the plan is expected to take
+};
+
+// Microseconds on GB300 that the choice of a plan goes by: a k-block of a whole tile and of its
+// half-width unit, what a unit adds (its first loads, and its epilogue where the MMAs wait for it), the
+// join, and bytes of partial sums a microsecond, written and read.
+constexpr double kBlockUs = 0.66, kHalfBlockUs = 0.40, kUnitUs = 0.4, kJoinUs = 2.5;
+constexpr double kWriteBytes = 5e6, kReadBytes = 4e6;
+constexpr uint64_t kMinBlocks = 4;   // k-blocks of a unit when K is split
+
+Plan plan_of(const Product& p, uint64_t pairs, uint64_t splits, bool sums) {
+  Plan w;
+  w.m_tiles = static_cast<uint32_t>(ceil_div(p.M, tg::kPairBM));
+  const uint64_t tile_n = p.epi == tg::kEpiGated ? tg::kGatedTileN : tg::kBN;
+  w.n_seg = static_cast<uint32_t>(ceil_div(p.N, tile_n));
+  w.n_tiles = w.n_seg * p.segs_n;
+  w.k_seg = static_cast<uint32_t>(ceil_div(p.K, tg::kLinBK));
+  w.k_blocks = w.k_seg * p.segs_k;
+  const uint32_t tiles = w.m_tiles * w.n_tiles;
+  w.blocks_per_split = static_cast<uint32_t>(ceil_div(w.k_blocks, splits));
+  w.splits = static_cast<uint32_t>(ceil_div(w.k_blocks, w.blocks_per_split));
+  w.split_from = w.units = tiles;
+  if (w.splits == 1)
+    tg::PersistentTileScheduler::tail_split(tiles, static_cast<uint32_t>(pairs), w.split_from,
+                                            w.units);
+  const uint64_t all = static_cast<uint64_t>(w.units) * w.splits;
+  w.pairs = static_cast<uint32_t>(all < pairs ? all : pairs);
+  const double whole = static_cast<double>(ceil_div(w.split_from * uint64_t(w.splits), pairs));
+  w.us = whole * (w.blocks_per_split * kBlockUs + kUnitUs);
+  if (w.units > w.split_from) w.us += w.k_blocks * kHalfBlockUs + kUnitUs;
+  w.part_rows = static_cast<uint32_t>(ceil_div(p.M, tg::kPartialRows)) * tg::kPartialRows;
+  w.partial_bytes = 0;
+  if (w.splits > 1 || sums) {
+    w.partial_bytes = uint64_t(w.splits) * w.part_rows * p.N * 4;
+    const double bytes = double(w.splits) * p.M * p.N * p.segs_n * 4.0;
+    w.us += bytes / kWriteBytes + kJoinUs + bytes / kReadBytes;
+  }
+  return w;
+}
+
+// Fewer tiles than pairs: K may be split, so that every pair has a unit, at the price of partial sums
+// in fp32 and a join.  The least expected time decides.  sums: results go to partial sums in any case.
+Plan plan_product(const Product& p, int max_pairs, bool sums = false) {
+  const uint64_t pairs = static_cast<uint64_t>(max_pairs);
+  Plan best = plan_of(p, pairs, 1, sums);
+  if (p.epi != tg::kEpiStore) return best;
+  const uint64_t tiles = uint64_t(best.m_tiles) * best.n_tiles;
+  uint64_t most = pairs / tiles;
+  if (most > best.k_blocks / kMinBlocks) most = best.k_blocks / kMinBlocks;
+  for (uint64_t splits = 2; splits <= most; ++splits) {
+    const Plan cut = plan_of(p, pairs, splits, sums);
+    if (cut.us < best.us) best = cut;
+  }
+  return best;
+}
+
+constexpr uint64_t kWorkspaceAlign = 256;
+uint64_t padded(uint64_t bytes) { return ceil_div(bytes, kWorkspaceAlign) * kWorkspaceAlign; }
+
+CUtensorMapDataType type16(int dtype) {
+  return dtype == TG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// The operand ``m`` of a product: boxes of one 64-value atom of K by 128 rows, or of 64 columns by a
+// stage's rows of K.
+int encode_operand(CUtensorMap* map, const Mat& m, bool mn, int dtype) {
+  return encode_tiled(map, type16(dtype), 2, m.p, m.cols, m.rows, 64,
+                      mn ? tg::kLinBK : tg::kBM, m.name, true, m.ld * 2);
+}
+
+// Enqueues the product by its plan.  partials: fp32 sums of each N segment where the plan has them
+// (joined by the caller).
+int run_product(const Product& p, const Plan& w, void* const partials[2], uint64_t watchdog_ns,
+                int64_t inject, cudaStream_t stream) {
+  tg::LinearLaunch l = {};
+  for (int i = 0; i < 2; ++i) {
+    const Mat& a = p.a[p.segs_k == 2 ? i : 0];
+    const bool two_b = p.segs_k == 2 || p.segs_n == 2 || p.epi == tg::kEpiGated;
+    const Mat& b = p.b[two_b ? i : 0];
+    if (i == 0 || p.segs_k == 2) TG_TRY(encode_operand(&l.a[i], a, p.a_mn, p.dtype));
+    else l.a[i] = l.a[0];
+    if (i == 0 || two_b) TG_TRY(encode_operand(&l.b[i], b, p.b_mn, p.dtype));
+    else l.b[i] = l.b[0];
+  }
+  if (w.partial_bytes) {
+    for (int i = 0; i < p.segs_n; ++i)
+      TG_TRY(encode_tiled(&l.c[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, partials[i], p.N,
+                          uint64_t(w.splits) * w.part_rows, 32, tg::kPartialRows, "workspace"));
+    l.partial = p.accumulate == 2 ? 2 : 1;
+  } else {
+    for (int i = 0; i < 3; ++i)
+      if (p.c[i].p)
+        TG_TRY(encode_tiled(&l.c[i], type16(p.dtype), 2, p.c[i].p, p.c[i].cols, p.c[i].rows,
+                            tg::kEpiN, 32, p.c[i].name, true, p.c[i].ld * 2));
+  }
+  l.dtype = p.dtype;
+  l.a_mn = p.a_mn;
+  l.b_mn = p.b_mn;
+  l.epi = p.epi;
+  l.M = static_cast<uint32_t>(p.M);
+  l.N = static_cast<uint32_t>(p.N);
+  l.m_blocks = w.m_tiles;
+  l.n_blocks = w.n_tiles;
+  l.k_blocks = w.k_blocks;
+  l.n_seg = w.n_seg;
+  l.k_seg = w.k_seg;
+  l.group = tg::kGroup;
+  l.column_major = 0;
+  l.split_from = w.split_from;
+  l.total_units = w.units;
+  l.splits = w.splits;
+  l.blocks_per_split = w.blocks_per_split;
+  l.part_rows = w.part_rows;
+  l.alpha = p.alpha;
+  l.act = p.act;
+  l.keep = p.keep;
+  l.targets = p.targets;
+  l.first_col = p.first_col;
+  l.slots = p.slots;
+  l.stats = p.stats;
+  l.hit = p.hit;
+  l.lse = p.lse;
+  l.weight = p.weight;
+  l.grid = 2 * w.pairs;
+  // a k-block of this kernel is two of the 64-deep ones that the default limit counts
+  l.watchdog_ns = watchdog_ns ? watchdog_ns : default_watchdog_ns(2 * w.k_blocks);
+  l.inject_skip_phase = inject;
+  const cudaError_t e = tg::launch_linear(l, stream);
+  return e == cudaSuccess ? TG_OK : fail_cuda("product launch", e);
+}
+
+// Adds the partial sums of a product's N segments into its outputs.
+int join_product(const Product& p, const Plan& w, void* const partials[2], int sms,
+                 cudaStream_t stream) {
+  for (int i = 0; i < p.segs_n; ++i) {
+    tg::LinearJoin j;
+    j.partials = static_cast<const float*>(partials[i]);
+    j.splits = w.splits;
+    j.part_rows = w.part_rows;
+    j.rows = static_cast<uint32_t>(p.M);
+    j.cols = static_cast<uint32_t>(p.N);
+    j.alpha = p.alpha;
+    j.out = const_cast<void*>(p.c[i].p);
+    j.ld_out = p.c[i].ld;
+    j.dtype = p.dtype;
+    j.sms = sms;
+    const cudaError_t e = tg::launch_linear_join(j, stream);
+    if (e != cudaSuccess) return fail_cuda("join launch", e);
+  }
+  return TG_OK;
+}
+
+// A product by itself: its units, and the join of its partial sums at ``ws`` where it has them.
+int whole_product(const Product& p, const Plan& w, void* ws, int sms, cudaStream_t stream,
+                  uint64_t watchdog_ns = 0, int64_t inject = -1) {
+  void* const partials[2] = {ws, static_cast<char*>(ws) + padded(w.partial_bytes)};
+  TG_TRY(run_product(p, w, partials, watchdog_ns, inject, stream));
+  return w.partial_bytes ? join_product(p, w, partials, sms, stream) : TG_OK;
+}
+
+uint64_t partials_of(const Product& p, const Plan& w) {
+  return w.partial_bytes ? p.segs_n * padded(w.partial_bytes) : 0;
+}
+
+// ---------------------------------------------------------------- checks
+int check_dtype16(int dtype) {
+  if (dtype != TG_F16 && dtype != TG_BF16) return fail(TG_ERR_ARG, "unknown dtype %d", dtype);
+  return TG_OK;
+}
+
+// Sizes of a layer: multiples of 8 along the contiguous rows of every matrix.
+int check_layer(int64_t rows, int64_t cols, int64_t outs) {
+  TG_TRY(check_sizes(rows, cols));
+  if (outs < 0 || outs > kMaxDim)
+    return fail(TG_ERR_ARG, "outs=%lld must be in [0, 2^31)", (long long)outs);
+  if (cols % 8 != 0 || outs % 8 != 0)
+    return fail(TG_ERR_ALIGN, "cols=%lld and outs=%lld must be multiples of 8 (16-byte rows)",
+                (long long)cols, (long long)outs);
+  return TG_OK;
+}
+
+int check_tiles(int64_t m, int64_t n, int64_t segs = 1) {
+  if (ceil_div(m, 128) * ceil_div(n, 128) * segs > static_cast<uint64_t>(kMaxDim))
+    return fail(TG_ERR_ARG, "too many output tiles");
+  return TG_OK;
+}
+
+struct Ld {
+  int64_t ld, cols;
+  const char* name;
+};
+int check_lds(std::initializer_list<Ld> lds) {
+  for (const Ld& l : lds) {
+    TG_TRY(check_ld(l.ld, l.cols, l.name));
+    if (l.ld % 8 != 0)
+      return fail(TG_ERR_ALIGN, "%s=%lld must be a multiple of 8 (16-byte rows)", l.name,
+                  (long long)l.ld);
+  }
+  return TG_OK;
+}
+
+int check_mats(std::initializer_list<Mat> mats) {
+  for (const Mat& m : mats)
+    if (m.rows > 0 && m.cols > 0) TG_TRY(check_array(m.p, 16, m.name));
+  return TG_OK;
+}
+
+Region region(const Mat& m) {
+  return matrix(m.rows > 0 && m.cols > 0 ? m.p : nullptr, m.rows, m.cols, m.ld, 2, m.name);
+}
+
+int check_workspace(const void* ws, int64_t bytes, uint64_t need) {
+  if (bytes < 0) return fail(TG_ERR_ARG, "negative workspace size");
+  if (need == 0) return TG_OK;
+  if (!ws || static_cast<uint64_t>(bytes) < need)
+    return fail(TG_ERR_ARG, "workspace of %lld bytes; this call needs %llu",
+                (long long)(ws ? bytes : 0), (unsigned long long)need);
+  return check_array(ws, kWorkspaceAlign, "workspace");
+}
+
+// C = 0 for a matrix with 16-bit values
+int zero_fill(const Mat& m, cudaStream_t stream) {
+  if (m.rows == 0 || m.cols == 0) return TG_OK;
+  const cudaError_t e =
+      cudaMemset2DAsync(const_cast<void*>(m.p), m.ld * 2, 0, m.cols * 2, m.rows, stream);
+  return e == cudaSuccess ? TG_OK : fail_cuda("zero fill", e);
+}
+
+int watchdog_result(cudaStream_t stream) {
+  unsigned int word = 0;
+  const cudaError_t e = tg::read_and_clear_watchdog_status(&word, stream);
+  if (e != cudaSuccess) return fail_cuda("execution", e);
+  if (word)
+    return fail(TG_ERR_TIMEOUT, "watchdog: a wait gave up (roles 0x%x: 1 producer, 2 MMA, "
+                "4 epilogue, 8 shutdown)", word);
+  return TG_OK;
+}
+
+// ---------------------------------------------------------------- input gradient
+// dX [rows, cols] = dY [rows, outs] W^T, W [cols, outs]: K = outs, contiguous in both operands
+Product input_grad_product(const Mat& dy, const Mat& w, const Mat& dx, int dtype) {
+  Product p;
+  p.dtype = dtype;
+  p.M = dx.rows;
+  p.N = dx.cols;
+  p.K = dy.cols;
+  p.a[0] = dy;
+  p.b[0] = w;
+  p.c[0] = dx;
+  return p;
+}
+
+int input_grad_impl(const void* dy, const void* w, void* dx, int64_t rows, int64_t cols,
+                    int64_t outs, int64_t ld_dy, int64_t ld_w, int64_t ld_dx, int dtype, void* ws,
+                    int64_t ws_bytes, void* stream, bool debug, uint64_t watchdog_ns,
+                    int64_t inject) {
+  TG_TRY(check_dtype16(dtype));
+  TG_TRY(check_layer(rows, cols, outs));
+  TG_TRY(check_tiles(rows, cols));
+  TG_TRY(check_lds({{ld_dy, outs, "ld_dy"}, {ld_w, outs, "ld_w"}, {ld_dx, cols, "ld_dx"}}));
+  TG_TRY(check_workspace(nullptr, ws_bytes, 0));
+  if (rows == 0 || cols == 0) return TG_OK;
+  const Mat mdy = {dy, rows, outs, ld_dy, "dY"}, mw = {w, cols, outs, ld_w, "W"},
+            mdx = {dx, rows, cols, ld_dx, "dX"};
+  TG_TRY(check_mats({mdx, mdy, mw}));
+  int sms = 0, pairs = 0;
+  TG_TRY(linear_ready(&sms, &pairs));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (outs == 0) return zero_fill(mdx, st);
+  const Product p = input_grad_product(mdy, mw, mdx, dtype);
+  const Plan plan = plan_product(p, pairs);
+  const uint64_t need = partials_of(p, plan);
+  TG_TRY(check_workspace(ws, ws_bytes, need));
+  const Region r[] = {region(mdx), {need ? ws : nullptr, need, "workspace"}, region(mdy), region(mw)};
+  TG_TRY(check_apart(r, 2, 4));
+  if (debug) {
+    const cudaError_t e = tg::clear_watchdog_status(st);
+    if (e != cudaSuccess) return fail_cuda("clearing the watchdog word", e);
+  }
+  TG_TRY(whole_product(p, plan, ws, sms, st, watchdog_ns, inject));
+  return debug ? watchdog_result(st) : TG_OK;
+}
+
+// ---------------------------------------------------------------- gated feed-forward projections
+int check_act(int act) {
+  if (act != TG_ACT_SILU && act != TG_ACT_GELU)
+    return fail(TG_ERR_ARG, "unknown activation %d", act);
+  return TG_OK;
+}
+
+// g and u by one MMA side by side, or, with K split, as two N segments whose sums are joined
+struct GatedPlan {
+  Product p;
+  Plan plan;
+};
+GatedPlan gated_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& h, int dtype,
+                     int pairs) {
+  GatedPlan o;
+  Product& p = o.p;
+  p.epi = tg::kEpiGated;
+  p.dtype = dtype;
+  p.b_mn = true;
+  p.M = x.rows;
+  p.N = h.cols;
+  p.K = x.cols;
+  p.a[0] = x;
+  p.b[0] = wg;
+  p.b[1] = wu;
+  p.c[0] = h;
+  o.plan = plan_product(p, pairs);
+  Product two = p;
+  two.epi = tg::kEpiStore;
+  two.segs_n = 2;
+  const Plan cut = plan_product(two, pairs);
+  if (cut.splits > 1 && cut.us < o.plan.us) {
+    o.p = two;
+    o.plan = cut;
+  }
+  return o;
+}
+
+struct GatedBwd {
+  Product dx, dw;
+  Plan dx_plan, dw_plan;
+  uint64_t dgu_bytes, total;   // total: and the larger of the products' partial sums
+};
+// With null pointers where only sizes matter.
+GatedBwd gated_bwd_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& dx, const Mat& dwg,
+                        const Mat& dwu, void* dgu, int dtype, int pairs) {
+  GatedBwd o;
+  const int64_t rows = x.rows, cols = x.cols, outs = wg.cols;
+  const Mat dg = {dgu, rows, outs, 2 * outs, "dg"};
+  const Mat du = {dgu ? static_cast<char*>(dgu) + 2 * outs : nullptr, rows, outs, 2 * outs, "du"};
+  // dX = dg Wg^T + du Wu^T: K in two segments
+  o.dx.dtype = dtype;
+  o.dx.M = rows;
+  o.dx.N = cols;
+  o.dx.K = outs;
+  o.dx.segs_k = 2;
+  o.dx.a[0] = dg;
+  o.dx.a[1] = du;
+  o.dx.b[0] = wg;
+  o.dx.b[1] = wu;
+  o.dx.c[0] = dx;
+  o.dx_plan = plan_product(o.dx, pairs);
+  // dWg = X^T dg, dWu = X^T du: N in two segments
+  o.dw.dtype = dtype;
+  o.dw.a_mn = o.dw.b_mn = true;
+  o.dw.M = cols;
+  o.dw.N = outs;
+  o.dw.K = rows;
+  o.dw.segs_n = 2;
+  o.dw.a[0] = x;
+  o.dw.b[0] = dg;
+  o.dw.b[1] = du;
+  o.dw.c[0] = dwg;
+  o.dw.c[1] = dwu;
+  o.dw_plan = plan_product(o.dw, pairs);
+  o.dgu_bytes = padded(uint64_t(rows) * 2 * outs * 2);
+  const uint64_t a = partials_of(o.dx, o.dx_plan), b = partials_of(o.dw, o.dw_plan);
+  o.total = o.dgu_bytes + (a > b ? a : b);
+  return o;
+}
+
+// ---------------------------------------------------------------- cross entropy
+constexpr uint64_t kXentChunkBytes = 256u << 20;   // gradients of logits held at a time
+constexpr int64_t kXentMinChunk = 2048;
+
+int check_xent(int64_t rows, int64_t cols, int64_t vocab, int64_t ld_x, int64_t ld_w, int dtype) {
+  TG_TRY(check_dtype16(dtype));
+  TG_TRY(check_sizes(rows, cols));
+  if (vocab < 1 || vocab > kMaxDim)
+    return fail(TG_ERR_ARG, "vocab=%lld must be in [1, 2^31)", (long long)vocab);
+  if (cols == 0) return fail(TG_ERR_ARG, "cols must be at least 8");
+  if (cols % 8 != 0)
+    return fail(TG_ERR_ALIGN, "cols=%lld must be a multiple of 8 (16-byte rows)", (long long)cols);
+  TG_TRY(check_lds({{ld_x, cols, "ld_x"}, {ld_w, cols, "ld_w"}}));
+  return check_tiles(rows, vocab);
+}
+
+struct XentFwd {
+  uint32_t slots;
+  uint64_t stats_bytes, total;
+};
+XentFwd xent_fwd_plan(int64_t rows, int64_t vocab) {
+  XentFwd o;
+  o.slots = static_cast<uint32_t>(ceil_div(vocab, tg::kStatCols));
+  o.stats_bytes = padded(uint64_t(rows) * o.slots * 8);
+  o.total = o.stats_bytes + padded(uint64_t(rows) * 4);
+  return o;
+}
+
+// logits of columns [first, first + n) of the vocabulary, W's rows
+Product logits_product(int epi, const Mat& x, const Mat& w, int64_t first, int64_t n,
+                       const int64_t* targets, int dtype) {
+  Product p;
+  p.epi = epi;
+  p.dtype = dtype;
+  p.M = x.rows;
+  p.N = n;
+  p.K = x.cols;
+  p.a[0] = x;
+  p.b[0] = {static_cast<const char*>(w.p) + first * w.ld * 2, n, w.cols, w.ld, w.name};
+  p.targets = targets;
+  p.first_col = static_cast<uint32_t>(first);
+  return p;
+}
+
+// The gradients, a piece of ``chunk`` columns of the vocabulary at a time: the gradients of the piece's
+// logits, its rows of dW, and its share of dX, whose fp32 sums run over the pieces.
+struct XentBwd {
+  int64_t chunk, chunks;
+  bool sums;                // dX is summed in fp32 over the pieces
+  uint64_t dl_bytes, row_bytes, dx_bytes, dw_bytes, total;
+};
+
+Product xent_dx_product(const Mat& dl, const Mat& w, int64_t first, const Mat& dx, int dtype) {
+  Product p;
+  p.dtype = dtype;
+  p.b_mn = true;
+  p.M = dl.rows;
+  p.N = dx.cols;
+  p.K = dl.cols;
+  p.a[0] = dl;
+  p.b[0] = {static_cast<const char*>(w.p) + first * w.ld * 2, dl.cols, w.cols, w.ld, w.name};
+  p.c[0] = dx;
+  return p;
+}
+
+Product xent_dw_product(const Mat& dl, const Mat& x, const Mat& dw, int64_t first, int dtype) {
+  Product p;
+  p.dtype = dtype;
+  p.a_mn = p.b_mn = true;
+  p.M = dl.cols;
+  p.N = x.cols;
+  p.K = dl.rows;
+  p.a[0] = dl;
+  p.b[0] = x;
+  p.c[0] = {static_cast<const char*>(dw.p) + first * dw.ld * 2, dl.cols, dw.cols, dw.ld, dw.name};
+  return p;
+}
+
+XentBwd xent_bwd_plan(int64_t rows, int64_t cols, int64_t vocab, int dtype, int pairs) {
+  XentBwd o;
+  int64_t most = static_cast<int64_t>(kXentChunkBytes / (uint64_t(rows) * 2)) / tg::kBN * tg::kBN;
+  if (most < kXentMinChunk) most = kXentMinChunk;
+  o.chunks = static_cast<int64_t>(ceil_div(vocab, most));
+  o.chunk = static_cast<int64_t>(ceil_div(ceil_div(vocab, o.chunks), tg::kBN)) * tg::kBN;
+  o.chunks = static_cast<int64_t>(ceil_div(vocab, o.chunk));
+  o.sums = o.chunks > 1;
+  const int64_t n = o.chunks > 1 ? o.chunk : vocab;
+  const Mat dl = {nullptr, rows, n, o.chunk, ""}, x = {nullptr, rows, cols, cols, ""},
+            w = {nullptr, vocab, cols, cols, ""};
+  o.dl_bytes = padded(uint64_t(rows) * o.chunk * 2);
+  o.row_bytes = padded(uint64_t(rows) * 4);
+  const Product dx = xent_dx_product(dl, w, 0, x, dtype), dw = xent_dw_product(dl, x, w, 0, dtype);
+  o.dx_bytes = partials_of(dx, plan_product(dx, pairs, o.sums));
+  o.dw_bytes = partials_of(dw, plan_product(dw, pairs));
+  // the last piece may be narrower and split its tokens more finely
+  if (o.chunks > 1) {
+    const Mat last = {nullptr, rows, vocab - (o.chunks - 1) * o.chunk, o.chunk, ""};
+    const Product dwl = xent_dw_product(last, x, w, 0, dtype);
+    const uint64_t b = partials_of(dwl, plan_product(dwl, pairs));
+    if (b > o.dw_bytes) o.dw_bytes = b;
+  }
+  o.total = o.dl_bytes + o.row_bytes + kWorkspaceAlign + o.dx_bytes + o.dw_bytes;
+  return o;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t tg_input_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t outs) {
+  TG_TRY(check_layer(rows, cols, outs));
+  TG_TRY(check_tiles(rows, cols));
+  if (rows == 0 || cols == 0 || outs == 0) return 0;
+  int pairs = 0;
+  TG_TRY(linear_ready(nullptr, &pairs));
+  const Product p = input_grad_product({nullptr, rows, outs, outs, ""}, {nullptr, cols, outs, outs, ""},
+                                       {nullptr, rows, cols, cols, ""}, TG_BF16);
+  return static_cast<int64_t>(partials_of(p, plan_product(p, pairs)));
+}
+
+int tg_input_grad(const void* dY_dev, const void* W_dev, void* dX_dev, int64_t rows, int64_t cols,
+                  int64_t outs, int64_t ld_dy, int64_t ld_w, int64_t ld_dx, int dtype,
+                  void* workspace_dev, int64_t workspace_bytes, void* stream) {
+  return input_grad_impl(dY_dev, W_dev, dX_dev, rows, cols, outs, ld_dy, ld_w, ld_dx, dtype,
+                         workspace_dev, workspace_bytes, stream, false, 0, -1);
+}
+
+int tg_input_grad_debug(const void* dY_dev, const void* W_dev, void* dX_dev, int64_t rows,
+                        int64_t cols, int64_t outs, int64_t ld_dy, int64_t ld_w, int64_t ld_dx,
+                        int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream,
+                        uint64_t watchdog_ns, int64_t inject_skip_phase) {
+  return input_grad_impl(dY_dev, W_dev, dX_dev, rows, cols, outs, ld_dy, ld_w, ld_dx, dtype,
+                         workspace_dev, workspace_bytes, stream, true, watchdog_ns,
+                         inject_skip_phase);
+}
+
+int64_t tg_gated_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t outs) {
+  TG_TRY(check_layer(rows, cols, outs));
+  TG_TRY(check_tiles(rows, outs, 2));
+  if (rows == 0 || cols == 0 || outs == 0) return 0;
+  int pairs = 0;
+  TG_TRY(linear_ready(nullptr, &pairs));
+  const Mat w = {nullptr, cols, outs, outs, ""};
+  const GatedPlan o = gated_plan({nullptr, rows, cols, cols, ""}, w, w,
+                                 {nullptr, rows, outs, outs, ""}, TG_BF16, pairs);
+  return static_cast<int64_t>(partials_of(o.p, o.plan));
+}
+
+int tg_gated_fwd(const void* x_dev, const void* wg_dev, const void* wu_dev, void* h_dev,
+                 void* g_dev, void* u_dev, int64_t rows, int64_t cols, int64_t outs, int64_t ld_x,
+                 int64_t ld_wg, int64_t ld_wu, int64_t ld_h, int64_t ld_g, int64_t ld_u, int act,
+                 int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream) {
+  TG_TRY(check_dtype16(dtype));
+  TG_TRY(check_act(act));
+  TG_TRY(check_layer(rows, cols, outs));
+  TG_TRY(check_tiles(rows, outs, 2));
+  const bool keep = g_dev || u_dev;
+  if (keep && !(g_dev && u_dev)) return fail(TG_ERR_ARG, "g and u are kept together or not at all");
+  TG_TRY(check_lds({{ld_x, cols, "ld_x"}, {ld_wg, outs, "ld_wg"}, {ld_wu, outs, "ld_wu"},
+                    {ld_h, outs, "ld_h"}}));
+  if (keep) TG_TRY(check_lds({{ld_g, outs, "ld_g"}, {ld_u, outs, "ld_u"}}));
+  TG_TRY(check_workspace(nullptr, workspace_bytes, 0));
+  if (rows == 0 || outs == 0) return TG_OK;
+  const Mat x = {x_dev, rows, cols, ld_x, "x"}, wg = {wg_dev, cols, outs, ld_wg, "wg"},
+            wu = {wu_dev, cols, outs, ld_wu, "wu"}, h = {h_dev, rows, outs, ld_h, "h"},
+            g = {g_dev, keep ? rows : 0, outs, ld_g, "g"}, u = {u_dev, keep ? rows : 0, outs, ld_u, "u"};
+  TG_TRY(check_mats({h, g, u, x, wg, wu}));
+  int sms = 0, pairs = 0;
+  TG_TRY(linear_ready(&sms, &pairs));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cols == 0) {
+    for (const Mat& m : {h, g, u}) TG_TRY(zero_fill(m, st));
+    return TG_OK;
+  }
+  GatedPlan o = gated_plan(x, wg, wu, h, dtype, pairs);
+  const uint64_t need = partials_of(o.p, o.plan);
+  TG_TRY(check_workspace(workspace_dev, workspace_bytes, need));
+  const Region r[] = {region(h), region(g), region(u), {need ? workspace_dev : nullptr, need, "workspace"},
+                      region(x), region(wg), region(wu)};
+  TG_TRY(check_apart(r, 4, 7));
+  if (!need) {
+    o.p.act = act;
+    o.p.keep = keep;
+    o.p.c[1] = g;
+    o.p.c[2] = u;
+    return whole_product(o.p, o.plan, nullptr, sms, st);
+  }
+  void* const partials[2] = {workspace_dev,
+                             static_cast<char*>(workspace_dev) + padded(o.plan.partial_bytes)};
+  TG_TRY(run_product(o.p, o.plan, partials, 0, -1, st));
+  tg::GatedJoin j;
+  j.g_parts = static_cast<const float*>(partials[0]);
+  j.u_parts = static_cast<const float*>(partials[1]);
+  j.splits = o.plan.splits;
+  j.part_rows = o.plan.part_rows;
+  j.rows = static_cast<uint32_t>(rows);
+  j.outs = static_cast<uint32_t>(outs);
+  j.act = act;
+  j.h = h_dev;
+  j.g = g_dev;
+  j.u = u_dev;
+  j.ld_h = ld_h;
+  j.ld_g = ld_g;
+  j.ld_u = ld_u;
+  j.dtype = dtype;
+  j.sms = sms;
+  const cudaError_t e = tg::launch_gated_join(j, st);
+  return e == cudaSuccess ? TG_OK : fail_cuda("join launch", e);
+}
+
+int64_t tg_gated_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t outs) {
+  TG_TRY(check_layer(rows, cols, outs));
+  TG_TRY(check_tiles(rows, cols));
+  TG_TRY(check_tiles(cols, outs, 2));
+  if (rows == 0 || cols == 0 || outs == 0) return 0;
+  int pairs = 0;
+  TG_TRY(linear_ready(nullptr, &pairs));
+  const Mat x = {nullptr, rows, cols, cols, ""}, w = {nullptr, cols, outs, outs, ""};
+  return static_cast<int64_t>(gated_bwd_plan(x, w, w, x, w, w, nullptr, TG_BF16, pairs).total);
+}
+
+int tg_gated_bwd(const void* dh_dev, const void* g_dev, const void* u_dev, const void* x_dev,
+                 const void* wg_dev, const void* wu_dev, void* dx_dev, void* dwg_dev, void* dwu_dev,
+                 int64_t rows, int64_t cols, int64_t outs, int64_t ld_dh, int64_t ld_g,
+                 int64_t ld_u, int64_t ld_x, int64_t ld_wg, int64_t ld_wu, int64_t ld_dx,
+                 int64_t ld_dwg, int64_t ld_dwu, int act, int dtype, void* workspace_dev,
+                 int64_t workspace_bytes, void* stream) {
+  TG_TRY(check_dtype16(dtype));
+  TG_TRY(check_act(act));
+  TG_TRY(check_layer(rows, cols, outs));
+  TG_TRY(check_tiles(rows, cols));
+  TG_TRY(check_tiles(cols, outs, 2));
+  const bool weights = dwg_dev || dwu_dev;
+  if (weights && !(dwg_dev && dwu_dev))
+    return fail(TG_ERR_ARG, "dwg and dwu are asked for together or not at all");
+  TG_TRY(check_lds({{ld_dh, outs, "ld_dh"}, {ld_g, outs, "ld_g"}, {ld_u, outs, "ld_u"}}));
+  if (weights)
+    TG_TRY(check_lds({{ld_x, cols, "ld_x"}, {ld_dwg, outs, "ld_dwg"}, {ld_dwu, outs, "ld_dwu"}}));
+  if (dx_dev)
+    TG_TRY(check_lds({{ld_wg, outs, "ld_wg"}, {ld_wu, outs, "ld_wu"}, {ld_dx, cols, "ld_dx"}}));
+  TG_TRY(check_workspace(nullptr, workspace_bytes, 0));
+  if (cols == 0 || (!dx_dev && !weights)) return TG_OK;
+  const int64_t x_rows = weights ? rows : 0, w_rows = dx_dev ? cols : 0;
+  const Mat dh = {dh_dev, rows, outs, ld_dh, "dh"}, g = {g_dev, rows, outs, ld_g, "g"},
+            u = {u_dev, rows, outs, ld_u, "u"}, x = {x_dev, x_rows, cols, ld_x, "x"},
+            wg = {wg_dev, w_rows, outs, ld_wg, "wg"}, wu = {wu_dev, w_rows, outs, ld_wu, "wu"},
+            dx = {dx_dev, dx_dev ? rows : 0, cols, ld_dx, "dx"},
+            dwg = {dwg_dev, weights ? cols : 0, outs, ld_dwg, "dwg"},
+            dwu = {dwu_dev, weights ? cols : 0, outs, ld_dwu, "dwu"};
+  TG_TRY(check_mats({dx, dwg, dwu, dh, g, u, x, wg, wu}));
+  int sms = 0, pairs = 0;
+  TG_TRY(linear_ready(&sms, &pairs));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0 || outs == 0) {
+    for (const Mat& m : {dx, dwg, dwu}) TG_TRY(zero_fill(m, st));
+    return TG_OK;
+  }
+  const Mat sx = {x_dev, rows, cols, ld_x, "x"}, swg = {wg_dev, cols, outs, ld_wg, "wg"},
+            swu = {wu_dev, cols, outs, ld_wu, "wu"};   // sizes whether asked for or not
+  const GatedBwd o = gated_bwd_plan(sx, swg, swu, dx, dwg, dwu, workspace_dev, dtype, pairs);
+  TG_TRY(check_workspace(workspace_dev, workspace_bytes, o.total));
+  const Region r[] = {region(dx), region(dwg), region(dwu), {workspace_dev, o.total, "workspace"},
+                      region(dh), region(g), region(u), region(x), region(wg), region(wu)};
+  TG_TRY(check_apart(r, 4, 10));
+  tg::GatedGrad e;
+  e.dh = dh_dev;
+  e.g = g_dev;
+  e.u = u_dev;
+  e.dgu = workspace_dev;
+  e.rows = rows;
+  e.outs = outs;
+  e.ld_dh = ld_dh;
+  e.ld_g = ld_g;
+  e.ld_u = ld_u;
+  e.act = act;
+  e.dtype = dtype;
+  e.sms = sms;
+  const cudaError_t err = tg::launch_gated_grad(e, st);
+  if (err != cudaSuccess) return fail_cuda("gated gradient launch", err);
+  void* rest = static_cast<char*>(workspace_dev) + o.dgu_bytes;
+  if (dx_dev) TG_TRY(whole_product(o.dx, o.dx_plan, rest, sms, st));
+  if (weights) TG_TRY(whole_product(o.dw, o.dw_plan, rest, sms, st));
+  return TG_OK;
+}
+
+int64_t tg_xent_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab) {
+  TG_TRY(check_xent(rows, cols, vocab, cols, cols, TG_BF16));
+  return rows == 0 ? 0 : static_cast<int64_t>(xent_fwd_plan(rows, vocab).total);
+}
+
+int tg_xent_fwd(const void* x_dev, const void* w_dev, const int64_t* targets_dev, float* loss_dev,
+                float* lse_dev, int64_t rows, int64_t cols, int64_t vocab, int64_t ld_x,
+                int64_t ld_w, int64_t ignore_index, int dtype, void* workspace_dev,
+                int64_t workspace_bytes, void* stream) {
+  TG_TRY(check_xent(rows, cols, vocab, ld_x, ld_w, dtype));
+  TG_TRY(check_workspace(nullptr, workspace_bytes, 0));
+  if (rows == 0) return TG_OK;
+  const Mat x = {x_dev, rows, cols, ld_x, "x"}, w = {w_dev, vocab, cols, ld_w, "w"};
+  TG_TRY(check_array(loss_dev, 4, "loss"));
+  TG_TRY(check_array(lse_dev, 4, "lse"));
+  TG_TRY(check_mats({x, w}));
+  TG_TRY(check_array(targets_dev, 8, "targets"));
+  int sms = 0, pairs = 0;
+  TG_TRY(linear_ready(&sms, &pairs));
+  const XentFwd o = xent_fwd_plan(rows, vocab);
+  TG_TRY(check_workspace(workspace_dev, workspace_bytes, o.total));
+  const uint64_t row4 = uint64_t(rows) * 4;
+  const Region r[] = {{loss_dev, row4, "loss"}, {lse_dev, row4, "lse"},
+                      {workspace_dev, o.total, "workspace"}, region(x), region(w),
+                      {targets_dev, uint64_t(rows) * 8, "targets"}};
+  TG_TRY(check_apart(r, 3, 6));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Product p = logits_product(tg::kEpiStats, x, w, 0, vocab, targets_dev, dtype);
+  p.stats = workspace_dev;
+  p.slots = o.slots;
+  p.hit = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + o.stats_bytes);
+  TG_TRY(whole_product(p, plan_product(p, pairs), nullptr, sms, st));
+  tg::XentJoin j;
+  j.stats = p.stats;
+  j.hit = p.hit;
+  j.targets = targets_dev;
+  j.ignore = ignore_index;
+  j.loss = loss_dev;
+  j.lse = lse_dev;
+  j.rows = static_cast<uint32_t>(rows);
+  j.slots = o.slots;
+  j.vocab = static_cast<uint32_t>(vocab);
+  const cudaError_t e = tg::launch_xent_join(j, st);
+  return e == cudaSuccess ? TG_OK : fail_cuda("cross entropy launch", e);
+}
+
+int64_t tg_xent_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab) {
+  TG_TRY(check_xent(rows, cols, vocab, cols, cols, TG_BF16));
+  TG_TRY(check_tiles(vocab, cols));
+  if (rows == 0) return 0;
+  int pairs = 0;
+  TG_TRY(linear_ready(nullptr, &pairs));
+  return static_cast<int64_t>(xent_bwd_plan(rows, cols, vocab, TG_BF16, pairs).total);
+}
+
+int tg_xent_bwd(const float* dloss_dev, const void* x_dev, const void* w_dev,
+                const int64_t* targets_dev, const float* lse_dev, void* dx_dev, void* dw_dev,
+                int64_t rows, int64_t cols, int64_t vocab, int64_t ld_x, int64_t ld_w,
+                int64_t ld_dx, int64_t ld_dw, int64_t ignore_index, int dtype,
+                void* workspace_dev, int64_t workspace_bytes, void* stream) {
+  TG_TRY(check_xent(rows, cols, vocab, ld_x, ld_w, dtype));
+  TG_TRY(check_tiles(vocab, cols));
+  if (dx_dev) TG_TRY(check_lds({{ld_dx, cols, "ld_dx"}}));
+  if (dw_dev) TG_TRY(check_lds({{ld_dw, cols, "ld_dw"}}));
+  TG_TRY(check_workspace(nullptr, workspace_bytes, 0));
+  if (!dx_dev && !dw_dev) return TG_OK;
+  const Mat x = {x_dev, rows, cols, ld_x, "x"}, w = {w_dev, vocab, cols, ld_w, "w"},
+            dx = {dx_dev, dx_dev ? rows : 0, cols, ld_dx, "dx"},
+            dw = {dw_dev, dw_dev ? vocab : 0, cols, ld_dw, "dw"};
+  TG_TRY(check_mats({dx, dw}));
+  if (rows > 0) {
+    TG_TRY(check_mats({x, w}));
+    TG_TRY(check_array(targets_dev, 8, "targets"));
+    TG_TRY(check_array(dloss_dev, 4, "dloss"));
+    TG_TRY(check_array(lse_dev, 4, "lse"));
+  }
+  int sms = 0, pairs = 0;
+  TG_TRY(linear_ready(&sms, &pairs));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) return zero_fill(dw, st);
+  const XentBwd o = xent_bwd_plan(rows, cols, vocab, dtype, pairs);
+  TG_TRY(check_workspace(workspace_dev, workspace_bytes, o.total));
+  const uint64_t row4 = uint64_t(rows) * 4;
+  const Region r[] = {region(dx), region(dw), {workspace_dev, o.total, "workspace"}, region(x),
+                      region(w), {targets_dev, uint64_t(rows) * 8, "targets"},
+                      {dloss_dev, row4, "dloss"}, {lse_dev, row4, "lse"}};
+  TG_TRY(check_apart(r, 3, 8));
+  char* base = static_cast<char*>(workspace_dev);
+  float* weight = reinterpret_cast<float*>(base + o.dl_bytes);
+  float* alpha = reinterpret_cast<float*>(base + o.dl_bytes + o.row_bytes);
+  char* dx_sums = base + o.dl_bytes + o.row_bytes + kWorkspaceAlign;
+  char* dw_sums = dx_sums + o.dx_bytes;
+  tg::XentWeights xw;
+  xw.dloss = dloss_dev;
+  xw.targets = targets_dev;
+  xw.ignore = ignore_index;
+  xw.weight = weight;
+  xw.alpha = alpha;
+  xw.rows = static_cast<uint32_t>(rows);
+  xw.vocab = static_cast<uint32_t>(vocab);
+  xw.dtype = dtype;
+  const cudaError_t e = tg::launch_xent_weights(xw, st);
+  if (e != cudaSuccess) return fail_cuda("cross entropy launch", e);
+  Plan dx_plan = {};
+  Product dx_product;
+  void* const dx_partials[2] = {dx_sums, nullptr};
+  for (int64_t c = 0; c < o.chunks; ++c) {
+    const int64_t first = c * o.chunk, n = vocab - first < o.chunk ? vocab - first : o.chunk;
+    const Mat dl = {base, rows, n, o.chunk, "gradients of logits"};
+    Product p = logits_product(tg::kEpiDlogits, x, w, first, n, targets_dev, dtype);
+    p.c[0] = dl;
+    p.lse = lse_dev;
+    p.weight = weight;
+    TG_TRY(whole_product(p, plan_product(p, pairs), nullptr, sms, st));
+    if (dx_dev) {
+      dx_product = xent_dx_product(dl, w, first, dx, dtype);
+      dx_product.alpha = xw.alpha;
+      dx_product.accumulate = !o.sums ? 0 : c == 0 ? 1 : 2;
+      // pieces share the first one's splits, so that each has its place in every split's sums
+      if (c == 0) dx_plan = plan_product(dx_product, pairs, o.sums);
+      const Plan plan = c == 0 ? dx_plan : plan_of(dx_product, pairs, dx_plan.splits, o.sums);
+      TG_TRY(run_product(dx_product, plan, dx_partials, 0, -1, st));
+    }
+    if (dw_dev) {
+      Product q = xent_dw_product(dl, x, dw, first, dtype);
+      q.alpha = xw.alpha;
+      TG_TRY(whole_product(q, plan_product(q, pairs), dw_sums, sms, st));
+    }
+  }
+  if (dx_dev && dx_plan.partial_bytes)
+    TG_TRY(join_product(dx_product, dx_plan, dx_partials, sms, st));
+  return TG_OK;
+}
+
+}  // extern "C"

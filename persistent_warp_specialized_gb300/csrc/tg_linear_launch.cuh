@@ -1,0 +1,206 @@
+// tg_linear_launch.cuh -- instantiations and launchers of the products with fused epilogues and of the
+// small kernels around them: the gated feed-forward projections, the cross entropy of a vocabulary, and
+// the input gradient.  Included by tg_gemm.cu, whose watchdog status word the products share.
+#pragma once
+
+#include "tg_gated_kernel.cuh"
+#include "tg_internal.h"
+#include "tg_launch.cuh"
+#include "tg_linear_kernel.cuh"
+#include "tg_xent_kernel.cuh"
+
+namespace tg {
+
+namespace {
+
+LinearParams params_of(const LinearLaunch& l) {
+  LinearParams p = {};
+  p.M = l.M;
+  p.N = l.N;
+  p.m_blocks = l.m_blocks;
+  p.n_blocks = l.n_blocks;
+  p.k_blocks = l.k_blocks;
+  p.group = l.group;
+  p.split_from = l.split_from;
+  p.total_units = l.total_units;
+  p.column_major = l.column_major;
+  p.watchdog_ns = l.watchdog_ns;
+  p.inject_skip_phase = l.inject_skip_phase;
+  p.splits = l.splits;
+  p.blocks_per_split = l.blocks_per_split;
+  p.n_seg = l.n_seg;
+  p.k_seg = l.k_seg;
+  p.partial = l.partial;
+  p.part_rows = l.part_rows;
+  p.alpha = l.alpha;
+  p.act = l.act;
+  p.keep = l.keep;
+  p.targets = l.targets;
+  p.first_col = l.first_col;
+  p.stats = static_cast<float2*>(l.stats);
+  p.slots = l.slots;
+  p.hit = l.hit;
+  p.lse = l.lse;
+  p.weight = l.weight;
+  return p;
+}
+
+// Calls f with the kernel for what ``l`` asks for, or with null if there is none.
+template <int DT, typename F>
+cudaError_t with_kernel(bool a_mn, bool b_mn, int epi, F&& f) {
+  if (a_mn)
+    return b_mn && epi == kEpiStore ? f(linear_pair_kernel<DT, 1, 1, kEpiStore>)
+                                    : cudaErrorInvalidValue;
+  if (b_mn) {
+    if (epi == kEpiStore) return f(linear_pair_kernel<DT, 0, 1, kEpiStore>);
+    if (epi == kEpiGated) return f(linear_pair_kernel<DT, 0, 1, kEpiGated>);
+    return cudaErrorInvalidValue;
+  }
+  if (epi == kEpiStore) return f(linear_pair_kernel<DT, 0, 0, kEpiStore>);
+  if (epi == kEpiStats) return f(linear_pair_kernel<DT, 0, 0, kEpiStats>);
+  if (epi == kEpiDlogits) return f(linear_pair_kernel<DT, 0, 0, kEpiDlogits>);
+  return cudaErrorInvalidValue;
+}
+
+template <int DT>
+cudaError_t launch_one(const LinearLaunch& l, cudaStream_t stream) {
+  LinearMaps maps;
+  for (int i = 0; i < 2; ++i) maps.a[i] = l.a[i], maps.b[i] = l.b[i];
+  for (int i = 0; i < 3; ++i) maps.c[i] = l.c[i];
+  return with_kernel<DT>(l.a_mn, l.b_mn, l.epi, [&](auto kernel) {
+    return launch_pdl(kernel, dim3(l.grid), kLinThreads, kLinSmemBytes, stream, maps,
+                      params_of(l));
+  });
+}
+
+// Sets up every kernel of one type; *pairs: the least number resident at once so far.
+template <int DT>
+cudaError_t prepare_one(int* pairs) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kLinThreads, 1, 1);
+  cfg.dynamicSmemBytes = kLinSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  struct {
+    bool a_mn, b_mn;
+    int epi;
+  } const kinds[] = {{true, true, kEpiStore},   {false, true, kEpiStore},  {false, true, kEpiGated},
+                     {false, false, kEpiStore}, {false, false, kEpiStats}, {false, false, kEpiDlogits}};
+  for (const auto& k : kinds) {
+    const cudaError_t e = with_kernel<DT>(k.a_mn, k.b_mn, k.epi, [&](auto kernel) {
+      cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kLinSmemBytes));
+      // a launch with fewer registers could not hand over what its epilogue warps wait for
+      cudaFuncAttributes fa;
+      if (err == cudaSuccess) err = cudaFuncGetAttributes(&fa, kernel);
+      if (err == cudaSuccess && fa.numRegs != kLinLaunchRegs) err = cudaErrorInvalidKernelImage;
+      int n = 0;
+      if (err == cudaSuccess) err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (err == cudaSuccess && n < *pairs) *pairs = n;
+      return err;
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+uint32_t blocks_for(uint64_t threads, int sms, uint32_t most_per_sm) {
+  const uint64_t want = (threads + 255) / 256, most = static_cast<uint64_t>(sms) * most_per_sm;
+  return static_cast<uint32_t>(want < most ? want : most);
+}
+
+}  // namespace
+
+cudaError_t prepare_linear_kernels(int* max_pairs) {
+  int pairs = 1 << 20;
+  cudaError_t e = prepare_one<0>(&pairs);
+  if (e == cudaSuccess) e = prepare_one<1>(&pairs);
+  *max_pairs = pairs;
+  return e;
+}
+
+cudaError_t launch_linear(const LinearLaunch& l, cudaStream_t stream) {
+  return l.dtype == 0 ? launch_one<0>(l, stream) : launch_one<1>(l, stream);
+}
+
+cudaError_t launch_linear_join(const LinearJoin& l, cudaStream_t stream) {
+  const uint64_t vecs = static_cast<uint64_t>(l.rows) * (l.cols / 4u);
+  const dim3 grid(blocks_for(vecs, l.sms, 8));
+  const uint64_t stride = static_cast<uint64_t>(l.part_rows) * l.cols;
+  return l.dtype == 0 ? launch_pdl(linear_join_kernel<0>, grid, 256, 0, stream, l.partials, l.splits,
+                                   stride, l.rows, l.cols, l.alpha, l.out, l.ld_out)
+                      : launch_pdl(linear_join_kernel<1>, grid, 256, 0, stream, l.partials, l.splits,
+                                   stride, l.rows, l.cols, l.alpha, l.out, l.ld_out);
+}
+
+cudaError_t launch_gated_join(const GatedJoin& l, cudaStream_t stream) {
+  GatedJoinParams p;
+  p.g_parts = l.g_parts;
+  p.u_parts = l.u_parts;
+  p.split_stride = static_cast<uint64_t>(l.part_rows) * l.outs;
+  p.splits = l.splits;
+  p.rows = l.rows;
+  p.outs = l.outs;
+  p.act = l.act;
+  p.h = l.h;
+  p.g = l.g;
+  p.u = l.u;
+  p.ld_h = l.ld_h;
+  p.ld_g = l.ld_g;
+  p.ld_u = l.ld_u;
+  const dim3 grid(blocks_for(static_cast<uint64_t>(l.rows) * (l.outs / 4u), l.sms, 8));
+  return l.dtype == 0 ? launch_pdl(gated_join_kernel<0>, grid, 256, 0, stream, p)
+                      : launch_pdl(gated_join_kernel<1>, grid, 256, 0, stream, p);
+}
+
+cudaError_t launch_gated_grad(const GatedGrad& l, cudaStream_t stream) {
+  GatedGradParams p;
+  p.dh = l.dh;
+  p.g = l.g;
+  p.u = l.u;
+  p.dgu = l.dgu;
+  p.ld_dh = l.ld_dh;
+  p.ld_g = l.ld_g;
+  p.ld_u = l.ld_u;
+  p.rows = static_cast<uint32_t>(l.rows);
+  p.vecs = static_cast<uint32_t>(l.outs / 8);
+  p.act = l.act;
+  const dim3 grid(blocks_for(static_cast<uint64_t>(p.rows) * p.vecs, l.sms, 8));
+  return l.dtype == 0 ? launch_pdl(gated_grad_kernel<0>, grid, 256, 0, stream, p)
+                      : launch_pdl(gated_grad_kernel<1>, grid, 256, 0, stream, p);
+}
+
+cudaError_t launch_xent_join(const XentJoin& l, cudaStream_t stream) {
+  XentJoinParams p;
+  p.stats = static_cast<const float2*>(l.stats);
+  p.hit = l.hit;
+  p.targets = l.targets;
+  p.ignore = l.ignore;
+  p.loss = l.loss;
+  p.lse = l.lse;
+  p.rows = l.rows;
+  p.slots = l.slots;
+  p.vocab = l.vocab;
+  return launch_pdl(xent_join_kernel, dim3((l.rows + 7u) / 8u), 256, 0, stream, p);
+}
+
+cudaError_t launch_xent_weights(const XentWeights& l, cudaStream_t stream) {
+  XentWeightParams p;
+  p.dloss = l.dloss;
+  p.targets = l.targets;
+  p.ignore = l.ignore;
+  p.weight = l.weight;
+  p.alpha = l.alpha;
+  p.rows = l.rows;
+  p.vocab = l.vocab;
+  p.whole = l.dtype == 0 ? 32768.0f : 1.0f;
+  return launch_pdl(xent_weight_kernel, dim3(1), 1024, 0, stream, p);
+}
+
+}  // namespace tg
