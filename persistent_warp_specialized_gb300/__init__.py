@@ -843,6 +843,8 @@ def _workspace(nbytes, like):
 def input_grad(dy, w, out=None, stream=None):
     """torch convenience: dx = dy w^T [rows, cols], what a linear layer y = x w hands back to x, of dy
     [rows, outs] and w [cols, outs], both float16 or both bfloat16.  w is not transposed in memory."""
+    import torch
+
     dtype, rows, outs, ld_dy = _matrix16(dy, "dy")
     _, cols, w_outs, ld_w = _matrix16(w, "w", dy)
     if w_outs != outs:
@@ -852,7 +854,7 @@ def input_grad(dy, w, out=None, stream=None):
     nbytes = _check(lib.tg_input_grad_workspace_bytes(rows, cols, outs))
     with _allocating_on(stream):
         if out is None:
-            out = dy.new_empty((rows, cols))
+            out = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
         ws, wsp = _workspace(nbytes, dy)
     _check(lib.tg_input_grad(dy.data_ptr(), w.data_ptr(), out.data_ptr(), rows, cols, outs, ld_dy,
                              ld_w, ld_dx, dtype, wsp, nbytes, _stream(stream)))
@@ -863,6 +865,8 @@ def gated_forward(x, w_gate, w_up, act="silu", keep=False, out=None, stream=None
     """torch convenience: h = act(x w_gate) (x w_up) of x [rows, cols] and weights [cols, outs], all
     float16 or all bfloat16; act is "silu" or "gelu" (tanh form).  keep: (h, g, u), with g = x w_gate
     and u = x w_up for gated_backward."""
+    import torch
+
     dtype, rows, cols, ld_x = _matrix16(x, "x")
     outs = w_gate.shape[-1]
     ld_wg = _matrix16(w_gate, "w_gate", x, (cols, outs))[3]
@@ -873,9 +877,9 @@ def gated_forward(x, w_gate, w_up, act="silu", keep=False, out=None, stream=None
     nbytes = _check(lib.tg_gated_fwd_workspace_bytes(rows, cols, outs))
     with _allocating_on(stream):
         if out is None:
-            out = x.new_empty((rows, outs))
-        g = x.new_empty((rows, outs)) if keep else None
-        u = x.new_empty((rows, outs)) if keep else None
+            out = torch.empty((rows, outs), dtype=x.dtype, device=x.device)
+        g = torch.empty((rows, outs), dtype=x.dtype, device=x.device) if keep else None
+        u = torch.empty((rows, outs), dtype=x.dtype, device=x.device) if keep else None
         ws, wsp = _workspace(nbytes, x)
     _check(lib.tg_gated_fwd(
         x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(),
@@ -887,6 +891,8 @@ def gated_forward(x, w_gate, w_up, act="silu", keep=False, out=None, stream=None
 def gated_backward(dh, g, u, x, w_gate, w_up, act="silu", stream=None):
     """torch convenience: (dx, dw_gate, dw_up) of gated_forward from dh [rows, outs] and the g and u
     that it kept."""
+    import torch
+
     dtype, rows, outs, ld_dh = _matrix16(dh, "dh")
     ld_g = _matrix16(g, "g", dh, (rows, outs))[3]
     ld_u = _matrix16(u, "u", dh, (rows, outs))[3]
@@ -898,9 +904,9 @@ def gated_backward(dh, g, u, x, w_gate, w_up, act="silu", stream=None):
     lib = load_library()
     nbytes = _check(lib.tg_gated_bwd_workspace_bytes(rows, cols, outs))
     with _allocating_on(stream):
-        dx = dh.new_empty((rows, cols))
-        dwg = dh.new_empty((cols, outs))
-        dwu = dh.new_empty((cols, outs))
+        dx = torch.empty((rows, cols), dtype=dh.dtype, device=dh.device)
+        dwg = torch.empty((cols, outs), dtype=dh.dtype, device=dh.device)
+        dwu = torch.empty((cols, outs), dtype=dh.dtype, device=dh.device)
         ws, wsp = _workspace(nbytes, dh)
     _check(lib.tg_gated_bwd(
         dh.data_ptr(), g.data_ptr(), u.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
@@ -946,8 +952,8 @@ def linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index=-100, 
     lib = load_library()
     nbytes = _check(lib.tg_xent_bwd_workspace_bytes(rows, cols, vocab))
     with _allocating_on(stream):
-        dx = x.new_empty((rows, cols))
-        dw = x.new_empty((vocab, cols))
+        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        dw = torch.empty((vocab, cols), dtype=x.dtype, device=x.device)
         ws, wsp = _workspace(nbytes, x)
     _check(lib.tg_xent_bwd(dp, x.data_ptr(), w.data_ptr(), at, lp, dx.data_ptr(), dw.data_ptr(),
                            rows, cols, vocab, ld_x, ld_w, cols, cols, ignore_index, dtype, wsp,

@@ -1,0 +1,46 @@
+// tg_few_config.h -- compile-time constants of the products with few rows (tg_few_kernel.cuh), shared
+// by that kernel and the host code that sizes its launches and tensor maps.
+#pragma once
+
+#include "tg_config.h"
+#include "tg_linear_config.h"
+
+namespace tg {
+
+constexpr int kFewRows = 64;             // rows at most
+constexpr int kFewM = 128;               // weights' rows or columns (results) in a tile
+constexpr int kFewBK = kKAtom;           // 64 of K in a stage
+// A sum is cut into segments of 1024 products, as tg_linear_config.h explains.
+constexpr uint32_t kFewSegment = 16;
+// warp 0 loads, warp 1 issues the MMAs and owns the TMEM, warps 2..5 are the epilogue
+constexpr uint32_t kFewThreads = 192;
+constexpr int kFewEpiThreads = 128;
+constexpr int kFewMaxCluster = 8;
+constexpr int kFewMaxStages = 6;
+// Two CTAs share an SM, so that one's start and end fall into the other's loads.
+constexpr uint32_t kFewRingBudget = 110u * 1024u;
+
+constexpr uint32_t kFewWeightBytes = kFewM * kFewBK * kElemBytes;       // 16 KiB
+
+// rows as the MMA takes them: 16, 32 or 64
+constexpr uint32_t few_padded(int64_t rows) { return rows <= 16 ? 16u : rows <= 32 ? 32u : 64u; }
+
+constexpr uint32_t few_stage_bytes(bool gated, uint32_t n) {
+  return (gated ? 2u : 1u) * kFewWeightBytes + n * kFewBK * kElemBytes;
+}
+constexpr uint32_t few_stages(bool gated, uint32_t n) {
+  const uint32_t most = kFewRingBudget / few_stage_bytes(gated, n);
+  return most < kFewMaxStages ? most : kFewMaxStages;
+}
+// the ring, which the sums of a cluster's CTAs take over at the end: 128 x n floats of each product
+constexpr uint32_t few_smem_bytes(bool gated, uint32_t n) {
+  return kSmemAlignSlack + few_stages(gated, n) * few_stage_bytes(gated, n);
+}
+static_assert(few_stages(true, 64) >= 2 && few_stages(false, 64) >= 3, "a ring has to run ahead");
+// ... or, for statistics, the sums, half as many again by rows (padded) and a pair for each thread
+static_assert(2u * kFewM * 64u * 4u <= few_stages(true, 64) * few_stage_bytes(true, 64) &&
+              (kFewM * 64u + (kFewM + 1u) * 64u + 2u * 128u + 2u) * 4u <=
+                  few_stages(false, 64) * few_stage_bytes(false, 64),
+              "sums fit into the ring");
+
+}  // namespace tg

@@ -1,0 +1,384 @@
+// tg_few_kernel.cuh -- the products of tg_linear_kernel.cuh for at most 64 rows: a token or a few that are
+// being generated, a short text's loss.
+//
+//   D[r, n] = sum_k A[r, k] B[k, n]
+//
+// What bounds them is reading B, the weights, once: 2 bytes for at most 128 operations.  The pair
+// kernel's MMA has 256 rows whatever there are, so it multiplies 250 rows of zeros as long as the weights
+// take to arrive; and its tiles are few and large.  Here the weights are the MMA's M operand (128 of
+// their rows or columns, cta_group::1) and the rows its N, padded to 16, 32 or 64: 32 cycles for each
+// 16 of K where the weights' 4 KiB take about 90 to arrive.
+//
+// A CTA has one tile of 128 results per row.  Few tiles: a cluster of up to 8 CTAs shares one along K; each
+// adds its range, then the sums are handed out by rows through distributed shared memory, every CTA
+// adds its rows' in the order of the ranges and finishes them.  Nothing goes through global memory
+// and no second launch follows.  Two CTAs an SM.
+//
+// Measured (bf16, us, L2 flushed / pair kernel with its join): see tg_linear_api.cu at few_rows.
+//
+// Included by exactly one translation unit, after tg_linear_kernel.cuh.
+#pragma once
+
+#include "tg_few_config.h"
+#include "tg_linear_kernel.cuh"
+
+namespace tg {
+
+struct FewMaps {
+  CUtensorMap w[2], x[2];
+};
+
+struct FewParams {
+  uint32_t rows, n_pad;              // rows, and as the MMA takes them
+  uint32_t outs;                     // results of a row
+  uint32_t k_blocks, k_seg;          // of 64; from k_seg on the second maps
+  uint32_t stages, stage_bytes;
+  const float* alpha;                // kEpiStore
+  uint32_t act;                      // kEpiGated
+  void *out, *g, *u;                 // results; kEpiGated: g and u too, or null
+  int64_t ld_out, ld_g, ld_u;
+  const int64_t* targets;            // kEpiStats, kEpiDlogits: logits of words first_col ..
+  uint32_t first_col;
+  float2* stats;                     // [rows][slots], a slot for each tile
+  uint32_t slots;
+  float* hit;
+  const float *lse, *weight;
+  uint64_t watchdog_ns;
+};
+
+struct __align__(8) FewCtl {
+  uint64_t loaded[kFewMaxStages];
+  uint64_t consumed[kFewMaxStages];
+  uint64_t tmem_full[2];
+  uint64_t tmem_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+
+// As tmem_ld_32x32b_x32, for 16 consecutive columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Floats between rows of summed logits: threads with a row each read without bank conflicts.
+constexpr uint32_t kStatPitch = kFewM + 1;
+
+template <int DT>
+__device__ __forceinline__ void st_result(void* base, int64_t at, float v) {
+  if constexpr (DT == 1)
+    static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(base)[at] = __float2half_rn(v);
+}
+
+// DT: 0 = fp16, 1 = bf16.  W_MN: the weights lie with the results' index contiguous ([k, n]), not k.
+template <int DT, int W_MN, int EPI>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    few_rows_kernel(const __grid_constant__ FewMaps maps, const FewParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ FewCtl ctl;
+  constexpr uint32_t kMats = EPI == kEpiGated ? 2u : 1u;
+  constexpr uint32_t kChunkBytes = kFewBK * 128u;          // W_MN: 64 rows of 64 columns
+
+  const uint32_t warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31u;
+  const uint32_t ranks = cluster_nctarank(), rank = cluster_ctarank();
+  const uint32_t n0 = blockIdx.x / ranks * kFewM;
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t stage_bytes = p.stage_bytes;
+  const uint32_t per_rank = (p.k_blocks + ranks - 1u) / ranks;
+  const uint32_t k_lo = min(rank * per_rank, p.k_blocks), k_hi = min(k_lo + per_rank, p.k_blocks);
+  const uint32_t segments = (k_hi - k_lo + kFewSegment - 1u) / kFewSegment;
+
+  const uint32_t bar_loaded = smem_u32(&ctl.loaded[0]);
+  const uint32_t bar_consumed = smem_u32(&ctl.consumed[0]);
+  const uint32_t bar_tmem_full = smem_u32(&ctl.tmem_full[0]);
+  const uint32_t bar_tmem_empty = smem_u32(&ctl.tmem_empty[0]);
+  const uint32_t bar_drain = smem_u32(&ctl.drain);
+  const uint32_t tmem_cols = 2u * kMats * p.n_pad;         // two accumulators; 32 .. 256
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kFewMaxStages; ++s) {
+      mbar_init(bar_loaded + 8u * s, 1);
+      mbar_init(bar_consumed + 8u * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_tmem_full + 8u * b, 1);
+      mbar_init(bar_tmem_empty + 8u * b, kFewEpiThreads / 32);
+    }
+    mbar_init(bar_drain, 1);
+    ctl.abort = 0;
+    fence_mbarrier_init();
+    prefetch_tensormap(&maps.w[0]);
+    if (kMats == 2) prefetch_tensormap(&maps.w[1]);
+    prefetch_tensormap(&maps.x[0]);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), tmem_cols);
+    tmem_relinquish_alloc_permit();
+  }
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  tcgen05_fence_after_sync();
+  grid_dependency_wait();      // launched with programmatic stream serialization
+  grid_launch_dependents();
+
+  const uint32_t tmem_base = ctl.tmem_base;
+  volatile int* abort_flag = &ctl.abort;
+  const uint64_t limit = p.watchdog_ns;
+  // results of this thread's lane of the accumulator, row by row (epilogue warps)
+  float v[kMats][kFewRows];
+  // This CTA finishes rows row0 .. row0 + share - 1.  What is read for each (their targets' places
+  // among the tile's results, lse, weights) is read ahead: lane i has rows i and i + 32.
+  const uint32_t share = p.n_pad / ranks;   // both powers of two
+  const uint32_t share_log = 31u - __clz(share);
+  const uint32_t row0 = rank * share;
+  int32_t hot[2] = {-1, -1};
+  float lse[2] = {}, weight[2] = {};
+  if constexpr (EPI == kEpiStats || EPI == kEpiDlogits) {
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) {
+      const uint32_t r = lane + 32u * i;
+      if (warp < 2 || r >= share || row0 + r >= p.rows) continue;
+      const int64_t at = p.targets[row0 + r] - static_cast<int64_t>(p.first_col + n0);
+      if (at >= 0 && at < kFewM) hot[i] = static_cast<int32_t>(at);
+      if constexpr (EPI == kEpiDlogits) lse[i] = p.lse[row0 + r], weight[i] = p.weight[row0 + r];
+    }
+  }
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      uint32_t slot = 0, parity = 0, pending = 0, pending_par = 0;
+      bool ok = true;
+      for (uint32_t k = k_lo; k < k_hi; ++k) {
+        if (!wait_or_abort(bar_consumed + 8u * slot, parity ^ 1u, abort_flag, limit,
+                           kRoleProducer)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = bar_loaded + 8u * slot;
+        mbar_arrive_expect_tx(bar, stage_bytes);
+        const uint32_t seg = k >= p.k_seg ? 1u : 0u;
+        const int32_t kx = static_cast<int32_t>(k - seg * p.k_seg) * kFewBK;
+        const uint32_t dst = sbase + slot * stage_bytes;
+#pragma unroll
+        for (uint32_t m = 0; m < kMats; ++m) {
+          const CUtensorMap* map = &maps.w[EPI == kEpiGated ? m : seg];
+          const uint32_t w_dst = dst + m * kFewWeightBytes;
+          if constexpr (W_MN) {
+            tma_load_2d(w_dst, map, bar, static_cast<int32_t>(n0), kx);
+            tma_load_2d(w_dst + kChunkBytes, map, bar, static_cast<int32_t>(n0) + 64, kx);
+          } else {
+            tma_load_2d(w_dst, map, bar, kx, static_cast<int32_t>(n0));
+          }
+        }
+        tma_load_2d(dst + kMats * kFewWeightBytes, &maps.x[seg], bar, kx, 0);
+        pending |= 1u << slot;
+        pending_par = (pending_par & ~(1u << slot)) | (parity << slot);
+        if (++slot == p.stages) slot = 0, parity ^= 1u;
+      }
+      if (!ok)   // no copy may still be under way when the CTA leaves
+        for (uint32_t s = 0; s < p.stages; ++s)
+          if ((pending >> s) & 1u)
+            wait_bounded(bar_loaded + 8u * s, (pending_par >> s) & 1u, limit, kRoleDrain);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t idesc = idesc_f16(DT, kFewM, 0, W_MN, 0) | ((p.n_pad >> 3) << 17);
+    const bool leader = elect_one();
+    const uint64_t a0 = smem_desc_sw128(sbase, W_MN ? kChunkBytes : 16u, 1024);
+    const uint64_t b0 = smem_desc_sw128(sbase + kMats * kFewWeightBytes, 16u, 1024);
+    uint32_t slot = 0, parity = 0, in_seg = 0, acc = 0, acc_parity = 0;
+    for (uint32_t k = k_lo; k < k_hi; ++k) {
+      bool got = wait_or_abort(bar_loaded + 8u * slot, parity, abort_flag, limit, kRoleMma);
+      if (got && in_seg == 0)   // the accumulator's last segment has been read out
+        got = wait_or_abort(bar_tmem_empty + 8u * acc, acc_parity ^ 1u, abort_flag, limit, kRoleMma);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tcgen05_fence_after_sync();
+      if (leader) {
+        const uint64_t at = slot * (stage_bytes >> 4);
+#pragma unroll
+        for (uint32_t m = 0; m < kMats; ++m) {
+          const uint32_t d = tmem_base + (acc * kMats + m) * p.n_pad;
+#pragma unroll
+          for (uint32_t kk = 0; kk < kFewBK / kUmmaK; ++kk)
+            umma_f16(d, a0 + at + m * (kFewWeightBytes >> 4) + (W_MN ? kk * 128u : kk * 2u),
+                     b0 + at + kk * 2u, idesc, in_seg != 0u || kk != 0u ? 1u : 0u);
+        }
+        umma_commit(bar_consumed + 8u * slot);
+      }
+      __syncwarp();
+      if (++slot == p.stages) slot = 0, parity ^= 1u;
+      if (++in_seg == kFewSegment || k + 1u == k_hi) {
+        if (leader) umma_commit(bar_tmem_full + 8u * acc);
+        __syncwarp();
+        in_seg = 0;
+        acc ^= 1u;
+        acc_parity ^= acc ^ 1u;
+      }
+    }
+    if (leader) {
+      umma_commit(bar_drain);
+      wait_bounded(bar_drain, 0, limit, kRoleDrain);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ sums of the segments
+    const uint32_t q = warp & 3u;
+#pragma unroll
+    for (uint32_t m = 0; m < kMats; ++m)
+#pragma unroll
+      for (uint32_t i = 0; i < kFewRows; ++i) v[m][i] = 0.0f;
+    uint32_t acc = 0, acc_parity = 0;
+    for (uint32_t sg = 0; sg < segments; ++sg) {
+      const bool got = wait_or_abort(bar_tmem_full + 8u * acc, acc_parity, abort_flag, limit,
+                                     kRoleEpilogue);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tcgen05_fence_after_sync();
+      const uint32_t t_row = tmem_base + ((q * 32u) << 16) + acc * kMats * p.n_pad;
+#pragma unroll
+      for (uint32_t m = 0; m < kMats; ++m)
+#pragma unroll
+        for (uint32_t j = 0; j < kFewRows / 16; ++j) {
+          if (16u * j >= p.n_pad) break;
+          uint32_t t[16];
+          tmem_ld_32x32b_x16(t_row + m * p.n_pad + 16u * j, t);
+#pragma unroll
+          for (uint32_t i = 0; i < 16; ++i) v[m][16 * j + i] += __uint_as_float(t[i]);
+        }
+      tcgen05_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_tmem_empty + 8u * acc);
+      acc ^= 1u;
+      acc_parity ^= acc ^ 1u;
+    }
+  }
+
+  // Every load of this CTA has been multiplied, or waited for: the ring is idle.
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tcgen05_fence_after_sync();
+    tmem_dealloc(tmem_base, tmem_cols);
+  }
+  float* const sums = reinterpret_cast<float*>(smem_raw + (sbase - smem_u32(smem_raw)));
+  // statistics: the summed logits by rows, behind what the ranks hand out
+  float* const stat_rows = sums + (ranks == 1u ? 0u : p.n_pad * kFewM);
+  // this thread's result of every row (warps 2..5): its lane of the accumulator
+  const uint32_t f = (warp & 3u) * 32u + lane;
+  const bool in = n0 + f < p.outs;
+  const float alpha = EPI == kEpiStore && p.alpha ? *p.alpha : 1.0f;
+  // result f of row row0 + r (b: the up projection's)
+  auto finish = [&](uint32_t r, float a, float b) {
+    const int64_t row = row0 + r, n = n0 + f;
+    if constexpr (EPI == kEpiGated) {
+      if (!in) return;
+      st_result<DT>(p.out, row * p.ld_out + n, a * gate_of(a, p.act).s * b);
+      if (p.g != nullptr) {
+        st_result<DT>(p.g, row * p.ld_g + n, a);
+        st_result<DT>(p.u, row * p.ld_u + n, b);
+      }
+    } else if constexpr (EPI == kEpiStore) {
+      if (in) st_result<DT>(p.out, row * p.ld_out + n, a * alpha);
+    } else if constexpr (EPI == kEpiDlogits) {
+      const int32_t at = __shfl_sync(0xffffffffu, r < 32u ? hot[0] : hot[1], r & 31u);
+      const float row_lse = __shfl_sync(0xffffffffu, r < 32u ? lse[0] : lse[1], r & 31u);
+      const float w = __shfl_sync(0xffffffffu, r < 32u ? weight[0] : weight[1], r & 31u);
+      float d = exp2_fast((a - row_lse) * kLog2e);
+      if (at == static_cast<int32_t>(f)) d -= 1.0f;
+      if (in) st_result<DT>(p.out, row * p.ld_out + n, w == 0.0f ? 0.0f : d * w);
+    } else {
+      stat_rows[r * kStatPitch + f] = in ? a : -INFINITY;
+    }
+  };
+  if (ranks == 1u) {
+    if (warp < 2 || *abort_flag) return;
+#pragma unroll
+    for (uint32_t i = 0; i < kFewRows; ++i) {
+      if (i >= p.rows) break;
+      finish(i, v[0][i], v[kMats - 1][i]);
+    }
+  } else {
+    // Sums are handed out by rows: [rank][product][row of the receiver's][128] in the receiver's
+    // ring, once all CTAs of the cluster are here.
+    cluster_sync();
+    if (warp >= 2) {
+#pragma unroll
+      for (uint32_t m = 0; m < kMats; ++m)
+#pragma unroll
+        for (uint32_t i = 0; i < kFewRows; ++i) {
+          if (i >= p.rows) break;
+          const uint32_t to = i >> share_log, r = i & (share - 1u);
+          st_shared_cluster_u32(
+              mapa_shared(sbase + 4u * (((rank * kMats + m) * share + r) * kFewM + f), to),
+              __float_as_uint(v[m][i]));
+        }
+    }
+    cluster_sync();
+    if (warp < 2 || *abort_flag) return;
+    const uint32_t mine = p.rows > row0 ? min(p.rows - row0, share) : 0u;
+    // the ranks' sums in order
+#pragma unroll 4
+    for (uint32_t r = 0; r < mine; ++r) {
+      float t[2] = {0.0f, 0.0f};
+      for (uint32_t c = 0; c < ranks; ++c)
+#pragma unroll
+        for (uint32_t m = 0; m < kMats; ++m)
+          t[m] += sums[((c * kMats + m) * share + r) * kFewM + f];
+      finish(r, t[0], t[kMats - 1]);
+    }
+  }
+  if constexpr (EPI == kEpiStats) {
+    // 128 / share threads to a row, each with every so many'th of its logits, then one joins them
+    asm volatile("bar.sync 1, %0;" ::"n"(kFewEpiThreads) : "memory");
+    const uint32_t parts = kFewEpiThreads >> share_log;
+    const uint32_t r = f & (share - 1u), part = f >> share_log;
+    const float* const l = stat_rows + r * kStatPitch;
+    float top = -INFINITY, sum = 0.0f;
+    const bool row_in = row0 + r < p.rows;
+    if (row_in) {
+#pragma unroll 8
+      for (uint32_t i = part; i < kFewM; i += parts) top = fmaxf(top, l[i]);
+      const float base = top == -INFINITY ? 0.0f : top;   // nothing but -inf: exponentials 0
+#pragma unroll 8
+      for (uint32_t i = part; i < kFewM; i += parts) sum += exp2_fast((l[i] - base) * kLog2e);
+    }
+    float2* const joint = reinterpret_cast<float2*>(stat_rows + ((share * kStatPitch + 1u) & ~1u));
+    joint[f] = make_float2(top, sum);
+    asm volatile("bar.sync 1, %0;" ::"n"(kFewEpiThreads) : "memory");
+    if (part == 0 && row_in) {
+      float m = top;
+      for (uint32_t c = 1; c < parts; ++c) m = fmaxf(m, joint[(c << share_log) + r].x);
+      const float base = m == -INFINITY ? 0.0f : m;
+      float s = 0.0f;
+      for (uint32_t c = 0; c < parts; ++c) {
+        const float2 j = joint[(c << share_log) + r];
+        s += j.y * exp2_fast((j.x - base) * kLog2e);
+      }
+      const uint64_t row = row0 + r;
+      p.stats[row * p.slots + n0 / kFewM] = make_float2(m, s);
+      const int32_t at = r < 32u ? hot[0] : hot[1];   // rows r < share: lane r % 32 has them
+      if (at >= 0 && n0 + at < p.outs) p.hit[row] = l[at];
+    }
+  }
+}
+
+}  // namespace tg

@@ -154,6 +154,27 @@ struct LinearLaunch {
 cudaError_t prepare_linear_kernels(int* max_pairs);
 cudaError_t launch_linear(const LinearLaunch& l, cudaStream_t stream);
 
+// The same products for few rows (tg_few_kernel.cuh): ``ranks`` CTAs share a tile of 128 results a row.
+struct FewLaunch {
+  CUtensorMap w[2], x[2];       // weights and rows; the second ones along K, or of the gated pair
+  int dtype;
+  bool w_mn;                    // the weights lie with the results' index contiguous
+  int epi;                      // LinearEpi
+  uint32_t rows, outs, tiles, ranks;
+  uint32_t k_blocks, k_seg;     // of 64
+  const float* alpha;
+  uint32_t act;
+  void *out, *g, *u;
+  int64_t ld_out, ld_g, ld_u;
+  const int64_t* targets;
+  uint32_t first_col, slots;
+  void* stats;
+  float* hit;
+  const float *lse, *weight;
+  uint64_t watchdog_ns;
+};
+cudaError_t launch_few(const FewLaunch& l, cudaStream_t stream);
+
 // out [rows, cols] = alpha (null: 1) times the sum over splits of partials [splits][part_rows][cols]
 struct LinearJoin {
   const float* partials;

@@ -9,6 +9,7 @@
 #include "../../include/tg.h"
 #include "tg_api_checks.h"
 #include "tg_api_common.h"
+#include "tg_few_config.h"
 #include "tg_internal.h"
 #include "tg_linear_config.h"
 #include "tg_tile_scheduler.cuh"
@@ -50,6 +51,7 @@ struct Plan {
   uint32_t m_tiles, n_tiles, n_seg, k_blocks, k_seg, splits, blocks_per_split, split_from, units,
       pairs;
   uint32_t part_rows;
+  bool few;                 // the kernel for few rows takes it, and nothing above counts
   uint64_t partial_bytes;   // fp32 sums of one N segment (0: results are stored rounded)
   double us;                // what the plan is expected to take
 };
@@ -63,6 +65,7 @@ constexpr uint64_t kMinBlocks = 4;   // k-blocks of a unit when K is split
 
 Plan plan_of(const Product& p, uint64_t pairs, uint64_t splits, bool sums) {
   Plan w;
+  w.few = false;
   w.m_tiles = static_cast<uint32_t>(ceil_div(p.M, tg::kPairBM));
   const uint64_t tile_n = p.epi == tg::kEpiGated ? tg::kGatedTileN : tg::kBN;
   w.n_seg = static_cast<uint32_t>(ceil_div(p.N, tile_n));
@@ -91,11 +94,20 @@ Plan plan_of(const Product& p, uint64_t pairs, uint64_t splits, bool sums) {
   return w;
 }
 
+// Few rows: the weights are the MMA's larger operand, and clusters share a tile along K.
+bool few_rows(const Product& p, bool sums = false) {
+  return p.M <= tg::kFewRows && !p.a_mn && p.segs_n == 1 && !sums;
+}
+
 // Fewer tiles than pairs: K may be split, so that every pair has a unit, at the price of partial sums
 // in fp32 and a join.  The least expected time decides.  sums: results go to partial sums in any case.
 Plan plan_product(const Product& p, int max_pairs, bool sums = false) {
   const uint64_t pairs = static_cast<uint64_t>(max_pairs);
   Plan best = plan_of(p, pairs, 1, sums);
+  if (few_rows(p, sums)) {
+    best.few = true;
+    return best;
+  }
   if (p.epi != tg::kEpiStore) return best;
   const uint64_t tiles = uint64_t(best.m_tiles) * best.n_tiles;
   uint64_t most = pairs / tiles;
@@ -119,6 +131,53 @@ CUtensorMapDataType type16(int dtype) {
 int encode_operand(CUtensorMap* map, const Mat& m, bool mn, int dtype) {
   return encode_tiled(map, type16(dtype), 2, m.p, m.cols, m.rows, 64,
                       mn ? tg::kLinBK : tg::kBM, m.name, true, m.ld * 2);
+}
+
+// Enqueues a product with few rows.  Its tiles are shared by as many CTAs (a power of two) as it takes
+// for one on every SM, of at least two k-blocks each.
+int run_few(const Product& p, int sms, uint64_t watchdog_ns, cudaStream_t stream) {
+  tg::FewLaunch l = {};
+  const uint32_t n_pad = tg::few_padded(p.M);
+  const int mats = p.epi == tg::kEpiGated || p.segs_k == 2 ? 2 : 1;
+  for (int i = 0; i < mats; ++i) {
+    TG_TRY(encode_tiled(&l.w[i], type16(p.dtype), 2, p.b[i].p, p.b[i].cols, p.b[i].rows, 64,
+                        p.b_mn ? tg::kFewBK : tg::kFewM, p.b[i].name, true, p.b[i].ld * 2));
+    const Mat& x = p.a[p.segs_k == 2 ? i : 0];
+    TG_TRY(encode_tiled(&l.x[i], type16(p.dtype), 2, x.p, x.cols, x.rows, 64, n_pad, x.name, true,
+                        x.ld * 2));
+  }
+  l.dtype = p.dtype;
+  l.w_mn = p.b_mn;
+  l.epi = p.epi;
+  l.rows = static_cast<uint32_t>(p.M);
+  l.outs = static_cast<uint32_t>(p.N);
+  l.tiles = static_cast<uint32_t>(ceil_div(p.N, tg::kFewM));
+  l.k_seg = static_cast<uint32_t>(ceil_div(p.K, tg::kFewBK));
+  l.k_blocks = l.k_seg * p.segs_k;
+  l.ranks = 1;
+  while (l.ranks < tg::kFewMaxCluster && l.tiles * l.ranks < static_cast<uint32_t>(sms) &&
+         l.k_blocks >= 4 * l.ranks)
+    l.ranks *= 2;
+  l.alpha = p.alpha;
+  l.act = p.act;
+  l.out = const_cast<void*>(p.c[0].p);
+  l.ld_out = p.c[0].ld;
+  if (p.keep) {
+    l.g = const_cast<void*>(p.c[1].p);
+    l.u = const_cast<void*>(p.c[2].p);
+    l.ld_g = p.c[1].ld;
+    l.ld_u = p.c[2].ld;
+  }
+  l.targets = p.targets;
+  l.first_col = p.first_col;
+  l.slots = p.slots;
+  l.stats = p.stats;
+  l.hit = p.hit;
+  l.lse = p.lse;
+  l.weight = p.weight;
+  l.watchdog_ns = watchdog_ns ? watchdog_ns : default_watchdog_ns(l.k_blocks);
+  const cudaError_t e = tg::launch_few(l, stream);
+  return e == cudaSuccess ? TG_OK : fail_cuda("product launch", e);
 }
 
 // Enqueues the product by its plan.  partials: fp32 sums of each N segment where the plan has them
@@ -206,13 +265,14 @@ int join_product(const Product& p, const Plan& w, void* const partials[2], int s
 // A product by itself: its units, and the join of its partial sums at ``ws`` where it has them.
 int whole_product(const Product& p, const Plan& w, void* ws, int sms, cudaStream_t stream,
                   uint64_t watchdog_ns = 0, int64_t inject = -1) {
+  if (w.few) return run_few(p, sms, watchdog_ns, stream);
   void* const partials[2] = {ws, static_cast<char*>(ws) + padded(w.partial_bytes)};
   TG_TRY(run_product(p, w, partials, watchdog_ns, inject, stream));
   return w.partial_bytes ? join_product(p, w, partials, sms, stream) : TG_OK;
 }
 
 uint64_t partials_of(const Product& p, const Plan& w) {
-  return w.partial_bytes ? p.segs_n * padded(w.partial_bytes) : 0;
+  return w.partial_bytes && !w.few ? p.segs_n * padded(w.partial_bytes) : 0;
 }
 
 // ---------------------------------------------------------------- checks
@@ -361,6 +421,7 @@ GatedPlan gated_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& h, i
   p.b[1] = wu;
   p.c[0] = h;
   o.plan = plan_product(p, pairs);
+  if (o.plan.few) return o;
   Product two = p;
   two.epi = tg::kEpiStore;
   two.segs_n = 2;
@@ -437,7 +498,7 @@ struct XentFwd {
 };
 XentFwd xent_fwd_plan(int64_t rows, int64_t vocab) {
   XentFwd o;
-  o.slots = static_cast<uint32_t>(ceil_div(vocab, tg::kStatCols));
+  o.slots = static_cast<uint32_t>(ceil_div(vocab, rows <= tg::kFewRows ? tg::kFewM : tg::kStatCols));
   o.stats_bytes = padded(uint64_t(rows) * o.slots * 8);
   o.total = o.stats_bytes + padded(uint64_t(rows) * 4);
   return o;
@@ -821,7 +882,10 @@ int tg_xent_bwd(const float* dloss_dev, const void* x_dev, const void* w_dev,
       // pieces share the first one's splits, so that each has its place in every split's sums
       if (c == 0) dx_plan = plan_product(dx_product, pairs, o.sums);
       const Plan plan = c == 0 ? dx_plan : plan_of(dx_product, pairs, dx_plan.splits, o.sums);
-      TG_TRY(run_product(dx_product, plan, dx_partials, 0, -1, st));
+      if (plan.few)
+        TG_TRY(run_few(dx_product, sms, 0, st));
+      else
+        TG_TRY(run_product(dx_product, plan, dx_partials, 0, -1, st));
     }
     if (dw_dev) {
       Product q = xent_dw_product(dl, x, dw, first, dtype);
@@ -829,7 +893,7 @@ int tg_xent_bwd(const float* dloss_dev, const void* x_dev, const void* w_dev,
       TG_TRY(whole_product(q, plan_product(q, pairs), dw_sums, sms, st));
     }
   }
-  if (dx_dev && dx_plan.partial_bytes)
+  if (dx_dev && partials_of(dx_product, dx_plan))
     TG_TRY(join_product(dx_product, dx_plan, dx_partials, sms, st));
   return TG_OK;
 }

@@ -3,6 +3,7 @@
 // the input gradient.  Included by tg_gemm.cu, whose watchdog status word the products share.
 #pragma once
 
+#include "tg_few_kernel.cuh"
 #include "tg_gated_kernel.cuh"
 #include "tg_internal.h"
 #include "tg_launch.cuh"
@@ -110,6 +111,60 @@ cudaError_t prepare_one(int* pairs) {
   return cudaSuccess;
 }
 
+// As with_kernel, for the products with few rows.
+template <int DT, typename F>
+cudaError_t with_few_kernel(bool w_mn, int epi, F&& f) {
+  if (epi == kEpiGated) return w_mn ? f(few_rows_kernel<DT, 1, kEpiGated>) : cudaErrorInvalidValue;
+  if (epi == kEpiStore)
+    return w_mn ? f(few_rows_kernel<DT, 1, kEpiStore>) : f(few_rows_kernel<DT, 0, kEpiStore>);
+  if (w_mn) return cudaErrorInvalidValue;
+  if (epi == kEpiStats) return f(few_rows_kernel<DT, 0, kEpiStats>);
+  return f(few_rows_kernel<DT, 0, kEpiDlogits>);
+}
+
+template <int DT>
+cudaError_t prepare_few() {
+  for (int epi = kEpiStore; epi <= kEpiDlogits; ++epi)
+    for (int w_mn = 0; w_mn < 2; ++w_mn) {
+      if (epi != kEpiStore && w_mn != (epi == kEpiGated)) continue;
+      const cudaError_t e = with_few_kernel<DT>(w_mn, epi, [&](auto kernel) {
+        uint32_t smem = 0;
+        for (uint32_t n = 16; n <= kFewRows; n *= 2)
+          smem = few_smem_bytes(epi == kEpiGated, n) > smem ? few_smem_bytes(epi == kEpiGated, n) : smem;
+        const cudaError_t err = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        return err != cudaSuccess
+                   ? err
+                   : cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                          cudaSharedmemCarveoutMaxShared);   // two CTAs an SM
+      });
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
+}
+
+template <int DT>
+cudaError_t launch_few_one(const FewLaunch& l, const FewMaps& maps, const FewParams& p,
+                           cudaStream_t stream) {
+  return with_few_kernel<DT>(l.w_mn, l.epi, [&](auto kernel) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = l.ranks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(l.tiles * l.ranks);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = few_smem_bytes(l.epi == kEpiGated, p.n_pad);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p);
+  });
+}
+
 uint32_t blocks_for(uint64_t threads, int sms, uint32_t most_per_sm) {
   const uint64_t want = (threads + 255) / 256, most = static_cast<uint64_t>(sms) * most_per_sm;
   return static_cast<uint32_t>(want < most ? want : most);
@@ -121,12 +176,45 @@ cudaError_t prepare_linear_kernels(int* max_pairs) {
   int pairs = 1 << 20;
   cudaError_t e = prepare_one<0>(&pairs);
   if (e == cudaSuccess) e = prepare_one<1>(&pairs);
+  if (e == cudaSuccess) e = prepare_few<0>();
+  if (e == cudaSuccess) e = prepare_few<1>();
   *max_pairs = pairs;
   return e;
 }
 
 cudaError_t launch_linear(const LinearLaunch& l, cudaStream_t stream) {
   return l.dtype == 0 ? launch_one<0>(l, stream) : launch_one<1>(l, stream);
+}
+
+cudaError_t launch_few(const FewLaunch& l, cudaStream_t stream) {
+  FewMaps maps;
+  FewParams p;
+  for (int i = 0; i < 2; ++i) maps.w[i] = l.w[i], maps.x[i] = l.x[i];
+  p.rows = l.rows;
+  p.n_pad = few_padded(l.rows);
+  p.outs = l.outs;
+  p.k_blocks = l.k_blocks;
+  p.k_seg = l.k_seg;
+  p.stages = few_stages(l.epi == kEpiGated, p.n_pad);
+  p.stage_bytes = few_stage_bytes(l.epi == kEpiGated, p.n_pad);
+  p.alpha = l.alpha;
+  p.act = l.act;
+  p.out = l.out;
+  p.g = l.g;
+  p.u = l.u;
+  p.ld_out = l.ld_out;
+  p.ld_g = l.ld_g;
+  p.ld_u = l.ld_u;
+  p.targets = l.targets;
+  p.first_col = l.first_col;
+  p.stats = static_cast<float2*>(l.stats);
+  p.slots = l.slots;
+  p.hit = l.hit;
+  p.lse = l.lse;
+  p.weight = l.weight;
+  p.watchdog_ns = l.watchdog_ns;
+  return l.dtype == 0 ? launch_few_one<0>(l, maps, p, stream)
+                      : launch_few_one<1>(l, maps, p, stream);
 }
 
 cudaError_t launch_linear_join(const LinearJoin& l, cudaStream_t stream) {
@@ -187,7 +275,7 @@ cudaError_t launch_xent_join(const XentJoin& l, cudaStream_t stream) {
   p.rows = l.rows;
   p.slots = l.slots;
   p.vocab = l.vocab;
-  return launch_pdl(xent_join_kernel, dim3((l.rows + 7u) / 8u), 256, 0, stream, p);
+  return launch_pdl(xent_join_kernel, dim3((l.rows + 3u) / 4u), 128, 0, stream, p);
 }
 
 cudaError_t launch_xent_weights(const XentWeights& l, cudaStream_t stream) {

@@ -24,30 +24,39 @@ struct XentJoinParams {
   uint32_t rows, slots, vocab;
 };
 
-// One warp a row.  Lanes take every 32nd slot; the largest maximum first, then the scaled sums in a
-// fixed order.
-__global__ void __launch_bounds__(256) xent_join_kernel(const XentJoinParams p) {
+// One warp a row.  A lane takes every 32nd slot, four at a time, and keeps a running maximum and the sum
+// relative to it; lanes are joined in a fixed order.
+__global__ void __launch_bounds__(128) xent_join_kernel(const XentJoinParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t lane = threadIdx.x & 31u;
   const uint64_t row = (static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32u;
   if (row >= p.rows) return;
   const float2* src = p.stats + row * p.slots;
-  float top = -INFINITY;
-  for (uint32_t i = lane; i < p.slots; i += 32u) top = fmaxf(top, src[i].x);
+  const int64_t target = p.targets[row];
+  float top = -INFINITY, sum = 0.0f;
+  // to a new maximum; where there is none yet the exponentials are 0
+  auto join = [](float& top, float& sum, float m, float s) {
+    const float t = fmaxf(top, m), base = t == -INFINITY ? 0.0f : t;
+    sum = sum * __expf(top - base) + s * __expf(m - base);
+    top = t;
+  };
+  for (uint32_t i = lane; i < p.slots; i += 128u) {
+    float2 c[4];
 #pragma unroll
-  for (uint32_t o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
-  for (uint32_t i = lane; i < p.slots; i += 32u) {
-    const float2 c = src[i];
-    sum += c.y * expf(c.x - base);
+    for (uint32_t j = 0; j < 4; ++j)
+      c[j] = i + 32u * j < p.slots ? src[i + 32u * j] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) join(top, sum, c[j].x, c[j].y);
   }
 #pragma unroll
-  for (uint32_t o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (uint32_t o = 16; o > 0; o /= 2) {
+    const float m = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
+    join(top, sum, m, s);
+  }
   if (lane == 0) {
     const float lse = top + logf(sum);
-    const TargetKind kind = target_kind(p.targets[row], p.ignore, p.vocab);
+    const TargetKind kind = target_kind(target, p.ignore, p.vocab);
     p.lse[row] = lse;
     p.loss[row] = kind == kTargetIgnored ? 0.0f
                   : kind == kTargetValid ? lse - p.hit[row]
