@@ -15,6 +15,7 @@ import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtg.so")
+TORCH_PATH = os.path.join(HERE, "tg_torch.so")   # the calls of the fused products on torch tensors
 
 TG_F16 = 0
 TG_BF16 = 1
@@ -811,151 +812,76 @@ def tg_xent_bwd_workspace_bytes(rows, cols, vocab):
     return _check(load_library().tg_xent_bwd_workspace_bytes(rows, cols, vocab))
 
 
-def _matrix16(x, name, like=None, shape=None):
-    """(type code, rows, cols, row stride) of a float16 or bfloat16 matrix; of ``like``'s type and of
-    ``shape``, where they are given."""
-    code = _type_code(x.dtype)
-    if code == TG_F32 or (like is not None and x.dtype != like.dtype):
-        raise TypeError(f"{name} must be float16 or bfloat16"
-                        + (", the other matrices' type" if like is not None else ""))
-    rows, cols, ld = _rows_of(x, name)
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{name} must be [{shape[0]}, {shape[1]}], not [{rows}, {cols}]")
-    return code, rows, cols, ld
+_torch_calls = None
 
 
-def _row_values(x, name, dtype, rows):
-    if x.dtype != dtype or x.dim() != 1 or x.shape[0] != rows or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {rows} values")
-    return x.data_ptr()
+def _calls():
+    """tg_torch.so, the module that makes the calls below (loaded once)."""
+    global _torch_calls
+    if _torch_calls is None:
+        import importlib.util
 
+        import torch  # noqa: F401  (its libraries have to be there first)
 
-def _workspace(nbytes, like):
-    """(tensor, pointer) of ``nbytes`` on like's device."""
-    import torch
-
-    if nbytes == 0:
-        return None, None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    return ws, ws.data_ptr()
+        load_library()
+        if not os.path.exists(TORCH_PATH):
+            raise RuntimeError(
+                f"{TORCH_PATH} is not built; run persistent_warp_specialized_gb300._build.build()")
+        spec = importlib.util.spec_from_file_location("tg_torch", TORCH_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(TgError)
+        _torch_calls = module
+    return _torch_calls
 
 
 def input_grad(dy, w, out=None, stream=None):
     """torch convenience: dx = dy w^T [rows, cols], what a linear layer y = x w hands back to x, of dy
     [rows, outs] and w [cols, outs], both float16 or both bfloat16.  w is not transposed in memory."""
-    import torch
-
-    dtype, rows, outs, ld_dy = _matrix16(dy, "dy")
-    _, cols, w_outs, ld_w = _matrix16(w, "w", dy)
-    if w_outs != outs:
-        raise ValueError(f"dy has {outs} columns and w {w_outs}")
-    ld_dx = cols if out is None else _matrix16(out, "out", dy, (rows, cols))[3]
-    lib = load_library()
-    nbytes = _check(lib.tg_input_grad_workspace_bytes(rows, cols, outs))
+    calls = _torch_calls or _calls()
+    if stream is None:
+        return calls.input_grad(dy, w, out)
     with _allocating_on(stream):
-        if out is None:
-            out = torch.empty((rows, cols), dtype=dy.dtype, device=dy.device)
-        ws, wsp = _workspace(nbytes, dy)
-    _check(lib.tg_input_grad(dy.data_ptr(), w.data_ptr(), out.data_ptr(), rows, cols, outs, ld_dy,
-                             ld_w, ld_dx, dtype, wsp, nbytes, _stream(stream)))
-    return out
+        return calls.input_grad(dy, w, out)
 
 
 def gated_forward(x, w_gate, w_up, act="silu", keep=False, out=None, stream=None):
     """torch convenience: h = act(x w_gate) (x w_up) of x [rows, cols] and weights [cols, outs], all
     float16 or all bfloat16; act is "silu" or "gelu" (tanh form).  keep: (h, g, u), with g = x w_gate
     and u = x w_up for gated_backward."""
-    import torch
-
-    dtype, rows, cols, ld_x = _matrix16(x, "x")
-    outs = w_gate.shape[-1]
-    ld_wg = _matrix16(w_gate, "w_gate", x, (cols, outs))[3]
-    ld_wu = _matrix16(w_up, "w_up", x, (cols, outs))[3]
-    ld_h = outs if out is None else _matrix16(out, "out", x, (rows, outs))[3]
-    code = _act(act)
-    lib = load_library()
-    nbytes = _check(lib.tg_gated_fwd_workspace_bytes(rows, cols, outs))
+    calls = _torch_calls or _calls()
+    if stream is None:
+        return calls.gated_forward(x, w_gate, w_up, _act(act), keep, out)
     with _allocating_on(stream):
-        if out is None:
-            out = torch.empty((rows, outs), dtype=x.dtype, device=x.device)
-        g = torch.empty((rows, outs), dtype=x.dtype, device=x.device) if keep else None
-        u = torch.empty((rows, outs), dtype=x.dtype, device=x.device) if keep else None
-        ws, wsp = _workspace(nbytes, x)
-    _check(lib.tg_gated_fwd(
-        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(),
-        g.data_ptr() if keep else None, u.data_ptr() if keep else None, rows, cols, outs, ld_x,
-        ld_wg, ld_wu, ld_h, outs, outs, code, dtype, wsp, nbytes, _stream(stream)))
-    return (out, g, u) if keep else out
+        return calls.gated_forward(x, w_gate, w_up, _act(act), keep, out)
 
 
 def gated_backward(dh, g, u, x, w_gate, w_up, act="silu", stream=None):
     """torch convenience: (dx, dw_gate, dw_up) of gated_forward from dh [rows, outs] and the g and u
     that it kept."""
-    import torch
-
-    dtype, rows, outs, ld_dh = _matrix16(dh, "dh")
-    ld_g = _matrix16(g, "g", dh, (rows, outs))[3]
-    ld_u = _matrix16(u, "u", dh, (rows, outs))[3]
-    cols = x.shape[-1]
-    ld_x = _matrix16(x, "x", dh, (rows, cols))[3]
-    ld_wg = _matrix16(w_gate, "w_gate", dh, (cols, outs))[3]
-    ld_wu = _matrix16(w_up, "w_up", dh, (cols, outs))[3]
-    code = _act(act)
-    lib = load_library()
-    nbytes = _check(lib.tg_gated_bwd_workspace_bytes(rows, cols, outs))
+    calls = _torch_calls or _calls()
+    if stream is None:
+        return calls.gated_backward(dh, g, u, x, w_gate, w_up, _act(act))
     with _allocating_on(stream):
-        dx = torch.empty((rows, cols), dtype=dh.dtype, device=dh.device)
-        dwg = torch.empty((cols, outs), dtype=dh.dtype, device=dh.device)
-        dwu = torch.empty((cols, outs), dtype=dh.dtype, device=dh.device)
-        ws, wsp = _workspace(nbytes, dh)
-    _check(lib.tg_gated_bwd(
-        dh.data_ptr(), g.data_ptr(), u.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
-        w_up.data_ptr(), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), rows, cols, outs, ld_dh,
-        ld_g, ld_u, ld_x, ld_wg, ld_wu, cols, outs, outs, code, dtype, wsp, nbytes,
-        _stream(stream)))
-    return dx, dwg, dwu
+        return calls.gated_backward(dh, g, u, x, w_gate, w_up, _act(act))
 
 
 def linear_cross_entropy(x, w, targets, ignore_index=-100, stream=None):
     """torch convenience: (loss, lse), float32 [rows], of the logits x w^T, which are not kept: x
     [rows, cols] and w [vocab, cols] float16 or bfloat16, targets int64 [rows].  Rows whose target is
     ignore_index have loss 0; other targets outside the vocabulary give NaN."""
-    import torch
-
-    dtype, rows, cols, ld_x = _matrix16(x, "x")
-    vocab = w.shape[0]
-    ld_w = _matrix16(w, "w", x, (vocab, cols))[3]
-    at = _row_values(targets, "targets", torch.int64, rows)
-    lib = load_library()
-    nbytes = _check(lib.tg_xent_fwd_workspace_bytes(rows, cols, vocab))
+    calls = _torch_calls or _calls()
+    if stream is None:
+        return calls.linear_cross_entropy(x, w, targets, ignore_index)
     with _allocating_on(stream):
-        loss = torch.empty(rows, dtype=torch.float32, device=x.device)
-        lse = torch.empty(rows, dtype=torch.float32, device=x.device)
-        ws, wsp = _workspace(nbytes, x)
-    _check(lib.tg_xent_fwd(x.data_ptr(), w.data_ptr(), at, loss.data_ptr(), lse.data_ptr(), rows,
-                           cols, vocab, ld_x, ld_w, ignore_index, dtype, wsp, nbytes,
-                           _stream(stream)))
-    return loss, lse
+        return calls.linear_cross_entropy(x, w, targets, ignore_index)
 
 
 def linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index=-100, stream=None):
     """torch convenience: (dx, dw) of linear_cross_entropy from the gradient of each row's loss,
     float32 [rows], and the lse that it returned."""
-    import torch
-
-    dtype, rows, cols, ld_x = _matrix16(x, "x")
-    vocab = w.shape[0]
-    ld_w = _matrix16(w, "w", x, (vocab, cols))[3]
-    at = _row_values(targets, "targets", torch.int64, rows)
-    dp = _row_values(dloss, "dloss", torch.float32, rows)
-    lp = _row_values(lse, "lse", torch.float32, rows)
-    lib = load_library()
-    nbytes = _check(lib.tg_xent_bwd_workspace_bytes(rows, cols, vocab))
+    calls = _torch_calls or _calls()
+    if stream is None:
+        return calls.linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index)
     with _allocating_on(stream):
-        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-        dw = torch.empty((vocab, cols), dtype=x.dtype, device=x.device)
-        ws, wsp = _workspace(nbytes, x)
-    _check(lib.tg_xent_bwd(dp, x.data_ptr(), w.data_ptr(), at, lp, dx.data_ptr(), dw.data_ptr(),
-                           rows, cols, vocab, ld_x, ld_w, cols, cols, ignore_index, dtype, wsp,
-                           nbytes, _stream(stream)))
-    return dx, dw
+        return calls.linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index)

