@@ -37,12 +37,12 @@ struct FewParams {
   uint32_t act;                      // kEpiGated
   void *out, *g, *u;                 // results; kEpiGated: g and u too, or null
   int64_t ld_out, ld_g, ld_u;
-  const int64_t* targets;            // kEpiStats, kEpiDlogits: logits of words first_col ..
-  uint32_t first_col;
+  RowWeights loss;                   // kEpiStats: targets; kEpiDlogits: all of it
+  uint32_t first_col;                // logits of words first_col ..
   float2* stats;                     // [rows][slots], a slot for each tile
   uint32_t slots;
   float* hit;
-  const float *lse, *weight;
+  const float* lse;                  // kEpiDlogits
   uint64_t watchdog_ns;
 };
 
@@ -152,13 +152,23 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   int32_t hot[2] = {-1, -1};
   float lse[2] = {}, weight[2] = {};
   if constexpr (EPI == kEpiStats || EPI == kEpiDlogits) {
+    float top = 0.0f;   // the largest |dloss| of all rows: every warp looks for itself
+    if constexpr (EPI == kEpiDlogits) {
+      for (uint32_t r = lane; r < p.rows; r += 32u) top = fmaxf(top, p.loss.counted(r));
+#pragma unroll
+      for (uint32_t o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (blockIdx.x == 0 && threadIdx.x == 0) p.loss.template write_alpha<DT>(top);
+    }
 #pragma unroll
     for (uint32_t i = 0; i < 2; ++i) {
       const uint32_t r = lane + 32u * i;
       if (warp < 2 || r >= share || row0 + r >= p.rows) continue;
-      const int64_t at = p.targets[row0 + r] - static_cast<int64_t>(p.first_col + n0);
+      const int64_t at = p.loss.targets[row0 + r] - static_cast<int64_t>(p.first_col + n0);
       if (at >= 0 && at < kFewM) hot[i] = static_cast<int32_t>(at);
-      if constexpr (EPI == kEpiDlogits) lse[i] = p.lse[row0 + r], weight[i] = p.weight[row0 + r];
+      if constexpr (EPI == kEpiDlogits) {
+        lse[i] = p.lse[row0 + r];
+        weight[i] = p.loss.template weight<DT>(row0 + r, top);
+      }
     }
   }
 

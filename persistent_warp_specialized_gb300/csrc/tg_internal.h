@@ -129,23 +129,36 @@ cudaError_t prepare_wgrad_kernels(int* max_pairs);
 cudaError_t launch_wgrad(int dtype, bool debug, const WgradLaunch& l, cudaStream_t stream);
 
 // Products with fused epilogues (tg_linear_kernel.cuh).  Matrices, tile counts and segments as
-// LinearParams has them.
-struct LinearLaunch {
+// LinearProblem has them.
+struct LinearProduct {
   CUtensorMap a[2], b[2], c[3];
-  int dtype;
   bool a_mn, b_mn;              // the operand lies with m (n) contiguous
-  int epi;                      // LinearEpi
   uint32_t M, N;
   uint32_t m_blocks, n_blocks, k_blocks, n_seg, k_seg, group, column_major;
   uint32_t split_from, total_units, splits, blocks_per_split;   // units: per split
   uint32_t partial, part_rows;
   const float* alpha;
-  uint32_t act, keep;
+};
+// The cross entropy's rows (RowWeights)
+struct XentRows {
+  const float* dloss;
   const int64_t* targets;
+  int64_t ignore;
+  uint32_t vocab;
+  float* alpha;
+};
+struct LinearLaunch {
+  LinearProduct q[2];
+  int products;                 // 1; with kEpiStore also 2, the one with the longer units first
+  uint32_t extra;               // units of the second that take as long as one of the first
+  int dtype;
+  int epi;                      // LinearEpi
+  uint32_t act, keep;
   uint32_t first_col, slots;
   void* stats;
   float* hit;
-  const float *lse, *weight;
+  const float* lse;
+  XentRows loss;
   uint32_t grid;                // CTAs
   uint64_t watchdog_ns;
   int64_t inject_skip_phase;
@@ -166,25 +179,26 @@ struct FewLaunch {
   uint32_t act;
   void *out, *g, *u;
   int64_t ld_out, ld_g, ld_u;
-  const int64_t* targets;
   uint32_t first_col, slots;
   void* stats;
   float* hit;
-  const float *lse, *weight;
+  const float* lse;
+  XentRows loss;
   uint64_t watchdog_ns;
 };
 cudaError_t launch_few(const FewLaunch& l, cudaStream_t stream);
 
-// out [rows, cols] = alpha (null: 1) times the sum over splits of partials [splits][part_rows][cols]
+// out [rows, cols] = alpha (null: 1) times the sum over splits of partials [splits][part_rows][cols];
+// up to three at once
 struct LinearJoin {
   const float* partials;
   uint32_t splits, part_rows, rows, cols;
   const float* alpha;
   void* out;
   int64_t ld_out;
-  int dtype, sms;
 };
-cudaError_t launch_linear_join(const LinearJoin& l, cudaStream_t stream);
+cudaError_t launch_linear_join(const LinearJoin* joins, int count, int dtype, int sms,
+                               cudaStream_t stream);
 
 // h = act(g) u of partial sums of g and u, each [splits][part_rows][outs]; g and u too where given
 struct GatedJoin {
@@ -207,8 +221,7 @@ struct GatedGrad {
 };
 cudaError_t launch_gated_grad(const GatedGrad& l, cudaStream_t stream);
 
-// Cross entropy (tg_xent_kernel.cuh): loss and lse of each row from its statistics; and the weight of
-// each row's gradient relative to the largest, with the factor that undoes that.
+// Cross entropy (tg_xent_kernel.cuh): loss and lse of each row from its statistics.
 struct XentJoin {
   const void* stats;     // float2 [rows][slots]
   const float* hit;
@@ -218,16 +231,6 @@ struct XentJoin {
   uint32_t rows, slots, vocab;
 };
 cudaError_t launch_xent_join(const XentJoin& l, cudaStream_t stream);
-struct XentWeights {
-  const float* dloss;
-  const int64_t* targets;
-  int64_t ignore;
-  float *weight, *alpha;
-  uint32_t rows, vocab;
-  int dtype;
-};
-cudaError_t launch_xent_weights(const XentWeights& l, cudaStream_t stream);
-
 cudaError_t clear_watchdog_status(cudaStream_t stream);
 // synchronises ``stream``, returns the status word in *out and clears it
 cudaError_t read_and_clear_watchdog_status(unsigned int* out, cudaStream_t stream);

@@ -39,84 +39,109 @@ struct Product {
   // the first's; the caller joins them after the last
   int accumulate = 0;
   uint32_t act = 0, keep = 0;
-  const int64_t* targets = nullptr;
   uint32_t first_col = 0, slots = 0;
   void* stats = nullptr;
   float* hit = nullptr;
-  const float *lse = nullptr, *weight = nullptr;
+  const float* lse = nullptr;
+  tg::XentRows loss = {};
 };
 
 // How a product is cut into units.
 struct Plan {
-  uint32_t m_tiles, n_tiles, n_seg, k_blocks, k_seg, splits, blocks_per_split, split_from, units,
-      pairs;
+  bool few;                 // the kernel for few rows takes it, and nothing below counts
+  uint32_t m_tiles, n_tiles, n_seg, k_blocks, k_seg, splits, blocks_per_split;
+  uint32_t units;           // tiles
   uint32_t part_rows;
-  bool few;                 // the kernel for few rows takes it, and nothing above counts
   uint64_t partial_bytes;   // fp32 sums of one N segment (0: results are stored rounded)
-  double us;                // what the plan is expected to take
 };
 
-// Microseconds on GB300 that the choice of a plan goes by: a k-block of a whole tile and of its
-// half-width unit, what a unit adds (its first loads, and its epilogue where the MMAs wait for it), the
+// Microseconds on GB300 that the choice of splits goes by: a k-block of a tile; what a unit adds; the
 // join, and bytes of partial sums a microsecond, written and read.
-constexpr double kBlockUs = 0.66, kHalfBlockUs = 0.40, kUnitUs = 0.4, kJoinUs = 2.5;
+constexpr double kBlockUs = 0.66, kUnitUs = 0.4, kJoinUs = 2.5;
 constexpr double kWriteBytes = 5e6, kReadBytes = 4e6;
-constexpr uint64_t kMinBlocks = 4;   // k-blocks of a unit when K is split
-
-Plan plan_of(const Product& p, uint64_t pairs, uint64_t splits, bool sums) {
-  Plan w;
-  w.few = false;
-  w.m_tiles = static_cast<uint32_t>(ceil_div(p.M, tg::kPairBM));
-  const uint64_t tile_n = p.epi == tg::kEpiGated ? tg::kGatedTileN : tg::kBN;
-  w.n_seg = static_cast<uint32_t>(ceil_div(p.N, tile_n));
-  w.n_tiles = w.n_seg * p.segs_n;
-  w.k_seg = static_cast<uint32_t>(ceil_div(p.K, tg::kLinBK));
-  w.k_blocks = w.k_seg * p.segs_k;
-  const uint32_t tiles = w.m_tiles * w.n_tiles;
-  w.blocks_per_split = static_cast<uint32_t>(ceil_div(w.k_blocks, splits));
-  w.splits = static_cast<uint32_t>(ceil_div(w.k_blocks, w.blocks_per_split));
-  w.split_from = w.units = tiles;
-  if (w.splits == 1)
-    tg::PersistentTileScheduler::tail_split(tiles, static_cast<uint32_t>(pairs), w.split_from,
-                                            w.units);
-  const uint64_t all = static_cast<uint64_t>(w.units) * w.splits;
-  w.pairs = static_cast<uint32_t>(all < pairs ? all : pairs);
-  const double whole = static_cast<double>(ceil_div(w.split_from * uint64_t(w.splits), pairs));
-  w.us = whole * (w.blocks_per_split * kBlockUs + kUnitUs);
-  if (w.units > w.split_from) w.us += w.k_blocks * kHalfBlockUs + kUnitUs;
-  w.part_rows = static_cast<uint32_t>(ceil_div(p.M, tg::kPartialRows)) * tg::kPartialRows;
-  w.partial_bytes = 0;
-  if (w.splits > 1 || sums) {
-    w.partial_bytes = uint64_t(w.splits) * w.part_rows * p.N * 4;
-    const double bytes = double(w.splits) * p.M * p.N * p.segs_n * 4.0;
-    w.us += bytes / kWriteBytes + kJoinUs + bytes / kReadBytes;
-  }
-  return w;
-}
+constexpr uint32_t kMinBlocks = 4;   // k-blocks of a unit when K is split
 
 // Few rows: the weights are the MMA's larger operand, and clusters share a tile along K.
-bool few_rows(const Product& p, bool sums = false) {
+bool few_rows(const Product& p, bool sums) {
   return p.M <= tg::kFewRows && !p.a_mn && p.segs_n == 1 && !sums;
 }
 
-// Fewer tiles than pairs: K may be split, so that every pair has a unit, at the price of partial sums
-// in fp32 and a join.  The least expected time decides.  sums: results go to partial sums in any case.
-Plan plan_product(const Product& p, int max_pairs, bool sums = false) {
-  const uint64_t pairs = static_cast<uint64_t>(max_pairs);
-  Plan best = plan_of(p, pairs, 1, sums);
-  if (few_rows(p, sums)) {
-    best.few = true;
-    return best;
+// The plan with K in about ``splits`` ranges.  sums: results go to partial sums in any case.
+Plan plan_of(const Product& p, uint32_t splits, bool sums = false) {
+  Plan w;
+  w.few = false;
+  w.m_tiles = static_cast<uint32_t>(ceil_div(p.M, tg::kPairBM));
+  w.n_seg = static_cast<uint32_t>(ceil_div(p.N, p.epi == tg::kEpiGated ? tg::kGatedTileN : tg::kBN));
+  w.n_tiles = w.n_seg * p.segs_n;
+  w.k_seg = static_cast<uint32_t>(ceil_div(p.K, tg::kLinBK));
+  w.k_blocks = w.k_seg * p.segs_k;
+  w.blocks_per_split = (w.k_blocks + splits - 1) / splits;
+  w.splits = (w.k_blocks + w.blocks_per_split - 1) / w.blocks_per_split;
+  w.units = w.m_tiles * w.n_tiles;
+  w.part_rows = static_cast<uint32_t>(ceil_div(p.M, tg::kPartialRows)) * tg::kPartialRows;
+  w.partial_bytes = w.splits > 1 || sums ? uint64_t(w.splits) * w.part_rows * p.N * 4 : 0;
+  return w;
+}
+
+// What the products' units are expected to take over ``pairs`` CTA pairs, and the joins: the longest
+// unit, or every pair's share of all.
+double expected_us(const Product* p, const Plan* w, int count, uint32_t pairs) {
+  double longest = 0, all = 0, join = 0;
+  for (int i = 0; i < count; ++i) {
+    const double unit = w[i].blocks_per_split * kBlockUs + kUnitUs;
+    const uint32_t units = w[i].units * w[i].splits;
+    if (unit > longest) longest = unit;
+    all += units * unit;
+    if (count == 1) all = ((units + pairs - 1) / pairs) * pairs * unit;   // whole waves
+    if (w[i].partial_bytes) {
+      const double bytes = double(w[i].splits) * p[i].M * p[i].N * p[i].segs_n * 4.0;
+      join = kJoinUs + (join > kJoinUs ? join - kJoinUs : 0) + bytes / kWriteBytes + bytes / kReadBytes;
+    }
   }
-  if (p.epi != tg::kEpiStore) return best;
-  const uint64_t tiles = uint64_t(best.m_tiles) * best.n_tiles;
-  uint64_t most = pairs / tiles;
-  if (most > best.k_blocks / kMinBlocks) most = best.k_blocks / kMinBlocks;
-  for (uint64_t splits = 2; splits <= most; ++splits) {
-    const Plan cut = plan_of(p, pairs, splits, sums);
-    if (cut.us < best.us) best = cut;
+  return (all / pairs > longest ? all / pairs : longest) + join;
+}
+
+// Plans of up to two products in one launch.  Where the units would not fill the pairs, or one product's
+// are much longer than a pair's share of all, K may be split at the price of partial sums in fp32 and a
+// join: the least expected time decides.  sums: see plan_of, for the first product.
+void plan_products(const Product* p, Plan* best, int count, int max_pairs, bool sums = false) {
+  const uint32_t pairs = static_cast<uint32_t>(max_pairs);
+  uint32_t most[2] = {1, 1};
+  for (int i = 0; i < count; ++i) {
+    best[i] = plan_of(p[i], 1, i == 0 && sums);
+    if (p[i].epi == tg::kEpiStore && best[i].units < pairs) {
+      const uint32_t fill = pairs / best[i].units, deep = best[i].k_blocks / kMinBlocks;
+      most[i] = fill < deep ? fill : deep;
+    }
   }
-  return best;
+  double least = expected_us(p, best, count, pairs);
+  const uint32_t tries[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 19, 25, 38, 76};
+  for (uint32_t s0 : tries) {
+    if (s0 > 1 && s0 > most[0]) break;
+    for (uint32_t s1 : tries) {
+      if (s1 > 1 && (count < 2 || s1 > most[1])) break;
+      if (s0 == 1 && s1 == 1) continue;
+      Plan cut[2];
+      cut[0] = plan_of(p[0], s0, sums);
+      if (count == 2) cut[1] = plan_of(p[1], s1);
+      const double us = expected_us(p, cut, count, pairs);
+      if (us < least) {
+        least = us;
+        for (int i = 0; i < count; ++i) best[i] = cut[i];
+      }
+    }
+  }
+}
+
+Plan plan_product(const Product& p, int max_pairs) {
+  Plan w;
+  if (few_rows(p, false)) {
+    w = plan_of(p, 1);
+    w.few = true;
+  } else {
+    plan_products(&p, &w, 1, max_pairs);
+  }
+  return w;
 }
 
 constexpr uint64_t kWorkspaceAlign = 256;
@@ -168,111 +193,192 @@ int run_few(const Product& p, int sms, uint64_t watchdog_ns, cudaStream_t stream
     l.ld_g = p.c[1].ld;
     l.ld_u = p.c[2].ld;
   }
-  l.targets = p.targets;
   l.first_col = p.first_col;
   l.slots = p.slots;
   l.stats = p.stats;
   l.hit = p.hit;
   l.lse = p.lse;
-  l.weight = p.weight;
+  l.loss = p.loss;
   l.watchdog_ns = watchdog_ns ? watchdog_ns : default_watchdog_ns(l.k_blocks);
   const cudaError_t e = tg::launch_few(l, stream);
   return e == cudaSuccess ? TG_OK : fail_cuda("product launch", e);
 }
 
-// Enqueues the product by its plan.  partials: fp32 sums of each N segment where the plan has them
-// (joined by the caller).
-int run_product(const Product& p, const Plan& w, void* const partials[2], uint64_t watchdog_ns,
-                int64_t inject, cudaStream_t stream) {
-  tg::LinearLaunch l = {};
+// What a product's units are to the kernel.  partials: fp32 sums of its N segments, where the plan has
+// them.
+int encode_product(tg::LinearProduct* l, const Product& p, const Plan& w, char* partials) {
   for (int i = 0; i < 2; ++i) {
-    const Mat& a = p.a[p.segs_k == 2 ? i : 0];
-    const bool two_b = p.segs_k == 2 || p.segs_n == 2 || p.epi == tg::kEpiGated;
-    const Mat& b = p.b[two_b ? i : 0];
-    if (i == 0 || p.segs_k == 2) TG_TRY(encode_operand(&l.a[i], a, p.a_mn, p.dtype));
-    else l.a[i] = l.a[0];
-    if (i == 0 || two_b) TG_TRY(encode_operand(&l.b[i], b, p.b_mn, p.dtype));
-    else l.b[i] = l.b[0];
+    const bool two_a = p.segs_k == 2;
+    const bool two_b = two_a || p.segs_n == 2 || p.epi == tg::kEpiGated;
+    if (i == 0 || two_a)
+      TG_TRY(encode_operand(&l->a[i], p.a[i], p.a_mn, p.dtype));
+    else
+      l->a[i] = l->a[0];
+    if (i == 0 || two_b)
+      TG_TRY(encode_operand(&l->b[i], p.b[i], p.b_mn, p.dtype));
+    else
+      l->b[i] = l->b[0];
   }
+  l->partial = 0;
   if (w.partial_bytes) {
     for (int i = 0; i < p.segs_n; ++i)
-      TG_TRY(encode_tiled(&l.c[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, partials[i], p.N,
+      TG_TRY(encode_tiled(&l->c[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+                          partials + i * padded(w.partial_bytes), p.N,
                           uint64_t(w.splits) * w.part_rows, 32, tg::kPartialRows, "workspace"));
-    l.partial = p.accumulate == 2 ? 2 : 1;
+    l->partial = p.accumulate == 2 ? 2 : 1;
   } else {
     for (int i = 0; i < 3; ++i)
       if (p.c[i].p)
-        TG_TRY(encode_tiled(&l.c[i], type16(p.dtype), 2, p.c[i].p, p.c[i].cols, p.c[i].rows,
+        TG_TRY(encode_tiled(&l->c[i], type16(p.dtype), 2, p.c[i].p, p.c[i].cols, p.c[i].rows,
                             tg::kEpiN, 32, p.c[i].name, true, p.c[i].ld * 2));
   }
-  l.dtype = p.dtype;
-  l.a_mn = p.a_mn;
-  l.b_mn = p.b_mn;
-  l.epi = p.epi;
-  l.M = static_cast<uint32_t>(p.M);
-  l.N = static_cast<uint32_t>(p.N);
-  l.m_blocks = w.m_tiles;
-  l.n_blocks = w.n_tiles;
-  l.k_blocks = w.k_blocks;
-  l.n_seg = w.n_seg;
-  l.k_seg = w.k_seg;
-  l.group = tg::kGroup;
-  l.column_major = 0;
-  l.split_from = w.split_from;
-  l.total_units = w.units;
-  l.splits = w.splits;
-  l.blocks_per_split = w.blocks_per_split;
-  l.part_rows = w.part_rows;
-  l.alpha = p.alpha;
-  l.act = p.act;
-  l.keep = p.keep;
-  l.targets = p.targets;
-  l.first_col = p.first_col;
-  l.slots = p.slots;
-  l.stats = p.stats;
-  l.hit = p.hit;
-  l.lse = p.lse;
-  l.weight = p.weight;
-  l.grid = 2 * w.pairs;
+  l->a_mn = p.a_mn;
+  l->b_mn = p.b_mn;
+  l->M = static_cast<uint32_t>(p.M);
+  l->N = static_cast<uint32_t>(p.N);
+  l->m_blocks = w.m_tiles;
+  l->n_blocks = w.n_tiles;
+  l->k_blocks = w.k_blocks;
+  l->n_seg = w.n_seg;
+  l->k_seg = w.k_seg;
+  l->group = tg::kGroup;
+  l->column_major = 0;
+  l->split_from = l->total_units = w.units;
+  l->splits = w.splits;
+  l->blocks_per_split = w.blocks_per_split;
+  l->part_rows = w.part_rows;
+  l->alpha = p.alpha;
+  return TG_OK;
+}
+
+// Enqueues up to two products in one launch, the one with the longer units first.
+int run_products(const Product* p, const Plan* w, char* const* partials, int count, int max_pairs,
+                 uint64_t watchdog_ns, int64_t inject, cudaStream_t stream) {
+  tg::LinearLaunch l = {};
+  const uint32_t pairs = static_cast<uint32_t>(max_pairs);
+  const int first = count == 2 && w[1].blocks_per_split > w[0].blocks_per_split ? 1 : 0;
+  uint32_t units = 0, k_blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    const int at = first ? 1 - i : i;
+    TG_TRY(encode_product(&l.q[i], p[at], w[at], partials[at]));
+    units += w[at].units * w[at].splits;
+    k_blocks = w[at].k_blocks > k_blocks ? w[at].k_blocks : k_blocks;
+  }
+  // Workers without a unit in the first product's last round take units of the second one meanwhile
+  // (LinearUnits), and the rounds go through what is left.  Where their last one would keep at most
+  // half of the pairs busy, its tiles are cut in halves.
+  tg::LinearProduct& last = l.q[count - 1];
+  uint32_t workers = units < pairs ? units : pairs, ahead = 0;
+  if (count == 2) {
+    const uint32_t idle = workers - l.q[0].total_units * l.q[0].splits % workers;
+    if (idle < workers) {
+      const uint32_t as_long = l.q[0].blocks_per_split / last.blocks_per_split;
+      const uint32_t share = (last.total_units * last.splits + idle - 1) / idle;
+      l.extra = as_long < share ? as_long : share;
+      ahead = idle * l.extra;
+    }
+  }
+  if (last.splits == 1 && last.total_units > ahead && (count == 1 || units >= pairs)) {
+    uint32_t from, all;
+    tg::PersistentTileScheduler::tail_split(last.total_units - ahead, pairs, from, all);
+    last.split_from = ahead + from;
+    last.total_units = ahead + all;
+    if (count == 1) workers = all < pairs ? all : pairs;
+  }
+  l.products = count;
+  l.dtype = p[0].dtype;
+  l.epi = p[0].epi;
+  l.act = p[0].act;
+  l.keep = p[0].keep;
+  l.first_col = p[0].first_col;
+  l.slots = p[0].slots;
+  l.stats = p[0].stats;
+  l.hit = p[0].hit;
+  l.lse = p[0].lse;
+  l.loss = p[0].loss;
+  l.grid = 2 * workers;
   // a k-block of this kernel is two of the 64-deep ones that the default limit counts
-  l.watchdog_ns = watchdog_ns ? watchdog_ns : default_watchdog_ns(2 * w.k_blocks);
+  l.watchdog_ns = watchdog_ns ? watchdog_ns : default_watchdog_ns(2 * k_blocks);
   l.inject_skip_phase = inject;
   const cudaError_t e = tg::launch_linear(l, stream);
   return e == cudaSuccess ? TG_OK : fail_cuda("product launch", e);
 }
 
-// Adds the partial sums of a product's N segments into its outputs.
-int join_product(const Product& p, const Plan& w, void* const partials[2], int sms,
-                 cudaStream_t stream) {
-  for (int i = 0; i < p.segs_n; ++i) {
-    tg::LinearJoin j;
-    j.partials = static_cast<const float*>(partials[i]);
-    j.splits = w.splits;
-    j.part_rows = w.part_rows;
-    j.rows = static_cast<uint32_t>(p.M);
-    j.cols = static_cast<uint32_t>(p.N);
-    j.alpha = p.alpha;
-    j.out = const_cast<void*>(p.c[i].p);
-    j.ld_out = p.c[i].ld;
-    j.dtype = p.dtype;
-    j.sms = sms;
-    const cudaError_t e = tg::launch_linear_join(j, stream);
-    if (e != cudaSuccess) return fail_cuda("join launch", e);
-  }
-  return TG_OK;
-}
-
-// A product by itself: its units, and the join of its partial sums at ``ws`` where it has them.
-int whole_product(const Product& p, const Plan& w, void* ws, int sms, cudaStream_t stream,
-                  uint64_t watchdog_ns = 0, int64_t inject = -1) {
-  if (w.few) return run_few(p, sms, watchdog_ns, stream);
-  void* const partials[2] = {ws, static_cast<char*>(ws) + padded(w.partial_bytes)};
-  TG_TRY(run_product(p, w, partials, watchdog_ns, inject, stream));
-  return w.partial_bytes ? join_product(p, w, partials, sms, stream) : TG_OK;
+// Adds the partial sums of the products that have them into their outputs, in one launch.
+int join_products(const Product* p, const Plan* w, char* const* partials, int count, int sms,
+                  cudaStream_t stream) {
+  tg::LinearJoin jobs[3];
+  int n = 0;
+  for (int q = 0; q < count; ++q)
+    for (int i = 0; i < p[q].segs_n && w[q].partial_bytes; ++i) {
+      tg::LinearJoin& j = jobs[n++];
+      j.partials = reinterpret_cast<const float*>(partials[q] + i * padded(w[q].partial_bytes));
+      j.splits = w[q].splits;
+      j.part_rows = w[q].part_rows;
+      j.rows = static_cast<uint32_t>(p[q].M);
+      j.cols = static_cast<uint32_t>(p[q].N);
+      j.alpha = p[q].alpha;
+      j.out = const_cast<void*>(p[q].c[i].p);
+      j.ld_out = p[q].c[i].ld;
+    }
+  if (n == 0) return TG_OK;
+  const cudaError_t e = tg::launch_linear_join(jobs, n, p[0].dtype, sms, stream);
+  return e == cudaSuccess ? TG_OK : fail_cuda("join launch", e);
 }
 
 uint64_t partials_of(const Product& p, const Plan& w) {
   return w.partial_bytes && !w.few ? p.segs_n * padded(w.partial_bytes) : 0;
+}
+
+// A product by itself: its units, and the join of its partial sums at ``ws`` where it has them.
+int whole_product(const Product& p, const Plan& w, void* ws, int sms, int pairs, cudaStream_t stream,
+                  uint64_t watchdog_ns = 0, int64_t inject = -1) {
+  if (w.few) return run_few(p, sms, watchdog_ns, stream);
+  char* const partials[1] = {static_cast<char*>(ws)};
+  TG_TRY(run_products(&p, &w, partials, 1, pairs, watchdog_ns, inject, stream));
+  return join_products(&p, &w, partials, 1, sms, stream);
+}
+
+// The gradients towards an input and towards weights that are taken from the same matrices: p[0] and
+// p[1] in one launch, or p[0] by the kernel for few rows.  sums: p[0]'s fp32 sums run over several
+// launches and are joined by the caller.
+struct GradPlans {
+  Plan w[2];
+  uint64_t bytes[2];        // partial sums of each
+
+  GradPlans(const Product* p, int pairs, bool sums = false) {
+    if (few_rows(p[0], sums)) {
+      w[0] = plan_product(p[0], pairs);
+      plan_products(&p[1], &w[1], 1, pairs);
+    } else {
+      plan_products(p, w, 2, pairs, sums);
+    }
+    for (int i = 0; i < 2; ++i) bytes[i] = partials_of(p[i], w[i]);
+  }
+};
+
+// Enqueues what is asked for of the two.  Their plans hold for both together and for either.
+int run_grads(const Product* p, const GradPlans& o, const bool (&wanted)[2], bool join_first,
+              char* const* partials, int sms, int pairs, cudaStream_t stream) {
+  Product q[2];
+  Plan w[2];
+  char* at[2];
+  int n = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (!wanted[i]) continue;
+    if (o.w[i].few) {
+      TG_TRY(run_few(p[i], sms, 0, stream));
+      continue;
+    }
+    q[n] = p[i];
+    w[n] = o.w[i];
+    at[n++] = partials[i];
+  }
+  if (n == 0) return TG_OK;
+  TG_TRY(run_products(q, w, at, n, pairs, 0, -1, stream));
+  if (wanted[0] && !o.w[0].few && !join_first)
+    return join_products(q + 1, w + 1, at + 1, n - 1, sms, stream);
+  return join_products(q, w, at, n, sms, stream);
 }
 
 // ---------------------------------------------------------------- checks
@@ -390,7 +496,7 @@ int input_grad_impl(const void* dy, const void* w, void* dx, int64_t rows, int64
     const cudaError_t e = tg::clear_watchdog_status(st);
     if (e != cudaSuccess) return fail_cuda("clearing the watchdog word", e);
   }
-  TG_TRY(whole_product(p, plan, ws, sms, st, watchdog_ns, inject));
+  TG_TRY(whole_product(p, plan, ws, sms, pairs, st, watchdog_ns, inject));
   return debug ? watchdog_result(st) : TG_OK;
 }
 
@@ -425,8 +531,9 @@ GatedPlan gated_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& h, i
   Product two = p;
   two.epi = tg::kEpiStore;
   two.segs_n = 2;
-  const Plan cut = plan_product(two, pairs);
-  if (cut.splits > 1 && cut.us < o.plan.us) {
+  Plan cut;
+  plan_products(&two, &cut, 1, pairs);
+  if (cut.splits > 1 && expected_us(&two, &cut, 1, pairs) < expected_us(&p, &o.plan, 1, pairs)) {
     o.p = two;
     o.plan = cut;
   }
@@ -434,45 +541,42 @@ GatedPlan gated_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& h, i
 }
 
 struct GatedBwd {
-  Product dx, dw;
-  Plan dx_plan, dw_plan;
-  uint64_t dgu_bytes, total;   // total: and the larger of the products' partial sums
+  Product p[2];             // dx; dwg and dwu
+  GradPlans plans;
+  uint64_t dgu_bytes, total;
 };
 // With null pointers where only sizes matter.
 GatedBwd gated_bwd_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& dx, const Mat& dwg,
                         const Mat& dwu, void* dgu, int dtype, int pairs) {
-  GatedBwd o;
   const int64_t rows = x.rows, cols = x.cols, outs = wg.cols;
   const Mat dg = {dgu, rows, outs, 2 * outs, "dg"};
   const Mat du = {dgu ? static_cast<char*>(dgu) + 2 * outs : nullptr, rows, outs, 2 * outs, "du"};
+  Product p[2];
   // dX = dg Wg^T + du Wu^T: K in two segments
-  o.dx.dtype = dtype;
-  o.dx.M = rows;
-  o.dx.N = cols;
-  o.dx.K = outs;
-  o.dx.segs_k = 2;
-  o.dx.a[0] = dg;
-  o.dx.a[1] = du;
-  o.dx.b[0] = wg;
-  o.dx.b[1] = wu;
-  o.dx.c[0] = dx;
-  o.dx_plan = plan_product(o.dx, pairs);
+  p[0].dtype = dtype;
+  p[0].M = rows;
+  p[0].N = cols;
+  p[0].K = outs;
+  p[0].segs_k = 2;
+  p[0].a[0] = dg;
+  p[0].a[1] = du;
+  p[0].b[0] = wg;
+  p[0].b[1] = wu;
+  p[0].c[0] = dx;
   // dWg = X^T dg, dWu = X^T du: N in two segments
-  o.dw.dtype = dtype;
-  o.dw.a_mn = o.dw.b_mn = true;
-  o.dw.M = cols;
-  o.dw.N = outs;
-  o.dw.K = rows;
-  o.dw.segs_n = 2;
-  o.dw.a[0] = x;
-  o.dw.b[0] = dg;
-  o.dw.b[1] = du;
-  o.dw.c[0] = dwg;
-  o.dw.c[1] = dwu;
-  o.dw_plan = plan_product(o.dw, pairs);
-  o.dgu_bytes = padded(uint64_t(rows) * 2 * outs * 2);
-  const uint64_t a = partials_of(o.dx, o.dx_plan), b = partials_of(o.dw, o.dw_plan);
-  o.total = o.dgu_bytes + (a > b ? a : b);
+  p[1].dtype = dtype;
+  p[1].a_mn = p[1].b_mn = true;
+  p[1].M = cols;
+  p[1].N = outs;
+  p[1].K = rows;
+  p[1].segs_n = 2;
+  p[1].a[0] = x;
+  p[1].b[0] = dg;
+  p[1].b[1] = du;
+  p[1].c[0] = dwg;
+  p[1].c[1] = dwu;
+  GatedBwd o = {{p[0], p[1]}, GradPlans(p, pairs), padded(uint64_t(rows) * 2 * outs * 2), 0};
+  o.total = o.dgu_bytes + o.plans.bytes[0] + o.plans.bytes[1];
   return o;
 }
 
@@ -506,7 +610,7 @@ XentFwd xent_fwd_plan(int64_t rows, int64_t vocab) {
 
 // logits of columns [first, first + n) of the vocabulary, W's rows
 Product logits_product(int epi, const Mat& x, const Mat& w, int64_t first, int64_t n,
-                       const int64_t* targets, int dtype) {
+                       const tg::XentRows& loss, int dtype) {
   Product p;
   p.epi = epi;
   p.dtype = dtype;
@@ -515,7 +619,7 @@ Product logits_product(int epi, const Mat& x, const Mat& w, int64_t first, int64
   p.K = x.cols;
   p.a[0] = x;
   p.b[0] = {static_cast<const char*>(w.p) + first * w.ld * 2, n, w.cols, w.ld, w.name};
-  p.targets = targets;
+  p.loss = loss;
   p.first_col = static_cast<uint32_t>(first);
   return p;
 }
@@ -525,7 +629,7 @@ Product logits_product(int epi, const Mat& x, const Mat& w, int64_t first, int64
 struct XentBwd {
   int64_t chunk, chunks;
   bool sums;                // dX is summed in fp32 over the pieces
-  uint64_t dl_bytes, row_bytes, dx_bytes, dw_bytes, total;
+  uint64_t dl_bytes, dx_bytes, dw_bytes, total;
 };
 
 Product xent_dx_product(const Mat& dl, const Mat& w, int64_t first, const Mat& dx, int dtype) {
@@ -562,22 +666,19 @@ XentBwd xent_bwd_plan(int64_t rows, int64_t cols, int64_t vocab, int dtype, int 
   o.chunk = static_cast<int64_t>(ceil_div(ceil_div(vocab, o.chunks), tg::kBN)) * tg::kBN;
   o.chunks = static_cast<int64_t>(ceil_div(vocab, o.chunk));
   o.sums = o.chunks > 1;
-  const int64_t n = o.chunks > 1 ? o.chunk : vocab;
-  const Mat dl = {nullptr, rows, n, o.chunk, ""}, x = {nullptr, rows, cols, cols, ""},
-            w = {nullptr, vocab, cols, cols, ""};
   o.dl_bytes = padded(uint64_t(rows) * o.chunk * 2);
-  o.row_bytes = padded(uint64_t(rows) * 4);
-  const Product dx = xent_dx_product(dl, w, 0, x, dtype), dw = xent_dw_product(dl, x, w, 0, dtype);
-  o.dx_bytes = partials_of(dx, plan_product(dx, pairs, o.sums));
-  o.dw_bytes = partials_of(dw, plan_product(dw, pairs));
+  o.dx_bytes = o.dw_bytes = 0;
+  const Mat x = {nullptr, rows, cols, cols, ""}, w = {nullptr, vocab, cols, cols, ""};
   // the last piece may be narrower and split its tokens more finely
-  if (o.chunks > 1) {
-    const Mat last = {nullptr, rows, vocab - (o.chunks - 1) * o.chunk, o.chunk, ""};
-    const Product dwl = xent_dw_product(last, x, w, 0, dtype);
-    const uint64_t b = partials_of(dwl, plan_product(dwl, pairs));
-    if (b > o.dw_bytes) o.dw_bytes = b;
+  for (const int64_t first : {int64_t(0), (o.chunks - 1) * o.chunk}) {
+    const Mat dl = {nullptr, rows, vocab - first < o.chunk ? vocab - first : o.chunk, o.chunk, ""};
+    const Product p[2] = {xent_dx_product(dl, w, first, x, dtype),
+                          xent_dw_product(dl, x, w, first, dtype)};
+    const GradPlans plans(p, pairs, o.sums);
+    if (first == 0) o.dx_bytes = plans.bytes[0];
+    if (plans.bytes[1] > o.dw_bytes) o.dw_bytes = plans.bytes[1];
   }
-  o.total = o.dl_bytes + o.row_bytes + kWorkspaceAlign + o.dx_bytes + o.dw_bytes;
+  o.total = o.dl_bytes + kWorkspaceAlign + o.dx_bytes + o.dw_bytes;
   return o;
 }
 
@@ -661,14 +762,13 @@ int tg_gated_fwd(const void* x_dev, const void* wg_dev, const void* wu_dev, void
     o.p.keep = keep;
     o.p.c[1] = g;
     o.p.c[2] = u;
-    return whole_product(o.p, o.plan, nullptr, sms, st);
+    return whole_product(o.p, o.plan, nullptr, sms, pairs, st);
   }
-  void* const partials[2] = {workspace_dev,
-                             static_cast<char*>(workspace_dev) + padded(o.plan.partial_bytes)};
-  TG_TRY(run_product(o.p, o.plan, partials, 0, -1, st));
+  char* const partials[1] = {static_cast<char*>(workspace_dev)};
+  TG_TRY(run_products(&o.p, &o.plan, partials, 1, pairs, 0, -1, st));
   tg::GatedJoin j;
-  j.g_parts = static_cast<const float*>(partials[0]);
-  j.u_parts = static_cast<const float*>(partials[1]);
+  j.g_parts = reinterpret_cast<const float*>(partials[0]);
+  j.u_parts = reinterpret_cast<const float*>(partials[0] + padded(o.plan.partial_bytes));
   j.splits = o.plan.splits;
   j.part_rows = o.plan.part_rows;
   j.rows = static_cast<uint32_t>(rows);
@@ -755,10 +855,9 @@ int tg_gated_bwd(const void* dh_dev, const void* g_dev, const void* u_dev, const
   e.sms = sms;
   const cudaError_t err = tg::launch_gated_grad(e, st);
   if (err != cudaSuccess) return fail_cuda("gated gradient launch", err);
-  void* rest = static_cast<char*>(workspace_dev) + o.dgu_bytes;
-  if (dx_dev) TG_TRY(whole_product(o.dx, o.dx_plan, rest, sms, st));
-  if (weights) TG_TRY(whole_product(o.dw, o.dw_plan, rest, sms, st));
-  return TG_OK;
+  char* const rest = static_cast<char*>(workspace_dev) + o.dgu_bytes;
+  char* const partials[2] = {rest, rest + o.plans.bytes[0]};
+  return run_grads(o.p, o.plans, {dx_dev != nullptr, weights}, true, partials, sms, pairs, st);
 }
 
 int64_t tg_xent_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab) {
@@ -788,11 +887,13 @@ int tg_xent_fwd(const void* x_dev, const void* w_dev, const int64_t* targets_dev
                       {targets_dev, uint64_t(rows) * 8, "targets"}};
   TG_TRY(check_apart(r, 3, 6));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Product p = logits_product(tg::kEpiStats, x, w, 0, vocab, targets_dev, dtype);
+  tg::XentRows loss = {};
+  loss.targets = targets_dev;
+  Product p = logits_product(tg::kEpiStats, x, w, 0, vocab, loss, dtype);
   p.stats = workspace_dev;
   p.slots = o.slots;
   p.hit = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + o.stats_bytes);
-  TG_TRY(whole_product(p, plan_product(p, pairs), nullptr, sms, st));
+  TG_TRY(whole_product(p, plan_product(p, pairs), nullptr, sms, pairs, st));
   tg::XentJoin j;
   j.stats = p.stats;
   j.hit = p.hit;
@@ -849,53 +950,32 @@ int tg_xent_bwd(const float* dloss_dev, const void* x_dev, const void* w_dev,
                       {dloss_dev, row4, "dloss"}, {lse_dev, row4, "lse"}};
   TG_TRY(check_apart(r, 3, 8));
   char* base = static_cast<char*>(workspace_dev);
-  float* weight = reinterpret_cast<float*>(base + o.dl_bytes);
-  float* alpha = reinterpret_cast<float*>(base + o.dl_bytes + o.row_bytes);
-  char* dx_sums = base + o.dl_bytes + o.row_bytes + kWorkspaceAlign;
-  char* dw_sums = dx_sums + o.dx_bytes;
-  tg::XentWeights xw;
-  xw.dloss = dloss_dev;
-  xw.targets = targets_dev;
-  xw.ignore = ignore_index;
-  xw.weight = weight;
-  xw.alpha = alpha;
-  xw.rows = static_cast<uint32_t>(rows);
-  xw.vocab = static_cast<uint32_t>(vocab);
-  xw.dtype = dtype;
-  const cudaError_t e = tg::launch_xent_weights(xw, st);
-  if (e != cudaSuccess) return fail_cuda("cross entropy launch", e);
+  float* alpha = reinterpret_cast<float*>(base + o.dl_bytes);
+  char* dx_sums = base + o.dl_bytes + kWorkspaceAlign;
+  char* const partials[2] = {dx_sums, dx_sums + o.dx_bytes};
+  const tg::XentRows loss = {dloss_dev, targets_dev, ignore_index, static_cast<uint32_t>(vocab), alpha};
+  Product dx_first;
   Plan dx_plan = {};
-  Product dx_product;
-  void* const dx_partials[2] = {dx_sums, nullptr};
   for (int64_t c = 0; c < o.chunks; ++c) {
     const int64_t first = c * o.chunk, n = vocab - first < o.chunk ? vocab - first : o.chunk;
     const Mat dl = {base, rows, n, o.chunk, "gradients of logits"};
-    Product p = logits_product(tg::kEpiDlogits, x, w, first, n, targets_dev, dtype);
+    Product p = logits_product(tg::kEpiDlogits, x, w, first, n, loss, dtype);
     p.c[0] = dl;
     p.lse = lse_dev;
-    p.weight = weight;
-    TG_TRY(whole_product(p, plan_product(p, pairs), nullptr, sms, st));
-    if (dx_dev) {
-      dx_product = xent_dx_product(dl, w, first, dx, dtype);
-      dx_product.alpha = xw.alpha;
-      dx_product.accumulate = !o.sums ? 0 : c == 0 ? 1 : 2;
-      // pieces share the first one's splits, so that each has its place in every split's sums
-      if (c == 0) dx_plan = plan_product(dx_product, pairs, o.sums);
-      const Plan plan = c == 0 ? dx_plan : plan_of(dx_product, pairs, dx_plan.splits, o.sums);
-      if (plan.few)
-        TG_TRY(run_few(dx_product, sms, 0, st));
-      else
-        TG_TRY(run_product(dx_product, plan, dx_partials, 0, -1, st));
-    }
-    if (dw_dev) {
-      Product q = xent_dw_product(dl, x, dw, first, dtype);
-      q.alpha = xw.alpha;
-      TG_TRY(whole_product(q, plan_product(q, pairs), dw_sums, sms, st));
-    }
+    TG_TRY(whole_product(p, plan_product(p, pairs), nullptr, sms, pairs, st));
+    Product q[2] = {xent_dx_product(dl, w, first, dx, dtype), xent_dw_product(dl, x, dw, first, dtype)};
+    q[0].alpha = q[1].alpha = alpha;
+    q[0].accumulate = !o.sums ? 0 : c == 0 ? 1 : 2;
+    GradPlans plans(q, pairs, o.sums);
+    if (c == 0)
+      dx_first = q[0], dx_plan = plans.w[0];
+    else if (plans.w[0].splits > dx_plan.splits)
+      // each piece's sums have a place among the first one's
+      plans.w[0] = plan_of(q[0], dx_plan.splits, true);
+    TG_TRY(run_grads(q, plans, {dx_dev != nullptr, dw_dev != nullptr}, !o.sums, partials, sms, pairs, st));
   }
-  if (dx_dev && partials_of(dx_product, dx_plan))
-    TG_TRY(join_product(dx_product, dx_plan, dx_partials, sms, st));
-  return TG_OK;
+  char* const sums[1] = {dx_sums};
+  return dx_dev && o.sums ? join_products(&dx_first, &dx_plan, sums, 1, sms, st) : TG_OK;
 }
 
 }  // extern "C"

@@ -14,6 +14,8 @@
 //     and u in columns 128..255 of each CTA's accumulator, and act(g) u needs no other CTA's data;
 //   * along K (k_seg): k-blocks from k_seg on come from the second A and the second B;
 //   * along N (n_seg): tiles from n_seg on come from the second B and go to the second C.
+// And two products may share a launch (kEpiStore): their units are walked as one list, so that one
+// fills the pairs that the other leaves idle (the gradients towards an input and towards its weights).
 //
 // The pair structure is that of tg_gemm_pair_kernel.cuh; the MMA warp walks its loop together and one
 // elected lane issues, as in tg_wgrad_kernel.cuh.  Sums are cut into segments (tg_linear_config.h): eight
@@ -29,24 +31,134 @@
 
 namespace tg {
 
+// Two products share a launch with kEpiStore only.
+template <int EPI>
+constexpr int kProducts = EPI == 0 ? 2 : 1;
+
+template <int PRODUCTS>
 struct LinearMaps {
-  CUtensorMap a[2], b[2], c[3];
+  CUtensorMap a[PRODUCTS][2], b[PRODUCTS][2], c[PRODUCTS][3];
 };
 
-struct LinearParams : GemmParams {   // M, N: of one segment; m_, n_, k_blocks: of all of them
-  uint32_t splits, blocks_per_split;
+// The cross entropy's rows: one counts where its target is not ``ignore``; a target outside the
+// vocabulary makes NaN of it.
+enum TargetKind { kTargetIgnored, kTargetValid, kTargetWrong };
+__device__ __forceinline__ TargetKind target_kind(int64_t t, int64_t ignore, uint32_t vocab) {
+  if (t == ignore) return kTargetIgnored;
+  return t >= 0 && t < static_cast<int64_t>(vocab) ? kTargetValid : kTargetWrong;
+}
+
+// The gradient of row r's loss as a weight of its logits' gradients: whole dloss / d where the row counts,
+// with d the largest |dloss| of such rows (``top``); 0 for ignored rows, NaN for wrong targets.  alpha = d
+// / whole undoes it.  Gradients of logits are so rounded relative to d: where dloss is the same in every
+// row, a target's -1 is exact instead of off by one rounding in all rows alike (4096 rows of 65536
+// words, bf16: dx 2.9e-3 off, now 1.9e-3; its own rounding makes 1.7e-3).  whole: 1 in bf16; in fp16, which
+// has few exponents, 2^15, so that probabilities 2^29 times smaller keep all their bits.
+struct RowWeights {
+  const float* dloss;
+  const int64_t* targets;
+  int64_t ignore;
+  uint32_t vocab;
+  float* alpha;          // written by the first CTA
+
+  __device__ float counted(uint32_t r) const {   // |dloss| of a row that counts, else 0
+    return target_kind(targets[r], ignore, vocab) == kTargetValid ? fabsf(dloss[r]) : 0.0f;
+  }
+  // nothing to be relative to: no gradient at all, or an infinite one
+  __device__ static bool plain(float top) { return !(top > 0.0f && top < INFINITY); }
+  template <int DT>
+  __device__ static constexpr float whole() { return DT == 0 ? 32768.0f : 1.0f; }
+  template <int DT>
+  __device__ float weight(uint32_t r, float top) const {
+    const TargetKind kind = target_kind(targets[r], ignore, vocab);
+    if (kind == kTargetWrong) return __int_as_float(0x7fffffff);
+    const float d = kind == kTargetValid ? dloss[r] : 0.0f;
+    return plain(top) ? d : d / top * whole<DT>();
+  }
+  template <int DT>
+  __device__ void write_alpha(float top) const { *alpha = plain(top) ? 1.0f : top / whole<DT>(); }
+};
+
+struct LinearProblem {
+  uint32_t M, N;                     // N: of one segment; m_, n_, k_blocks: of all of them
+  uint32_t m_blocks, n_blocks, k_blocks, group, column_major;
+  uint32_t split_from, total_units, splits, blocks_per_split;   // units: per split
   uint32_t n_seg, k_seg;             // first tile along N, first k-block, of the second matrices
+  uint32_t a_mn, b_mn;               // the operand lies with m (n) contiguous
   uint32_t partial;                  // kEpiStore: 0 rounded, 1 fp32 stored, 2 fp32 added to what is there
   uint32_t part_rows;                // rows of one split's partial sums
   const float* alpha;                // kEpiStore: a factor of every result, or null
+};
+
+struct LinearParams {
+  LinearProblem q[2];                // the second one's units follow the first one's
+  uint32_t units[2];                 // of each (0: no second one)
+  uint32_t extra;                    // units of the second that take as long as one of the first
   uint32_t act, keep;                // kEpiGated: the activation; 1: g and u are stored as well
   // cross entropy: logits of columns first_col .. of the vocabulary
-  const int64_t* targets;
-  uint32_t first_col;
+  uint32_t first_col, slots;
   float2* stats;                     // kEpiStats: [M][slots] maximum, sum of exponentials
-  uint32_t slots;
   float* hit;                        // kEpiStats: [M] the target's logit
-  const float *lse, *weight;         // kEpiDlogits: [M]
+  const float* lse;                  // kEpiDlogits: [M]
+  RowWeights rows;                   // targets; the rest for kEpiDlogits
+  uint64_t watchdog_ns;
+  int64_t inject_skip_phase;
+};
+
+// One worker's walk over the units of the products in turn: worker, worker + workers, ... (of a product,
+// the tile units of every split in turn).  The first product has the longer units.  Workers that go
+// without one in its last round take ``extra`` units each of the second one meanwhile, so that all begin the
+// second one's rounds together.
+struct LinearUnits {
+  const LinearParams& p;
+  uint32_t worker, step, at, which, ahead;   // ahead: units of the second one still to take first
+  PersistentTileScheduler sched;
+  uint32_t split, k_lo, k_hi;
+
+  __device__ LinearUnits(const LinearParams& params, uint32_t c, uint32_t workers)
+      : p(params), worker(c), step(workers), at(c), which(0), ahead(0), sched(1, 1, 1, 1) {
+    if (at >= p.units[0]) second();
+    decode();
+  }
+  __device__ bool valid() const { return at < p.units[which]; }
+  __device__ const LinearProblem& q() const { return p.q[which]; }
+  __device__ void second() {
+    const uint32_t busy = p.units[0] % step;   // workers with a unit in the first one's last round
+    which = 1;
+    if (p.extra != 0u && busy != 0u && worker >= busy) {
+      ahead = p.extra;
+      at = (worker - busy) * p.extra;
+    } else {
+      rounds();
+    }
+  }
+  __device__ void rounds() {   // behind what was taken ahead
+    const uint32_t busy = p.units[0] % step;
+    at = worker + (busy != 0u ? (step - busy) * p.extra : 0u);
+  }
+  __device__ void next() {
+    if (ahead > 1u) {
+      --ahead;
+      ++at;
+    } else if (ahead == 1u) {
+      ahead = 0;
+      rounds();
+    } else {
+      at += step;
+      if (which == 0u && at >= p.units[0]) second();
+    }
+    decode();
+  }
+  __device__ void decode() {
+    if (!valid()) return;
+    const LinearProblem& o = p.q[which];
+    split = at / o.total_units;
+    sched = PersistentTileScheduler(o.m_blocks, o.n_blocks, o.group, step, o.split_from,
+                                    o.total_units, o.column_major);
+    sched.jump(at - split * o.total_units, 0);
+    k_lo = split * o.blocks_per_split;
+    k_hi = k_lo + o.blocks_per_split < o.k_blocks ? k_lo + o.blocks_per_split : o.k_blocks;
+  }
 };
 
 struct __align__(8) LinearCtl {
@@ -58,6 +170,7 @@ struct __align__(8) LinearCtl {
   uint64_t odd_done;
   PairFills<kLinStages> fills;
   uint32_t sink[kLinEpiWarps];
+  float top[kLinEpiWarps];           // kEpiDlogits: the warps' largest |dloss|
   uint32_t tmem_base;
   int abort;
 };
@@ -161,16 +274,22 @@ __device__ __forceinline__ void pack64(const float* v, uint32_t (&pk)[32]) {
     pk[i] = pack_out<DT>(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
 }
 
-// DT: 0 = fp16, 1 = bf16.  A_MN, B_MN: the operand lies with m (n) contiguous.
-template <int DT, int A_MN, int B_MN, int EPI>
+// DT: 0 = fp16, 1 = bf16.
+template <int DT, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
-    linear_pair_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
+    linear_pair_kernel(const __grid_constant__ LinearMaps<kProducts<EPI>> maps,
+                       const __grid_constant__ LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
   constexpr uint32_t kStages = kLinStages, kStageBytes = kLinStageBytes;
   constexpr uint32_t kOperand = kLinOperandBytes;
   constexpr uint32_t kAtomBytes = kBM * 128u;              // K-major: 128 rows of 128 bytes
   constexpr uint32_t kChunkBytes = kLinBK * 128u;          // MN-major: kLinBK rows of 64 columns
   constexpr int kTile = EPI == kEpiGated ? kGatedTileN : kBN;
+  // which way an operand lies: any with kEpiStore, one way with the other epilogues
+  auto a_lies_mn = [](const LinearProblem& q) { return EPI == kEpiStore && q.a_mn != 0u; };
+  auto b_lies_mn = [](const LinearProblem& q) {
+    return EPI == kEpiGated || (EPI == kEpiStore && q.b_mn != 0u);
+  };
   __shared__ LinearCtl ctl;
 
   const uint32_t warp = threadIdx.x >> 5;
@@ -207,9 +326,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     fence_mbarrier_init();
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tensormap(&maps.a[0]);
-    prefetch_tensormap(&maps.b[EPI == kEpiGated ? rank : 0u]);
-    if (EPI != kEpiStats) prefetch_tensormap(&maps.c[0]);
+    prefetch_tensormap(&maps.a[0][0]);
+    prefetch_tensormap(&maps.b[0][EPI == kEpiGated ? rank : 0u]);
+    if (EPI != kEpiStats) prefetch_tensormap(&maps.c[0][0]);
+    if (EPI == kEpiStore && p.units[1] != 0u) {
+      prefetch_tensormap(&maps.a[kProducts<EPI> - 1][0]);
+      prefetch_tensormap(&maps.b[kProducts<EPI> - 1][0]);
+      prefetch_tensormap(&maps.c[kProducts<EPI> - 1][0]);
+    }
   }
   __syncwarp();
   if (warp == 2) {
@@ -235,11 +359,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         bool ok = true;
         uint64_t phase = 0;
         RingPos<kStages> at;
-        for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
+        for (LinearUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
           const PersistentTileScheduler& sched = un.sched;
+          const LinearProblem& q = un.q();
+          const bool a_mn = a_lies_mn(q), b_mn = b_lies_mn(q);
           const bool half = sched.half_unit();
-          const uint32_t seg_n = sched.n_idx >= p.n_seg ? 1u : 0u;
-          const int32_t nt = static_cast<int32_t>(sched.n_idx - seg_n * p.n_seg);
+          const uint32_t seg_n = sched.n_idx >= q.n_seg ? 1u : 0u;
+          const int32_t nt = static_cast<int32_t>(sched.n_idx - seg_n * q.n_seg);
           const int32_t m0 = static_cast<int32_t>(sched.m_idx * kPairBM + rank * kBM);
           // this CTA's first column (gated: the same columns of the gate's matrix in the even CTA, of
           // the up projection's in the odd one)
@@ -247,8 +373,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           const int32_t n0 = nt * kTile + (half ? sched.part * (kTile / 2) : 0) + own;
           // a half-width unit's B with columns contiguous is one chunk of 64; of rows of K all 128
           // rows are loaded and the MMA reads 64
-          const uint32_t b_chunks = B_MN && half ? 1u : 2u;
-          const uint32_t own_bytes = kOperand + (B_MN ? b_chunks * kChunkBytes : kOperand);
+          const uint32_t b_chunks = b_mn && half ? 1u : 2u;
+          const uint32_t own_bytes = kOperand + b_chunks * (kOperand / 2u);
           for (uint32_t k = un.k_lo; k < un.k_hi; ++k, ++phase, at.advance(1)) {
             const uint32_t s = at.slot, par = at.parity;
             if (!pair_wait_or_abort(bar_consumed + 8u * s, par ^ 1u, abort_flag, peer_abort, limit,
@@ -260,29 +386,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               continue;  // injected fault: this CTA never arms or fills this phase
             const uint32_t full_even = mapa_shared(bar_loaded + 8u * s, 0);
             if (rank == 0) mbar_arrive_expect_tx(bar_loaded + 8u * s, 2u * own_bytes);
-            const uint32_t seg_k = k >= p.k_seg ? 1u : 0u;
-            const int32_t kx = static_cast<int32_t>(k - seg_k * p.k_seg) * kLinBK;
-            const CUtensorMap* tmA = &maps.a[seg_k];
-            const CUtensorMap* tmB = &maps.b[EPI == kEpiGated ? rank : seg_k | seg_n];
+            const uint32_t seg_k = k >= q.k_seg ? 1u : 0u;
+            const int32_t kx = static_cast<int32_t>(k - seg_k * q.k_seg) * kLinBK;
+            const CUtensorMap* tmA = &maps.a[un.which][seg_k];
+            const CUtensorMap* tmB = &maps.b[un.which][EPI == kEpiGated ? rank : seg_k | seg_n];
             const uint32_t a_dst = sA0 + s * kStageBytes, b_dst = sB0 + s * kStageBytes;
-            // two boxes each: 64-column chunks, or 64-deep atoms of K
+            // two boxes of 16 KiB each: 64-column chunks, or 64-deep atoms of K
 #pragma unroll
             for (uint32_t c = 0; c < 2; ++c) {
               const int32_t on = static_cast<int32_t>(c * 64u);
-              if constexpr (A_MN)
-                tma_load_2d_pair(a_dst + c * kChunkBytes, tmA, full_even, m0 + on, kx);
-              else
-                tma_load_2d_pair(a_dst + c * kAtomBytes, tmA, full_even, kx + on, m0);
+              tma_load_2d_pair(a_dst + c * kAtomBytes, tmA, full_even, a_mn ? m0 + on : kx + on,
+                               a_mn ? kx : m0);
             }
 #pragma unroll
             for (uint32_t c = 0; c < 2; ++c) {
               const int32_t on = static_cast<int32_t>(c * 64u);
-              if constexpr (B_MN) {
-                if (c < b_chunks)
-                  tma_load_2d_pair(b_dst + c * kChunkBytes, tmB, full_even, n0 + on, kx);
-              } else {
-                tma_load_2d_pair(b_dst + c * kAtomBytes, tmB, full_even, kx + on, n0);
-              }
+              if (c < b_chunks)
+                tma_load_2d_pair(b_dst + c * kAtomBytes, tmB, full_even, b_mn ? n0 + on : kx + on,
+                                 b_mn ? kx : n0);
             }
             record_fill(ctl.fills, s, phase, par, own_bytes);
           }
@@ -294,21 +415,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer (even CTA)
       if (rank == 0) {
-        constexpr uint32_t idesc_full = idesc_f16(DT, kPairBM, kBN, A_MN, B_MN);
-        constexpr uint32_t idesc_half = idesc_f16(DT, kPairBM, kBN / 2, A_MN, B_MN);
+        constexpr uint32_t idesc_full = idesc_f16(DT, kPairBM, kBN, 0, 0);
+        constexpr uint32_t idesc_half = idesc_f16(DT, kPairBM, kBN / 2, 0, 0);
         const bool leader = elect_one();
         bool ok = true;
         RingPos<kStages> ring;
         RingPos<2> acc;                 // the accumulator of the next segment
         // a descriptor is an addition to the low word of a constant one (the address field: 16-byte
         // units, below 2^14)
-        const uint64_t a0 = smem_desc_sw128(sA0, A_MN ? kChunkBytes : 16u, 1024);
-        const uint64_t b0 = smem_desc_sw128(sB0, B_MN ? kChunkBytes : 16u, 1024);
-        const uint32_t a_lo = static_cast<uint32_t>(a0), b_lo = static_cast<uint32_t>(b0);
-        const uint32_t a_hi = static_cast<uint32_t>(a0 >> 32);
-        const uint32_t b_hi = static_cast<uint32_t>(b0 >> 32);
+        const uint64_t k_desc = smem_desc_sw128(sA0, 16u, 1024);
+        const uint64_t mn_desc = smem_desc_sw128(sA0, kChunkBytes, 1024);
+        const uint32_t hi = static_cast<uint32_t>(k_desc >> 32);   // the same for both
         // where K-step kk (16 deep) begins: 16 rows of 128 bytes on, or 32 bytes on within an atom
-        auto step = [](uint32_t mn, uint32_t kk) {
+        auto step = [](bool mn, uint32_t kk) {
           return mn ? kk * 128u : (kk / 4u) * (kAtomBytes >> 4) + (kk % 4u) * 2u;
         };
         auto commit = [&](uint32_t bar) {
@@ -320,8 +439,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                                     kRoleMma);
           return __all_sync(0xffffffffu, got) != 0;
         };
-        for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
-          const uint32_t idesc = un.sched.half_unit() ? idesc_half : idesc_full;
+        for (LinearUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
+          const bool a_mn = a_lies_mn(un.q()), b_mn = b_lies_mn(un.q());
+          const uint32_t idesc = (un.sched.half_unit() ? idesc_half : idesc_full) |
+                                 (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+          const uint32_t a_lo = static_cast<uint32_t>(a_mn ? mn_desc : k_desc);
+          const uint32_t b_lo = static_cast<uint32_t>(b_mn ? mn_desc : k_desc) + (kOperand >> 4);
           const uint32_t nk = un.k_hi - un.k_lo;
           uint32_t in_seg = 0;          // k-blocks of the segment so far
           for (uint32_t k = 0; k < nk; ++k, ring.advance(1)) {
@@ -338,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             if (leader) {
 #pragma unroll
               for (uint32_t kk = 0; kk < kLinBK / kUmmaK; ++kk)
-                umma_f16_pair_words(d, a + step(A_MN, kk), a_hi, b + step(B_MN, kk), b_hi, idesc,
+                umma_f16_pair_words(d, a + step(a_mn, kk), hi, b + step(b_mn, kk), hi, idesc,
                                     in_seg != 0u || kk != 0u ? 1u : 0u);
             }
             commit(bar_consumed + 8u * s);
@@ -362,17 +485,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     const uint32_t e = warp - kFirstEpiWarp, q = e & 3u, side = e >> 2;
     const uint32_t sink_even = mapa_shared(smem_u32(&ctl.sink[e]), 0);
     const uint32_t sbuf = sEpi + e * kEpiBufBytes;
-    const float alpha = EPI == kEpiStore && p.alpha ? *p.alpha : 1.0f;
+    float row_top = 0.0f;   // kEpiDlogits: the largest |dloss| of all rows
+    if constexpr (EPI == kEpiDlogits) {
+      const uint32_t tt = threadIdx.x - 32u * kFirstEpiWarp;
+      for (uint32_t r = tt; r < p.q[0].M; r += 32u * kLinEpiWarps)
+        row_top = fmaxf(row_top, p.rows.counted(r));
+#pragma unroll
+      for (uint32_t o = 16; o > 0; o /= 2)
+        row_top = fmaxf(row_top, __shfl_xor_sync(0xffffffffu, row_top, o));
+      if (lane == 0) ctl.top[e] = row_top;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kLinEpiWarps) : "memory");
+#pragma unroll
+      for (int o = 0; o < kLinEpiWarps; ++o) row_top = fmaxf(row_top, ctl.top[o]);
+      if (blockIdx.x == 0 && tt == 0) p.rows.template write_alpha<DT>(row_top);
+    }
     RingPos<2> acc;
     bool ok = true;
-    for (WgradUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
+    for (LinearUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
       const PersistentTileScheduler& sched = un.sched;
+      const LinearProblem& o = un.q();
+      const CUtensorMap* const maps_c = &maps.c[un.which][0];
       const bool half = sched.half_unit();      // the accumulator has 128 columns
-      const uint32_t seg_n = sched.n_idx >= p.n_seg ? 1u : 0u;
-      const int32_t nt = static_cast<int32_t>(sched.n_idx - seg_n * p.n_seg);
+      const uint32_t seg_n = sched.n_idx >= o.n_seg ? 1u : 0u;
+      const int32_t nt = static_cast<int32_t>(sched.n_idx - seg_n * o.n_seg);
       const int32_t row0 = static_cast<int32_t>(sched.m_idx * kPairBM + rank * kBM + q * 32u);
       const uint32_t row = static_cast<uint32_t>(row0) + lane;
-      const bool row_in = row < p.M;
+      const bool row_in = row < o.M;
       // this warp's columns of the accumulator, 64 at a time: two chunks, or one of a half unit's.
       // Gated: one of g and the one of u that goes with it; of a half unit's single one side 0 takes
       // both
@@ -432,28 +570,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           uint32_t pk[32];
           if (p.keep) {
             pack64<DT>(v, pk);
-            linear_store_packed(pk, lane, sbuf, &maps.c[1], row0, x0, p.M, p.N);
+            linear_store_packed(pk, lane, sbuf, maps_c + 1, row0, x0, o.M, o.N);
             pack64<DT>(v + 64, pk);
-            linear_store_packed(pk, lane, sbuf, &maps.c[2], row0, x0, p.M, p.N);
+            linear_store_packed(pk, lane, sbuf, maps_c + 2, row0, x0, o.M, o.N);
           }
           // from the unrounded g and u
 #pragma unroll
           for (uint32_t i = 0; i < 64; ++i) v[i] = v[i] * gate_of(v[i], p.act).s * v[64 + i];
           pack64<DT>(v, pk);
-          linear_store_packed(pk, lane, sbuf, &maps.c[0], row0, x0, p.M, p.N);
+          linear_store_packed(pk, lane, sbuf, maps_c, row0, x0, o.M, o.N);
         }
       } else if constexpr (EPI == kEpiStore) {
-        if (p.partial) {
-          const int32_t to = static_cast<int32_t>(un.split * p.part_rows) + row0;
-          const bool in = row0 < static_cast<int32_t>(p.M);
+        if (o.partial) {
+          const int32_t to = static_cast<int32_t>(un.split * o.part_rows) + row0;
+          const bool in = row0 < static_cast<int32_t>(o.M);
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j) {
             if (j / 2u >= chunks) break;
-            linear_store_sums(v + 32 * j, lane, sbuf, &maps.c[seg_n], to, in,
-                              x0 + static_cast<int32_t>(32u * j), p.N, p.partial == 2);
+            linear_store_sums(v + 32 * j, lane, sbuf, maps_c + seg_n, to, in,
+                              x0 + static_cast<int32_t>(32u * j), o.N, o.partial == 2);
           }
         } else {
-          if (p.alpha) {
+          if (o.alpha) {
+            const float alpha = *o.alpha;
 #pragma unroll
             for (uint32_t i = 0; i < 128; ++i) v[i] *= alpha;
           }
@@ -462,18 +601,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             if (j >= chunks) break;
             uint32_t pk[32];
             pack64<DT>(v + 64 * j, pk);
-            linear_store_packed(pk, lane, sbuf, &maps.c[seg_n], row0,
-                                x0 + static_cast<int32_t>(64u * j), p.M, p.N);
+            linear_store_packed(pk, lane, sbuf, maps_c + seg_n, row0,
+                                x0 + static_cast<int32_t>(64u * j), o.M, o.N);
           }
         }
       } else {
         // the target's place among this warp's columns, or a place that none of them has
-        const int64_t hot = row_in ? p.targets[row] - static_cast<int64_t>(p.first_col) : -1;
+        const int64_t hot = row_in ? p.rows.targets[row] - static_cast<int64_t>(p.first_col) : -1;
         const int32_t at = hot >= x0 && hot < x0 + 128 ? static_cast<int32_t>(hot) - x0 : -1;
         if constexpr (EPI == kEpiStats) {
-          if (chunks == 1 || x0 + 128 > static_cast<int32_t>(p.N)) {
+          if (chunks == 1 || x0 + 128 > static_cast<int32_t>(o.N)) {
             // columns that another warp has, or past the vocabulary
-            const int32_t end = min(x0 + static_cast<int32_t>(64u * chunks), static_cast<int32_t>(p.N));
+            const int32_t end = min(x0 + static_cast<int32_t>(64u * chunks), static_cast<int32_t>(o.N));
 #pragma unroll
             for (uint32_t i = 0; i < 128; ++i)
               if (x0 + static_cast<int32_t>(i) >= end) v[i] = -INFINITY;
@@ -495,14 +634,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 #pragma unroll
           for (uint32_t i = 0; i < 128; ++i) s4[i & 3u] += exp2_fast((v[i] - base) * kLog2e);
           // slots of 64 columns; two chunks leave the second one's empty
-          if (row_in && x0 < static_cast<int32_t>(p.N)) {
+          if (row_in && x0 < static_cast<int32_t>(o.N)) {
             const uint32_t slot = static_cast<uint32_t>(x0) / kStatCols;
             float2* to = p.stats + static_cast<uint64_t>(row) * p.slots + slot;
             to[0] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
             if (chunks == 2 && slot + 1u < p.slots) to[1] = make_float2(-INFINITY, 0.0f);
           }
         } else {
-          const float lse = row_in ? p.lse[row] : 0.0f, weight = row_in ? p.weight[row] : 0.0f;
+          const float lse = row_in ? p.lse[row] : 0.0f;
+          const float weight = row_in ? p.rows.template weight<DT>(row, row_top) : 0.0f;
 #pragma unroll
           for (uint32_t j = 0; j < 2; ++j) {
             if (j >= chunks) break;
@@ -514,13 +654,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             }
             uint32_t pk[32];
             pack64<DT>(v + 64 * j, pk);
-            linear_store_packed(pk, lane, sbuf, &maps.c[0], row0,
-                                x0 + static_cast<int32_t>(64u * j), p.M, p.N);
+            linear_store_packed(pk, lane, sbuf, maps_c, row0,
+                                x0 + static_cast<int32_t>(64u * j), o.M, o.N);
           }
         }
       }
     }
-    if (lane == 0) bulk_wait_group<0>();
+    // the stores have read shared memory; the grid's end makes them visible
+    if (lane == 0) bulk_wait_group_read<0>();
     __syncwarp();
   }
 
@@ -538,39 +679,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 
 // out = alpha times the sum of the splits' partial sums [splits][part_rows][cols], in order, rounded
 // once.  A thread takes 4 neighbouring columns of a row (cols is a multiple of 4) and reads four splits
-// at a time.
+// at a time.  One launch joins what one launch of products left (blockIdx.y).
+struct JoinParams {
+  const float* partials;
+  const float* alpha;
+  void* out;
+  int64_t ld_out;
+  uint64_t stride4;          // float4s between splits
+  uint32_t splits, rows, cols;
+};
+struct JoinJobs {
+  JoinParams job[3];
+};
 template <int DT>
-__global__ void __launch_bounds__(256)
-    linear_join_kernel(const float* __restrict__ partials, uint32_t splits, uint64_t split_stride,
-                       uint32_t rows, uint32_t cols, const float* alpha, void* __restrict__ out,
-                       int64_t ld_out) {
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ JoinJobs jobs) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const float f = alpha ? *alpha : 1.0f;
-  const uint32_t vecs = cols / 4u;
-  const uint64_t total = static_cast<uint64_t>(rows) * vecs, stride4 = split_stride / 4u;
+  const JoinParams& p = jobs.job[blockIdx.y];
+  const float f = p.alpha ? *p.alpha : 1.0f;
+  const uint32_t vecs = p.cols / 4u;
+  const uint64_t total = static_cast<uint64_t>(p.rows) * vecs, stride4 = p.stride4;
   for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
        i += static_cast<uint64_t>(gridDim.x) * blockDim.x) {
-    const uint32_t row = static_cast<uint32_t>(i / vecs), v = static_cast<uint32_t>(i % vecs);
-    const float4* src = reinterpret_cast<const float4*>(partials) + i;
+    const uint64_t row = i / vecs;
+    const uint32_t v = static_cast<uint32_t>(i - row * vecs);
+    const float4* src = reinterpret_cast<const float4*>(p.partials) + i;
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     uint32_t s = 0;
-    for (; s + 4u <= splits; s += 4u, src += 4u * stride4) {
+    for (; s + 4u <= p.splits; s += 4u, src += 4u * stride4) {
       float4 c[4];
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) c[j] = __ldcg(src + j * stride4);
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) a.x += c[j].x, a.y += c[j].y, a.z += c[j].z, a.w += c[j].w;
     }
-    for (; s < splits; ++s, src += stride4) {
+    for (; s < p.splits; ++s, src += stride4) {
       const float4 c = __ldcg(src);
       a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
     }
     uint2 o;
     o.x = pack_out<DT>(__float_as_uint(a.x * f), __float_as_uint(a.y * f));
     o.y = pack_out<DT>(__float_as_uint(a.z * f), __float_as_uint(a.w * f));
-    *reinterpret_cast<uint2*>(static_cast<char*>(out) +
-                              (static_cast<int64_t>(row) * ld_out + 4 * v) * 2) = o;
+    *reinterpret_cast<uint2*>(static_cast<char*>(p.out) +
+                              (static_cast<int64_t>(row) * p.ld_out + 4ll * v) * 2) = o;
   }
 }
 

@@ -14,63 +14,75 @@ namespace tg {
 
 namespace {
 
+RowWeights row_weights_of(const XentRows& l) {
+  RowWeights w;
+  w.dloss = l.dloss;
+  w.targets = l.targets;
+  w.ignore = l.ignore;
+  w.vocab = l.vocab;
+  w.alpha = l.alpha;
+  return w;
+}
+
 LinearParams params_of(const LinearLaunch& l) {
   LinearParams p = {};
-  p.M = l.M;
-  p.N = l.N;
-  p.m_blocks = l.m_blocks;
-  p.n_blocks = l.n_blocks;
-  p.k_blocks = l.k_blocks;
-  p.group = l.group;
-  p.split_from = l.split_from;
-  p.total_units = l.total_units;
-  p.column_major = l.column_major;
-  p.watchdog_ns = l.watchdog_ns;
-  p.inject_skip_phase = l.inject_skip_phase;
-  p.splits = l.splits;
-  p.blocks_per_split = l.blocks_per_split;
-  p.n_seg = l.n_seg;
-  p.k_seg = l.k_seg;
-  p.partial = l.partial;
-  p.part_rows = l.part_rows;
-  p.alpha = l.alpha;
+  for (int i = 0; i < l.products; ++i) {
+    const LinearProduct& from = l.q[i];
+    LinearProblem& to = p.q[i];
+    to.M = from.M;
+    to.N = from.N;
+    to.m_blocks = from.m_blocks;
+    to.n_blocks = from.n_blocks;
+    to.k_blocks = from.k_blocks;
+    to.group = from.group;
+    to.column_major = from.column_major;
+    to.split_from = from.split_from;
+    to.total_units = from.total_units;
+    to.splits = from.splits;
+    to.blocks_per_split = from.blocks_per_split;
+    to.n_seg = from.n_seg;
+    to.k_seg = from.k_seg;
+    to.a_mn = from.a_mn;
+    to.b_mn = from.b_mn;
+    to.partial = from.partial;
+    to.part_rows = from.part_rows;
+    to.alpha = from.alpha;
+    p.units[i] = to.total_units * to.splits;
+  }
+  p.extra = l.extra;
   p.act = l.act;
   p.keep = l.keep;
-  p.targets = l.targets;
   p.first_col = l.first_col;
-  p.stats = static_cast<float2*>(l.stats);
   p.slots = l.slots;
+  p.stats = static_cast<float2*>(l.stats);
   p.hit = l.hit;
   p.lse = l.lse;
-  p.weight = l.weight;
+  p.rows = row_weights_of(l.loss);
+  p.watchdog_ns = l.watchdog_ns;
+  p.inject_skip_phase = l.inject_skip_phase;
   return p;
 }
 
-// Calls f with the kernel for what ``l`` asks for, or with null if there is none.
+// Calls f with the kernel of an epilogue.
 template <int DT, typename F>
-cudaError_t with_kernel(bool a_mn, bool b_mn, int epi, F&& f) {
-  if (a_mn)
-    return b_mn && epi == kEpiStore ? f(linear_pair_kernel<DT, 1, 1, kEpiStore>)
-                                    : cudaErrorInvalidValue;
-  if (b_mn) {
-    if (epi == kEpiStore) return f(linear_pair_kernel<DT, 0, 1, kEpiStore>);
-    if (epi == kEpiGated) return f(linear_pair_kernel<DT, 0, 1, kEpiGated>);
-    return cudaErrorInvalidValue;
-  }
-  if (epi == kEpiStore) return f(linear_pair_kernel<DT, 0, 0, kEpiStore>);
-  if (epi == kEpiStats) return f(linear_pair_kernel<DT, 0, 0, kEpiStats>);
-  if (epi == kEpiDlogits) return f(linear_pair_kernel<DT, 0, 0, kEpiDlogits>);
-  return cudaErrorInvalidValue;
+cudaError_t with_kernel(int epi, F&& f) {
+  if (epi == kEpiStore) return f(linear_pair_kernel<DT, kEpiStore>, std::integral_constant<int, 2>());
+  if (epi == kEpiGated) return f(linear_pair_kernel<DT, kEpiGated>, std::integral_constant<int, 1>());
+  if (epi == kEpiStats) return f(linear_pair_kernel<DT, kEpiStats>, std::integral_constant<int, 1>());
+  return f(linear_pair_kernel<DT, kEpiDlogits>, std::integral_constant<int, 1>());
 }
 
 template <int DT>
 cudaError_t launch_one(const LinearLaunch& l, cudaStream_t stream) {
-  LinearMaps maps;
-  for (int i = 0; i < 2; ++i) maps.a[i] = l.a[i], maps.b[i] = l.b[i];
-  for (int i = 0; i < 3; ++i) maps.c[i] = l.c[i];
-  return with_kernel<DT>(l.a_mn, l.b_mn, l.epi, [&](auto kernel) {
-    return launch_pdl(kernel, dim3(l.grid), kLinThreads, kLinSmemBytes, stream, maps,
-                      params_of(l));
+  return with_kernel<DT>(l.epi, [&](auto kernel, auto products) {
+    constexpr int kMost = decltype(products)::value;
+    LinearMaps<kMost> maps;
+    for (int q = 0; q < kMost; ++q) {
+      const LinearProduct& from = l.q[q < l.products ? q : 0];
+      for (int i = 0; i < 2; ++i) maps.a[q][i] = from.a[i], maps.b[q][i] = from.b[i];
+      for (int i = 0; i < 3; ++i) maps.c[q][i] = from.c[i];
+    }
+    return launch_pdl(kernel, dim3(l.grid), kLinThreads, kLinSmemBytes, stream, maps, params_of(l));
   });
 }
 
@@ -88,13 +100,8 @@ cudaError_t prepare_one(int* pairs) {
   cfg.dynamicSmemBytes = kLinSmemBytes;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  struct {
-    bool a_mn, b_mn;
-    int epi;
-  } const kinds[] = {{true, true, kEpiStore},   {false, true, kEpiStore},  {false, true, kEpiGated},
-                     {false, false, kEpiStore}, {false, false, kEpiStats}, {false, false, kEpiDlogits}};
-  for (const auto& k : kinds) {
-    const cudaError_t e = with_kernel<DT>(k.a_mn, k.b_mn, k.epi, [&](auto kernel) {
+  for (int epi = kEpiStore; epi <= kEpiDlogits; ++epi) {
+    const cudaError_t e = with_kernel<DT>(epi, [&](auto kernel, auto) {
       cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kLinSmemBytes));
       // a launch with fewer registers could not hand over what its epilogue warps wait for
@@ -205,26 +212,38 @@ cudaError_t launch_few(const FewLaunch& l, cudaStream_t stream) {
   p.ld_out = l.ld_out;
   p.ld_g = l.ld_g;
   p.ld_u = l.ld_u;
-  p.targets = l.targets;
+  p.loss = row_weights_of(l.loss);
   p.first_col = l.first_col;
   p.stats = static_cast<float2*>(l.stats);
   p.slots = l.slots;
   p.hit = l.hit;
   p.lse = l.lse;
-  p.weight = l.weight;
   p.watchdog_ns = l.watchdog_ns;
   return l.dtype == 0 ? launch_few_one<0>(l, maps, p, stream)
                       : launch_few_one<1>(l, maps, p, stream);
 }
 
-cudaError_t launch_linear_join(const LinearJoin& l, cudaStream_t stream) {
-  const uint64_t vecs = static_cast<uint64_t>(l.rows) * (l.cols / 4u);
-  const dim3 grid(blocks_for(vecs, l.sms, 8));
-  const uint64_t stride = static_cast<uint64_t>(l.part_rows) * l.cols;
-  return l.dtype == 0 ? launch_pdl(linear_join_kernel<0>, grid, 256, 0, stream, l.partials, l.splits,
-                                   stride, l.rows, l.cols, l.alpha, l.out, l.ld_out)
-                      : launch_pdl(linear_join_kernel<1>, grid, 256, 0, stream, l.partials, l.splits,
-                                   stride, l.rows, l.cols, l.alpha, l.out, l.ld_out);
+cudaError_t launch_linear_join(const LinearJoin* joins, int count, int dtype, int sms,
+                               cudaStream_t stream) {
+  JoinJobs jobs = {};
+  uint32_t blocks = 1;
+  for (int i = 0; i < count; ++i) {
+    const LinearJoin& l = joins[i];
+    JoinParams& p = jobs.job[i];
+    p.partials = l.partials;
+    p.alpha = l.alpha;
+    p.out = l.out;
+    p.ld_out = l.ld_out;
+    p.stride4 = static_cast<uint64_t>(l.part_rows) * l.cols / 4u;
+    p.splits = l.splits;
+    p.rows = l.rows;
+    p.cols = l.cols;
+    const uint32_t want = blocks_for(static_cast<uint64_t>(l.rows) * (l.cols / 4u), sms, 8);
+    blocks = want > blocks ? want : blocks;
+  }
+  const dim3 grid(blocks, count);
+  return dtype == 0 ? launch_pdl(linear_join_kernel<0>, grid, 256, 0, stream, jobs)
+                    : launch_pdl(linear_join_kernel<1>, grid, 256, 0, stream, jobs);
 }
 
 cudaError_t launch_gated_join(const GatedJoin& l, cudaStream_t stream) {
@@ -276,19 +295,6 @@ cudaError_t launch_xent_join(const XentJoin& l, cudaStream_t stream) {
   p.slots = l.slots;
   p.vocab = l.vocab;
   return launch_pdl(xent_join_kernel, dim3((l.rows + 3u) / 4u), 128, 0, stream, p);
-}
-
-cudaError_t launch_xent_weights(const XentWeights& l, cudaStream_t stream) {
-  XentWeightParams p;
-  p.dloss = l.dloss;
-  p.targets = l.targets;
-  p.ignore = l.ignore;
-  p.weight = l.weight;
-  p.alpha = l.alpha;
-  p.rows = l.rows;
-  p.vocab = l.vocab;
-  p.whole = l.dtype == 0 ? 32768.0f : 1.0f;
-  return launch_pdl(xent_weight_kernel, dim3(1), 1024, 0, stream, p);
 }
 
 }  // namespace tg
