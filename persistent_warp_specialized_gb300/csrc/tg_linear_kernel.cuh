@@ -26,6 +26,8 @@
 // Included by exactly one translation unit, after tg_wgrad_kernel.cuh.
 #pragma once
 
+#include <type_traits>
+
 #include "tg_linear_config.h"
 #include "tg_wgrad_kernel.cuh"
 
@@ -84,7 +86,7 @@ struct LinearProblem {
   uint32_t m_blocks, n_blocks, k_blocks, group, column_major;
   uint32_t split_from, total_units, splits, blocks_per_split;   // units: per split
   uint32_t n_seg, k_seg;             // first tile along N, first k-block, of the second matrices
-  uint32_t a_mn, b_mn;               // the operand lies with m (n) contiguous
+  uint32_t a_mn, b_mn;               // the operand lies with m (n) contiguous; a_mn: b_mn too
   uint32_t partial;                  // kEpiStore: 0 rounded, 1 fp32 stored, 2 fp32 added to what is there
   uint32_t part_rows;                // rows of one split's partial sums
   const float* alpha;                // kEpiStore: a factor of every result, or null
@@ -109,6 +111,7 @@ struct LinearParams {
 // the tile units of every split in turn).  The first product has the longer units.  Workers that go
 // without one in its last round take ``extra`` units each of the second one meanwhile, so that all begin the
 // second one's rounds together.
+template <int PRODUCTS>
 struct LinearUnits {
   const LinearParams& p;
   uint32_t worker, step, at, which, ahead;   // ahead: units of the second one still to take first
@@ -117,11 +120,12 @@ struct LinearUnits {
 
   __device__ LinearUnits(const LinearParams& params, uint32_t c, uint32_t workers)
       : p(params), worker(c), step(workers), at(c), which(0), ahead(0), sched(1, 1, 1, 1) {
-    if (at >= p.units[0]) second();
+    if (PRODUCTS == 2 && at >= p.units[0]) second();
     decode();
   }
-  __device__ bool valid() const { return at < p.units[which]; }
-  __device__ const LinearProblem& q() const { return p.q[which]; }
+  __device__ uint32_t product() const { return PRODUCTS == 1 ? 0u : which; }
+  __device__ bool valid() const { return at < p.units[product()]; }
+  __device__ const LinearProblem& q() const { return p.q[product()]; }
   __device__ void second() {
     const uint32_t busy = p.units[0] % step;   // workers with a unit in the first one's last round
     which = 1;
@@ -137,7 +141,9 @@ struct LinearUnits {
     at = worker + (busy != 0u ? (step - busy) * p.extra : 0u);
   }
   __device__ void next() {
-    if (ahead > 1u) {
+    if (PRODUCTS == 1) {
+      at += step;
+    } else if (ahead > 1u) {
       --ahead;
       ++at;
     } else if (ahead == 1u) {
@@ -151,7 +157,7 @@ struct LinearUnits {
   }
   __device__ void decode() {
     if (!valid()) return;
-    const LinearProblem& o = p.q[which];
+    const LinearProblem& o = q();
     split = at / o.total_units;
     sched = PersistentTileScheduler(o.m_blocks, o.n_blocks, o.group, step, o.split_from,
                                     o.total_units, o.column_major);
@@ -359,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         bool ok = true;
         uint64_t phase = 0;
         RingPos<kStages> at;
-        for (LinearUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
+        for (LinearUnits<kProducts<EPI>> un(p, pair, num_pairs); ok && un.valid(); un.next()) {
           const PersistentTileScheduler& sched = un.sched;
           const LinearProblem& q = un.q();
           const bool a_mn = a_lies_mn(q), b_mn = b_lies_mn(q);
@@ -375,6 +381,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           // rows are loaded and the MMA reads 64
           const uint32_t b_chunks = b_mn && half ? 1u : 2u;
           const uint32_t own_bytes = kOperand + b_chunks * (kOperand / 2u);
+          const uint32_t k_seg = q.k_seg;
+          const CUtensorMap* const maps_a = &maps.a[un.product()][0];
+          const CUtensorMap* const maps_b = &maps.b[un.product()][EPI == kEpiGated ? rank : seg_n];
           for (uint32_t k = un.k_lo; k < un.k_hi; ++k, ++phase, at.advance(1)) {
             const uint32_t s = at.slot, par = at.parity;
             if (!pair_wait_or_abort(bar_consumed + 8u * s, par ^ 1u, abort_flag, peer_abort, limit,
@@ -386,10 +395,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               continue;  // injected fault: this CTA never arms or fills this phase
             const uint32_t full_even = mapa_shared(bar_loaded + 8u * s, 0);
             if (rank == 0) mbar_arrive_expect_tx(bar_loaded + 8u * s, 2u * own_bytes);
-            const uint32_t seg_k = k >= q.k_seg ? 1u : 0u;
-            const int32_t kx = static_cast<int32_t>(k - seg_k * q.k_seg) * kLinBK;
-            const CUtensorMap* tmA = &maps.a[un.which][seg_k];
-            const CUtensorMap* tmB = &maps.b[un.which][EPI == kEpiGated ? rank : seg_k | seg_n];
+            const uint32_t seg_k = k >= k_seg ? 1u : 0u;   // at most one of seg_k and seg_n is 1
+            const int32_t kx = static_cast<int32_t>(k - seg_k * k_seg) * kLinBK;
+            const CUtensorMap* tmA = maps_a + seg_k;
+            const CUtensorMap* tmB = maps_b + seg_k;
             const uint32_t a_dst = sA0 + s * kStageBytes, b_dst = sB0 + s * kStageBytes;
             // two boxes of 16 KiB each: 64-column chunks, or 64-deep atoms of K
 #pragma unroll
@@ -426,10 +435,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         const uint64_t k_desc = smem_desc_sw128(sA0, 16u, 1024);
         const uint64_t mn_desc = smem_desc_sw128(sA0, kChunkBytes, 1024);
         const uint32_t hi = static_cast<uint32_t>(k_desc >> 32);   // the same for both
-        // where K-step kk (16 deep) begins: 16 rows of 128 bytes on, or 32 bytes on within an atom
-        auto step = [](bool mn, uint32_t kk) {
-          return mn ? kk * 128u : (kk / 4u) * (kAtomBytes >> 4) + (kk % 4u) * 2u;
-        };
         auto commit = [&](uint32_t bar) {
           if (leader) umma_commit_pair_multicast(bar, 0x3);
           __syncwarp();
@@ -439,30 +444,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                                     kRoleMma);
           return __all_sync(0xffffffffu, got) != 0;
         };
-        for (LinearUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
-          const bool a_mn = a_lies_mn(un.q()), b_mn = b_lies_mn(un.q());
+        // One unit.  How the operands lie is fixed in each copy of the loop: descriptors that had to
+        // be chosen between in it made the MMAs wait (input gradient 8192^3 597 -> 606 us).
+        auto unit = [&](const LinearUnits<kProducts<EPI>>& un, auto a_mn, auto b_mn) {
+          constexpr bool A = decltype(a_mn)::value, B = decltype(b_mn)::value;
+          // where K-step kk (16 deep) begins: 16 rows of 128 bytes on, or 32 bytes on within an atom
+          auto step = [](bool mn, uint32_t kk) {
+            return mn ? kk * 128u : (kk / 4u) * (kAtomBytes >> 4) + (kk % 4u) * 2u;
+          };
           const uint32_t idesc = (un.sched.half_unit() ? idesc_half : idesc_full) |
-                                 (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-          const uint32_t a_lo = static_cast<uint32_t>(a_mn ? mn_desc : k_desc);
-          const uint32_t b_lo = static_cast<uint32_t>(b_mn ? mn_desc : k_desc) + (kOperand >> 4);
+                                 (A ? 1u << 15 : 0u) | (B ? 1u << 16 : 0u);
+          const uint32_t a_lo = static_cast<uint32_t>(A ? mn_desc : k_desc);
+          const uint32_t b_lo = static_cast<uint32_t>(B ? mn_desc : k_desc) + (kOperand >> 4);
           const uint32_t nk = un.k_hi - un.k_lo;
           uint32_t in_seg = 0;          // k-blocks of the segment so far
           for (uint32_t k = 0; k < nk; ++k, ring.advance(1)) {
             const uint32_t s = ring.slot;
             // both CTAs' epilogues have read the accumulator's last segment out
             if (!wait(bar_loaded + 8u * s, ring.parity) ||
-                (in_seg == 0 && !wait(bar_tmem_empty + 8u * acc.slot, acc.parity ^ 1u))) {
-              ok = false;
-              break;
-            }
+                (in_seg == 0 && !wait(bar_tmem_empty + 8u * acc.slot, acc.parity ^ 1u)))
+              return false;
             tcgen05_fence_after_sync();
             const uint32_t d = tmem_base + acc.slot * kBN;
-            const uint32_t a = a_lo + s * (kStageBytes >> 4), b = b_lo + s * (kStageBytes >> 4);
+            const uint32_t at = s * (kStageBytes >> 4);
             if (leader) {
 #pragma unroll
               for (uint32_t kk = 0; kk < kLinBK / kUmmaK; ++kk)
-                umma_f16_pair_words(d, a + step(a_mn, kk), hi, b + step(b_mn, kk), hi, idesc,
-                                    in_seg != 0u || kk != 0u ? 1u : 0u);
+                umma_f16_pair_words(d, a_lo + at + step(A, kk), hi, b_lo + at + step(B, kk), hi,
+                                    idesc, in_seg != 0u || kk != 0u ? 1u : 0u);
             }
             commit(bar_consumed + 8u * s);
             if (++in_seg == kLinSegment || k + 1 == nk) {
@@ -471,6 +480,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               in_seg = 0;
             }
           }
+          return true;
+        };
+        using No = std::false_type;
+        using Yes = std::true_type;
+        for (LinearUnits<kProducts<EPI>> un(p, pair, num_pairs); ok && un.valid(); un.next()) {
+          if constexpr (EPI == kEpiStore)
+            ok = un.q().a_mn   ? unit(un, Yes(), Yes())
+                 : un.q().b_mn ? unit(un, No(), Yes())
+                               : unit(un, No(), No());
+          else if constexpr (EPI == kEpiGated)
+            ok = unit(un, No(), Yes());
+          else
+            ok = unit(un, No(), No());
         }
         if (leader) {
           umma_commit_pair_multicast(bar_drain, 0x1);
@@ -501,10 +523,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
     RingPos<2> acc;
     bool ok = true;
-    for (LinearUnits un(p, pair, num_pairs); ok && un.valid(); un.next()) {
+    for (LinearUnits<kProducts<EPI>> un(p, pair, num_pairs); ok && un.valid(); un.next()) {
       const PersistentTileScheduler& sched = un.sched;
       const LinearProblem& o = un.q();
-      const CUtensorMap* const maps_c = &maps.c[un.which][0];
+      const CUtensorMap* const maps_c = &maps.c[un.product()][0];
       const bool half = sched.half_unit();      // the accumulator has 128 columns
       const uint32_t seg_n = sched.n_idx >= o.n_seg ? 1u : 0u;
       const int32_t nt = static_cast<int32_t>(sched.n_idx - seg_n * o.n_seg);
