@@ -8,6 +8,9 @@
 namespace tg {
 
 constexpr int kFewRows = 64;             // rows at most
+// Rows up to which gradients that are rounded on the way come in two terms: past 16 rows of at least 128
+// values their errors average out to within 2 % of what they are in the mean.
+constexpr int kTwoTermRows = 16;
 constexpr int kFewM = 128;               // weights' rows or columns (results) in a tile
 constexpr int kFewBK = kKAtom;           // 64 of K in a stage
 // A sum is cut into segments of 1024 products, as tg_linear_config.h explains.
@@ -25,6 +28,7 @@ constexpr uint32_t kFewWeightBytes = kFewM * kFewBK * kElemBytes;       // 16 Ki
 // rows as the MMA takes them: 16, 32 or 64
 constexpr uint32_t few_padded(int64_t rows) { return rows <= 16 ? 16u : rows <= 32 ? 32u : 64u; }
 
+// n: padded rows, times two where they come in two terms
 constexpr uint32_t few_stage_bytes(bool gated, uint32_t n) {
   return (gated ? 2u : 1u) * kFewWeightBytes + n * kFewBK * kElemBytes;
 }
@@ -36,7 +40,7 @@ constexpr uint32_t few_stages(bool gated, uint32_t n) {
 constexpr uint32_t few_smem_bytes(bool gated, uint32_t n) {
   return kSmemAlignSlack + few_stages(gated, n) * few_stage_bytes(gated, n);
 }
-static_assert(few_stages(true, 64) >= 2 && few_stages(false, 64) >= 3, "a ring has to run ahead");
+static_assert(few_stages(true, 64) >= 2 && few_stages(false, 128) >= 3, "a ring has to run ahead");
 // ... or, for statistics, the sums, half as many again by rows (padded) and a pair for each thread
 static_assert(2u * kFewM * 64u * 4u <= few_stages(true, 64) * few_stage_bytes(true, 64) &&
               (kFewM * 64u + (kFewM + 1u) * 64u + 2u * 128u + 2u) * 4u <=

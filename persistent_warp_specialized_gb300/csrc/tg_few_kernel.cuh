@@ -12,9 +12,14 @@
 // A CTA has one tile of 128 results per row.  Few tiles: a cluster of up to 8 CTAs shares one along K; each
 // adds its range, then the sums are handed out by rows through distributed shared memory, every CTA
 // adds its rows' in the order of the ranges and finishes them.  Nothing goes through global memory
-// and no second launch follows.  Two CTAs an SM.
+// and no second launch follows.  Two CTAs an SM.  Where even clusters leave most SMs idle before a long
+// K (a gradient towards x over a large vocabulary), K is cut between ``groups`` of clusters first, whose
+// fp32 sums linear_join_kernel adds in order.
 //
-// Measured (bf16, us, L2 flushed / pair kernel with its join): see tg_linear_api.cu at few_rows.
+// Gradients that were rounded to 16 bits on the way come in two terms, what was rounded and what that
+// left: with few rows their errors do not average out in a result (of one row, a gradient towards x
+// could be 1.5 times as far off as one rounding of the result alone).  The second term is multiplied
+// with the same weights in shared memory.
 //
 // Included by exactly one translation unit, after tg_linear_kernel.cuh.
 #pragma once
@@ -25,17 +30,21 @@
 namespace tg {
 
 struct FewMaps {
-  CUtensorMap w[2], x[2];
+  CUtensorMap w[2], x[2], x_rest[2];
 };
 
 struct FewParams {
   uint32_t rows, n_pad;              // rows, and as the MMA takes them
+  uint32_t terms;                    // 2: x_rest is added to x
   uint32_t outs;                     // results of a row
   uint32_t k_blocks, k_seg;          // of 64; from k_seg on the second maps
+  uint32_t tiles, groups;
+  float* partials;                   // kEpiStore, groups > 1: [groups][rows][outs]
   uint32_t stages, stage_bytes;
   const float* alpha;                // kEpiStore
   uint32_t act;                      // kEpiGated
   void *out, *g, *u;                 // results; kEpiGated: g and u too, or null
+  void* rest;                        // kEpiDlogits: what rounding the results left, or null
   int64_t ld_out, ld_g, ld_u;
   RowWeights loss;                   // kEpiStats: targets; kEpiDlogits: all of it
   uint32_t first_col;                // logits of words first_col ..
@@ -78,12 +87,18 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 // Floats between rows of summed logits: threads with a row each read without bank conflicts.
 constexpr uint32_t kStatPitch = kFewM + 1;
 
+// Stores v rounded to 16 bits and gives what it became.
 template <int DT>
-__device__ __forceinline__ void st_result(void* base, int64_t at, float v) {
-  if constexpr (DT == 1)
-    static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(v);
-  else
-    static_cast<__half*>(base)[at] = __float2half_rn(v);
+__device__ __forceinline__ float st_result(void* base, int64_t at, float v) {
+  if constexpr (DT == 1) {
+    const __nv_bfloat16 r = __float2bfloat16_rn(v);
+    static_cast<__nv_bfloat16*>(base)[at] = r;
+    return __bfloat162float(r);
+  } else {
+    const __half r = __float2half_rn(v);
+    static_cast<__half*>(base)[at] = r;
+    return __half2float(r);
+  }
 }
 
 // DT: 0 = fp16, 1 = bf16.  W_MN: the weights lie with the results' index contiguous ([k, n]), not k.
@@ -98,11 +113,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
   const uint32_t ranks = cluster_nctarank(), rank = cluster_ctarank();
-  const uint32_t n0 = blockIdx.x / ranks * kFewM;
+  const uint32_t unit = blockIdx.x / ranks, group = unit / p.tiles;
+  const uint32_t n0 = (unit - group * p.tiles) * kFewM;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t stage_bytes = p.stage_bytes;
-  const uint32_t per_rank = (p.k_blocks + ranks - 1u) / ranks;
-  const uint32_t k_lo = min(rank * per_rank, p.k_blocks), k_hi = min(k_lo + per_rank, p.k_blocks);
+  const uint32_t per_group = (p.k_blocks + p.groups - 1u) / p.groups;
+  const uint32_t g_lo = min(group * per_group, p.k_blocks), g_hi = min(g_lo + per_group, p.k_blocks);
+  const uint32_t per_rank = (per_group + ranks - 1u) / ranks;
+  const uint32_t k_lo = min(g_lo + rank * per_rank, g_hi), k_hi = min(k_lo + per_rank, g_hi);
   const uint32_t segments = (k_hi - k_lo + kFewSegment - 1u) / kFewSegment;
 
   const uint32_t bar_loaded = smem_u32(&ctl.loaded[0]);
@@ -200,6 +218,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           }
         }
         tma_load_2d(dst + kMats * kFewWeightBytes, &maps.x[seg], bar, kx, 0);
+        if (p.terms == 2u)
+          tma_load_2d(dst + kMats * kFewWeightBytes + p.n_pad * 128u, &maps.x_rest[seg], bar, kx, 0);
         pending |= 1u << slot;
         pending_par = (pending_par & ~(1u << slot)) | (parity << slot);
         if (++slot == p.stages) slot = 0, parity ^= 1u;
@@ -232,6 +252,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           for (uint32_t kk = 0; kk < kFewBK / kUmmaK; ++kk)
             umma_f16(d, a0 + at + m * (kFewWeightBytes >> 4) + (W_MN ? kk * 128u : kk * 2u),
                      b0 + at + kk * 2u, idesc, in_seg != 0u || kk != 0u ? 1u : 0u);
+          if (EPI == kEpiStore && p.terms == 2u) {
+#pragma unroll
+            for (uint32_t kk = 0; kk < kFewBK / kUmmaK; ++kk)
+              umma_f16(d, a0 + at + (W_MN ? kk * 128u : kk * 2u),
+                       b0 + at + p.n_pad * 8u + kk * 2u, idesc, 1u);
+          }
         }
         umma_commit(bar_consumed + 8u * slot);
       }
@@ -307,14 +333,21 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         st_result<DT>(p.u, row * p.ld_u + n, b);
       }
     } else if constexpr (EPI == kEpiStore) {
-      if (in) st_result<DT>(p.out, row * p.ld_out + n, a * alpha);
+      if (!in) return;
+      if (p.partials != nullptr)
+        p.partials[(static_cast<int64_t>(group) * p.rows + row) * p.outs + n] = a;
+      else
+        st_result<DT>(p.out, row * p.ld_out + n, a * alpha);
     } else if constexpr (EPI == kEpiDlogits) {
       const int32_t at = __shfl_sync(0xffffffffu, r < 32u ? hot[0] : hot[1], r & 31u);
       const float row_lse = __shfl_sync(0xffffffffu, r < 32u ? lse[0] : lse[1], r & 31u);
       const float w = __shfl_sync(0xffffffffu, r < 32u ? weight[0] : weight[1], r & 31u);
       float d = exp2_fast((a - row_lse) * kLog2e);
       if (at == static_cast<int32_t>(f)) d -= 1.0f;
-      if (in) st_result<DT>(p.out, row * p.ld_out + n, w == 0.0f ? 0.0f : d * w);
+      d = w == 0.0f ? 0.0f : d * w;
+      if (!in) return;
+      const float back = st_result<DT>(p.out, row * p.ld_out + n, d);
+      if (p.rest != nullptr) st_result<DT>(p.rest, row * p.ld_out + n, left_over(d, back));
     } else {
       stat_rows[r * kStatPitch + f] = in ? a : -INFINITY;
     }

@@ -22,6 +22,7 @@ __device__ __forceinline__ float2 unpack_in(uint32_t w) {
 struct GatedGradParams {
   const void *dh, *g, *u;
   void* dgu;                       // [rows][2 vecs x 8]: dg, then du
+  void* rest;                      // null, or the same of what rounding them left
   int64_t ld_dh, ld_g, ld_u;       // elements
   uint32_t rows, vecs;             // vectors of 8 values in a row
   uint32_t act;
@@ -41,20 +42,31 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p
   auto work = [&](uint64_t row, uint32_t v, const uint4& dh4, const uint4& g4, const uint4& u4) {
     const uint32_t dhw[4] = {dh4.x, dh4.y, dh4.z, dh4.w}, gw[4] = {g4.x, g4.y, g4.z, g4.w},
                    uw[4] = {u4.x, u4.y, u4.z, u4.w};
-    uint32_t dgw[4], duw[4];
+    uint32_t dgw[4], duw[4], dg_rest[4], du_rest[4];
+    auto pack = [](float x, float y, uint32_t& rest) {
+      const uint32_t w = pack_out<DT>(__float_as_uint(x), __float_as_uint(y));
+      const float2 back = unpack_in<DT>(w);
+      rest = pack_out<DT>(__float_as_uint(left_over(x, back.x)), __float_as_uint(left_over(y, back.y)));
+      return w;
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 dh = unpack_in<DT>(dhw[i]), g = unpack_in<DT>(gw[i]), u = unpack_in<DT>(uw[i]);
       const Gate a = gate_of(g.x, p.act), b = gate_of(g.y, p.act);
       const float ax = g.x * a.s, bx = g.y * b.s;
-      dgw[i] = pack_out<DT>(
-          __float_as_uint(dh.x * u.x * fmaf(ax * (1.0f - a.s), a.slope, a.s)),
-          __float_as_uint(dh.y * u.y * fmaf(bx * (1.0f - b.s), b.slope, b.s)));
-      duw[i] = pack_out<DT>(__float_as_uint(dh.x * ax), __float_as_uint(dh.y * bx));
+      dgw[i] = pack(dh.x * u.x * fmaf(ax * (1.0f - a.s), a.slope, a.s),
+                    dh.y * u.y * fmaf(bx * (1.0f - b.s), b.slope, b.s), dg_rest[i]);
+      duw[i] = pack(dh.x * ax, dh.y * bx, du_rest[i]);
     }
-    char* to = static_cast<char*>(p.dgu) + (row * 2u * p.vecs + v) * 16u;
+    const uint64_t at = (row * 2u * p.vecs + v) * 16u, next = static_cast<uint64_t>(p.vecs) * 16u;
+    char* to = static_cast<char*>(p.dgu) + at;
     st_global_v4(to, dgw[0], dgw[1], dgw[2], dgw[3]);
-    st_global_v4(to + static_cast<uint64_t>(p.vecs) * 16u, duw[0], duw[1], duw[2], duw[3]);
+    st_global_v4(to + next, duw[0], duw[1], duw[2], duw[3]);
+    if (p.rest != nullptr) {
+      to = static_cast<char*>(p.rest) + at;
+      st_global_v4(to, dg_rest[0], dg_rest[1], dg_rest[2], dg_rest[3]);
+      st_global_v4(to + next, du_rest[0], du_rest[1], du_rest[2], du_rest[3]);
+    }
   };
   for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
        i += 2u * stride) {

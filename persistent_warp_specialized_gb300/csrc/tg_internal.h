@@ -131,7 +131,7 @@ cudaError_t launch_wgrad(int dtype, bool debug, const WgradLaunch& l, cudaStream
 // Products with fused epilogues (tg_linear_kernel.cuh).  Matrices, tile counts and segments as
 // LinearProblem has them.
 struct LinearProduct {
-  CUtensorMap a[2], b[2], c[3];
+  CUtensorMap a[2], b[4], c[3];
   bool a_mn, b_mn;              // the operand lies with m (n) contiguous
   uint32_t M, N;
   uint32_t m_blocks, n_blocks, k_blocks, n_seg, k_seg, group, column_major;
@@ -167,17 +167,22 @@ struct LinearLaunch {
 cudaError_t prepare_linear_kernels(int* max_pairs);
 cudaError_t launch_linear(const LinearLaunch& l, cudaStream_t stream);
 
-// The same products for few rows (tg_few_kernel.cuh): ``ranks`` CTAs share a tile of 128 results a row.
+// The same products for few rows (tg_few_kernel.cuh): ``ranks`` CTAs share a tile of 128 results a row,
+// and ``groups`` of them cut K, with fp32 sums [groups][rows][outs] where there are several.
 struct FewLaunch {
   CUtensorMap w[2], x[2];       // weights and rows; the second ones along K, or of the gated pair
+  CUtensorMap x_rest[2];        // terms == 2: what rounding the rows to 16 bits left
+  uint32_t terms;
   int dtype;
   bool w_mn;                    // the weights lie with the results' index contiguous
   int epi;                      // LinearEpi
-  uint32_t rows, outs, tiles, ranks;
+  uint32_t rows, outs, tiles, ranks, groups;
+  float* partials;
   uint32_t k_blocks, k_seg;     // of 64
   const float* alpha;
   uint32_t act;
   void *out, *g, *u;
+  void* rest;                   // kEpiDlogits: what rounding ``out`` left, or null
   int64_t ld_out, ld_g, ld_u;
   uint32_t first_col, slots;
   void* stats;
@@ -211,10 +216,11 @@ struct GatedJoin {
 };
 cudaError_t launch_gated_join(const GatedJoin& l, cudaStream_t stream);
 
-// dgu [rows, 2 outs] = (dh u act'(g), dh act(g)), side by side (tg_gated_kernel.cuh)
+// dgu [rows, 2 outs] = (dh u act'(g), dh act(g)), side by side (tg_gated_kernel.cuh); rest: null, or the
+// same of what rounding them left
 struct GatedGrad {
   const void *dh, *g, *u;
-  void* dgu;
+  void *dgu, *rest;
   int64_t rows, outs, ld_dh, ld_g, ld_u;
   uint32_t act;
   int dtype, sms;
@@ -231,6 +237,20 @@ struct XentJoin {
   uint32_t rows, slots, vocab;
 };
 cudaError_t launch_xent_join(const XentJoin& l, cudaStream_t stream);
+// The same from fp32 parts of the logits [splits][part_rows][pitch], and the gradients of logits from them.
+struct XentParts {
+  const float* parts;
+  uint32_t splits, part_rows, pitch;
+};
+struct XentDlogits {
+  XentRows loss;
+  const float* lse;
+  void* out;
+  uint32_t rows, cols, first_col, pitch_out;
+  int dtype, sms;
+};
+cudaError_t launch_xent_rows(const XentJoin& l, const XentParts& parts, cudaStream_t stream);
+cudaError_t launch_xent_dlogits(const XentDlogits& l, const XentParts& parts, cudaStream_t stream);
 cudaError_t clear_watchdog_status(cudaStream_t stream);
 // synchronises ``stream``, returns the status word in *out and clears it
 cudaError_t read_and_clear_watchdog_status(unsigned int* out, cudaStream_t stream);

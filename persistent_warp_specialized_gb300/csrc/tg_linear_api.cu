@@ -26,14 +26,16 @@ struct Mat {
 };
 
 // D[M, N] = A B, before its plan.  Two matrices may stand in an operand's place (tg_linear_kernel.cuh):
-// segs_n: N columns each of b[0], b[1] to c[0], c[1]; segs_k: K values each of a[i], b[i].
+// segs_n: N columns each of b[0], b[1] to c[0], c[1]; segs_k: K values each of a[0], b[0 .. 1] and of
+// a[1], b[2 .. 3].  a_rest: for few rows, what rounding a[i] left.
 struct Product {
   int epi = tg::kEpiStore;
   int dtype = 0;
   bool a_mn = false, b_mn = false;
   int64_t M = 0, N = 0, K = 0;
   int segs_n = 1, segs_k = 1;
-  Mat a[2], b[2], c[3];
+  Mat a[2], b[4], c[3], a_rest[2];
+  bool two_terms = false;
   const float* alpha = nullptr;
   // kEpiStore over several launches: 0 alone, 1 the first, 2 a later one, whose fp32 sums are added to
   // the first's; the caller joins them after the last
@@ -48,16 +50,18 @@ struct Product {
 
 // How a product is cut into units.
 struct Plan {
-  bool few;                 // the kernel for few rows takes it, and nothing below counts
+  bool few;                 // the kernel for few rows takes it: splits are its groups
+  uint32_t ranks;           // of few rows: CTAs that share a tile
   uint32_t m_tiles, n_tiles, n_seg, k_blocks, k_seg, splits, blocks_per_split;
   uint32_t units;           // tiles
-  uint32_t part_rows;
+  uint32_t part_rows, part_pitch;   // rows of one split's sums, and values from one to the next
   uint64_t partial_bytes;   // fp32 sums of one N segment (0: results are stored rounded)
 };
 
-// Microseconds on GB300 that the choice of splits goes by: a k-block of a tile; what a unit adds; the
-// join, and bytes of partial sums a microsecond, written and read.
-constexpr double kBlockUs = 0.66, kUnitUs = 0.4, kJoinUs = 2.5;
+// Microseconds on GB300 that the choice of splits goes by: a k-block of a tile where few pairs are at work
+// and where all are (they share the L2); what a unit adds; the join, and bytes of partial sums a
+// microsecond, written and read.
+constexpr double kBlockUs = 0.35, kFullBlockUs = 0.66, kUnitUs = 0.4, kJoinUs = 3.0;
 constexpr double kWriteBytes = 5e6, kReadBytes = 4e6;
 constexpr uint32_t kMinBlocks = 4;   // k-blocks of a unit when K is split
 
@@ -70,6 +74,7 @@ bool few_rows(const Product& p, bool sums) {
 Plan plan_of(const Product& p, uint32_t splits, bool sums = false) {
   Plan w;
   w.few = false;
+  w.ranks = 1;
   w.m_tiles = static_cast<uint32_t>(ceil_div(p.M, tg::kPairBM));
   w.n_seg = static_cast<uint32_t>(ceil_div(p.N, p.epi == tg::kEpiGated ? tg::kGatedTileN : tg::kBN));
   w.n_tiles = w.n_seg * p.segs_n;
@@ -79,16 +84,21 @@ Plan plan_of(const Product& p, uint32_t splits, bool sums = false) {
   w.splits = (w.k_blocks + w.blocks_per_split - 1) / w.blocks_per_split;
   w.units = w.m_tiles * w.n_tiles;
   w.part_rows = static_cast<uint32_t>(ceil_div(p.M, tg::kPartialRows)) * tg::kPartialRows;
-  w.partial_bytes = w.splits > 1 || sums ? uint64_t(w.splits) * w.part_rows * p.N * 4 : 0;
+  w.part_pitch = static_cast<uint32_t>(ceil_div(p.N, 4)) * 4;   // 16 bytes
+  w.partial_bytes = w.splits > 1 || sums ? uint64_t(w.splits) * w.part_rows * w.part_pitch * 4 : 0;
   return w;
 }
 
 // What the products' units are expected to take over ``pairs`` CTA pairs, and the joins: the longest
 // unit, or every pair's share of all.
 double expected_us(const Product* p, const Plan* w, int count, uint32_t pairs) {
+  uint32_t at_work = 0;
+  for (int i = 0; i < count; ++i) at_work += w[i].units * w[i].splits;
+  const double full = at_work < pairs ? double(at_work) / pairs : 1.0;
+  const double block = kBlockUs + (kFullBlockUs - kBlockUs) * full;
   double longest = 0, all = 0, join = 0;
   for (int i = 0; i < count; ++i) {
-    const double unit = w[i].blocks_per_split * kBlockUs + kUnitUs;
+    const double unit = w[i].blocks_per_split * block + kUnitUs;
     const uint32_t units = w[i].units * w[i].splits;
     if (unit > longest) longest = unit;
     all += units * unit;
@@ -133,14 +143,32 @@ void plan_products(const Product* p, Plan* best, int count, int max_pairs, bool 
   }
 }
 
-Plan plan_product(const Product& p, int max_pairs) {
-  Plan w;
-  if (few_rows(p, false)) {
-    w = plan_of(p, 1);
-    w.few = true;
-  } else {
-    plan_products(&p, &w, 1, max_pairs);
+// Few rows: a tile is shared by as many CTAs (a power of two) as it takes for one on every SM, of at least
+// two k-blocks of 64 each.  Where 8 do not fill the SMs and have many k-blocks left, K is cut between
+// groups first: a CTA has about 0.3 us of a k-block in flight for every one it multiplies, the join of
+// the groups' sums takes 3 us.  Measured (bf16, us, one group / groups): gradient towards x of 44 rows,
+// 312 columns, 33823 words 33 / 9.
+Plan plan_few(const Product& p, int max_pairs) {
+  const uint32_t sms = 2 * static_cast<uint32_t>(max_pairs);
+  const uint32_t tiles = static_cast<uint32_t>(ceil_div(p.N, tg::kFewM));
+  const uint32_t k_blocks = static_cast<uint32_t>(ceil_div(p.K, tg::kFewBK)) * p.segs_k;
+  Plan w = plan_of(p, 1);
+  w.few = true;
+  while (w.ranks < tg::kFewMaxCluster && tiles * w.ranks < sms && k_blocks >= 4 * w.ranks) w.ranks *= 2;
+  const uint32_t each = k_blocks / w.ranks;
+  if (p.epi == tg::kEpiStore && tiles * w.ranks < sms && each > 20) {
+    const uint32_t fill = 2 * sms / (tiles * w.ranks), deep = each / 6;
+    w.splits = fill < deep ? fill : deep;
+    w.part_rows = static_cast<uint32_t>(p.M);
+    if (w.splits > 1) w.partial_bytes = uint64_t(w.splits) * w.part_rows * p.N * 4;
   }
+  return w;
+}
+
+Plan plan_product(const Product& p, int max_pairs) {
+  if (few_rows(p, false)) return plan_few(p, max_pairs);
+  Plan w;
+  plan_products(&p, &w, 1, max_pairs);
   return w;
 }
 
@@ -158,19 +186,24 @@ int encode_operand(CUtensorMap* map, const Mat& m, bool mn, int dtype) {
                       mn ? tg::kLinBK : tg::kBM, m.name, true, m.ld * 2);
 }
 
-// Enqueues a product with few rows.  Its tiles are shared by as many CTAs (a power of two) as it takes
-// for one on every SM, of at least two k-blocks each.
-int run_few(const Product& p, int sms, uint64_t watchdog_ns, cudaStream_t stream) {
+// Enqueues a product with few rows by its plan (without the join of its groups' sums).
+int run_few(const Product& p, const Plan& w, char* partials, uint64_t watchdog_ns,
+            cudaStream_t stream) {
   tg::FewLaunch l = {};
   const uint32_t n_pad = tg::few_padded(p.M);
   const int mats = p.epi == tg::kEpiGated || p.segs_k == 2 ? 2 : 1;
   for (int i = 0; i < mats; ++i) {
-    TG_TRY(encode_tiled(&l.w[i], type16(p.dtype), 2, p.b[i].p, p.b[i].cols, p.b[i].rows, 64,
-                        p.b_mn ? tg::kFewBK : tg::kFewM, p.b[i].name, true, p.b[i].ld * 2));
+    const Mat& b = p.b[p.segs_k == 2 ? 2 * i : i];
+    TG_TRY(encode_tiled(&l.w[i], type16(p.dtype), 2, b.p, b.cols, b.rows, 64,
+                        p.b_mn ? tg::kFewBK : tg::kFewM, b.name, true, b.ld * 2));
     const Mat& x = p.a[p.segs_k == 2 ? i : 0];
     TG_TRY(encode_tiled(&l.x[i], type16(p.dtype), 2, x.p, x.cols, x.rows, 64, n_pad, x.name, true,
                         x.ld * 2));
+    if (p.two_terms)
+      TG_TRY(encode_tiled(&l.x_rest[i], type16(p.dtype), 2, p.a_rest[i].p, x.cols, x.rows, 64, n_pad,
+                          x.name, true, x.ld * 2));
   }
+  l.terms = p.two_terms ? 2 : 1;
   l.dtype = p.dtype;
   l.w_mn = p.b_mn;
   l.epi = p.epi;
@@ -179,14 +212,14 @@ int run_few(const Product& p, int sms, uint64_t watchdog_ns, cudaStream_t stream
   l.tiles = static_cast<uint32_t>(ceil_div(p.N, tg::kFewM));
   l.k_seg = static_cast<uint32_t>(ceil_div(p.K, tg::kFewBK));
   l.k_blocks = l.k_seg * p.segs_k;
-  l.ranks = 1;
-  while (l.ranks < tg::kFewMaxCluster && l.tiles * l.ranks < static_cast<uint32_t>(sms) &&
-         l.k_blocks >= 4 * l.ranks)
-    l.ranks *= 2;
+  l.ranks = w.ranks;
+  l.groups = w.splits;
+  l.partials = w.partial_bytes ? reinterpret_cast<float*>(partials) : nullptr;
   l.alpha = p.alpha;
   l.act = p.act;
   l.out = const_cast<void*>(p.c[0].p);
   l.ld_out = p.c[0].ld;
+  if (p.epi == tg::kEpiDlogits) l.rest = const_cast<void*>(p.c[1].p);
   if (p.keep) {
     l.g = const_cast<void*>(p.c[1].p);
     l.u = const_cast<void*>(p.c[2].p);
@@ -207,24 +240,18 @@ int run_few(const Product& p, int sms, uint64_t watchdog_ns, cudaStream_t stream
 // What a product's units are to the kernel.  partials: fp32 sums of its N segments, where the plan has
 // them.
 int encode_product(tg::LinearProduct* l, const Product& p, const Plan& w, char* partials) {
-  for (int i = 0; i < 2; ++i) {
-    const bool two_a = p.segs_k == 2;
-    const bool two_b = two_a || p.segs_n == 2 || p.epi == tg::kEpiGated;
-    if (i == 0 || two_a)
-      TG_TRY(encode_operand(&l->a[i], p.a[i], p.a_mn, p.dtype));
-    else
-      l->a[i] = l->a[0];
-    if (i == 0 || two_b)
-      TG_TRY(encode_operand(&l->b[i], p.b[i], p.b_mn, p.dtype));
-    else
-      l->b[i] = l->b[0];
-  }
+  for (int i = 0; i < p.segs_k; ++i) TG_TRY(encode_operand(&l->a[i], p.a[i], p.a_mn, p.dtype));
+  const int across = p.segs_n == 2 || p.epi == tg::kEpiGated ? 2 : 1;
+  for (int k = 0; k < p.segs_k; ++k)
+    for (int i = 0; i < across; ++i)
+      TG_TRY(encode_operand(&l->b[2 * k + i], p.b[2 * k + i], p.b_mn, p.dtype));
   l->partial = 0;
   if (w.partial_bytes) {
     for (int i = 0; i < p.segs_n; ++i)
       TG_TRY(encode_tiled(&l->c[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
                           partials + i * padded(w.partial_bytes), p.N,
-                          uint64_t(w.splits) * w.part_rows, 32, tg::kPartialRows, "workspace"));
+                          uint64_t(w.splits) * w.part_rows, 32, tg::kPartialRows, "workspace", true,
+                          uint64_t(w.part_pitch) * 4));
     l->partial = p.accumulate == 2 ? 2 : 1;
   } else {
     for (int i = 0; i < 3; ++i)
@@ -327,15 +354,17 @@ int join_products(const Product* p, const Plan* w, char* const* partials, int co
 }
 
 uint64_t partials_of(const Product& p, const Plan& w) {
-  return w.partial_bytes && !w.few ? p.segs_n * padded(w.partial_bytes) : 0;
+  return w.partial_bytes ? p.segs_n * padded(w.partial_bytes) : 0;
 }
 
 // A product by itself: its units, and the join of its partial sums at ``ws`` where it has them.
 int whole_product(const Product& p, const Plan& w, void* ws, int sms, int pairs, cudaStream_t stream,
                   uint64_t watchdog_ns = 0, int64_t inject = -1) {
-  if (w.few) return run_few(p, sms, watchdog_ns, stream);
   char* const partials[1] = {static_cast<char*>(ws)};
-  TG_TRY(run_products(&p, &w, partials, 1, pairs, watchdog_ns, inject, stream));
+  if (w.few)
+    TG_TRY(run_few(p, w, partials[0], watchdog_ns, stream));
+  else
+    TG_TRY(run_products(&p, &w, partials, 1, pairs, watchdog_ns, inject, stream));
   return join_products(&p, &w, partials, 1, sms, stream);
 }
 
@@ -366,19 +395,16 @@ int run_grads(const Product* p, const GradPlans& o, const bool (&wanted)[2], boo
   int n = 0;
   for (int i = 0; i < 2; ++i) {
     if (!wanted[i]) continue;
-    if (o.w[i].few) {
-      TG_TRY(run_few(p[i], sms, 0, stream));
-      continue;
-    }
     q[n] = p[i];
     w[n] = o.w[i];
     at[n++] = partials[i];
   }
   if (n == 0) return TG_OK;
-  TG_TRY(run_products(q, w, at, n, pairs, 0, -1, stream));
-  if (wanted[0] && !o.w[0].few && !join_first)
-    return join_products(q + 1, w + 1, at + 1, n - 1, sms, stream);
-  return join_products(q, w, at, n, sms, stream);
+  const int few = w[0].few ? 1 : 0;   // the second one never is
+  if (few) TG_TRY(run_few(q[0], w[0], at[0], 0, stream));
+  if (n > few) TG_TRY(run_products(q + few, w + few, at + few, n - few, pairs, 0, -1, stream));
+  const int skip = wanted[0] && !join_first ? 1 : 0;
+  return join_products(q + skip, w + skip, at + skip, n - skip, sms, stream);
 }
 
 // ---------------------------------------------------------------- checks
@@ -540,17 +566,27 @@ GatedPlan gated_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& h, i
   return o;
 }
 
+// Gradients that are rounded to 16 bits on the way to both products: with few rows their errors do not
+// average out, so they come in two terms (tg_few_kernel.cuh), the second one as a second segment of K
+// in the product over rows.
+bool two_terms(int64_t rows) { return rows <= tg::kTwoTermRows; }
+
 struct GatedBwd {
   Product p[2];             // dx; dwg and dwu
   GradPlans plans;
-  uint64_t dgu_bytes, total;
+  uint64_t dgu_bytes, total;   // dgu_bytes: of one term
 };
 // With null pointers where only sizes matter.
 GatedBwd gated_bwd_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& dx, const Mat& dwg,
                         const Mat& dwu, void* dgu, int dtype, int pairs) {
   const int64_t rows = x.rows, cols = x.cols, outs = wg.cols;
-  const Mat dg = {dgu, rows, outs, 2 * outs, "dg"};
-  const Mat du = {dgu ? static_cast<char*>(dgu) + 2 * outs : nullptr, rows, outs, 2 * outs, "du"};
+  const uint64_t dgu_bytes = padded(uint64_t(rows) * 2 * outs * 2);
+  const bool two = two_terms(rows);
+  // dg or du of a term
+  auto part = [&](int term, int which) {
+    char* at = dgu ? static_cast<char*>(dgu) + term * dgu_bytes + which * 2 * outs : nullptr;
+    return Mat{at, rows, outs, 2 * outs, which ? "du" : "dg"};
+  };
   Product p[2];
   // dX = dg Wg^T + du Wu^T: K in two segments
   p[0].dtype = dtype;
@@ -558,11 +594,10 @@ GatedBwd gated_bwd_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& d
   p[0].N = cols;
   p[0].K = outs;
   p[0].segs_k = 2;
-  p[0].a[0] = dg;
-  p[0].a[1] = du;
   p[0].b[0] = wg;
-  p[0].b[1] = wu;
+  p[0].b[2] = wu;
   p[0].c[0] = dx;
+  p[0].two_terms = two;
   // dWg = X^T dg, dWu = X^T du: N in two segments
   p[1].dtype = dtype;
   p[1].a_mn = p[1].b_mn = true;
@@ -570,13 +605,18 @@ GatedBwd gated_bwd_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& d
   p[1].N = outs;
   p[1].K = rows;
   p[1].segs_n = 2;
-  p[1].a[0] = x;
-  p[1].b[0] = dg;
-  p[1].b[1] = du;
+  p[1].segs_k = two ? 2 : 1;
   p[1].c[0] = dwg;
   p[1].c[1] = dwu;
-  GatedBwd o = {{p[0], p[1]}, GradPlans(p, pairs), padded(uint64_t(rows) * 2 * outs * 2), 0};
-  o.total = o.dgu_bytes + o.plans.bytes[0] + o.plans.bytes[1];
+  for (int i = 0; i < 2; ++i) {
+    p[0].a[i] = part(0, i);
+    p[0].a_rest[i] = part(1, i);
+    p[1].a[i] = x;
+    p[1].b[i] = part(0, i);
+    p[1].b[2 + i] = part(1, i);
+  }
+  GatedBwd o = {{p[0], p[1]}, GradPlans(p, pairs), dgu_bytes, 0};
+  o.total = (two ? 2 : 1) * dgu_bytes + o.plans.bytes[0] + o.plans.bytes[1];
   return o;
 }
 
@@ -596,18 +636,6 @@ int check_xent(int64_t rows, int64_t cols, int64_t vocab, int64_t ld_x, int64_t 
   return check_tiles(rows, vocab);
 }
 
-struct XentFwd {
-  uint32_t slots;
-  uint64_t stats_bytes, total;
-};
-XentFwd xent_fwd_plan(int64_t rows, int64_t vocab) {
-  XentFwd o;
-  o.slots = static_cast<uint32_t>(ceil_div(vocab, rows <= tg::kFewRows ? tg::kFewM : tg::kStatCols));
-  o.stats_bytes = padded(uint64_t(rows) * o.slots * 8);
-  o.total = o.stats_bytes + padded(uint64_t(rows) * 4);
-  return o;
-}
-
 // logits of columns [first, first + n) of the vocabulary, W's rows
 Product logits_product(int epi, const Mat& x, const Mat& w, int64_t first, int64_t n,
                        const tg::XentRows& loss, int dtype) {
@@ -624,16 +652,62 @@ Product logits_product(int epi, const Mat& x, const Mat& w, int64_t first, int64
   return p;
 }
 
+// How logits are made: by an epilogue of the product, or, where few tiles have long sums, from the parts
+// of split sums.
+struct LogitsPlan {
+  Product p;                // with kEpiStore: parts
+  Plan plan;
+  uint64_t part_bytes;
+};
+LogitsPlan logits_plan(const Product& p, int pairs) {
+  LogitsPlan o = {p, plan_product(p, pairs), 0};
+  if (o.plan.few) return o;
+  Product parts = p;
+  parts.epi = tg::kEpiStore;
+  Plan cut;
+  plan_products(&parts, &cut, 1, pairs);
+  if (cut.splits > 1 && expected_us(&parts, &cut, 1, pairs) < expected_us(&p, &o.plan, 1, pairs)) {
+    o.p = parts;
+    o.plan = cut;
+    o.part_bytes = partials_of(parts, cut);
+  }
+  return o;
+}
+tg::XentParts parts_of(const Plan& w, const char* parts) {
+  return {reinterpret_cast<const float*>(parts), w.splits, w.part_rows, w.part_pitch};
+}
+
+struct XentFwd {
+  LogitsPlan logits;
+  uint32_t slots;
+  uint64_t stats_bytes, total;
+};
+XentFwd xent_fwd_plan(const Mat& x, const Mat& w, const tg::XentRows& loss, int dtype, int pairs) {
+  XentFwd o;
+  o.logits = logits_plan(logits_product(tg::kEpiStats, x, w, 0, w.rows, loss, dtype), pairs);
+  o.slots = static_cast<uint32_t>(ceil_div(w.rows, o.logits.plan.few ? tg::kFewM : tg::kStatCols));
+  o.stats_bytes = padded(uint64_t(x.rows) * o.slots * 8);
+  o.total = o.logits.part_bytes ? o.logits.part_bytes
+                                : o.stats_bytes + padded(uint64_t(x.rows) * 4);
+  return o;
+}
+
 // The gradients, a piece of ``chunk`` columns of the vocabulary at a time: the gradients of the piece's
 // logits, its rows of dW, and its share of dX, whose fp32 sums run over the pieces.
 struct XentBwd {
   int64_t chunk, chunks;
   bool sums;                // dX is summed in fp32 over the pieces
-  uint64_t dl_bytes, dx_bytes, dw_bytes, total;
+  bool two;                 // the gradients of the logits come in two terms
+  uint64_t dl_bytes;        // of one term
+  uint64_t part_bytes, dx_bytes, dw_bytes, total;
 };
 
-Product xent_dx_product(const Mat& dl, const Mat& w, int64_t first, const Mat& dx, int dtype) {
+// rest: the second term of dl, or null
+Product xent_dx_product(const Mat& dl, const Mat* rest, const Mat& w, int64_t first, const Mat& dx,
+                        int dtype) {
   Product p;
+  p.two_terms = rest != nullptr;
+  if (rest) p.a_rest[0] = *rest;
   p.dtype = dtype;
   p.b_mn = true;
   p.M = dl.rows;
@@ -645,8 +719,11 @@ Product xent_dx_product(const Mat& dl, const Mat& w, int64_t first, const Mat& d
   return p;
 }
 
-Product xent_dw_product(const Mat& dl, const Mat& x, const Mat& dw, int64_t first, int dtype) {
+Product xent_dw_product(const Mat& dl, const Mat* rest, const Mat& x, const Mat& dw, int64_t first,
+                        int dtype) {
   Product p;
+  p.segs_k = rest ? 2 : 1;
+  if (rest) p.a[1] = *rest, p.b[2] = x;
   p.dtype = dtype;
   p.a_mn = p.b_mn = true;
   p.M = dl.cols;
@@ -666,19 +743,25 @@ XentBwd xent_bwd_plan(int64_t rows, int64_t cols, int64_t vocab, int dtype, int 
   o.chunk = static_cast<int64_t>(ceil_div(ceil_div(vocab, o.chunks), tg::kBN)) * tg::kBN;
   o.chunks = static_cast<int64_t>(ceil_div(vocab, o.chunk));
   o.sums = o.chunks > 1;
+  o.two = two_terms(rows) && !o.sums;
   o.dl_bytes = padded(uint64_t(rows) * o.chunk * 2);
-  o.dx_bytes = o.dw_bytes = 0;
+  o.part_bytes = o.dx_bytes = o.dw_bytes = 0;
   const Mat x = {nullptr, rows, cols, cols, ""}, w = {nullptr, vocab, cols, cols, ""};
   // the last piece may be narrower and split its tokens more finely
   for (const int64_t first : {int64_t(0), (o.chunks - 1) * o.chunk}) {
     const Mat dl = {nullptr, rows, vocab - first < o.chunk ? vocab - first : o.chunk, o.chunk, ""};
-    const Product p[2] = {xent_dx_product(dl, w, first, x, dtype),
-                          xent_dw_product(dl, x, w, first, dtype)};
+    const Mat* rest = o.two ? &dl : nullptr;
+    const Product p[2] = {xent_dx_product(dl, rest, w, first, x, dtype),
+                          xent_dw_product(dl, rest, x, w, first, dtype)};
     const GradPlans plans(p, pairs, o.sums);
+    const LogitsPlan logits =
+        logits_plan(logits_product(tg::kEpiDlogits, x, w, first, dl.cols, {}, dtype), pairs);
+    if (logits.part_bytes > o.part_bytes) o.part_bytes = logits.part_bytes;
     if (first == 0) o.dx_bytes = plans.bytes[0];
     if (plans.bytes[1] > o.dw_bytes) o.dw_bytes = plans.bytes[1];
   }
-  o.total = o.dl_bytes + kWorkspaceAlign + o.dx_bytes + o.dw_bytes;
+  o.total = (o.two ? 2 : 1) * o.dl_bytes + kWorkspaceAlign + o.part_bytes + o.dx_bytes +
+            o.dw_bytes;
   return o;
 }
 
@@ -845,6 +928,7 @@ int tg_gated_bwd(const void* dh_dev, const void* g_dev, const void* u_dev, const
   e.g = g_dev;
   e.u = u_dev;
   e.dgu = workspace_dev;
+  e.rest = two_terms(rows) ? static_cast<char*>(workspace_dev) + o.dgu_bytes : nullptr;
   e.rows = rows;
   e.outs = outs;
   e.ld_dh = ld_dh;
@@ -855,14 +939,19 @@ int tg_gated_bwd(const void* dh_dev, const void* g_dev, const void* u_dev, const
   e.sms = sms;
   const cudaError_t err = tg::launch_gated_grad(e, st);
   if (err != cudaSuccess) return fail_cuda("gated gradient launch", err);
-  char* const rest = static_cast<char*>(workspace_dev) + o.dgu_bytes;
+  char* const rest = static_cast<char*>(workspace_dev) + (two_terms(rows) ? 2 : 1) * o.dgu_bytes;
   char* const partials[2] = {rest, rest + o.plans.bytes[0]};
   return run_grads(o.p, o.plans, {dx_dev != nullptr, weights}, true, partials, sms, pairs, st);
 }
 
 int64_t tg_xent_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab) {
   TG_TRY(check_xent(rows, cols, vocab, cols, cols, TG_BF16));
-  return rows == 0 ? 0 : static_cast<int64_t>(xent_fwd_plan(rows, vocab).total);
+  if (rows == 0) return 0;
+  int pairs = 0;
+  TG_TRY(linear_ready(nullptr, &pairs));
+  return static_cast<int64_t>(xent_fwd_plan({nullptr, rows, cols, cols, ""},
+                                            {nullptr, vocab, cols, cols, ""}, {}, TG_BF16, pairs)
+                                  .total);
 }
 
 int tg_xent_fwd(const void* x_dev, const void* w_dev, const int64_t* targets_dev, float* loss_dev,
@@ -879,7 +968,9 @@ int tg_xent_fwd(const void* x_dev, const void* w_dev, const int64_t* targets_dev
   TG_TRY(check_array(targets_dev, 8, "targets"));
   int sms = 0, pairs = 0;
   TG_TRY(linear_ready(&sms, &pairs));
-  const XentFwd o = xent_fwd_plan(rows, vocab);
+  tg::XentRows loss = {};
+  loss.targets = targets_dev;
+  XentFwd o = xent_fwd_plan(x, w, loss, dtype, pairs);
   TG_TRY(check_workspace(workspace_dev, workspace_bytes, o.total));
   const uint64_t row4 = uint64_t(rows) * 4;
   const Region r[] = {{loss_dev, row4, "loss"}, {lse_dev, row4, "lse"},
@@ -887,24 +978,29 @@ int tg_xent_fwd(const void* x_dev, const void* w_dev, const int64_t* targets_dev
                       {targets_dev, uint64_t(rows) * 8, "targets"}};
   TG_TRY(check_apart(r, 3, 6));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  tg::XentRows loss = {};
-  loss.targets = targets_dev;
-  Product p = logits_product(tg::kEpiStats, x, w, 0, vocab, loss, dtype);
-  p.stats = workspace_dev;
-  p.slots = o.slots;
-  p.hit = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + o.stats_bytes);
-  TG_TRY(whole_product(p, plan_product(p, pairs), nullptr, sms, pairs, st));
-  tg::XentJoin j;
-  j.stats = p.stats;
-  j.hit = p.hit;
+  tg::XentJoin j = {};
   j.targets = targets_dev;
   j.ignore = ignore_index;
   j.loss = loss_dev;
   j.lse = lse_dev;
   j.rows = static_cast<uint32_t>(rows);
-  j.slots = o.slots;
   j.vocab = static_cast<uint32_t>(vocab);
-  const cudaError_t e = tg::launch_xent_join(j, st);
+  cudaError_t e;
+  if (o.logits.part_bytes) {
+    char* const parts[1] = {static_cast<char*>(workspace_dev)};
+    TG_TRY(run_products(&o.logits.p, &o.logits.plan, parts, 1, pairs, 0, -1, st));
+    e = tg::launch_xent_rows(j, parts_of(o.logits.plan, parts[0]), st);
+  } else {
+    Product& p = o.logits.p;
+    p.stats = workspace_dev;
+    p.slots = o.slots;
+    p.hit = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + o.stats_bytes);
+    TG_TRY(whole_product(p, o.logits.plan, nullptr, sms, pairs, st));
+    j.stats = p.stats;
+    j.hit = p.hit;
+    j.slots = o.slots;
+    e = tg::launch_xent_join(j, st);
+  }
   return e == cudaSuccess ? TG_OK : fail_cuda("cross entropy launch", e);
 }
 
@@ -950,8 +1046,10 @@ int tg_xent_bwd(const float* dloss_dev, const void* x_dev, const void* w_dev,
                       {dloss_dev, row4, "dloss"}, {lse_dev, row4, "lse"}};
   TG_TRY(check_apart(r, 3, 8));
   char* base = static_cast<char*>(workspace_dev);
-  float* alpha = reinterpret_cast<float*>(base + o.dl_bytes);
-  char* dx_sums = base + o.dl_bytes + kWorkspaceAlign;
+  char* const behind = base + (o.two ? 2 : 1) * o.dl_bytes;
+  float* alpha = reinterpret_cast<float*>(behind);
+  char* const parts[1] = {behind + kWorkspaceAlign};
+  char* dx_sums = parts[0] + o.part_bytes;
   char* const partials[2] = {dx_sums, dx_sums + o.dx_bytes};
   const tg::XentRows loss = {dloss_dev, targets_dev, ignore_index, static_cast<uint32_t>(vocab), alpha};
   Product dx_first;
@@ -959,11 +1057,33 @@ int tg_xent_bwd(const float* dloss_dev, const void* x_dev, const void* w_dev,
   for (int64_t c = 0; c < o.chunks; ++c) {
     const int64_t first = c * o.chunk, n = vocab - first < o.chunk ? vocab - first : o.chunk;
     const Mat dl = {base, rows, n, o.chunk, "gradients of logits"};
-    Product p = logits_product(tg::kEpiDlogits, x, w, first, n, loss, dtype);
-    p.c[0] = dl;
-    p.lse = lse_dev;
-    TG_TRY(whole_product(p, plan_product(p, pairs), nullptr, sms, pairs, st));
-    Product q[2] = {xent_dx_product(dl, w, first, dx, dtype), xent_dw_product(dl, x, dw, first, dtype)};
+    LogitsPlan logits =
+        logits_plan(logits_product(tg::kEpiDlogits, x, w, first, n, loss, dtype), pairs);
+    Product& p = logits.p;
+    const Mat dl_rest = {base + o.dl_bytes, rows, n, o.chunk, "gradients of logits"};
+    const Mat* rest = o.two ? &dl_rest : nullptr;
+    if (logits.part_bytes) {
+      TG_TRY(run_products(&p, &logits.plan, parts, 1, pairs, 0, -1, st));
+      tg::XentDlogits d;
+      d.loss = loss;
+      d.lse = lse_dev;
+      d.out = base;
+      d.rows = static_cast<uint32_t>(rows);
+      d.cols = static_cast<uint32_t>(n);
+      d.first_col = static_cast<uint32_t>(first);
+      d.pitch_out = static_cast<uint32_t>(o.chunk);
+      d.dtype = dtype;
+      d.sms = sms;
+      const cudaError_t e = tg::launch_xent_dlogits(d, parts_of(logits.plan, parts[0]), st);
+      if (e != cudaSuccess) return fail_cuda("cross entropy launch", e);
+    } else {
+      p.c[0] = dl;
+      if (rest) p.c[1] = *rest;
+      p.lse = lse_dev;
+      TG_TRY(whole_product(p, logits.plan, nullptr, sms, pairs, st));
+    }
+    Product q[2] = {xent_dx_product(dl, rest, w, first, dx, dtype),
+                    xent_dw_product(dl, rest, x, dw, first, dtype)};
     q[0].alpha = q[1].alpha = alpha;
     q[0].accumulate = !o.sums ? 0 : c == 0 ? 1 : 2;
     GradPlans plans(q, pairs, o.sums);

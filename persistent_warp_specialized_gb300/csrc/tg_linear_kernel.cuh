@@ -39,7 +39,9 @@ constexpr int kProducts = EPI == 0 ? 2 : 1;
 
 template <int PRODUCTS>
 struct LinearMaps {
-  CUtensorMap a[PRODUCTS][2], b[PRODUCTS][2], c[PRODUCTS][3];
+  CUtensorMap a[PRODUCTS][2];   // by segment of K
+  CUtensorMap b[PRODUCTS][4];   // by segment of N, then of K
+  CUtensorMap c[PRODUCTS][3];
 };
 
 // The cross entropy's rows: one counts where its target is not ``ignore``; a target outside the
@@ -273,6 +275,11 @@ __device__ __forceinline__ void linear_store_sums(const float* v, uint32_t lane,
   __syncwarp();
 }
 
+// What rounding v to ``back`` left; nothing where that overflowed.
+__device__ __forceinline__ float left_over(float v, float back) {
+  return fabsf(back) == INFINITY ? 0.0f : v - back;
+}
+
 template <int DT>
 __device__ __forceinline__ void pack64(const float* v, uint32_t (&pk)[32]) {
 #pragma unroll
@@ -395,10 +402,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               continue;  // injected fault: this CTA never arms or fills this phase
             const uint32_t full_even = mapa_shared(bar_loaded + 8u * s, 0);
             if (rank == 0) mbar_arrive_expect_tx(bar_loaded + 8u * s, 2u * own_bytes);
-            const uint32_t seg_k = k >= k_seg ? 1u : 0u;   // at most one of seg_k and seg_n is 1
+            const uint32_t seg_k = k >= k_seg ? 1u : 0u;
             const int32_t kx = static_cast<int32_t>(k - seg_k * k_seg) * kLinBK;
             const CUtensorMap* tmA = maps_a + seg_k;
-            const CUtensorMap* tmB = maps_b + seg_k;
+            const CUtensorMap* tmB = maps_b + 2u * seg_k;
             const uint32_t a_dst = sA0 + s * kStageBytes, b_dst = sB0 + s * kStageBytes;
             // two boxes of 16 KiB each: 64-column chunks, or 64-deep atoms of K
 #pragma unroll
@@ -507,6 +514,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     const uint32_t e = warp - kFirstEpiWarp, q = e & 3u, side = e >> 2;
     const uint32_t sink_even = mapa_shared(smem_u32(&ctl.sink[e]), 0);
     const uint32_t sbuf = sEpi + e * kEpiBufBytes;
+    // read once: in every unit it kept the stores waiting
+    const float alphas[2] = {EPI == kEpiStore && p.q[0].alpha ? *p.q[0].alpha : 1.0f,
+                             EPI == kEpiStore && p.q[1].alpha ? *p.q[1].alpha : 1.0f};
     float row_top = 0.0f;   // kEpiDlogits: the largest |dloss| of all rows
     if constexpr (EPI == kEpiDlogits) {
       const uint32_t tt = threadIdx.x - 32u * kFirstEpiWarp;
@@ -614,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           }
         } else {
           if (o.alpha) {
-            const float alpha = *o.alpha;
+            const float alpha = un.product() == 0u ? alphas[0] : alphas[1];
 #pragma unroll
             for (uint32_t i = 0; i < 128; ++i) v[i] *= alpha;
           }

@@ -79,7 +79,8 @@ cudaError_t launch_one(const LinearLaunch& l, cudaStream_t stream) {
     LinearMaps<kMost> maps;
     for (int q = 0; q < kMost; ++q) {
       const LinearProduct& from = l.q[q < l.products ? q : 0];
-      for (int i = 0; i < 2; ++i) maps.a[q][i] = from.a[i], maps.b[q][i] = from.b[i];
+      for (int i = 0; i < 2; ++i) maps.a[q][i] = from.a[i];
+      for (int i = 0; i < 4; ++i) maps.b[q][i] = from.b[i];
       for (int i = 0; i < 3; ++i) maps.c[q][i] = from.c[i];
     }
     return launch_pdl(kernel, dim3(l.grid), kLinThreads, kLinSmemBytes, stream, maps, params_of(l));
@@ -136,7 +137,7 @@ cudaError_t prepare_few() {
       if (epi != kEpiStore && w_mn != (epi == kEpiGated)) continue;
       const cudaError_t e = with_few_kernel<DT>(w_mn, epi, [&](auto kernel) {
         uint32_t smem = 0;
-        for (uint32_t n = 16; n <= kFewRows; n *= 2)
+        for (uint32_t n = 16; n <= 2 * kFewRows; n *= 2)
           smem = few_smem_bytes(epi == kEpiGated, n) > smem ? few_smem_bytes(epi == kEpiGated, n) : smem;
         const cudaError_t err = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -162,9 +163,9 @@ cudaError_t launch_few_one(const FewLaunch& l, const FewMaps& maps, const FewPar
     attr[1].val.clusterDim.x = l.ranks;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(l.tiles * l.ranks);
+    cfg.gridDim = dim3(l.tiles * l.groups * l.ranks);
     cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = few_smem_bytes(l.epi == kEpiGated, p.n_pad);
+    cfg.dynamicSmemBytes = few_smem_bytes(l.epi == kEpiGated, p.n_pad * p.terms);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -196,16 +197,21 @@ cudaError_t launch_linear(const LinearLaunch& l, cudaStream_t stream) {
 cudaError_t launch_few(const FewLaunch& l, cudaStream_t stream) {
   FewMaps maps;
   FewParams p;
-  for (int i = 0; i < 2; ++i) maps.w[i] = l.w[i], maps.x[i] = l.x[i];
+  for (int i = 0; i < 2; ++i) maps.w[i] = l.w[i], maps.x[i] = l.x[i], maps.x_rest[i] = l.x_rest[i];
   p.rows = l.rows;
   p.n_pad = few_padded(l.rows);
   p.outs = l.outs;
   p.k_blocks = l.k_blocks;
   p.k_seg = l.k_seg;
-  p.stages = few_stages(l.epi == kEpiGated, p.n_pad);
-  p.stage_bytes = few_stage_bytes(l.epi == kEpiGated, p.n_pad);
+  p.tiles = l.tiles;
+  p.groups = l.groups;
+  p.partials = l.partials;
+  p.terms = l.terms;
+  p.stages = few_stages(l.epi == kEpiGated, p.n_pad * p.terms);
+  p.stage_bytes = few_stage_bytes(l.epi == kEpiGated, p.n_pad * p.terms);
   p.alpha = l.alpha;
   p.act = l.act;
+  p.rest = l.rest;
   p.out = l.out;
   p.g = l.g;
   p.u = l.u;
@@ -272,6 +278,7 @@ cudaError_t launch_gated_grad(const GatedGrad& l, cudaStream_t stream) {
   p.g = l.g;
   p.u = l.u;
   p.dgu = l.dgu;
+  p.rest = l.rest;
   p.ld_dh = l.ld_dh;
   p.ld_g = l.ld_g;
   p.ld_u = l.ld_u;
@@ -283,7 +290,9 @@ cudaError_t launch_gated_grad(const GatedGrad& l, cudaStream_t stream) {
                       : launch_pdl(gated_grad_kernel<1>, grid, 256, 0, stream, p);
 }
 
-cudaError_t launch_xent_join(const XentJoin& l, cudaStream_t stream) {
+namespace {
+
+XentJoinParams xent_params_of(const XentJoin& l) {
   XentJoinParams p;
   p.stats = static_cast<const float2*>(l.stats);
   p.hit = l.hit;
@@ -294,7 +303,42 @@ cudaError_t launch_xent_join(const XentJoin& l, cudaStream_t stream) {
   p.rows = l.rows;
   p.slots = l.slots;
   p.vocab = l.vocab;
-  return launch_pdl(xent_join_kernel, dim3((l.rows + 3u) / 4u), 128, 0, stream, p);
+  return p;
+}
+
+LogitParts parts_of(const XentParts& l) {
+  LogitParts p;
+  p.parts = l.parts;
+  p.stride4 = static_cast<uint64_t>(l.part_rows) * l.pitch / 4u;
+  p.splits = l.splits;
+  p.pitch4 = l.pitch / 4u;
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_xent_join(const XentJoin& l, cudaStream_t stream) {
+  return launch_pdl(xent_join_kernel, dim3((l.rows + 3u) / 4u), 128, 0, stream, xent_params_of(l));
+}
+
+cudaError_t launch_xent_rows(const XentJoin& l, const XentParts& parts, cudaStream_t stream) {
+  return launch_pdl(xent_rows_kernel, dim3(l.rows), 128, 0, stream, xent_params_of(l),
+                    parts_of(parts));
+}
+
+cudaError_t launch_xent_dlogits(const XentDlogits& l, const XentParts& parts, cudaStream_t stream) {
+  DlogitsParams p;
+  p.parts = parts_of(parts);
+  p.rows = row_weights_of(l.loss);
+  p.lse = l.lse;
+  p.out = l.out;
+  p.m = l.rows;
+  p.n = l.cols;
+  p.first_col = l.first_col;
+  p.pitch_out = l.pitch_out;
+  const dim3 grid(blocks_for(static_cast<uint64_t>(l.rows) * ((l.cols + 3u) / 4u), l.sms, 4));
+  return l.dtype == 0 ? launch_pdl(xent_dlogits_kernel<0>, grid, 256, 0, stream, p)
+                      : launch_pdl(xent_dlogits_kernel<1>, grid, 256, 0, stream, p);
 }
 
 }  // namespace tg

@@ -23,6 +23,15 @@ def rounding(ref, dtype):
     return ref.abs() * (info.eps / 2) + info.smallest_normal * info.eps / 2
 
 
+def kept(ref, dtype):
+    """Rounding of what goes into a second product over the rows [rows, n]: up to 16 rows are kept in two
+    terms, so that only the second one's rounding is left."""
+    if ref.shape[0] > 16:
+        return rounding(ref, dtype)
+    info = torch.finfo(dtype)
+    return ref.abs() * (info.eps / 2) ** 2 + info.smallest_normal * info.eps
+
+
 def product(a, b):
     """(a b, sum of magnitudes)"""
     a, b = a.to(F64), b.to(F64)
@@ -65,14 +74,14 @@ def gated(x, wg, wu, act):
 
 
 def gated_grads(dh, g, u, x, wg, wu, act):
-    """{name: (value, bound)} of dx, dwg and dwu; dg and du are rounded once on the way."""
+    """{name: (value, bound)} of dx, dwg and dwu; dg and du are rounded on the way."""
     dt = dh.dtype
     dh, g, u, x, wg, wu = (t.to(F64) for t in (dh, g, u, x, wg, wu))
     a, slope = gate(g, act)
     dg, du = dh * u * slope, dh * a
     # act' is a sum of two terms of at most 1.2 (1 + |g|): its own error is relative to those
-    eg = rounding(dg, dt) + FUNCTION * (dh * u).abs() * 1.2 * (1 + g.abs())
-    eu = rounding(du, dt) + FUNCTION * du.abs()
+    eg = kept(dg, dt) + FUNCTION * (dh * u).abs() * 1.2 * (1 + g.abs())
+    eu = kept(du, dt) + FUNCTION * du.abs()
     out = {}
     dx = dg @ wg.t() + du @ wu.t()
     s = dg.abs() @ wg.abs().t() + du.abs() @ wu.abs().t()
@@ -99,7 +108,7 @@ def xent(x, w, targets, ignore):
 
 
 def xent_grads(dloss, x, w, targets, lse, ignore):
-    """{name: (value, bound)} of dx and dw; the gradients of the logits are rounded once on the way."""
+    """{name: (value, bound)} of dx and dw; the gradients of the logits are rounded on the way."""
     dt = x.dtype
     x, w, lse = x.to(F64), w.to(F64), lse.to(F64)
     logits, s = product(x, w.t())
@@ -112,8 +121,8 @@ def xent_grads(dloss, x, w, targets, lse, ignore):
     # a logit that is off by e makes p off by e p; weights are scaled and scaled back (2^-22); fp16
     # gradients are held relative to 2^15, so their smallest step is 2^-24-15 of the largest weight
     e = p * weight.abs() * (gamma(x.shape[1]) * s * 1.01 + FUNCTION) + d.abs() * 2.0 ** -22
-    info = torch.finfo(dt)
-    e = e + d.abs() * (info.eps / 2) + weight.abs().max() * 2.0 ** -39
+    step = torch.finfo(dt).eps / 2
+    e = e + d.abs() * (step if d.shape[0] > 16 else step ** 2) + weight.abs().max() * 2.0 ** -39
     out = {}
     dx = d @ w
     out["dx"] = (dx, rounding(dx, dt) + 1.02 * (e @ w.abs() + gamma(w.shape[0]) * (d.abs() @ w.abs())))

@@ -32,10 +32,11 @@ def done():
     assert tg.tg_device_status() == 0
 
 
-# one row, one word; edges of warps, CTAs, tiles and 64-word slots; a last tile in two half units; 8 of
+# one row, one word; edges of warps, CTAs, tiles and 64-word slots; a last tile in two half units; sums of
+# logits that are split (few tiles, many columns), of an odd vocabulary too; 8 of
 # K, and several segments of 1024
 SIZES = [(1, 8, 1), (1, 64, 500), (5, 8, 63), (33, 128, 65), (128, 264, 256), (129, 136, 257),
-         (300, 2056, 1000), (257, 64, 10007), (2600, 72, 2111)]
+         (300, 2056, 1000), (155, 4432, 1961), (100, 8192, 259), (257, 64, 10007), (2600, 72, 2111)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
