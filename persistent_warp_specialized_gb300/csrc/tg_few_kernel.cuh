@@ -53,6 +53,7 @@ struct FewParams {
   float* hit;
   const float* lse;                  // kEpiDlogits
   uint64_t watchdog_ns;
+  int64_t inject_skip_phase;
 };
 
 struct __align__(8) FewCtl {
@@ -61,6 +62,7 @@ struct __align__(8) FewCtl {
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t drain;
+  uint32_t filled, filled_par;       // slots that were filled, and the parity of their last fill
   uint32_t tmem_base;
   int abort;
 };
@@ -193,41 +195,39 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      uint32_t slot = 0, parity = 0, pending = 0, pending_par = 0;
-      bool ok = true;
+      uint32_t slot = 0, parity = 0, filled = 0, filled_par = 0;
       for (uint32_t k = k_lo; k < k_hi; ++k) {
         if (!wait_or_abort(bar_consumed + 8u * slot, parity ^ 1u, abort_flag, limit,
-                           kRoleProducer)) {
-          ok = false;
+                           kRoleProducer))
           break;
-        }
-        const uint32_t bar = bar_loaded + 8u * slot;
-        mbar_arrive_expect_tx(bar, stage_bytes);
-        const uint32_t seg = k >= p.k_seg ? 1u : 0u;
-        const int32_t kx = static_cast<int32_t>(k - seg * p.k_seg) * kFewBK;
-        const uint32_t dst = sbase + slot * stage_bytes;
+        if (!injected_skip(p.inject_skip_phase, k - k_lo)) {   // else: never armed, never filled
+          const uint32_t bar = bar_loaded + 8u * slot;
+          mbar_arrive_expect_tx(bar, stage_bytes);
+          const uint32_t seg = k >= p.k_seg ? 1u : 0u;
+          const int32_t kx = static_cast<int32_t>(k - seg * p.k_seg) * kFewBK;
+          const uint32_t dst = sbase + slot * stage_bytes;
 #pragma unroll
-        for (uint32_t m = 0; m < kMats; ++m) {
-          const CUtensorMap* map = &maps.w[EPI == kEpiGated ? m : seg];
-          const uint32_t w_dst = dst + m * kFewWeightBytes;
-          if constexpr (W_MN) {
-            tma_load_2d(w_dst, map, bar, static_cast<int32_t>(n0), kx);
-            tma_load_2d(w_dst + kChunkBytes, map, bar, static_cast<int32_t>(n0) + 64, kx);
-          } else {
-            tma_load_2d(w_dst, map, bar, kx, static_cast<int32_t>(n0));
+          for (uint32_t m = 0; m < kMats; ++m) {
+            const CUtensorMap* map = &maps.w[EPI == kEpiGated ? m : seg];
+            const uint32_t w_dst = dst + m * kFewWeightBytes;
+            if constexpr (W_MN) {
+              tma_load_2d(w_dst, map, bar, static_cast<int32_t>(n0), kx);
+              tma_load_2d(w_dst + kChunkBytes, map, bar, static_cast<int32_t>(n0) + 64, kx);
+            } else {
+              tma_load_2d(w_dst, map, bar, kx, static_cast<int32_t>(n0));
+            }
           }
+          tma_load_2d(dst + kMats * kFewWeightBytes, &maps.x[seg], bar, kx, 0);
+          if (p.terms == 2u)
+            tma_load_2d(dst + kMats * kFewWeightBytes + p.n_pad * 128u, &maps.x_rest[seg], bar, kx,
+                        0);
+          filled |= 1u << slot;
+          filled_par = (filled_par & ~(1u << slot)) | (parity << slot);
         }
-        tma_load_2d(dst + kMats * kFewWeightBytes, &maps.x[seg], bar, kx, 0);
-        if (p.terms == 2u)
-          tma_load_2d(dst + kMats * kFewWeightBytes + p.n_pad * 128u, &maps.x_rest[seg], bar, kx, 0);
-        pending |= 1u << slot;
-        pending_par = (pending_par & ~(1u << slot)) | (parity << slot);
         if (++slot == p.stages) slot = 0, parity ^= 1u;
       }
-      if (!ok)   // no copy may still be under way when the CTA leaves
-        for (uint32_t s = 0; s < p.stages; ++s)
-          if ((pending >> s) & 1u)
-            wait_bounded(bar_loaded + 8u * s, (pending_par >> s) & 1u, limit, kRoleDrain);
+      ctl.filled = filled;
+      ctl.filled_par = filled_par;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -308,9 +308,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
   }
 
-  // Every load of this CTA has been multiplied, or waited for: the ring is idle.
+  // Every load of this CTA has been multiplied, so the ring is idle; after an abort they are waited for.
   tcgen05_fence_before_sync();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag)
+    for (uint32_t s = 0; s < p.stages; ++s)
+      if ((ctl.filled >> s) & 1u)
+        wait_bounded(bar_loaded + 8u * s, (ctl.filled_par >> s) & 1u, limit, kRoleDrain);
+  __syncwarp();
   if (warp == 1) {
     tcgen05_fence_after_sync();
     tmem_dealloc(tmem_base, tmem_cols);

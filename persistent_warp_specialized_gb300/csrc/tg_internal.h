@@ -190,6 +190,7 @@ struct FewLaunch {
   const float* lse;
   XentRows loss;
   uint64_t watchdog_ns;
+  int64_t inject_skip_phase;
 };
 cudaError_t launch_few(const FewLaunch& l, cudaStream_t stream);
 

@@ -187,7 +187,7 @@ int encode_operand(CUtensorMap* map, const Mat& m, bool mn, int dtype) {
 }
 
 // Enqueues a product with few rows by its plan (without the join of its groups' sums).
-int run_few(const Product& p, const Plan& w, char* partials, uint64_t watchdog_ns,
+int run_few(const Product& p, const Plan& w, char* partials, uint64_t watchdog_ns, int64_t inject,
             cudaStream_t stream) {
   tg::FewLaunch l = {};
   const uint32_t n_pad = tg::few_padded(p.M);
@@ -233,6 +233,7 @@ int run_few(const Product& p, const Plan& w, char* partials, uint64_t watchdog_n
   l.lse = p.lse;
   l.loss = p.loss;
   l.watchdog_ns = watchdog_ns ? watchdog_ns : default_watchdog_ns(l.k_blocks);
+  l.inject_skip_phase = inject;
   const cudaError_t e = tg::launch_few(l, stream);
   return e == cudaSuccess ? TG_OK : fail_cuda("product launch", e);
 }
@@ -362,7 +363,7 @@ int whole_product(const Product& p, const Plan& w, void* ws, int sms, int pairs,
                   uint64_t watchdog_ns = 0, int64_t inject = -1) {
   char* const partials[1] = {static_cast<char*>(ws)};
   if (w.few)
-    TG_TRY(run_few(p, w, partials[0], watchdog_ns, stream));
+    TG_TRY(run_few(p, w, partials[0], watchdog_ns, inject, stream));
   else
     TG_TRY(run_products(&p, &w, partials, 1, pairs, watchdog_ns, inject, stream));
   return join_products(&p, &w, partials, 1, sms, stream);
@@ -401,7 +402,7 @@ int run_grads(const Product* p, const GradPlans& o, const bool (&wanted)[2], boo
   }
   if (n == 0) return TG_OK;
   const int few = w[0].few ? 1 : 0;   // the second one never is
-  if (few) TG_TRY(run_few(q[0], w[0], at[0], 0, stream));
+  if (few) TG_TRY(run_few(q[0], w[0], at[0], 0, -1, stream));
   if (n > few) TG_TRY(run_products(q + few, w + few, at + few, n - few, pairs, 0, -1, stream));
   const int skip = wanted[0] && !join_first ? 1 : 0;
   return join_products(q + skip, w + skip, at + skip, n - skip, sms, stream);

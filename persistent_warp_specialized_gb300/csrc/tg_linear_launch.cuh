@@ -225,6 +225,7 @@ cudaError_t launch_few(const FewLaunch& l, cudaStream_t stream) {
   p.hit = l.hit;
   p.lse = l.lse;
   p.watchdog_ns = l.watchdog_ns;
+  p.inject_skip_phase = l.inject_skip_phase;
   return l.dtype == 0 ? launch_few_one<0>(l, maps, p, stream)
                       : launch_few_one<1>(l, maps, p, stream);
 }

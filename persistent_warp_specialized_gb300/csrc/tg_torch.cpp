@@ -69,7 +69,7 @@ struct Matrix {
     ld = t.stride(0);
     if (t.stride(1) != 1 && cols > 1)
       raise(PyExc_ValueError, std::string(name) + " must have unit stride along its rows");
-    if (rows <= 1)
+    if (rows <= 1 || cols == 0)
       ld = cols;
     else if (ld < cols)
       raise(PyExc_ValueError, std::string("the rows of ") + name + " overlap");
@@ -166,7 +166,9 @@ PyObject* gated_forward(PyObject* const* a) {
   const int64_t rows = x.rows, cols = x.cols, outs = wg.cols;
   const Matrix wu(a[2], "w_up", x, cols, outs);
   const int act = static_cast<int>(integer(a[3]));
-  const bool keep = PyObject_IsTrue(a[4]) == 1;
+  const int kept = PyObject_IsTrue(a[4]);
+  if (kept < 0) throw PythonError();
+  const bool keep = kept != 0;
   const Matrix h = a[5] == Py_None ? Matrix(x, rows, outs) : Matrix(a[5], "out", x, rows, outs);
   const Workspace ws(x, checked(tg_gated_fwd_workspace_bytes(rows, cols, outs)));
   void* const s = stream();

@@ -36,8 +36,10 @@ def check(got, want, what=""):
 
 # rows, cols, outs: one token; edges of warps (32), CTAs (128), pairs (256), atoms (64) and k-blocks (128);
 # K split into ranges (few tiles, long K); several segments of 1024; half-width units (77 tiles and more)
+# up to 64 rows: 16, 32 or 64 to an MMA, tiles of 128, clusters that share a tile, groups of them (17, 300, 20000)
 GRADS = [(1, 8, 8), (3, 136, 72), (33, 128, 128), (129, 264, 200), (255, 520, 1032), (257, 256, 2048),
-         (2, 2048, 4104), (300, 392, 8192), (1300, 3200, 256), (2600, 2600, 136)]
+         (2, 2048, 4104), (64, 640, 3000), (17, 304, 20000), (16, 20000, 72), (300, 392, 8192),
+         (1300, 3200, 256), (2600, 2600, 136)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -158,6 +160,7 @@ def test_gradients_asked_for_one_by_one_and_empty_sizes():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(all_, (dx, dwg, dwu)))
     # no rows: gradients of weights are zero; no columns of h: so is dx
+    assert not tg.gated_forward(torch.empty((rows, 0), dtype=dt, device="cuda"), wg[:0], wu[:0]).any()
     zero = tg.gated_backward(dh[:0], g[:0], u[:0], x[:0], wg, wu)
     assert zero[0].shape == (0, cols) and not zero[1].any() and not zero[2].any()
     none = tg.gated_backward(dh[:, :0], g[:, :0], u[:, :0], x, wg[:, :0], wu[:, :0])
@@ -228,14 +231,18 @@ def test_equal_calls_give_equal_bits_on_any_stream_and_in_graphs():
         assert all(torch.equal(a, b) for a, b in zip(first, got))
 
 
-def test_the_watchdog_stops_a_missing_fill():
-    dt, rows, cols, outs = torch.bfloat16, 512, 512, 1024
+@pytest.mark.parametrize("rows,cols,outs,ctas", [
+    (512, 512, 1024, (0, 1)),       # the even and the odd CTA of pair 0
+    (20, 512, 2048, (0, 5)),        # few rows: the first and a later CTA of a cluster
+    (20, 25000, 512, (3,))])        # and one without a cluster
+def test_the_watchdog_stops_a_missing_fill(rows, cols, outs, ctas):
+    dt = torch.bfloat16
     dy, w = normal((rows, outs), dt, 28).cuda(), normal((cols, outs), dt, 29).cuda()
     dx = torch.empty((rows, cols), dtype=dt, device="cuda")
     n = tg.tg_input_grad_workspace_bytes(rows, cols, outs)
     ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
     args = (dy, w, dx, rows, cols, outs, outs, outs, cols, "bf16", ws)
-    for cta in (0, 1):                       # the even and the odd CTA of pair 0
+    for cta in ctas:
         with pytest.raises(tg.TgError) as e:
             tg.tg_input_grad_debug(*args, watchdog_ns=20_000_000, inject_skip_phase=(cta << 32) + 1)
         assert e.value.code == tg.TG_ERR_TIMEOUT
