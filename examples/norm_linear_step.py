@@ -3,9 +3,9 @@
     python examples/norm_linear_step.py [--rows 4096 --cols 2048 --outs 2048 --steps 20 --dtype bf16]
 
 The forward pass packs x and y = layer_norm(x) to 8 bits as it goes and drops both; the backward pass
-takes the weight gradient from y's checkpoint and the norm's gradients from x's.  Products with W are
-the dense GEMM's (its B operand is row-major, so the gradient towards y multiplies by a transposed
-copy of W).  Needs a GB300 and the built library (see the README).
+takes the weight gradient from y's checkpoint and the norm's gradients from x's.  The product with W is
+the dense GEMM's; the gradient towards y reads W as it lies (input_grad).  Needs a GB300 and the built
+library (see the README).
 """
 
 import argparse
@@ -39,7 +39,7 @@ class NormLinear:
         """(dx, dgamma, dbeta, dw) from dz [rows, outs]."""
         kept_x, kept_y, mean, rstd = saved
         dw = tg.ckpt8_wgrad(kept_y, dz)
-        dy = tg.gemm(dz, self.w.t().to(self.dtype).contiguous())
+        dy = tg.input_grad(dz, self.w.to(self.dtype))
         dx, dgamma, dbeta = tg.layer_norm_backward(dy, kept_x, mean, rstd, self.gamma)
         return dx, dgamma, dbeta, dw
 
