@@ -139,6 +139,29 @@ def test_column_slices_and_guards():
     assert (gbuf == 7.0).all()
 
 
+@pytest.mark.parametrize("rows,ld", [(40, 1 << 27), (600, 1 << 23)])
+def test_results_more_than_2_to_32_values_apart(rows, ld):
+    """Row strides that take the last rows' offsets past 32 bits, of inputs and outputs."""
+    dt, cols, outs = torch.float16, 136, 72
+    wide = torch.empty((rows, ld), dtype=dt, device="cuda")
+    x, h = wide[:, 64:64 + cols], wide[:, 1024:1024 + outs]
+    x.copy_(normal((rows, cols), dt, 30))
+    wg, wu = normal((cols, outs), dt, 31, 0.1).cuda(), normal((cols, outs), dt, 32, 0.1).cuda()
+    tg.gated_forward(x, wg, wu, out=h)
+    same = tg.gated_forward(x.contiguous(), wg, wu)
+    dx = tg.input_grad(h, wg, out=wide[:, 2048:2048 + cols])
+    torch.cuda.synchronize()
+    assert torch.equal(h, same) and torch.equal(dx, tg.input_grad(same, wg))
+    n = tg.tg_gated_bwd_workspace_bytes(rows, cols, outs)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dwg, dwu = torch.empty_like(wg), torch.empty_like(wu)
+    back = wide[:, 4096:4096 + cols]
+    tg.tg_gated_bwd(h, h, h, x, wg, wu, back, dwg, dwu, rows, cols, outs, ld, ld, ld, ld, outs, outs, ld, outs,
+                    outs, "silu", "f16", ws)
+    want = tg.gated_backward(same, same, same, x.contiguous(), wg, wu)
+    assert all(torch.equal(a, b) for a, b in zip((back, dwg, dwu), want))
+
+
 def raw_bwd(dh, g, u, x, wg, wu, dx, dwg, dwu, act="silu"):
     rows, outs, cols = dh.shape[0], dh.shape[1], wg.shape[0]
     n = tg.tg_gated_bwd_workspace_bytes(rows, cols, outs)

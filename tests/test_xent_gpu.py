@@ -256,3 +256,42 @@ def test_only_what_is_asked_for():
     with pytest.raises(tg.TgError, match="workspace"):
         tg.tg_xent_bwd(dloss, x, w, targets, lse, dx, None, rows, cols, vocab, cols, cols, cols, cols,
                        IGNORE, "f16", ws, workspace_bytes=n - 1)
+
+
+@pytest.mark.parametrize("rows", [3, 70])
+def test_a_vocabulary_of_more_than_2_to_31_values(rows):
+    """Offsets into w and dw past 31 and 32 bits: 270000 words of 8192 columns (4.4 GB), all of them zero but
+    some at the end."""
+    cols, vocab, last = 8192, 270000, 7
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn((rows, cols), generator=gen, device="cuda").bfloat16()
+    w = torch.zeros((vocab, cols), dtype=torch.bfloat16, device="cuda")
+    w[-last:] = torch.randn((last, cols), generator=gen, device="cuda") * 0.1
+    targets = torch.randint(vocab - last, vocab, (rows,), generator=gen, device="cuda")
+    targets[1] = 5
+    loss, lse = tg.linear_cross_entropy(x, w, targets)
+    logits = x.double() @ w[-last:].double().t()
+    top = logits.max(dim=1).values.clamp(min=0)
+    want = top + torch.log((vocab - last) * torch.exp(-top) + torch.exp(logits - top[:, None]).sum(dim=1))
+    hit = torch.zeros(rows, dtype=torch.float64, device="cuda")
+    end = targets >= vocab - last
+    hit[end] = logits[end].gather(1, (targets[end] - (vocab - last))[:, None])[:, 0]
+    # segments of 1024 products: off by at most 2^-23 of the magnitudes each; as fused_ref.xent otherwise
+    off = ref.gamma(cols) * (x.double().abs() @ w[-last:].double().abs().t()).max() + 2 * ref.FUNCTION \
+        + 2.0 ** -21 * want.abs().max()
+    assert (lse - want).abs().max() <= off and (loss - (want - hit)).abs().max() <= 2 * off
+    dloss = torch.ones(rows, device="cuda")
+    dx, dw = tg.linear_cross_entropy_backward(dloss, x, w, targets, lse)
+    done()
+    p = torch.exp(logits - want[:, None])
+    p[end] = p[end].scatter_add(1, (targets[end] - (vocab - last))[:, None],
+                                -torch.ones_like(hit[end])[:, None])
+    # p off by what lse and a logit are (2 off) and one rounding; the results by one more
+    rel = 2.0 ** -8 + 3 * off
+    assert (dx.double() - p @ w[-last:].double()).norm() <= 2 * rel * (p.abs() @ w[-last:].double().abs()).norm()
+    got = dw[-last:].double()
+    assert (got - p.t() @ x.double()).norm() <= 2 * rel * (p.abs().t() @ x.double().abs()).norm()
+    d5 = -x[1].double() + torch.exp(-want) @ x.double()          # word 5: row 1's target
+    assert (dw[5].double() - d5).norm() <= 2 * rel * d5.norm()
+    zero = torch.exp(-want) @ x.double()                         # a word that is nobody's target
+    assert (dw[vocab - last - 1].double() - zero).norm() <= 4 * rel * (torch.exp(-want) @ x.double().abs()).norm()
