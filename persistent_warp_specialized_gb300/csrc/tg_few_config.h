@@ -8,13 +8,18 @@
 namespace tg {
 
 constexpr int kFewRows = 64;             // rows at most
-// Rows up to which gradients that are rounded on the way come in two terms: past 16 rows of at least 128
-// values their errors average out to within 2 % of what they are in the mean.
-constexpr int kTwoTermRows = 16;
+// Rows up to which gradients that are rounded on the way come in two terms (past 8 rows of at least 128
+// values their errors average out), and up to which gradients towards weights are tg_outer_kernel.cuh's:
+// measured (bf16, us, gated backward 1200 x 5896 / 2232 x 2592): 8 rows 22.9 / 20.4, 17 rows on the tensor
+// core 24.2 / 20.9, 16 rows without it 38 / 35.
+constexpr int kTwoTermRows = 8;
 constexpr int kFewM = 128;               // weights' rows or columns (results) in a tile
 constexpr int kFewBK = kKAtom;           // 64 of K in a stage
-// A sum is cut into segments of 1024 products, as tg_linear_config.h explains.
-constexpr uint32_t kFewSegment = 16;
+// A sum is cut into segments, as tg_linear_config.h explains: of 1024 products, of logits 128.  Where a
+// single row's target is nearly certain its gradient is what 1 - p leaves, and a logit's error counts
+// 1 / (1 - p) times (one fp16 row, p = 0.998: gradients 6.1e-4 off with 1024, plain fp32 2.5e-4).
+template <int EPI>
+constexpr uint32_t kFewSegment = EPI == kEpiStats || EPI == kEpiDlogits ? 2u : 16u;
 // warp 0 loads, warp 1 issues the MMAs and owns the TMEM, warps 2..5 are the epilogue
 constexpr uint32_t kFewThreads = 192;
 constexpr int kFewEpiThreads = 128;

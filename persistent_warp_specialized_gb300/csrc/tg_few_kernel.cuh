@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __shared__ FewCtl ctl;
   constexpr uint32_t kMats = EPI == kEpiGated ? 2u : 1u;
   constexpr uint32_t kChunkBytes = kFewBK * 128u;          // W_MN: 64 rows of 64 columns
+  constexpr uint32_t kSegment = kFewSegment<EPI>;
 
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t g_lo = min(group * per_group, p.k_blocks), g_hi = min(g_lo + per_group, p.k_blocks);
   const uint32_t per_rank = (per_group + ranks - 1u) / ranks;
   const uint32_t k_lo = min(g_lo + rank * per_rank, g_hi), k_hi = min(k_lo + per_rank, g_hi);
-  const uint32_t segments = (k_hi - k_lo + kFewSegment - 1u) / kFewSegment;
+  const uint32_t segments = (k_hi - k_lo + kSegment - 1u) / kSegment;
 
   const uint32_t bar_loaded = smem_u32(&ctl.loaded[0]);
   const uint32_t bar_consumed = smem_u32(&ctl.consumed[0]);
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       }
       __syncwarp();
       if (++slot == p.stages) slot = 0, parity ^= 1u;
-      if (++in_seg == kFewSegment || k + 1u == k_hi) {
+      if (++in_seg == kSegment || k + 1u == k_hi) {
         if (leader) umma_commit(bar_tmem_full + 8u * acc);
         __syncwarp();
         in_seg = 0;

@@ -194,6 +194,19 @@ struct FewLaunch {
 };
 cudaError_t launch_few(const FewLaunch& l, cudaStream_t stream);
 
+// out[i] [m, n] = alpha (null: 1) a^T b[i] of at most 8 rows, a [rows, m] and b[i] [rows, n] in one or two
+// terms (tg_outer_kernel.cuh); ``results`` of them, 1 or 2.
+struct OuterLaunch {
+  const void *a, *a_rest, *b[2], *b_rest[2];
+  void* out[2];
+  int64_t ld_a, ld_b, ld_out[2];
+  uint32_t rows, m, n;
+  int results;
+  const float* alpha;
+  int dtype, sms;
+};
+cudaError_t launch_outer(const OuterLaunch& l, cudaStream_t stream);
+
 // out [rows, cols] = alpha (null: 1) times the sum over splits of partials [splits][part_rows][cols];
 // up to three at once
 struct LinearJoin {

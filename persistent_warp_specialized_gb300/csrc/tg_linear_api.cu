@@ -27,14 +27,14 @@ struct Mat {
 
 // D[M, N] = A B, before its plan.  Two matrices may stand in an operand's place (tg_linear_kernel.cuh):
 // segs_n: N columns each of b[0], b[1] to c[0], c[1]; segs_k: K values each of a[0], b[0 .. 1] and of
-// a[1], b[2 .. 3].  a_rest: for few rows, what rounding a[i] left.
+// a[1], b[2 .. 3].  a_rest, b_rest: with few rows, what rounding a[i] and b[i] left.
 struct Product {
   int epi = tg::kEpiStore;
   int dtype = 0;
   bool a_mn = false, b_mn = false;
   int64_t M = 0, N = 0, K = 0;
   int segs_n = 1, segs_k = 1;
-  Mat a[2], b[4], c[3], a_rest[2];
+  Mat a[2], b[4], c[3], a_rest[2], b_rest[2];
   bool two_terms = false;
   const float* alpha = nullptr;
   // kEpiStore over several launches: 0 alone, 1 the first, 2 a later one, whose fp32 sums are added to
@@ -52,6 +52,7 @@ struct Product {
 struct Plan {
   bool few;                 // the kernel for few rows takes it: splits are its groups
   uint32_t ranks;           // of few rows: CTAs that share a tile
+  bool outer;               // tg_outer_kernel.cuh takes it, and nothing below counts
   uint32_t m_tiles, n_tiles, n_seg, k_blocks, k_seg, splits, blocks_per_split;
   uint32_t units;           // tiles
   uint32_t part_rows, part_pitch;   // rows of one split's sums, and values from one to the next
@@ -73,7 +74,7 @@ bool few_rows(const Product& p, bool sums) {
 // The plan with K in about ``splits`` ranges.  sums: results go to partial sums in any case.
 Plan plan_of(const Product& p, uint32_t splits, bool sums = false) {
   Plan w;
-  w.few = false;
+  w.few = w.outer = false;
   w.ranks = 1;
   w.m_tiles = static_cast<uint32_t>(ceil_div(p.M, tg::kPairBM));
   w.n_seg = static_cast<uint32_t>(ceil_div(p.N, p.epi == tg::kEpiGated ? tg::kGatedTileN : tg::kBN));
@@ -391,13 +392,42 @@ struct GradPlans {
   GradPlans(const Product* p, int pairs, bool sums = false) {
     if (few_rows(p[0], sums)) {
       w[0] = plan_product(p[0], pairs);
-      plan_products(&p[1], &w[1], 1, pairs);
+      if (p[1].K <= tg::kTwoTermRows) {
+        w[1] = plan_of(p[1], 1);
+        w[1].outer = true;
+      } else {
+        plan_products(&p[1], &w[1], 1, pairs);
+      }
     } else {
       plan_products(p, w, 2, pairs, sums);
     }
     for (int i = 0; i < 2; ++i) bytes[i] = partials_of(p[i], w[i]);
   }
 };
+
+// Enqueues a gradient towards weights from at most 8 rows: p.K of them, a_mn and b_mn.
+int run_outer(const Product& p, int sms, cudaStream_t stream) {
+  tg::OuterLaunch l = {};
+  l.a = p.a[0].p;
+  l.a_rest = p.a_rest[0].p;
+  l.ld_a = p.a[0].ld;
+  l.ld_b = p.b[0].ld;
+  l.results = p.segs_n;
+  for (int i = 0; i < p.segs_n; ++i) {
+    l.b[i] = p.b[i].p;
+    l.b_rest[i] = p.b_rest[i].p;
+    l.out[i] = const_cast<void*>(p.c[i].p);
+    l.ld_out[i] = p.c[i].ld;
+  }
+  l.rows = static_cast<uint32_t>(p.K);
+  l.m = static_cast<uint32_t>(p.M);
+  l.n = static_cast<uint32_t>(p.N);
+  l.alpha = p.alpha;
+  l.dtype = p.dtype;
+  l.sms = sms;
+  const cudaError_t e = tg::launch_outer(l, stream);
+  return e == cudaSuccess ? TG_OK : fail_cuda("product launch", e);
+}
 
 // Enqueues what is asked for of the two.  Their plans hold for both together and for either.
 int run_grads(const Product* p, const GradPlans& o, const bool (&wanted)[2], bool join_first,
@@ -415,7 +445,10 @@ int run_grads(const Product* p, const GradPlans& o, const bool (&wanted)[2], boo
   if (n == 0) return TG_OK;
   const int few = w[0].few ? 1 : 0;   // the second one never is
   if (few) TG_TRY(run_few(q[0], w[0], at[0], 0, -1, stream));
-  if (n > few) TG_TRY(run_products(q + few, w + few, at + few, n - few, pairs, 0, -1, stream));
+  if (n > few && w[n - 1].outer)
+    TG_TRY(run_outer(q[n - 1], sms, stream));
+  else if (n > few)
+    TG_TRY(run_products(q + few, w + few, at + few, n - few, pairs, 0, -1, stream));
   const int skip = wanted[0] && !join_first ? 1 : 0;
   return join_products(q + skip, w + skip, at + skip, n - skip, sms, stream);
 }
@@ -580,8 +613,7 @@ GatedPlan gated_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& h, i
 }
 
 // Gradients that are rounded to 16 bits on the way to both products: with few rows their errors do not
-// average out, so they come in two terms (tg_few_kernel.cuh), the second one as a second segment of K
-// in the product over rows.
+// average out, so they come in two terms (tg_few_kernel.cuh, tg_outer_kernel.cuh).
 bool two_terms(int64_t rows) { return rows <= tg::kTwoTermRows; }
 
 struct GatedBwd {
@@ -618,15 +650,12 @@ GatedBwd gated_bwd_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& d
   p[1].N = outs;
   p[1].K = rows;
   p[1].segs_n = 2;
-  p[1].segs_k = two ? 2 : 1;
+  p[1].a[0] = x;
   p[1].c[0] = dwg;
   p[1].c[1] = dwu;
   for (int i = 0; i < 2; ++i) {
-    p[0].a[i] = part(0, i);
-    p[0].a_rest[i] = part(1, i);
-    p[1].a[i] = x;
-    p[1].b[i] = part(0, i);
-    p[1].b[2 + i] = part(1, i);
+    p[0].a[i] = p[1].b[i] = part(0, i);
+    if (two) p[0].a_rest[i] = p[1].b_rest[i] = part(1, i);
   }
   GatedBwd o = {{p[0], p[1]}, GradPlans(p, pairs), dgu_bytes, 0};
   o.total = (two ? 2 : 1) * dgu_bytes + o.plans.bytes[0] + o.plans.bytes[1];
@@ -735,8 +764,7 @@ Product xent_dx_product(const Mat& dl, const Mat* rest, const Mat& w, int64_t fi
 Product xent_dw_product(const Mat& dl, const Mat* rest, const Mat& x, const Mat& dw, int64_t first,
                         int dtype) {
   Product p;
-  p.segs_k = rest ? 2 : 1;
-  if (rest) p.a[1] = *rest, p.b[2] = x;
+  if (rest) p.a_rest[0] = *rest;
   p.dtype = dtype;
   p.a_mn = p.b_mn = true;
   p.M = dl.cols;

@@ -7,6 +7,7 @@
 #include "tg_gated_kernel.cuh"
 #include "tg_internal.h"
 #include "tg_launch.cuh"
+#include "tg_outer_kernel.cuh"
 #include "tg_linear_kernel.cuh"
 #include "tg_xent_kernel.cuh"
 
@@ -228,6 +229,56 @@ cudaError_t launch_few(const FewLaunch& l, cudaStream_t stream) {
   p.inject_skip_phase = l.inject_skip_phase;
   return l.dtype == 0 ? launch_few_one<0>(l, maps, p, stream)
                       : launch_few_one<1>(l, maps, p, stream);
+}
+
+namespace {
+
+template <int DT>
+cudaError_t launch_outer_one(const OuterParams& p, dim3 grid, cudaStream_t stream) {
+  auto run = [&](auto kernel) { return launch_pdl(kernel, grid, kOuterThreads, 0, stream, p); };
+  if (p.rows <= 1) return run(outer_kernel<DT, 1>);
+  if (p.rows <= 2) return run(outer_kernel<DT, 2>);
+  if (p.rows <= 4) return run(outer_kernel<DT, 4>);
+  return run(outer_kernel<DT, 8>);
+}
+
+}  // namespace
+
+cudaError_t launch_outer(const OuterLaunch& l, cudaStream_t stream) {
+  OuterParams p;
+  p.a = l.a;
+  p.a_rest = l.a_rest;
+  for (int i = 0; i < 2; ++i) {
+    p.b[i] = l.b[i];
+    p.b_rest[i] = l.b_rest[i];
+    p.out[i] = l.out[i];
+    p.ld_out[i] = l.ld_out[i];
+  }
+  p.ld_a = l.ld_a;
+  p.ld_b = l.ld_b;
+  p.rows = l.rows;
+  p.m = l.m;
+  p.n = l.n;
+  p.alpha = l.alpha;
+  // as long a walk down m as leaves four blocks an SM: a block reads its columns of b once
+  const uint64_t across = static_cast<uint64_t>((l.n + kOuterCols - 1) / kOuterCols) * l.results;
+  p.block_m = kOuterMostM;
+  while (p.block_m > 16u && across * ((l.m + p.block_m - 1) / p.block_m) < 4ull * l.sms) p.block_m /= 2;
+  // blockIdx.y goes up to 65535: the rows of m that one launch takes
+  const uint32_t most = p.block_m * 65535u;
+  for (uint32_t m0 = 0; m0 < l.m; m0 += most) {
+    OuterParams part = p;
+    part.m = l.m - m0 < most ? l.m - m0 : most;
+    part.a = static_cast<const char*>(p.a) + 2ull * m0;
+    if (p.a_rest != nullptr) part.a_rest = static_cast<const char*>(p.a_rest) + 2ull * m0;
+    for (int i = 0; i < l.results; ++i)
+      part.out[i] = static_cast<char*>(p.out[i]) + 2ll * m0 * p.ld_out[i];
+    const dim3 grid((l.n + kOuterCols - 1) / kOuterCols, (part.m + p.block_m - 1) / p.block_m, l.results);
+    const cudaError_t e = l.dtype == 0 ? launch_outer_one<0>(part, grid, stream)
+                                       : launch_outer_one<1>(part, grid, stream);
+    if (e != cudaSuccess || l.m - m0 <= most) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_linear_join(const LinearJoin* joins, int count, int dtype, int sms,

@@ -26,12 +26,15 @@ __device__ __forceinline__ void join_stats(float& top, float& sum, float m, floa
   top = t;
 }
 
+// lse = M + log sum.  The loss is (M - t) + log sum and not lse - t: where the target is the likeliest word
+// its first part is 0, and the loss as exact as the logarithm, not as lse's last bit (2^-20 at 20).
 __device__ __forceinline__ void write_loss(const XentJoinParams& p, uint64_t row, int64_t target,
-                                           float lse, float hit) {
+                                           float top, float sum, float hit) {
   const TargetKind kind = target_kind(target, p.ignore, p.vocab);
-  p.lse[row] = lse;
+  const float rest = logf(sum);
+  p.lse[row] = top + rest;
   p.loss[row] = kind == kTargetIgnored ? 0.0f
-                : kind == kTargetValid ? lse - hit
+                : kind == kTargetValid ? (top - hit) + rest
                                        : __int_as_float(0x7fffffff);
 }
 
@@ -59,7 +62,7 @@ __global__ void __launch_bounds__(128) xent_join_kernel(const XentJoinParams p) 
     const float m = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
     join_stats(top, sum, m, s);
   }
-  if (lane == 0) write_loss(p, row, target, top + logf(sum), p.hit[row]);
+  if (lane == 0) write_loss(p, row, target, top, sum, p.hit[row]);
 }
 
 // Logits of split sums: parts [splits][part_rows][pitch] (pitch a multiple of 4).
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(128) xent_rows_kernel(const XentJoinParams p, 
   if (threadIdx.x != 0) return;
 #pragma unroll
   for (uint32_t w = 1; w < 4; ++w) join_stats(top, sum, joint[w].x, joint[w].y);
-  write_loss(p, row, target, top + logf(sum), hit);
+  write_loss(p, row, target, top, sum, hit);
 }
 
 struct DlogitsParams {

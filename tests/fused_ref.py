@@ -24,9 +24,9 @@ def rounding(ref, dtype):
 
 
 def kept(ref, dtype):
-    """Rounding of what goes into a second product over the rows [rows, n]: up to 16 rows are kept in two
+    """Rounding of what goes into a second product over the rows [rows, n]: up to 8 rows are kept in two
     terms, so that only the second one's rounding is left."""
-    if ref.shape[0] > 16:
+    if ref.shape[0] > 8:
         return rounding(ref, dtype)
     info = torch.finfo(dtype)
     return ref.abs() * (info.eps / 2) ** 2 + info.smallest_normal * info.eps
@@ -122,7 +122,7 @@ def xent_grads(dloss, x, w, targets, lse, ignore):
     # gradients are held relative to 2^15, so their smallest step is 2^-24-15 of the largest weight
     e = p * weight.abs() * (gamma(x.shape[1]) * s * 1.01 + FUNCTION) + d.abs() * 2.0 ** -22
     step = torch.finfo(dt).eps / 2
-    e = e + d.abs() * (step if d.shape[0] > 16 else step ** 2) + weight.abs().max() * 2.0 ** -39
+    e = e + d.abs() * (step if d.shape[0] > 8 else step ** 2) + weight.abs().max() * 2.0 ** -39
     out = {}
     dx = d @ w
     out["dx"] = (dx, rounding(dx, dt) + 1.02 * (e @ w.abs() + gamma(w.shape[0]) * (d.abs() @ w.abs())))

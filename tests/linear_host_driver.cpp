@@ -215,6 +215,19 @@ cudaError_t launch_few(const FewLaunch& l, cudaStream_t) {
   return fine();
 }
 
+cudaError_t launch_outer(const OuterLaunch& l, cudaStream_t) {
+  if (l.rows < 1 || l.rows > uint32_t(kTwoTermRows) || l.n % 8 || l.ld_b % 8) wrong("outer product");
+  const uint64_t a = 2 * ((l.rows - 1) * l.ld_a + l.m), b = 2 * ((l.rows - 1) * l.ld_b + l.n);
+  inside(l.a, a, "outer a");
+  if (l.a_rest) inside(l.a_rest, a, "outer a's rest");
+  for (int i = 0; i < l.results; ++i) {
+    inside(l.b[i], b, "outer b");
+    if (l.b_rest[i]) inside(l.b_rest[i], b, "outer b's rest");
+    inside(l.out[i], 2 * ((uint64_t(l.m) - 1) * l.ld_out[i] + l.n), "outer results");
+  }
+  return fine();
+}
+
 cudaError_t launch_linear_join(const LinearJoin* j, int n, int, int, cudaStream_t) {
   if (n < 1 || n > 3) wrong("joins");
   for (int i = 0; i < n; ++i) {

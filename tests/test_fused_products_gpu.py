@@ -62,7 +62,8 @@ def test_input_grad_of_integers_is_exact(rows, cols, outs, dtype):
 
 
 # rows, cols, outs of the gated projections; outs 128 wide tiles, half units 64
-LAYERS = [(1, 8, 8), (1, 1024, 2048), (2, 136, 72), (5, 2056, 1000), (33, 128, 128), (129, 264, 200),
+LAYERS = [(1, 8, 8), (1, 1024, 2048), (2, 136, 72), (5, 2056, 1000), (8, 600, 264), (9, 520, 304), (33, 128, 128),
+          (64, 344, 200), (129, 264, 200),
           (200, 1024, 640), (257, 72, 1032), (1300, 136, 2000), (300, 4104, 392)]
 
 
