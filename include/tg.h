@@ -480,7 +480,8 @@ int tg_input_grad(const void* dY_dev, const void* W_dev, void* dX_dev, int64_t r
 int64_t tg_input_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t outs);
 
 /* tg_input_grad, synchronously, with the watchdog limit and the injected missing fill of
-   tg_gemm_persistent_debug (its CTA-pair form; with up to 64 rows any CTA's). */
+   tg_gemm_persistent_debug (its CTA-pair form; with up to 64 rows any CTA's, which then fills
+   no later phase either). */
 int tg_input_grad_debug(const void* dY_dev, const void* W_dev, void* dX_dev, int64_t rows,
                         int64_t cols, int64_t outs, int64_t ld_dy, int64_t ld_w, int64_t ld_dx,
                         int dtype, void* workspace_dev, int64_t workspace_bytes, void* stream,
