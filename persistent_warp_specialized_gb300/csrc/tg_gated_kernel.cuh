@@ -22,14 +22,15 @@ __device__ __forceinline__ float2 unpack_in(uint32_t w) {
 struct GatedGradParams {
   const void *dh, *g, *u;
   void* dgu;                       // [rows][2 vecs x 8]: dg, then du
-  void* rest;                      // null, or the same of what rounding them left
+  void* rest;                      // TWO: the same of what rounding them left
   int64_t ld_dh, ld_g, ld_u;       // elements
   uint32_t rows, vecs;             // vectors of 8 values in a row
   uint32_t act;
 };
 
-// A block walks vectors of its rows: blockIdx.y strides over rows, blockIdx.x over a row's vectors.
-template <int DT>
+// A thread takes every so many'th vector of the matrix, two at a time.
+// TWO: in two terms.
+template <int DT, bool TWO>
 __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -45,8 +46,11 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p
     uint32_t dgw[4], duw[4], dg_rest[4], du_rest[4];
     auto pack = [](float x, float y, uint32_t& rest) {
       const uint32_t w = pack_out<DT>(__float_as_uint(x), __float_as_uint(y));
-      const float2 back = unpack_in<DT>(w);
-      rest = pack_out<DT>(__float_as_uint(left_over(x, back.x)), __float_as_uint(left_over(y, back.y)));
+      if constexpr (TWO) {
+        const float2 back = unpack_in<DT>(w);
+        rest = pack_out<DT>(__float_as_uint(left_over(x, back.x)),
+                            __float_as_uint(left_over(y, back.y)));
+      }
       return w;
     };
 #pragma unroll
@@ -62,7 +66,7 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p
     char* to = static_cast<char*>(p.dgu) + at;
     st_global_v4(to, dgw[0], dgw[1], dgw[2], dgw[3]);
     st_global_v4(to + next, duw[0], duw[1], duw[2], duw[3]);
-    if (p.rest != nullptr) {
+    if constexpr (TWO) {
       to = static_cast<char*>(p.rest) + at;
       st_global_v4(to, dg_rest[0], dg_rest[1], dg_rest[2], dg_rest[3]);
       st_global_v4(to + next, du_rest[0], du_rest[1], du_rest[2], du_rest[3]);

@@ -338,8 +338,10 @@ cudaError_t launch_gated_grad(const GatedGrad& l, cudaStream_t stream) {
   p.vecs = static_cast<uint32_t>(l.outs / 8);
   p.act = l.act;
   const dim3 grid(blocks_for(static_cast<uint64_t>(p.rows) * p.vecs, l.sms, 8));
-  return l.dtype == 0 ? launch_pdl(gated_grad_kernel<0>, grid, 256, 0, stream, p)
-                      : launch_pdl(gated_grad_kernel<1>, grid, 256, 0, stream, p);
+  auto run = [&](auto kernel) { return launch_pdl(kernel, grid, 256, 0, stream, p); };
+  if (l.rest != nullptr)
+    return l.dtype == 0 ? run(gated_grad_kernel<0, true>) : run(gated_grad_kernel<1, true>);
+  return l.dtype == 0 ? run(gated_grad_kernel<0, false>) : run(gated_grad_kernel<1, false>);
 }
 
 namespace {
