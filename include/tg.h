@@ -503,7 +503,8 @@ int64_t tg_gated_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t outs);
 /*
  * tg_gated_bwd -- the gradients of tg_gated_fwd from dh, with g and u as it kept them:
  *     dg = dh u act'(g),  du = dh act(g);   dx = dg Wg^T + du Wu^T,  dWg = x^T dg,  dWu = x^T du
- *   dg and du are rounded to ``dtype`` before the products.  dx_dev may be NULL (Wg and Wu are then
+ *   dg and du are rounded to ``dtype`` before the products (up to 8 rows: kept in two such terms, whose
+ *   sum is as good as fp32).  dx_dev may be NULL (Wg and Wu are then
  *   not read), or dwg_dev and dwu_dev (x is then not read).  cols == 0: nothing is done.  rows == 0 or
  *   outs == 0: what is asked for is zero-filled.
  */
@@ -535,9 +536,9 @@ int64_t tg_xent_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab);
  *   dloss_dev [rows] fp32: the gradient of each row's loss (1 / n in every row for the mean of n
  *   losses); lse_dev: what tg_xent_fwd wrote; dx_dev [rows, cols], dw_dev [vocab, cols], either may be
  *   NULL.  The logits are computed again, a piece of the vocabulary at a time (at most 256 MiB of
- *   their gradients, or 2048 words' where that is more); dl is rounded to ``dtype`` before the products
- *   (scaled by a power of two in fp16, so that small probabilities keep their bits).  Rows with a wrong
- *   target give NaN.  An ignored row's x adds zero times itself to dW.  rows == 0: dW is zero-filled.
+ *   their gradients, or 2048 words' where that is more); dl is rounded to ``dtype`` before the products,
+ *   relative to the largest |dloss| (in fp16 times 2^15, so that small probabilities keep their bits;
+ *   up to 8 rows: in two terms).  Rows with a wrong target give NaN.  An ignored row's x adds zero times itself to dW.  rows == 0: dW is zero-filled.
  */
 int tg_xent_bwd(const float* dloss_dev, const void* x_dev, const void* w_dev,
                 const int64_t* targets_dev, const float* lse_dev, void* dx_dev, void* dw_dev,

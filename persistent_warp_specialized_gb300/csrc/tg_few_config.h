@@ -20,6 +20,10 @@ constexpr int kFewBK = kKAtom;           // 64 of K in a stage
 // 1 / (1 - p) times (one fp16 row, p = 0.998: gradients 6.1e-4 off with 1024, plain fp32 2.5e-4).
 template <int EPI>
 constexpr uint32_t kFewSegment = EPI == kEpiStats || EPI == kEpiDlogits ? 2u : 16u;
+// Logits of up to 32 rows: an accumulator still has 64 columns, which are 2 or 4 (16 rows) parts that the
+// steps of 16 products take turns with, so a part is added to 3 times or once before it is read out.
+template <int EPI>
+constexpr bool kFewParted = EPI == kEpiStats || EPI == kEpiDlogits;
 // warp 0 loads, warp 1 issues the MMAs and owns the TMEM, warps 2..5 are the epilogue
 constexpr uint32_t kFewThreads = 192;
 constexpr int kFewEpiThreads = 128;

@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   constexpr uint32_t kMats = EPI == kEpiGated ? 2u : 1u;
   constexpr uint32_t kChunkBytes = kFewBK * 128u;          // W_MN: 64 rows of 64 columns
   constexpr uint32_t kSegment = kFewSegment<EPI>;
+  constexpr bool kParted = kFewParted<EPI>;
 
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
@@ -131,7 +132,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t bar_tmem_full = smem_u32(&ctl.tmem_full[0]);
   const uint32_t bar_tmem_empty = smem_u32(&ctl.tmem_empty[0]);
   const uint32_t bar_drain = smem_u32(&ctl.drain);
-  const uint32_t tmem_cols = 2u * kMats * p.n_pad;         // two accumulators; 32 .. 256
+  const uint32_t acc_cols = kParted ? kFewRows : kMats * p.n_pad;
+  const uint32_t tmem_cols = 2u * acc_cols;                // two accumulators; 32 .. 256
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kFewMaxStages; ++s) {
@@ -251,11 +253,16 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const uint64_t at = slot * (stage_bytes >> 4);
 #pragma unroll
         for (uint32_t m = 0; m < kMats; ++m) {
-          const uint32_t d = tmem_base + (acc * kMats + m) * p.n_pad;
+          const uint32_t d = tmem_base + acc * acc_cols + m * p.n_pad;
 #pragma unroll
-          for (uint32_t kk = 0; kk < kFewBK / kUmmaK; ++kk)
-            umma_f16(d, a0 + at + m * (kFewWeightBytes >> 4) + (W_MN ? kk * 128u : kk * 2u),
-                     b0 + at + kk * 2u, idesc, in_seg != 0u || kk != 0u ? 1u : 0u);
+          for (uint32_t kk = 0; kk < kFewBK / kUmmaK; ++kk) {
+            // parted: the steps take turns with the accumulator's parts
+            const uint32_t part = kParted ? kk * p.n_pad : 0u;
+            const bool add = in_seg != 0u || (kParted ? part >= kFewRows : kk != 0u);
+            umma_f16(d + part % kFewRows,
+                     a0 + at + m * (kFewWeightBytes >> 4) + (W_MN ? kk * 128u : kk * 2u),
+                     b0 + at + kk * 2u, idesc, add ? 1u : 0u);
+          }
           if (EPI == kEpiStore && p.terms == 2u) {
 #pragma unroll
             for (uint32_t kk = 0; kk < kFewBK / kUmmaK; ++kk)
@@ -293,16 +300,25 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                                      kRoleEpilogue);
       if (!__all_sync(0xffffffffu, got)) break;
       tcgen05_fence_after_sync();
-      const uint32_t t_row = tmem_base + ((q * 32u) << 16) + acc * kMats * p.n_pad;
+      const uint32_t t_row = tmem_base + ((q * 32u) << 16) + acc * acc_cols;
 #pragma unroll
       for (uint32_t m = 0; m < kMats; ++m)
 #pragma unroll
         for (uint32_t j = 0; j < kFewRows / 16; ++j) {
-          if (16u * j >= p.n_pad) break;
+          if (!kParted && 16u * j >= p.n_pad) break;
           uint32_t t[16];
           tmem_ld_32x32b_x16(t_row + m * p.n_pad + 16u * j, t);
+          auto add_to = [&](uint32_t r) {   // rows r .. r + 15
 #pragma unroll
-          for (uint32_t i = 0; i < 16; ++i) v[m][16 * j + i] += __uint_as_float(t[i]);
+            for (uint32_t i = 0; i < 16; ++i) v[m][r + i] += __uint_as_float(t[i]);
+          };
+          if (!kParted || p.n_pad == kFewRows) {
+            add_to(16 * j);
+          } else if (p.n_pad == 32u) {
+            add_to(16 * (j & 1u));
+          } else {
+            add_to(0);
+          }
         }
       tcgen05_fence_before_sync();
       __syncwarp();

@@ -46,8 +46,7 @@ struct WgradUnits {
   uint32_t u, w, step, units, per_split, kps, k_blocks;
   uint32_t split, k_lo, k_hi;
 
-  template <typename Params>
-  __device__ WgradUnits(const Params& p, uint32_t worker, uint32_t workers)
+  __device__ WgradUnits(const WgradParams& p, uint32_t worker, uint32_t workers)
       : sched(p.m_blocks, p.n_blocks, p.group, workers, p.split_from, p.total_units,
               p.column_major),
         u(worker), w(0), step(workers), units(p.total_units * p.splits), per_split(p.total_units),

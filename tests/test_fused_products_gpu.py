@@ -35,8 +35,8 @@ def check(got, want, what=""):
 
 
 # rows, cols, outs: one token; edges of warps (32), CTAs (128), pairs (256), atoms (64) and k-blocks (128);
-# K split into ranges (few tiles, long K); several segments of 1024; half-width units (77 tiles and more)
-# up to 64 rows: 16, 32 or 64 to an MMA, tiles of 128, clusters that share a tile, groups of them (17, 300, 20000)
+# K split into ranges (few tiles, long K); several segments of 1024; half-width units (77 tiles and more).
+# Up to 64 rows: 16, 32 or 64 to an MMA, tiles of 128, clusters that share a tile, groups of them (17, 300, 20000)
 GRADS = [(1, 8, 8), (3, 136, 72), (33, 128, 128), (129, 264, 200), (255, 520, 1032), (257, 256, 2048),
          (2, 2048, 4104), (64, 640, 3000), (17, 304, 20000), (16, 20000, 72), (300, 392, 8192),
          (1300, 3200, 256), (2600, 2600, 136)]
