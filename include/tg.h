@@ -503,10 +503,9 @@ int64_t tg_gated_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t outs);
 /*
  * tg_gated_bwd -- the gradients of tg_gated_fwd from dh, with g and u as it kept them:
  *     dg = dh u act'(g),  du = dh act(g);   dx = dg Wg^T + du Wu^T,  dWg = x^T dg,  dWu = x^T du
- *   dg and du are rounded to ``dtype`` before the products (up to 8 rows: kept in two such terms, whose
- *   sum is as good as fp32).  dx_dev may be NULL (Wg and Wu are then
- *   not read), or dwg_dev and dwu_dev (x is then not read).  cols == 0: nothing is done.  rows == 0 or
- *   outs == 0: what is asked for is zero-filled.
+ *   dg and du are rounded to ``dtype`` before the products (up to 8 rows: kept in two such terms).
+ *   dx_dev may be NULL (Wg and Wu are then not read), or dwg_dev and dwu_dev (x is then not read).
+ *   cols == 0: nothing is done.  rows == 0 or outs == 0: what is asked for is zero-filled.
  */
 int tg_gated_bwd(const void* dh_dev, const void* g_dev, const void* u_dev, const void* x_dev,
                  const void* wg_dev, const void* wu_dev, void* dx_dev, void* dwg_dev, void* dwu_dev,
@@ -538,7 +537,8 @@ int64_t tg_xent_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t vocab);
  *   NULL.  The logits are computed again, a piece of the vocabulary at a time (at most 256 MiB of
  *   their gradients, or 2048 words' where that is more); dl is rounded to ``dtype`` before the products,
  *   relative to the largest |dloss| (in fp16 times 2^15, so that small probabilities keep their bits;
- *   up to 8 rows: in two terms).  Rows with a wrong target give NaN.  An ignored row's x adds zero times itself to dW.  rows == 0: dW is zero-filled.
+ *   up to 8 rows: in two terms).  Rows with a wrong target give NaN.  An ignored row's x adds zero
+ *   times itself to dW.  rows == 0: dW is zero-filled.
  */
 int tg_xent_bwd(const float* dloss_dev, const void* x_dev, const void* w_dev,
                 const int64_t* targets_dev, const float* lse_dev, void* dx_dev, void* dw_dev,

@@ -21,6 +21,11 @@
 // could be 1.5 times as far off as one rounding of the result alone).  The second term is multiplied
 // with the same weights in shared memory.
 //
+// Measured (bf16, us): gated, 4 rows, 4096 x 8192 (134 MB of weights) 23.5, 5.7 TB/s; input gradient, 16
+// rows, 2048 x 8192 (34 MB) 7.5; loss over 32000 x 1024 of 64 rows 15.7, where the pair kernel takes 24.2
+// for 65; input gradient of 1024 x 32000 19.3 (23.6).  Gated tiles, 128 columns of two weights for 64 rows, are the
+// even point: 4096 x 8192 30.2 (29.5).
+//
 // Included by exactly one translation unit, after tg_linear_kernel.cuh.
 #pragma once
 

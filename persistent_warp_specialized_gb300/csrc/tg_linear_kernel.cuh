@@ -23,6 +23,10 @@
 // is free again before anything is stored.  Few tiles: K is split into ranges whose fp32 sums go to a
 // workspace [splits][rows rounded up to 32][N], and linear_join_kernel adds them in order.
 //
+// What bounds it is the tensor pipe, active 84 to 91 % of the time with every epilogue, and back to back
+// the card's power: 4096 x 4096 x 65536 with the statistics of a cross entropy 1069 us alone (2.06
+// PFLOP/s), 1240 among others at the power cap; input gradient 8192^3 593 and 682.
+//
 // Included by exactly one translation unit, after tg_wgrad_kernel.cuh.
 #pragma once
 
@@ -481,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                     idesc, in_seg != 0u || kk != 0u ? 1u : 0u);
             }
             commit(bar_consumed + 8u * s);
-            if (++in_seg == kLinSegment || k + 1 == nk) {
+            if (++in_seg == kLinSegment<EPI> || k + 1 == nk) {
               commit(bar_tmem_full + 8u * acc.slot);
               acc.advance(1);
               in_seg = 0;
@@ -563,7 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       // the sums of all segments: columns of chunk c0, then of c1
       float v[128];
       const uint32_t nk = un.k_hi - un.k_lo;
-      const uint32_t segments = (nk + kLinSegment - 1u) / kLinSegment;
+      const uint32_t segments = (nk + kLinSegment<EPI> - 1u) / kLinSegment<EPI>;
 #pragma unroll 1
       for (uint32_t sg = 0; sg < segments; ++sg, acc.advance(1)) {
         const bool got = pair_wait_or_abort(bar_tmem_full + 8u * acc.slot, acc.parity, abort_flag,

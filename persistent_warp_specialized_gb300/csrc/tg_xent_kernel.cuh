@@ -4,6 +4,9 @@
 // exp(l - m), and the target's logit t.  With M the largest m:  lse = M + log sum s exp(m - M),  loss =
 // lse - t.  Where a small vocabulary has few tiles and long sums, the sums are split instead and leave fp32
 // parts of the logits, which are added here before the same is done with them.
+//
+// Statistics are a 16th or a 32nd of what 16-bit logits would be: 8 bytes for 64 or 128 of them.  The join
+// of 4096 rows and 32768 words reads 17 MB in 8 us; that of a few rows is a launch's 3 to 4.
 #pragma once
 
 #include "tg_linear_kernel.cuh"
