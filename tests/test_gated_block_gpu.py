@@ -62,3 +62,46 @@ def test_gradients(example, rows, cols, outs, vocab, dtype):
     far["loss"] = float((loss.double() - want).detach().norm() / want.detach().norm())
     for name, d in far.items():
         assert d <= bound + (2 ** -5 if name == "wd" else 0), (name, far)
+
+
+def test_two_threads_at_once():
+    """Two host threads, each on a stream of its own, get what one alone gets: calls share no scratch."""
+    import threading
+
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def matrix(rows, cols, scale=1.0):
+        return (torch.randn((rows, cols), generator=gen, device="cuda") * scale).bfloat16()
+
+    sets = [(matrix(r, 264), matrix(264, 520, 0.06), matrix(264, 520, 0.06), matrix(3001, 264, 0.06),
+             torch.randint(0, 3001, (r,), generator=gen, device="cuda")) for r in (5, 300)]
+
+    def step(x, wg, wu, e, targets):
+        h, g, u = tg.gated_forward(x, wg, wu, keep=True)
+        loss, lse = tg.linear_cross_entropy(x, e, targets)
+        return (h, loss, lse, tg.input_grad(h, wg)) + tuple(tg.gated_backward(h, g, u, x, wg, wu)) + tuple(
+            tg.linear_cross_entropy_backward(torch.ones_like(loss), x, e, targets, lse))
+
+    alone = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    got, raised = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i].append(step(*sets[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # the main thread fails the test
+            raised.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not raised and tg.tg_device_status() == 0
+    for i in range(2):
+        assert len(got[i]) == 20
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(alone[i], outs))
