@@ -643,15 +643,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         }
       } else {
         // the target's place among this warp's columns, or a place that none of them has
-        const int64_t hot = row_in ? p.rows.targets[row] - static_cast<int64_t>(p.first_col) : -1;
-        const int32_t at = hot >= x0 && hot < x0 + 128 ? static_cast<int32_t>(hot) - x0 : -1;
+        // (differences from x0: x0 + 128 may be 2^31)
+        const uint64_t hot =
+            row_in ? static_cast<uint64_t>(p.rows.targets[row]) - p.first_col - static_cast<uint64_t>(x0)
+                   : 128u;
+        const int32_t at = hot < 128u ? static_cast<int32_t>(hot) : -1;
         if constexpr (EPI == kEpiStats) {
-          if (chunks == 1 || x0 + 128 > static_cast<int32_t>(o.N)) {
+          const int32_t left = static_cast<int32_t>(o.N) - x0;   // words from x0 on
+          if (chunks == 1 || left < 128) {
             // columns that another warp has, or past the vocabulary
-            const int32_t end = min(x0 + static_cast<int32_t>(64u * chunks), static_cast<int32_t>(o.N));
+            const int32_t end = min(static_cast<int32_t>(64u * chunks), left);
 #pragma unroll
             for (uint32_t i = 0; i < 128; ++i)
-              if (x0 + static_cast<int32_t>(i) >= end) v[i] = -INFINITY;
+              if (static_cast<int32_t>(i) >= end) v[i] = -INFINITY;
           }
           if (__any_sync(0xffffffffu, at >= 0)) {
             float l = 0.0f;
