@@ -503,7 +503,9 @@ int64_t tg_gated_fwd_workspace_bytes(int64_t rows, int64_t cols, int64_t outs);
 /*
  * tg_gated_bwd -- the gradients of tg_gated_fwd from dh, with g and u as it kept them:
  *     dg = dh u act'(g),  du = dh act(g);   dx = dg Wg^T + du Wu^T,  dWg = x^T dg,  dWu = x^T du
- *   dg and du are rounded to ``dtype`` before the products (up to 8 rows: kept in two such terms).
+ *   dg and du are rounded to ``dtype`` before the products (up to 8 rows: kept in two such terms); in fp16 times
+ *   a power of two that the largest of them determines, so that they may pass fp16's range where the
+ *   gradients do not, and small ones keep their bits (steps of at most 2^-26 of the largest).
  *   dx_dev may be NULL (Wg and Wu are then not read), or dwg_dev and dwu_dev (x is then not read).
  *   cols == 0: nothing is done.  rows == 0 or outs == 0: what is asked for is zero-filled.
  */

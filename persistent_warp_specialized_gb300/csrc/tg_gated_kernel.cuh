@@ -4,6 +4,15 @@
 //   and h from partial sums of g and u when K was split.
 //
 // Both are bound by memory: 8 values a thread and tensor in one 16-byte access each, two vectors ahead.
+//
+// fp16 has few exponents, and dg and du are products of three values: they may leave its range at either
+// end where the gradients that are made of them do not (dh of 2e-5 and u of 0.05: gradients 1.3e-3 off,
+// where a rounding makes 2e-4; dh of 8e3 and u of 20: no number at all).  So they are held times a power of two,
+// which the products' alpha undoes.  The first pass takes 2^4 and finds the largest; where that does not lie in
+// [4, 65504] then, which gradients of a scaled loss seldom miss, a second pass makes them again with the
+// power of two that takes the largest to 2^14 .. 2^15.  Steps are so at most 2^-26 of the largest value.  Measured
+// (fp16, whole backward pass, us; before / guess right / made again): 333 x 1000 x 2008 19.6 / 22.8 / 24.8,
+// 2048 x 2048 x 5632 131 / 136 / 152, 8192 x 4096 x 8192 1462 / 1436 / 1585.
 // Measured (bf16, 4096 x 8192, 336 MB read and written): SiLU 51 us, 6.5 TB/s; GELU 56, of which issuing
 // its instructions takes 68 % of the slots.
 #pragma once
@@ -28,14 +37,48 @@ struct GatedGradParams {
   int64_t ld_dh, ld_g, ld_u;       // elements
   uint32_t rows, vecs;             // vectors of 8 values in a row
   uint32_t act;
+  float* tops;                     // fp16: each block's largest |dg|, |du| that is finite
+  float* alpha;                    // fp16: what undoes the scale
 };
 
+constexpr int kGradGuess = 4;      // fp16: the first pass's power of two
+
+// The power of two for gradients of at most ``top``.
+__device__ __forceinline__ int grad_exponent(float top) {
+  const float guess = top * (1 << kGradGuess);
+  if (top == 0.0f || (guess >= 4.0f && guess <= 65504.0f)) return kGradGuess;
+  const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;   // top in 2^e .. 2^(e + 1)
+  return max(-30, min(14 - e, 60));   // |dg| < 2^33; past 2^-46 nothing is left in fp16 anyway
+}
+__device__ __forceinline__ float power_of_2(int e) { return __int_as_float((e + 127) << 23); }
+
+// The largest of a block's 256 threads' values, in every thread.
+__device__ __forceinline__ float block_top(float v) {
+  __shared__ float warps[8];
+#pragma unroll
+  for (uint32_t o = 16; o > 0; o /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if ((threadIdx.x & 31u) == 0) warps[threadIdx.x / 32u] = v;
+  __syncthreads();
+#pragma unroll
+  for (uint32_t w = 0; w < 8; ++w) v = fmaxf(v, warps[w]);
+  return v;
+}
+
 // A thread takes every so many'th vector of the matrix, two at a time.
-// TWO: in two terms.
-template <int DT, bool TWO>
+// TWO: in two terms.  AGAIN: the second pass in fp16, by as many blocks as the first.
+template <int DT, bool TWO, bool AGAIN>
 __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p) {
+  static_assert(DT == 0 || !AGAIN, "bf16 has fp32's exponents");
   grid_dependency_wait();
   grid_launch_dependents();
+  float factor = power_of_2(kGradGuess), top = 0.0f;
+  if constexpr (AGAIN) {
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += 256u) top = fmaxf(top, __ldcg(p.tops + i));
+    const int e = grad_exponent(block_top(top));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.alpha = power_of_2(-e);
+    if (e == kGradGuess) return;
+    factor = power_of_2(e);
+  }
   const uint64_t total = static_cast<uint64_t>(p.rows) * p.vecs;
   const uint64_t stride = static_cast<uint64_t>(gridDim.x) * blockDim.x;
   auto at = [](const void* base, uint64_t row, int64_t ld, uint32_t v) {
@@ -46,7 +89,15 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p
     const uint32_t dhw[4] = {dh4.x, dh4.y, dh4.z, dh4.w}, gw[4] = {g4.x, g4.y, g4.z, g4.w},
                    uw[4] = {u4.x, u4.y, u4.z, u4.w};
     uint32_t dgw[4], duw[4], dg_rest[4], du_rest[4];
-    auto pack = [](float x, float y, uint32_t& rest) {
+    auto pack = [&](float x, float y, uint32_t& rest) {
+      if constexpr (DT == 0) {
+        if constexpr (!AGAIN) {
+          top = fmaxf(top, fabsf(x) < INFINITY ? fabsf(x) : 0.0f);
+          top = fmaxf(top, fabsf(y) < INFINITY ? fabsf(y) : 0.0f);
+        }
+        x *= factor;
+        y *= factor;
+      }
       const uint32_t w = pack_out<DT>(__float_as_uint(x), __float_as_uint(y));
       if constexpr (TWO) {
         const float2 back = unpack_in<DT>(w);
@@ -91,6 +142,10 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p
     }
     work(r0, v0, dh0, g0, u0);
     if (two) work(r1, v1, dh1, g1, u1);
+  }
+  if constexpr (DT == 0 && !AGAIN) {
+    top = block_top(top);
+    if (threadIdx.x == 0) p.tops[blockIdx.x] = top;
   }
 }
 

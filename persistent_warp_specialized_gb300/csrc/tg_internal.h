@@ -231,10 +231,12 @@ struct GatedJoin {
 cudaError_t launch_gated_join(const GatedJoin& l, cudaStream_t stream);
 
 // dgu [rows, 2 outs] = (dh u act'(g), dh act(g)), side by side (tg_gated_kernel.cuh); rest: null, or the
-// same of what rounding them left
+// same of what rounding them left.  fp16: both times a power of two, *alpha its inverse; tops: kGradBlocks
+// values of scratch.
 struct GatedGrad {
   const void *dh, *g, *u;
   void *dgu, *rest;
+  float *tops, *alpha;          // bf16: not used
   int64_t rows, outs, ld_dh, ld_g, ld_u;
   uint32_t act;
   int dtype, sms;

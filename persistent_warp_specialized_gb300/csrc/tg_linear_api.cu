@@ -621,6 +621,8 @@ struct GatedBwd {
   GradPlans plans;
   uint64_t dgu_bytes, total;   // dgu_bytes: of one term
 };
+// In front of dg and du: the largest values of their blocks, and the factor that undoes their scale (fp16)
+constexpr uint64_t kGradTopsBytes = tg::kGradBlocks * 4, kGradScaleBytes = kGradTopsBytes + kWorkspaceAlign;
 // With null pointers where only sizes matter.
 GatedBwd gated_bwd_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& dx, const Mat& dwg,
                         const Mat& dwu, void* dgu, int dtype, int pairs) {
@@ -658,7 +660,7 @@ GatedBwd gated_bwd_plan(const Mat& x, const Mat& wg, const Mat& wu, const Mat& d
     if (two) p[0].a_rest[i] = p[1].b_rest[i] = part(1, i);
   }
   GatedBwd o = {{p[0], p[1]}, GradPlans(p, pairs), dgu_bytes, 0};
-  o.total = (two ? 2 : 1) * dgu_bytes + o.plans.bytes[0] + o.plans.bytes[1];
+  o.total = kGradScaleBytes + (two ? 2 : 1) * dgu_bytes + o.plans.bytes[0] + o.plans.bytes[1];
   return o;
 }
 
@@ -959,7 +961,9 @@ int tg_gated_bwd(const void* dh_dev, const void* g_dev, const void* u_dev, const
   }
   const Mat sx = {x_dev, rows, cols, ld_x, "x"}, swg = {wg_dev, cols, outs, ld_wg, "wg"},
             swu = {wu_dev, cols, outs, ld_wu, "wu"};   // sizes whether asked for or not
-  const GatedBwd o = gated_bwd_plan(sx, swg, swu, dx, dwg, dwu, workspace_dev, dtype, pairs);
+  char* const scale = static_cast<char*>(workspace_dev);
+  char* const dgu = scale ? scale + kGradScaleBytes : nullptr;
+  GatedBwd o = gated_bwd_plan(sx, swg, swu, dx, dwg, dwu, dgu, dtype, pairs);
   TG_TRY(check_workspace(workspace_dev, workspace_bytes, o.total));
   const Region r[] = {region(dx), region(dwg), region(dwu), {workspace_dev, o.total, "workspace"},
                       region(dh), region(g), region(u), region(x), region(wg), region(wu)};
@@ -968,8 +972,11 @@ int tg_gated_bwd(const void* dh_dev, const void* g_dev, const void* u_dev, const
   e.dh = dh_dev;
   e.g = g_dev;
   e.u = u_dev;
-  e.dgu = workspace_dev;
-  e.rest = two_terms(rows) ? static_cast<char*>(workspace_dev) + o.dgu_bytes : nullptr;
+  e.dgu = dgu;
+  e.rest = two_terms(rows) ? dgu + o.dgu_bytes : nullptr;
+  e.tops = reinterpret_cast<float*>(scale);
+  e.alpha = reinterpret_cast<float*>(scale + kGradTopsBytes);
+  if (dtype == TG_F16) o.p[0].alpha = o.p[1].alpha = e.alpha;
   e.rows = rows;
   e.outs = outs;
   e.ld_dh = ld_dh;
@@ -980,8 +987,8 @@ int tg_gated_bwd(const void* dh_dev, const void* g_dev, const void* u_dev, const
   e.sms = sms;
   const cudaError_t err = tg::launch_gated_grad(e, st);
   if (err != cudaSuccess) return fail_cuda("gated gradient launch", err);
-  char* const rest = static_cast<char*>(workspace_dev) + (two_terms(rows) ? 2 : 1) * o.dgu_bytes;
-  char* const partials[2] = {rest, rest + o.plans.bytes[0]};
+  char* const sums = dgu + (two_terms(rows) ? 2 : 1) * o.dgu_bytes;
+  char* const partials[2] = {sums, sums + o.plans.bytes[0]};
   return run_grads(o.p, o.plans, {dx_dev != nullptr, weights}, true, partials, sms, pairs, st);
 }
 

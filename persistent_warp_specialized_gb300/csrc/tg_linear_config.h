@@ -48,6 +48,10 @@ static_assert(128 * kLinFewRegs + 256 * kLinEpiRegs <= int(kLinThreads) * kLinLa
 // Columns of a gated product in one tile: half of the accumulator's are g, half u.
 constexpr int kGatedTileN = kBN / 2;
 
+// Blocks at most of the pass that makes dg and du of a gated product's gradient (8 an SM): in fp16 each
+// leaves its largest value.
+constexpr uint32_t kGradBlocks = 2048;
+
 // Rows of one split's partial sums: whole boxes of 32 rows
 constexpr uint32_t kPartialRows = 32;
 

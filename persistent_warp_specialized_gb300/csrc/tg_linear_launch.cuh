@@ -337,11 +337,18 @@ cudaError_t launch_gated_grad(const GatedGrad& l, cudaStream_t stream) {
   p.rows = static_cast<uint32_t>(l.rows);
   p.vecs = static_cast<uint32_t>(l.outs / 8);
   p.act = l.act;
-  const dim3 grid(blocks_for(static_cast<uint64_t>(p.rows) * p.vecs, l.sms, 8));
+  p.tops = l.tops;
+  p.alpha = l.alpha;
+  const uint32_t blocks = blocks_for(static_cast<uint64_t>(p.rows) * p.vecs, l.sms, 8);
+  const dim3 grid(blocks < kGradBlocks ? blocks : kGradBlocks);
   auto run = [&](auto kernel) { return launch_pdl(kernel, grid, 256, 0, stream, p); };
-  if (l.rest != nullptr)
-    return l.dtype == 0 ? run(gated_grad_kernel<0, true>) : run(gated_grad_kernel<1, true>);
-  return l.dtype == 0 ? run(gated_grad_kernel<0, false>) : run(gated_grad_kernel<1, false>);
+  const bool two = l.rest != nullptr;
+  if (l.dtype != 0)
+    return two ? run(gated_grad_kernel<1, true, false>) : run(gated_grad_kernel<1, false, false>);
+  const cudaError_t e =
+      two ? run(gated_grad_kernel<0, true, false>) : run(gated_grad_kernel<0, false, false>);
+  if (e != cudaSuccess) return e;
+  return two ? run(gated_grad_kernel<0, true, true>) : run(gated_grad_kernel<0, false, true>);
 }
 
 namespace {
