@@ -137,6 +137,7 @@ struct LinearProduct {
   uint32_t m_blocks, n_blocks, k_blocks, n_seg, k_seg, group, column_major;
   uint32_t split_from, total_units, splits, blocks_per_split;   // units: per split
   uint32_t partial, part_rows;
+  uint32_t segment_log;         // 2^segment_log k-blocks share an accumulator
   const float* alpha;
 };
 // The cross entropy's rows (RowWeights)

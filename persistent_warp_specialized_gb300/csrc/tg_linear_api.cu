@@ -41,6 +41,7 @@ struct Product {
   // the first's; the caller joins them after the last
   int accumulate = 0;
   uint32_t act = 0, keep = 0;
+  bool logits = false;      // sums of logits: shorter segments
   uint32_t first_col = 0, slots = 0;
   void* stats = nullptr;
   float* hit = nullptr;
@@ -288,6 +289,7 @@ int encode_product(tg::LinearProduct* l, const Product& p, const Plan& w, char* 
   l->splits = w.splits;
   l->blocks_per_split = w.blocks_per_split;
   l->part_rows = w.part_rows;
+  l->segment_log = p.logits ? tg::kLogitSegmentLog : tg::kLinSegmentLog;
   l->alpha = p.alpha;
   return TG_OK;
 }
@@ -685,6 +687,7 @@ Product logits_product(int epi, const Mat& x, const Mat& w, int64_t first, int64
                        const tg::XentRows& loss, int dtype) {
   Product p;
   p.epi = epi;
+  p.logits = true;
   p.dtype = dtype;
   p.M = x.rows;
   p.N = n;

@@ -95,6 +95,7 @@ struct LinearProblem {
   uint32_t a_mn, b_mn;               // the operand lies with m (n) contiguous; a_mn: b_mn too
   uint32_t partial;                  // kEpiStore: 0 rounded, 1 fp32 stored, 2 fp32 added to what is there
   uint32_t part_rows;                // rows of one split's partial sums
+  uint32_t segment_log;              // kEpiStore: 2^segment_log k-blocks share an accumulator
   const float* alpha;                // kEpiStore: a factor of every result, or null
 };
 
@@ -307,6 +308,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   auto b_lies_mn = [](const LinearProblem& q) {
     return EPI == kEpiGated || (EPI == kEpiStore && q.b_mn != 0u);
   };
+  // and how long its segments are: logits that are stored as parts have shorter ones than results
+  auto segment_log_of = [](const LinearProblem& q) {
+    return EPI == kEpiStore   ? q.segment_log
+           : EPI == kEpiGated ? kLinSegmentLog
+                              : kLogitSegmentLog;
+  };
   __shared__ LinearCtl ctl;
 
   const uint32_t warp = threadIdx.x >> 5;
@@ -467,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                  (A ? 1u << 15 : 0u) | (B ? 1u << 16 : 0u);
           const uint32_t a_lo = static_cast<uint32_t>(A ? mn_desc : k_desc);
           const uint32_t b_lo = static_cast<uint32_t>(B ? mn_desc : k_desc) + (kOperand >> 4);
-          const uint32_t nk = un.k_hi - un.k_lo;
+          const uint32_t nk = un.k_hi - un.k_lo, segment = 1u << segment_log_of(un.q());
           uint32_t in_seg = 0;          // k-blocks of the segment so far
           for (uint32_t k = 0; k < nk; ++k, ring.advance(1)) {
             const uint32_t s = ring.slot;
@@ -485,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                     idesc, in_seg != 0u || kk != 0u ? 1u : 0u);
             }
             commit(bar_consumed + 8u * s);
-            if (++in_seg == kLinSegment<EPI> || k + 1 == nk) {
+            if (++in_seg == segment || k + 1 == nk) {
               commit(bar_tmem_full + 8u * acc.slot);
               acc.advance(1);
               in_seg = 0;
@@ -567,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       // the sums of all segments: columns of chunk c0, then of c1
       float v[128];
       const uint32_t nk = un.k_hi - un.k_lo;
-      const uint32_t segments = (nk + kLinSegment<EPI> - 1u) / kLinSegment<EPI>;
+      const uint32_t segments = ((nk - 1u) >> segment_log_of(o)) + 1u;
 #pragma unroll 1
       for (uint32_t sg = 0; sg < segments; ++sg, acc.advance(1)) {
         const bool got = pair_wait_or_abort(bar_tmem_full + 8u * acc.slot, acc.parity, abort_flag,

@@ -47,6 +47,7 @@ LinearParams params_of(const LinearLaunch& l) {
     to.b_mn = from.b_mn;
     to.partial = from.partial;
     to.part_rows = from.part_rows;
+    to.segment_log = from.segment_log;
     to.alpha = from.alpha;
     p.units[i] = to.total_units * to.splits;
   }
