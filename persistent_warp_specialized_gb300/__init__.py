@@ -825,8 +825,12 @@ def _calls():
 
         load_library()
         if not os.path.exists(TORCH_PATH):
+            from . import _build
+
+            why = _build.torch_error()
             raise RuntimeError(
-                f"{TORCH_PATH} is not built; run persistent_warp_specialized_gb300._build.build()")
+                f"{TORCH_PATH} " + (f"could not be built: {why}" if why else
+                                    "is not built; run persistent_warp_specialized_gb300._build.build()"))
         spec = importlib.util.spec_from_file_location("tg_torch", TORCH_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -5,8 +5,10 @@
 Five translation units compile in parallel (kernels and C-ABI host code) and are
 linked into ``persistent_warp_specialized_gb300/libtg.so`` with the CUDA runtime linked
 statically.  Beside them, where torch is installed, ``tg_torch.so``: the CPython module by which
-Python calls the products with fused epilogues on torch tensors.  A stamp of the sources and flags
-(and of torch's and Python's versions) skips rebuilding when nothing changed.
+Python calls the products with fused epilogues on torch tensors.  It needs g++, Python's headers and
+a torch with CUDA, which the library and all other calls do without: where it cannot be built, the
+reason is printed and kept for the first call that needs the module.  Stamps of the sources and flags
+(for the module of torch's and Python's versions too) skip rebuilding when nothing changed.
 """
 
 import hashlib
@@ -25,6 +27,8 @@ LIB_PATH = os.path.join(HERE, "libtg.so")
 STAMP = os.path.join(BUILD_DIR, "libtg.stamp")
 TORCH_SOURCE = "tg_torch.cpp"
 TORCH_PATH = os.path.join(HERE, "tg_torch.so")
+TORCH_STAMP = os.path.join(BUILD_DIR, "tg_torch.stamp")
+TORCH_ERROR = os.path.join(BUILD_DIR, "tg_torch.error")   # why it could not be built
 
 SOURCES = ["tg_gemm.cu", "tg_train.cu", "tg_api.cu", "tg_train_api.cu", "tg_linear_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -47,32 +51,35 @@ def _torch_dir():
     return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
 
 
-def _torch_version(root):
-    """What tg_torch.so has to be built again for: torch's version file and Python's version."""
-    with open(os.path.join(root, "version.py")) as f:
-        return f.read() + sys.version
-
-
-def _inputs():
-    files = [os.path.join(ROOT, "include", "tg.h")]
-    for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".cu", ".cuh", ".h", ".cpp")):
-            files.append(os.path.join(CSRC, name))
-    return files
-
-
-def _stamp():
-    """sha256 of the library's sources (by path relative to the repository), flags and torch's
-    version."""
+def _hash(paths, *texts):
+    """sha256 of files (by path relative to the repository) and texts."""
     h = hashlib.sha256()
-    for path in _inputs():
+    for path in paths:
         h.update(os.path.relpath(path, ROOT).encode())
         with open(path, "rb") as f:
             h.update(f.read())
-    h.update(" ".join(FLAGS).encode())
-    root = _torch_dir()
-    h.update(_torch_version(root).encode() if root else b"no torch")
+    for text in texts:
+        h.update(text.encode())
     return h.hexdigest()
+
+
+HEADER = os.path.join(ROOT, "include", "tg.h")
+
+
+def _stamp():
+    """What libtg.so is built from."""
+    names = sorted(n for n in os.listdir(CSRC) if n.endswith((".cu", ".cuh", ".h")))
+    return _hash([HEADER] + [os.path.join(CSRC, n) for n in names], " ".join(FLAGS))
+
+
+def _torch_stamp(root):
+    """What tg_torch.so is built from, torch's version file and Python's version among it."""
+    try:
+        with open(os.path.join(root, "version.py")) as f:
+            version = f.read()
+    except OSError:
+        version = ""
+    return _hash([HEADER, os.path.join(CSRC, TORCH_SOURCE)], root, version, sys.version)
 
 
 # The sources each GEMM kernel's device code is built from (a profile taken of a kernel stays
@@ -104,71 +111,126 @@ def kernel_stamp(kernel):
     return h.hexdigest()
 
 
-def build(force=False, verbose=False, ptxas_info=False):
-    """Compile libtg.so if its sources changed; returns its path."""
-    stamp = _stamp()
-    root = _torch_dir()
-    if (not force and os.path.exists(LIB_PATH) and os.path.exists(STAMP)
-            and (root is None or os.path.exists(TORCH_PATH))):
-        with open(STAMP) as f:
-            if f.read().strip() == stamp:
-                return LIB_PATH
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    cc = nvcc()
-    extra = ["-Xptxas", "-v"] if ptxas_info else []
-    procs = []
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
-        objs.append(obj)
-        cmd = [cc] + FLAGS + PARALLEL + extra + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    if root is not None:
-        obj = os.path.join(BUILD_DIR, "tg_torch.o")
-        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
-               "-I", os.path.join(root, "include"),
-               "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-               "-I", sysconfig.get_paths()["include"],
-               "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include"),
-               "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((TORCH_SOURCE,
-                      subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = []
-    for src, p in procs:
-        out, _ = p.communicate()
-        text = out.decode(errors="replace")
-        if p.returncode != 0:
-            failed.append(f"--- {src}\n{text}")
-        elif verbose or ptxas_info:
-            print(text, end="", flush=True)
-    if failed:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
-    tmp = LIB_PATH + ".tmp"
-    cmd = [cc] + ARCH + ["-shared", "-Xlinker", "-soname=libtg.so", "-o", tmp] + objs
+def _read(path):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _write(path, text):
+    with open(path, "w") as f:
+        f.write(text)
+
+
+def torch_error():
+    """Why tg_torch.so could not be built the last time, or None."""
+    return _read(TORCH_ERROR)
+
+
+def _start(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
-    os.replace(tmp, LIB_PATH)
-    if root is not None:
-        tmp = TORCH_PATH + ".tmp"
-        cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp,
-               os.path.join(BUILD_DIR, "tg_torch.o"), "-L", os.path.join(root, "lib"), "-L", HERE,
-               "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-l:libtg.so",
-               "-Wl,-rpath,$ORIGIN"]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-        if r.returncode != 0:
-            raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
-        os.replace(tmp, TORCH_PATH)
-    with open(STAMP, "w") as f:
-        f.write(stamp)
+    try:
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except OSError as e:
+        raise RuntimeError(f"{cmd[0]}: {e}") from e
+
+
+def _finish(proc, what, verbose=False):
+    """Waits for a command of _start; raises with its output if it failed."""
+    text = proc.communicate()[0].decode(errors="replace")
+    if proc.returncode != 0:
+        raise RuntimeError(f"{what}\n{text}")
+    if verbose:
+        print(text, end="", flush=True)
+
+
+def _gxx():
+    return shutil.which("g++") or "g++"
+
+
+def _start_torch(root, cc, obj, verbose):
+    return _start([_gxx(), "-O2", "-std=c++17", "-fPIC", "-Wall",
+                   "-I", os.path.join(root, "include"),
+                   "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                   "-I", sysconfig.get_paths()["include"],
+                   "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include"),
+                   "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj], verbose)
+
+
+def _link_torch(root, obj, verbose):
+    tmp = TORCH_PATH + ".tmp"
+    _finish(_start([_gxx(), "-shared", "-o", tmp, obj, "-L", os.path.join(root, "lib"),
+                    "-L", os.path.dirname(LIB_PATH), "-ltorch_python", "-ltorch_cpu", "-lc10",
+                    "-lc10_cuda", "-l:libtg.so", "-Wl,-rpath,$ORIGIN"], verbose), "link failed:")
+    os.replace(tmp, TORCH_PATH)
+
+
+def _remove(path):
+    if os.path.exists(path):
+        os.remove(path)
+
+
+def build(force=False, verbose=False, ptxas_info=False):
+    """Compile libtg.so, and tg_torch.so beside it, if their sources changed; returns libtg.so's path.
+    Raises if libtg.so cannot be built (torch_error() says whether tg_torch.so could be)."""
+    stamp = _stamp()
+    root = _torch_dir()
+    torch_stamp = _torch_stamp(root) if root else None
+    library = force or not os.path.exists(LIB_PATH) or _read(STAMP) != stamp
+    # a failure is kept too: it is tried again when something changed, or by force
+    module = root is not None and (
+        force or _read(TORCH_STAMP) != torch_stamp
+        or not (os.path.exists(TORCH_PATH) or os.path.exists(TORCH_ERROR)))
+    if not library and not module:
+        return LIB_PATH
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    cc = nvcc()
+    torch_obj, torch_proc, why = os.path.join(BUILD_DIR, "tg_torch.o"), None, None
+    if module:
+        try:
+            torch_proc = _start_torch(root, cc, torch_obj, verbose)
+        except RuntimeError as e:
+            why = str(e)
+    if library:
+        extra = ["-Xptxas", "-v"] if ptxas_info else []
+        objs, procs, failed = [], [], []
+        for src in SOURCES:
+            obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
+            objs.append(obj)
+            procs.append((src, _start([cc] + FLAGS + PARALLEL + extra
+                                      + ["-c", os.path.join(CSRC, src), "-o", obj], verbose)))
+        for src, p in procs:
+            try:
+                _finish(p, f"--- {src}", verbose or ptxas_info)
+            except RuntimeError as e:
+                failed.append(str(e))
+        if failed:
+            if torch_proc is not None:
+                torch_proc.communicate()
+            raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+        tmp = LIB_PATH + ".tmp"
+        _finish(_start([cc] + ARCH + ["-shared", "-Xlinker", "-soname=libtg.so", "-o", tmp] + objs,
+                       verbose), "link failed:")
+        os.replace(tmp, LIB_PATH)
+        _write(STAMP, stamp)
+    if module:
+        try:
+            if torch_proc is not None:
+                _finish(torch_proc, f"--- {TORCH_SOURCE}", verbose)
+                _link_torch(root, torch_obj, verbose)
+        except RuntimeError as e:
+            why = str(e)
+        if why is None:
+            _remove(TORCH_ERROR)
+        else:
+            _remove(TORCH_PATH)      # not one of other sources
+            _write(TORCH_ERROR, why)
+            print(f"tg_torch.so was not built, so the fused products cannot be called on torch tensors "
+                  f"(--force tries again): {why}", file=sys.stderr)
+        _write(TORCH_STAMP, torch_stamp)
     return LIB_PATH
 
 
