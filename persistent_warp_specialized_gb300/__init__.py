@@ -872,8 +872,8 @@ def gated_backward(dh, g, u, x, w_gate, w_up, act="silu", stream=None):
 
 def linear_cross_entropy(x, w, targets, ignore_index=-100, stream=None):
     """torch convenience: (loss, lse), float32 [rows], of the logits x w^T, which are not kept: x
-    [rows, cols] and w [vocab, cols] float16 or bfloat16, targets int64 [rows].  Rows whose target is
-    ignore_index have loss 0; other targets outside the vocabulary give NaN."""
+    [rows, cols] and w [vocab, cols] float16 or bfloat16, targets int64 [rows] of any stride.  Rows
+    whose target is ignore_index have loss 0; other targets outside the vocabulary give NaN."""
     calls = _torch_calls or _calls()
     if stream is None:
         return calls.linear_cross_entropy(x, w, targets, ignore_index)
@@ -883,7 +883,7 @@ def linear_cross_entropy(x, w, targets, ignore_index=-100, stream=None):
 
 def linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index=-100, stream=None):
     """torch convenience: (dx, dw) of linear_cross_entropy from the gradient of each row's loss,
-    float32 [rows], and the lse that it returned."""
+    float32 [rows] of any stride (an expanded one too), and the lse that it returned."""
     calls = _torch_calls or _calls()
     if stream is None:
         return calls.linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index)

@@ -89,14 +89,16 @@ struct Matrix {
   void* p() const { return t.data_ptr(); }
 };
 
-// A contiguous vector of a value for each row.
-const at::Tensor& row_values(PyObject* o, const char* name, at::ScalarType type, int64_t rows) {
+// A value for each row, next to each other: the tensor itself, or a copy where it lies otherwise (an
+// expanded gradient, as sum() hands it back, or a column of a matrix).  A copy goes back to torch's
+// allocator as a workspace does.
+at::Tensor row_values(PyObject* o, const char* name, at::ScalarType type, int64_t rows) {
   const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != type || t.dim() != 1 || t.size(0) != rows || !t.is_contiguous())
-    raise(PyExc_ValueError, std::string(name) + " must be a contiguous " +
-                                (type == at::kLong ? "int64" : "float32") + " tensor of " +
+  if (t.scalar_type() != type || t.dim() != 1 || t.size(0) != rows)
+    raise(PyExc_ValueError, std::string(name) + " must be " +
+                                (type == at::kLong ? "an int64" : "a float32") + " tensor of " +
                                 std::to_string(rows) + " values");
-  return t;
+  return t.contiguous();
 }
 
 at::Tensor new_rows(const Matrix& like, int64_t rows) {
@@ -215,7 +217,7 @@ PyObject* linear_cross_entropy(PyObject* const* a) {
   if (w.cols != x.cols)
     raise(PyExc_ValueError, "x has " + std::to_string(x.cols) + " columns and w " +
                                 std::to_string(w.cols));
-  const at::Tensor& targets = row_values(a[2], "targets", at::kLong, x.rows);
+  const at::Tensor targets = row_values(a[2], "targets", at::kLong, x.rows);
   const int64_t ignore = integer(a[3]);
   const at::Tensor loss = new_rows(x, x.rows), lse = new_rows(x, x.rows);
   const Workspace ws(x, checked(tg_xent_fwd_workspace_bytes(x.rows, x.cols, w.rows)));
@@ -234,9 +236,9 @@ PyObject* linear_cross_entropy_backward(PyObject* const* a) {
   if (w.cols != x.cols)
     raise(PyExc_ValueError, "x has " + std::to_string(x.cols) + " columns and w " +
                                 std::to_string(w.cols));
-  const at::Tensor& dloss = row_values(a[0], "dloss", at::kFloat, x.rows);
-  const at::Tensor& targets = row_values(a[3], "targets", at::kLong, x.rows);
-  const at::Tensor& lse = row_values(a[4], "lse", at::kFloat, x.rows);
+  const at::Tensor dloss = row_values(a[0], "dloss", at::kFloat, x.rows);
+  const at::Tensor targets = row_values(a[3], "targets", at::kLong, x.rows);
+  const at::Tensor lse = row_values(a[4], "lse", at::kFloat, x.rows);
   const int64_t ignore = integer(a[5]);
   const Matrix dx(x, x.rows, x.cols), dw(x, w.rows, w.cols);
   const Workspace ws(x, checked(tg_xent_bwd_workspace_bytes(x.rows, x.cols, w.rows)));
