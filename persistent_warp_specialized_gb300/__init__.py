@@ -829,7 +829,7 @@ def _calls():
 
             why = _build.torch_error()
             raise RuntimeError(
-                f"{TORCH_PATH} " + (f"could not be built: {why}" if why else
+                f"{TORCH_PATH} " + (f"could not be built (build(force=True) tries again): {why}" if why else
                                     "is not built; run persistent_warp_specialized_gb300._build.build()"))
         spec = importlib.util.spec_from_file_location("tg_torch", TORCH_PATH)
         module = importlib.util.module_from_spec(spec)

@@ -97,6 +97,11 @@ KERNEL_SOURCES = {
     "gemm_mxfp8_pair_ws": ["tg_config.h", "tg_ptx.cuh", "tg_tile_scheduler.cuh",
                            "tg_gemm_kernel.cuh", "tg_gemm_pair_kernel.cuh", "tg_mx_kernel.cuh",
                            "tg_mx_pair_kernel.cuh"],
+    # the products with fused epilogues and the kernels around them, profiled together
+    "fused_products": ["tg_config.h", "tg_ptx.cuh", "tg_tile_scheduler.cuh", "tg_linear_config.h",
+                       "tg_linear_units.h", "tg_linear_kernel.cuh", "tg_few_config.h",
+                       "tg_few_kernel.cuh", "tg_gated_kernel.cuh", "tg_outer_kernel.cuh",
+                       "tg_xent_kernel.cuh"],
 }
 
 

@@ -134,7 +134,7 @@ int wgrad_ready(int* sms_out, int* max_pairs_out) {
 int linear_ready(int* sms_out, int* max_pairs_out) {
   return family_ready(sms_out, max_pairs_out, &DeviceInfo::linear_pairs,
                       tg::prepare_linear_kernels,
-                      "preparing the fused products (shared memory limit, cluster occupancy)");
+                      "preparing the fused products (shared memory limit, registers, cluster occupancy)");
 }
 
 int check_device_ptr(const void* p, const char* name) {
